@@ -249,9 +249,10 @@ def _run_own(s):
     from state_space_model_ssd_amd import binding as lib
     op = s["op"]
     if op == "conv_fwd":
-        return lib.conv_fwd(s["x"], s["weight"], s["bias"], splits=s["splits"],
-                            initial_states=s["init"], cu_seqlens=s["cu"], activation=s["act"],
-                            return_final_states=s["final"])
+        *out, final = lib.conv_fwd(s["x"], s["weight"], s["bias"], splits=s["splits"],
+                                   initial_states=s["init"], cu_seqlens=s["cu"],
+                                   activation=s["act"], return_final_states=s["final"])
+        return tuple(out), final
     if op == "conv_bwd":
         g = lib.conv_bwd(s["x"], s["weight"], s["dout"], s["bias"], splits=s["splits"],
                          initial_states=s["init"], cu_seqlens=s["cu"], activation=s["act"],
