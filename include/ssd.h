@@ -419,6 +419,215 @@ ssd_status_t ssd_fwd_noalloc(const ssd_problem_t* p,
                              const int32_t* cu_seqlens, const int32_t* seq_idx,
                              void* out, float* final_states, void* stream);
 
+/*
+ * The short causal convolution in front of the SSD in a Mamba-2 layer: it
+ * makes x, B and C from the layer's projection, channel by channel.  The
+ * pages do not write it out (they list the layer's kernels, clova.ai page,
+ * table "Share of compute time by kernel"); it is read here as the Mamba-2
+ * layer's depthwise convolution of `width` K taps over the channels
+ * x | B | C side by side.  For sequence s, token t of it and channel c:
+ *
+ *   pre[t,c] = bias[c] + sum_{k < K} weight[c,k] * in[t - (K-1) + k, c]
+ *   out[t,c] = pre * sigmoid(pre)   (activation 1: SiLU)   or   pre (0)
+ *   in[t] for -(K-1) <= t < 0 is initial_states[s, K-1 + t] (or 0)
+ *   final_states[s] = the last K-1 rows of in, oldest first (a sequence
+ *                     shorter than K-1 keeps rows of its initial state)
+ *
+ * Layouts (C = channels_x + channels_b + channels_c):
+ *   xbc      one row of C channels per token, `in_stride` elements from one
+ *            token to the next (0: C), so the rows may lie inside wider ones
+ *            (the projection's z | x | B | C | dt); batch rows follow one
+ *            another, seqlen * in_stride apart                       dtype
+ *   weight   [C][K] fp32;  bias [C] fp32 (nullable: 0)
+ *   initial_states, final_states  [nstates][K-1][C] dtype (nullable)
+ *   out_x, out_b, out_c  [batch][seqlen][channels_*] dtype, each contiguous:
+ *            ssd_fwd's x, B and C.  An output with no channels may be NULL.
+ * Any channel counts and any alignment of the dtype's size are taken.
+ * Accumulation in fp32, one rounding of each output to the dtype; final
+ * states are copies.  A packed batch (nseq > 0, batch 1) takes cu_seqlens
+ * (non-decreasing); tokens before its first entry and from its last entry on
+ * belong to no sequence, and their rows of the outputs keep what they held.
+ * Malformed cu_seqlens give unspecified outputs but never an access outside
+ * the given buffers.  No pointer may alias another.  Errors as for ssd_fwd;
+ * width outside 2..4 is SSD_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  int64_t batch;       /* rows; must be 1 for a packed batch               */
+  int64_t seqlen;      /* tokens per row (packed batch: total tokens); >= 0 */
+  int64_t nseq;        /* 0: rows are the sequences; > 0: packed batch      */
+  int64_t channels_x;  /* nheads * headdim of the SSD that follows; >= 1    */
+  int64_t channels_b;  /* ngroups * dstate; >= 0                            */
+  int64_t channels_c;  /* ngroups * dstate; >= 0                            */
+  int64_t width;       /* taps K, 2 to 4                                    */
+  int64_t in_stride;   /* elements between tokens of xbc; 0: contiguous     */
+  int64_t din_stride;  /* the same of dxbc (ssd_conv_bwd)                   */
+  int32_t dtype;       /* ssd_dtype_t of xbc, the states and the outputs    */
+  int32_t activation;  /* 0: none, 1: SiLU                                  */
+} ssd_conv_problem_t;
+
+ssd_status_t ssd_conv_fwd(const ssd_conv_problem_t* p, const void* xbc, const float* weight,
+                          const float* bias, const void* initial_states,
+                          const int32_t* cu_seqlens, void* out_x, void* out_b, void* out_c,
+                          void* final_states, void* stream);
+
+/*
+ * The backward of ssd_conv_fwd: gradients of sum(out * dout) +
+ * sum(final_states * dfinal_states).  With dpre = dout * act'(pre),
+ *
+ *   dxbc[t]     = sum_{j < K} weight[K-1-j] * dpre[t + j]   (t + j inside the
+ *                 sequence) + the row of dfinal_states that holds token t
+ *   dweight[k]  = sum_t dpre[t] * in[t - (K-1) + k];   dbias = sum_t dpre[t]
+ *   dinitial_states likewise for the rows before a sequence's first token.
+ *
+ *   dout_x, dout_b, dout_c  like the outputs (ssd_bwd's dx, dB and dC)
+ *   dfinal_states           like final_states (nullable: 0)
+ *   dxbc                    like xbc, din_stride elements from token to token
+ *                           (0: C); what lies between the rows is not written
+ *   dweight [C][K] fp32 (required);  dbias [C] fp32 (nullable: not computed)
+ *   dinitial_states         like initial_states (nullable: not computed)
+ * pre is computed again from xbc.  Tokens outside every sequence add nothing
+ * and their rows of dxbc are not written.  The workspace (no initial contents)
+ * is ssd_conv_bwd_workspace_size bytes, 256-byte aligned.  No atomics:
+ * results are deterministic.
+ */
+size_t ssd_conv_bwd_workspace_size(const ssd_conv_problem_t* p);
+
+ssd_status_t ssd_conv_bwd(const ssd_conv_problem_t* p, const void* xbc, const float* weight,
+                          const float* bias, const void* initial_states,
+                          const int32_t* cu_seqlens, const void* dout_x, const void* dout_b,
+                          const void* dout_c, const void* dfinal_states, void* dxbc,
+                          float* dweight, float* dbias, void* dinitial_states, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * ssd_conv_fwd for one new token per sequence, in place on a cache of states:
+ * p->seqlen is 1 and p->nseq 0, row b of xbc is the next token of the
+ * sequence whose state is conv_states[slots[b]] (slots NULL: conv_states[b]),
+ * [nslots][K-1][C] dtype as final_states.  The slot's rows move up by one and
+ * the token becomes the last.
+ *   - A row whose slot is outside [0, nslots) is padding: its outputs keep
+ *     what they held and no state changes.
+ *   - A row whose slot an earlier row (a lower b) has is padding as well, so
+ *     the same slot twice is well defined: the first row has it.
+ * Without slots, nslots >= batch.
+ */
+ssd_status_t ssd_conv_step(const ssd_conv_problem_t* p, const void* xbc, const float* weight,
+                           const float* bias, void* conv_states, int64_t nslots,
+                           const int32_t* slots, void* out_x, void* out_b, void* out_c,
+                           void* stream);
+
+/*
+ * The SSD for one new token per sequence: the recurrence at the top of this
+ * file, one update, in place on a cache of states (decoding after ssd_fwd,
+ * whose final_states are the first states).  For row b with its state h =
+ * states[slots[b]] and head i (group g = i / (nheads / ngroups)):
+ *
+ *   delta = clamp(softplus(dt[b,i] + dt_bias[i]), dt_min, dt_max)
+ *   h[i]  = exp(delta * A[i]) * h[i] + delta * x[b,i,:] (outer) B[b,g,:]
+ *   out[b,i,:] = h[i] . C[b,g,:]  +  D[i] * x[b,i,:]
+ *
+ *   x       [batch][nheads][headdim] dtype, rows x_stride elements apart
+ *   dt      [batch][nheads] fp32 or the dtype (dt_dtype), rows dt_stride apart
+ *   B, C    [batch][ngroups][dstate] dtype, rows b_stride and c_stride apart
+ *           (a stride of 0 is a contiguous tensor's; rows may lie inside
+ *           wider ones, as the projection and the convolution leave them)
+ *   A       [nheads] fp32;  D, dt_bias [nheads] fp32 (nullable)
+ *   states  [nslots][nheads][headdim][dstate] fp32, updated in place
+ *   slots   [batch] int32 (nullable: row b has slot b, nslots >= batch);
+ *           padding and repeated slots as for ssd_conv_step
+ *   out     [batch][nheads][headdim] dtype, contiguous
+ * Any headdim, and any dstate up to 256 (else SSD_ERR_UNSUPPORTED): the
+ * compiled chunk configurations do not matter here.  The state is held and
+ * updated in fp32; out is rounded once.  No workspace; `states` is the only
+ * buffer that is both read and written, and no pointer may alias another.
+ */
+typedef struct {
+  int64_t batch;      /* rows; >= 0                                         */
+  int64_t nheads;     /* H >= 1                                             */
+  int64_t headdim;    /* P >= 1                                             */
+  int64_t dstate;     /* N, 1 to 256                                        */
+  int64_t ngroups;    /* G >= 1, H % G == 0                                 */
+  int64_t nslots;     /* states in the cache                                */
+  int64_t x_stride, dt_stride, b_stride, c_stride;  /* elements; 0: contiguous */
+  int32_t dtype;      /* ssd_dtype_t of x, B, C and out                     */
+  int32_t dt_dtype;   /* ssd_dtype_t of dt                                  */
+  float dt_min;       /* clamp of delta, as in ssd_problem_t                */
+  float dt_max;
+} ssd_step_problem_t;
+
+ssd_status_t ssd_step(const ssd_step_problem_t* p, const void* x, const void* dt,
+                      const float* dt_bias, const float* A, const void* B, const void* C,
+                      const float* D, float* states, const int32_t* slots, void* out,
+                      void* stream);
+
+/*
+ * The norms around a block of the network (around a whole Mamba-2 layer; the
+ * gated norm above is the one inside it): the norm after the block with its
+ * gate and residual scale, the residual sum, and the norm before the next
+ * block, in one pass over the rows.  For every row t of `channels` channels:
+ *
+ *   p   = x * r1 * post_weight,  r1 = 1 / sqrt(mean(x^2) + eps)   (post_weight)
+ *       = x                                                      (NULL)
+ *   u   = p * act(gate)                                          (gate NULL: p)
+ *   h   = residual + residual_scale * scale * u        (residual NULL: 0,
+ *                                                       scale NULL: 1)
+ *   out = h * r2 * pre_weight,   r2 = 1 / sqrt(mean(h^2) + eps)
+ *
+ * act is gate_activation: 0 the gate itself, 1 its sigmoid, 2 its SiLU.
+ *   x, gate, out [tokens][channels] dtype;  residual, residual_out the same
+ *   shape in residual_dtype (the dtype or fp32);  weights [channels] fp32.
+ *   residual_out receives h (nullable).  h is normalised as summed, before
+ *   its rounding to residual_dtype.
+ * Any channel count up to 8192.  Accumulation in fp32, one rounding of each
+ * output.  residual_out may be residual, and out may be x (each element is
+ * read before it is written, by the same thread); else no pointer may alias
+ * another.  Errors as for ssd_fwd.
+ */
+typedef struct {
+  int64_t tokens;          /* rows                                          */
+  int64_t channels;        /* channels per row, 1 to 8192                   */
+  int32_t dtype;           /* ssd_dtype_t of x, gate, out and their gradients */
+  int32_t residual_dtype;  /* of residual, residual_out and their gradients */
+  int32_t gate_activation; /* 0: the gate itself, 1: sigmoid, 2: SiLU       */
+  float residual_scale;
+  float eps;
+} ssd_block_norm_problem_t;
+
+ssd_status_t ssd_block_norm_fwd(const ssd_block_norm_problem_t* p, const void* x,
+                                const void* residual, const void* gate,
+                                const float* post_weight, const float* scale,
+                                const float* pre_weight, void* out, void* residual_out,
+                                void* stream);
+
+/*
+ * The backward of ssd_block_norm_fwd: gradients of sum(out * dout) +
+ * sum(residual_out * dresidual_out).  With n = h r2 and dn = dout pre_weight:
+ *
+ *   dh   = r2 (dn - n mean(dn n)) + dresidual_out;      dresidual = dh
+ *   du   = dh residual_scale scale;    dgate = du p act'(gate)
+ *   dp   = du act(gate);               dx = dp, or with post_weight, m = x r1
+ *          and dm = dp post_weight:    dx = r1 (dm - m mean(dm m))
+ *   dpre_weight = sum_t dout n,  dscale = sum_t dh residual_scale u,
+ *   dpost_weight = sum_t dp m
+ *
+ * dresidual_out (nullable: 0) and dresidual (nullable: not written) are like
+ * residual, dx and dgate like x; dgate is required with a gate, dscale with a
+ * scale, dpost_weight with a post_weight, and NULL otherwise; dpre_weight is
+ * required.  h is computed again from the inputs.  The workspace (no initial
+ * contents) is ssd_block_norm_bwd_workspace_size bytes, 256-byte aligned.  No
+ * atomics: results are deterministic.
+ */
+size_t ssd_block_norm_bwd_workspace_size(const ssd_block_norm_problem_t* p);
+
+ssd_status_t ssd_block_norm_bwd(const ssd_block_norm_problem_t* p, const void* x,
+                                const void* residual, const void* gate,
+                                const float* post_weight, const float* scale,
+                                const float* pre_weight, const void* dout,
+                                const void* dresidual_out, void* dx, void* dresidual,
+                                void* dgate, float* dpost_weight, float* dscale,
+                                float* dpre_weight, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 /* Static description of a status code (library bookkeeping, not from the
  * pages). */
 const char* ssd_status_string(ssd_status_t s);

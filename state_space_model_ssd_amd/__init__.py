@@ -6,4 +6,5 @@ load the library; the first call does, and raises if it is not built.
 """
 from .binding import (ssd_fwd, ssd_fwd_seq_idx, load_library, workspace_size,  # noqa: F401
                       workspace_layout, intermediates, make_problem, config_supported,
+                      conv_fwd, conv_bwd, conv_step, ssd_step, block_norm_fwd, block_norm_bwd,
                       SsdError, STAGES, STAGE_ALL)

@@ -9,6 +9,7 @@ fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -33,7 +34,9 @@ EXPORTED = ("ssd_fwd_workspace_size", "ssd_workspace_layout", "ssd_config_suppor
             "ssd_fwd", "ssd_fwd_stages", "ssd_fwd_tuned", "ssd_bwd_workspace_size", "ssd_bwd",
             "ssd_bwd_after_fwd", "ssd_fwd_choices", "ssd_fwd_noalloc", "ssd_gated_norm_fwd",
             "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd", "ssd_fwd_gated",
-            "ssd_status_string")
+            "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step",
+            "ssd_step", "ssd_block_norm_fwd", "ssd_block_norm_bwd_workspace_size",
+            "ssd_block_norm_bwd", "ssd_status_string")
 
 
 class SsdError(RuntimeError):
@@ -71,6 +74,33 @@ class GateC(ctypes.Structure):
     """ssd_gate_t: the gated RMS norm ssd_fwd_gated applies to its output."""
     _fields_ = [("z", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("group_size", ctypes.c_int64)]
+
+
+class ConvProblemC(ctypes.Structure):
+    """ssd_conv_problem_t: the short causal convolution in front of the SSD."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nseq", ctypes.c_int64),
+                ("channels_x", ctypes.c_int64), ("channels_b", ctypes.c_int64),
+                ("channels_c", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("in_stride", ctypes.c_int64), ("din_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class StepProblemC(ctypes.Structure):
+    """ssd_step_problem_t: one token per sequence."""
+    _fields_ = [("batch", ctypes.c_int64), ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("nslots", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dt_dtype", ctypes.c_int32),
+                ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
+
+
+class BlockNormProblemC(ctypes.Structure):
+    """ssd_block_norm_problem_t: the norms around a block."""
+    _fields_ = [("tokens", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("gate_activation", ctypes.c_int32), ("residual_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class TuningC(ctypes.Structure):
@@ -128,6 +158,20 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_fwd_noalloc.restype = ctypes.c_int
     lib.ssd_fwd_choices.argtypes = [PP, ctypes.POINTER(TuningC)]
     lib.ssd_fwd_choices.restype = ctypes.c_int
+    CP, SP, BP = (ctypes.POINTER(s) for s in (ConvProblemC, StepProblemC, BlockNormProblemC))
+    lib.ssd_conv_fwd.argtypes = [CP] + [vp] * 10
+    lib.ssd_conv_bwd_workspace_size.argtypes = [CP]
+    lib.ssd_conv_bwd_workspace_size.restype = sz
+    lib.ssd_conv_bwd.argtypes = [CP] + [vp] * 13 + [vp, sz, vp]
+    lib.ssd_conv_step.argtypes = [CP] + [vp] * 4 + [ctypes.c_int64] + [vp] * 5
+    lib.ssd_step.argtypes = [SP] + [vp] * 11
+    lib.ssd_block_norm_fwd.argtypes = [BP] + [vp] * 9
+    lib.ssd_block_norm_bwd_workspace_size.argtypes = [BP]
+    lib.ssd_block_norm_bwd_workspace_size.restype = sz
+    lib.ssd_block_norm_bwd.argtypes = [BP] + [vp] * 14 + [vp, sz, vp]
+    for fn in (lib.ssd_conv_fwd, lib.ssd_conv_bwd, lib.ssd_conv_step, lib.ssd_step,
+               lib.ssd_block_norm_fwd, lib.ssd_block_norm_bwd):
+        fn.restype = ctypes.c_int
     lib.ssd_status_string.argtypes = [ctypes.c_int]
     lib.ssd_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -432,6 +476,347 @@ def ssd_fwd_gated(x, dt, A, B, C, chunk_size, z, norm_weight, group_size, eps=1e
                                  stream)
     _check(code)
     return out, final_states, workspace
+
+
+# ---------------------------------------------------------------------------
+# The operators around the scan: short convolution, single-token step, block
+# norms.  A decoding step is a few microseconds of GPU time, so these calls
+# keep the host's part small: problem structs and workspace sizes are made
+# once per set of sizes, and pointers go to ctypes as plain integers.
+# ---------------------------------------------------------------------------
+_DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_problem(*sizes):
+    p = ConvProblemC(*sizes)
+    return p, ctypes.byref(p), int(load_library().ssd_conv_bwd_workspace_size(ctypes.byref(p)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_problem(*sizes):
+    p = StepProblemC(*sizes)
+    return p, ctypes.byref(p)
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_norm_problem(*sizes):
+    p = BlockNormProblemC(*sizes)
+    return p, ctypes.byref(p), int(load_library().ssd_block_norm_bwd_workspace_size(ctypes.byref(p)))
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) with `dev` current, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if code != SSD_OK:
+        _check(code)
+
+
+def _on_gpu(t, name, what):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU only; {name} is on {dev}")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+    return dev
+
+
+def _row_stride(t, name, rows):
+    """Elements from one row to the next of a tensor whose last axes are
+    contiguous and whose first `rows` axes lie evenly behind one another."""
+    st, sh = t.stride(), t.shape
+    inner = 1
+    for i in range(len(sh) - 1, rows - 1, -1):
+        if sh[i] != 1 and st[i] != inner:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        inner *= sh[i]
+    # the distance of two rows: of the innermost row axis that has two
+    stride = None
+    step = 1
+    for i in range(rows - 1, -1, -1):
+        if sh[i] != 1:
+            if stride is None:
+                stride = st[i]
+                if stride < inner and t.numel() > 0:
+                    raise ValueError(f"{name}'s rows overlap")
+            elif st[i] != stride * step and t.numel() > 0:
+                raise ValueError(f"{name}'s rows must lie evenly behind one another")
+            step *= sh[i]
+    return inner if stride is None or t.numel() == 0 else stride
+
+
+_CONV_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+
+
+def _conv_checked(what, x, weight, bias, splits, activation):
+    dev = _on_gpu(x, "x", what)
+    C = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({C}, width)")
+    f32 = torch.float32
+    _need(weight, "weight", f32, weight.shape, dev)
+    _need(bias, "bias", f32, (C,), dev)
+    if splits is None:
+        splits = (C, 0, 0)
+    if len(splits) != 3 or sum(splits) != C:
+        raise ValueError(f"splits {tuple(splits)} are not three channel counts with sum {C}")
+    if activation not in _CONV_ACTIVATIONS:
+        raise ValueError("activation is 'silu' or None")
+    return dev, C, tuple(splits), _CONV_ACTIVATIONS[activation]
+
+
+def _conv_prompt(what, x, weight, bias, splits, activation, initial_states, cu_seqlens, dx_stride=0):
+    if x.dim() != 3:
+        raise ValueError(f"x has {x.dim()} dimensions, expected (batch, seqlen, channels)")
+    dev, C, splits, act = _conv_checked(what, x, weight, bias, splits, activation)
+    b, T = x.shape[0], x.shape[1]
+    nseq = 0
+    if cu_seqlens is not None:
+        nseq = cu_seqlens.numel() - 1
+        if nseq < 1:
+            raise ValueError("cu_seqlens needs at least two entries")
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
+    sshape = (nseq if nseq > 0 else b, weight.shape[1] - 1, C)
+    _need(initial_states, "initial_states", x.dtype, sshape, dev)
+    prob = _conv_problem(b, T, nseq, *splits, weight.shape[1], _row_stride(x, "x", 2), dx_stride,
+                         _DT[x.dtype], act)
+    return dev, b, T, C, splits, sshape, prob
+
+
+def _conv_outs(outs, splits, lead, dtype, dev, name):
+    if outs is None:
+        return [torch.empty(lead + (n,), dtype=dtype, device=dev) for n in splits]
+    if len(outs) != 3:
+        raise ValueError(f"{name} are three tensors")
+    for o, n in zip(outs, splits):
+        if o is None and n == 0:
+            continue
+        if o is None:
+            raise ValueError(f"{name}: a tensor is missing")
+        _need(o, name, dtype, lead + (n,), dev)
+    return outs
+
+
+def conv_fwd(x, weight, bias=None, splits=None, initial_states=None, cu_seqlens=None,
+             activation="silu", outs=None, final_states=None, return_final_states=True):
+    """ssd_conv_fwd: the short causal convolution that makes x, B and C.
+
+    x (b, T, C) fp32|bf16, its rows contiguous but possibly inside wider ones
+    (a slice of the projection's output); weight (C, K) fp32 with K 2..4; bias
+    (C) fp32 or None; splits: the channels of x, B and C (default: all C in
+    the first output); initial_states (nstates, K - 1, C) in x's dtype or
+    None; cu_seqlens (nseq + 1) int32 for a packed batch (b == 1); activation
+    'silu' or None.  Returns (x, B, C, final_states): contiguous (b, T,
+    splits[i]) tensors, which viewed as (b, T, heads, headdim) and (b, T,
+    groups, dstate) are ssd_fwd's inputs, and the states (nstates, K - 1, C)
+    that conv_step and a later call's initial_states take (None without
+    return_final_states)."""
+    dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_fwd", x, weight, bias, splits,
+                                                      activation, initial_states, cu_seqlens)
+    outs = _conv_outs(outs, splits, (b, T), x.dtype, dev, "outs")
+    if final_states is not None:
+        _need(final_states, "final_states", x.dtype, sshape, dev)
+    elif return_final_states:
+        final_states = torch.empty(sshape, dtype=x.dtype, device=dev)
+    _launch(dev, load_library().ssd_conv_fwd, prob[1], x.data_ptr(), weight.data_ptr(), _addr(bias),
+            _addr(initial_states), _addr(cu_seqlens), _addr(outs[0]), _addr(outs[1]),
+            _addr(outs[2]), _addr(final_states))
+    return outs[0], outs[1], outs[2], final_states
+
+
+def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_seqlens=None,
+             activation="silu", dfinal_states=None, dx=None, workspace=None):
+    """ssd_conv_bwd: gradients of sum(out_i * douts[i]) + sum(final_states *
+    dfinal_states) for conv_fwd's arguments; douts are three tensors like its
+    outputs (ssd_bwd's x, B and C gradients).  Returns a dict with x, weight,
+    bias (None without a bias), initial_states (None without one) and the
+    workspace.  dx: where x's gradient goes, a (b, T, C) tensor that may be a
+    slice of a wider one (the gradient of the projection's output).  Its rows of
+    tokens outside every sequence are not written: pass a zeroed dx where
+    cu_seqlens does not run from 0 to T."""
+    stride = 0
+    if dx is not None:
+        _on_gpu(dx, "dx", "conv_bwd")
+        if dx.dtype != x.dtype or dx.shape != x.shape or dx.device != x.device:
+            raise ValueError("dx must be like x")
+        stride = _row_stride(dx, "dx", 2)
+    dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_bwd", x, weight, bias, splits,
+                                                      activation, initial_states, cu_seqlens, stride)
+    douts = _conv_outs(douts, splits, (b, T), x.dtype, dev, "douts")
+    _need(dfinal_states, "dfinal_states", x.dtype, sshape, dev)
+    f32 = torch.float32
+    if dx is None:
+        dx = torch.empty((b, T, C), dtype=x.dtype, device=dev)
+    g = {"x": dx, "weight": torch.empty(weight.shape, dtype=f32, device=dev),
+         "bias": torch.empty((C,), dtype=f32, device=dev) if bias is not None else None,
+         "initial_states": torch.empty_like(initial_states) if initial_states is not None else None}
+    if workspace is None:
+        workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
+    _launch(dev, load_library().ssd_conv_bwd, prob[1], x.data_ptr(), weight.data_ptr(), _addr(bias),
+            _addr(initial_states), _addr(cu_seqlens), _addr(douts[0]), _addr(douts[1]),
+            _addr(douts[2]), _addr(dfinal_states), dx.data_ptr(), g["weight"].data_ptr(),
+            _addr(g["bias"]), _addr(g["initial_states"]), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    g["workspace"] = workspace
+    return g
+
+
+def conv_step(x, conv_states, weight, bias=None, splits=None, slots=None, activation="silu",
+              outs=None):
+    """ssd_conv_step: conv_fwd for one new token per sequence, in place on a
+    cache of states.  x (batch, C), its rows possibly inside wider ones;
+    conv_states (nslots, K - 1, C) in x's dtype, updated; slots (batch) int32:
+    each row's slot, rows outside [0, nslots) and rows whose slot an earlier
+    row has being padding (None: row b has slot b).  Returns (x, B, C), each
+    (batch, splits[i]); padding's rows of `outs` keep what they held (zeros
+    where the call makes the outputs)."""
+    if x.dim() != 2:
+        raise ValueError(f"x has {x.dim()} dimensions, expected (batch, channels)")
+    dev, C, splits, act = _conv_checked("conv_step", x, weight, bias, splits, activation)
+    b, K = x.shape[0], weight.shape[1]
+    nslots = conv_states.shape[0]
+    _need(conv_states, "conv_states", x.dtype, (nslots, K - 1, C), dev)
+    _need(slots, "slots", torch.int32, (b,), dev)
+    if outs is None and slots is not None:
+        outs = [torch.zeros((b, n), dtype=x.dtype, device=dev) for n in splits]
+    else:
+        outs = _conv_outs(outs, splits, (b,), x.dtype, dev, "outs")
+    prob = _conv_problem(b, 1, 0, *splits, K, _row_stride(x, "x", 1), 0, _DT[x.dtype], act)
+    _launch(dev, load_library().ssd_conv_step, prob[1], x.data_ptr(), weight.data_ptr(),
+            _addr(bias), conv_states.data_ptr(), nslots, _addr(slots), _addr(outs[0]),
+            _addr(outs[1]), _addr(outs[2]))
+    return outs[0], outs[1], outs[2]
+
+
+def ssd_step(x, dt, A, B, C, states, D=None, dt_bias=None, slots=None, dt_min=0.0, dt_max=math.inf,
+             out=None):
+    """ssd_step: the SSD for one new token per sequence, in place on a cache
+    of states.  x (batch, H, P), B and C (batch, G, N) in fp32 or bf16, dt
+    (batch, H) in fp32 or x's dtype; each row contiguous but possibly inside a
+    wider one.  A, D, dt_bias (H) fp32; states (nslots, H, P, N) fp32, updated
+    (ssd_fwd's final_states are such states); slots as for conv_step.  Returns
+    out (batch, H, P); padding's rows of it keep what they held (zeros where
+    the call makes it)."""
+    dev = _on_gpu(x, "x", "ssd_step")
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x is (batch, heads, headdim), B and C (batch, groups, dstate)")
+    b, H, P = x.shape
+    G, N = B.shape[1], B.shape[2]
+    f32 = torch.float32
+    for t, name, dtp, shape in ((dt, "dt", dt.dtype, (b, H)), (B, "B", x.dtype, (b, G, N)),
+                                (C, "C", x.dtype, (b, G, N))):
+        if t.device != dev or t.dtype != dtp or t.shape != shape:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                             f"{dtp} {shape} on {dev}")
+    if dt.dtype != f32 and dt.dtype != x.dtype:
+        raise ValueError(f"dt has dtype {dt.dtype}, expected torch.float32 or {x.dtype}")
+    for t, name in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")):
+        _need(t, name, f32, (H,), dev)
+    nslots = states.shape[0]
+    _need(states, "states", f32, (nslots, H, P, N), dev)
+    _need(slots, "slots", torch.int32, (b,), dev)
+    if out is None:
+        make = torch.empty if slots is None else torch.zeros
+        out = make((b, H, P), dtype=x.dtype, device=dev)
+    _need(out, "out", x.dtype, (b, H, P), dev)
+    prob = _step_problem(b, H, P, N, G, nslots, _row_stride(x, "x", 1), _row_stride(dt, "dt", 1),
+                         _row_stride(B, "B", 1), _row_stride(C, "C", 1), _DT[x.dtype],
+                         _DT[dt.dtype], float(dt_min), float(dt_max))
+    _launch(dev, load_library().ssd_step, prob[1], x.data_ptr(), dt.data_ptr(), _addr(dt_bias),
+            A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), states.data_ptr(), _addr(slots),
+            out.data_ptr())
+    return out
+
+
+_GATE_ACTIVATIONS = {"linear": 0, "sigmoid": 1, "silu": 2}
+
+
+def _block_norm_checked(what, x, residual, gate, post_weight, scale, pre_weight, gate_activation,
+                        residual_scale, eps, residual_dtype):
+    dev = _on_gpu(x, "x", what)
+    C = x.shape[-1]
+    shape = x.shape
+    _need(x, "x", x.dtype, shape, dev)
+    if residual is not None:
+        residual_dtype = residual.dtype
+    elif residual_dtype is None:
+        residual_dtype = x.dtype
+    if residual_dtype != torch.float32 and residual_dtype != x.dtype:
+        raise ValueError(f"residual has dtype {residual_dtype}, expected torch.float32 or {x.dtype}")
+    _need(residual, "residual", residual_dtype, shape, dev)
+    _need(gate, "gate", x.dtype, shape, dev)
+    for t, name in ((post_weight, "post_weight"), (scale, "scale"), (pre_weight, "pre_weight")):
+        _need(t, name, torch.float32, (C,), dev)
+    if gate_activation not in _GATE_ACTIVATIONS:
+        raise ValueError("gate_activation is 'linear', 'sigmoid' or 'silu'")
+    prob = _block_norm_problem(x.numel() // max(C, 1), C, _DT[x.dtype], _DT[residual_dtype],
+                               _GATE_ACTIVATIONS[gate_activation], float(residual_scale), float(eps))
+    return dev, C, shape, residual_dtype, prob
+
+
+def block_norm_fwd(x, residual, pre_weight, gate=None, gate_activation="sigmoid", post_weight=None,
+                   scale=None, residual_scale=1.0, eps=1e-5, out=None, residual_out=None,
+                   residual_dtype=None):
+    """ssd_block_norm_fwd: from a block's output x and the residual stream, the
+    stream after the block, h = residual + residual_scale * scale * p *
+    act(gate) with p = rmsnorm(x) * post_weight (x itself without one), and the
+    next block's input rmsnorm(h) * pre_weight.  x, gate (..., C) fp32|bf16;
+    residual (..., C) in x's dtype or fp32, or None (then h is in
+    residual_dtype, default x's); weights (C) fp32.  residual_out may be
+    residual and out may be x (in place).  Returns (out, residual_out)."""
+    dev, C, shape, rdt, prob = _block_norm_checked(
+        "block_norm_fwd", x, residual, gate, post_weight, scale, pre_weight, gate_activation,
+        residual_scale, eps, residual_dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _need(out, "out", x.dtype, shape, dev)
+    if residual_out is None:
+        residual_out = torch.empty(shape, dtype=rdt, device=dev)
+    else:
+        _need(residual_out, "residual_out", rdt, shape, dev)
+    _launch(dev, load_library().ssd_block_norm_fwd, prob[1], x.data_ptr(), _addr(residual),
+            _addr(gate), _addr(post_weight), _addr(scale), pre_weight.data_ptr(), out.data_ptr(),
+            residual_out.data_ptr())
+    return out, residual_out
+
+
+def block_norm_bwd(x, residual, pre_weight, dout, dresidual_out=None, gate=None,
+                   gate_activation="sigmoid", post_weight=None, scale=None, residual_scale=1.0,
+                   eps=1e-5, workspace=None, residual_dtype=None):
+    """ssd_block_norm_bwd: gradients of sum(out * dout) + sum(residual_out *
+    dresidual_out) for block_norm_fwd's arguments.  Returns a dict with x,
+    residual, gate, post_weight, scale, pre_weight (None for an argument that
+    is None) and the workspace."""
+    dev, C, shape, rdt, prob = _block_norm_checked(
+        "block_norm_bwd", x, residual, gate, post_weight, scale, pre_weight, gate_activation,
+        residual_scale, eps, residual_dtype)
+    _need(dout, "dout", x.dtype, shape, dev)
+    _need(dresidual_out, "dresidual_out", rdt, shape, dev)
+    f32 = torch.float32
+    g = {"x": torch.empty(shape, dtype=x.dtype, device=dev),
+         "residual": torch.empty(shape, dtype=rdt, device=dev) if residual is not None else None,
+         "gate": torch.empty(shape, dtype=x.dtype, device=dev) if gate is not None else None,
+         "post_weight": torch.empty((C,), dtype=f32, device=dev) if post_weight is not None else None,
+         "scale": torch.empty((C,), dtype=f32, device=dev) if scale is not None else None,
+         "pre_weight": torch.empty((C,), dtype=f32, device=dev)}
+    if workspace is None:
+        workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
+    _launch(dev, load_library().ssd_block_norm_bwd, prob[1], x.data_ptr(), _addr(residual),
+            _addr(gate), _addr(post_weight), _addr(scale), pre_weight.data_ptr(), dout.data_ptr(),
+            _addr(dresidual_out), g["x"].data_ptr(), _addr(g["residual"]), _addr(g["gate"]),
+            _addr(g["post_weight"]), _addr(g["scale"]), g["pre_weight"].data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    g["workspace"] = workspace
+    return g
 
 
 def fwd_choices(prob: ProblemC) -> dict:

@@ -1,0 +1,294 @@
+"""The short causal convolution on the GPU, whole prompts forward and backward
+and one token at a time, against the fp64 oracle.  Every element is held to the
+bound of tests/layer_bounds.py's count of operations:
+  pre   K + 1 products and sums: (K + 2) U S, S = |bias| + sum |w| |in|
+  out   silu moves by at most 1.1 of that; its own error is the sigmoid's + 1 U
+  dpre  act' moves by at most 0.5 of pre's error; its own error is 4 times the
+        sigmoid's and 4 U of (1 + |pre|)
+  dx    sum |w| err(dpre) + (K + 2) U sum |w dpre|
+  dw    sum |in| err(dpre) + n U sum |dpre in|, n the additions a term passes:
+        at most 64 in a thread's run (8 tokens a tile, up to 8 tiles here), 4
+        waves, 16 + 16 over the partial rows, so 110 covers them
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer
+from oracle.recurrence import to_f64
+from state_space_model_ssd_amd import binding
+from tests.layer_bounds import DT, RND, TINY, U, check, sigmoid_err
+
+pytestmark = pytest.mark.gpu
+
+
+def draw(b, T, C, K, dtype, seed, nseq=None, pad=0, bias=True, init=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    n = nseq or b
+    d = dict(x=r(b, T, C + pad).to(DT[dtype])[..., pad // 2:pad // 2 + C], w=r(C, K) * 0.5,
+             bias=r(C) if bias else None, dout=r(b, T, C).to(DT[dtype]),
+             init=r(n, K - 1, C).to(DT[dtype]) if init else None,
+             dfinal=r(n, K - 1, C).to(DT[dtype]))
+    return d
+
+
+def cuda(v):
+    if v is None:
+        return None
+    if v.dim() == 3 and not v.is_contiguous():        # keep the rows inside their wider ones
+        wide = torch.full((v.shape[0], v.shape[1], v.stride(1)), float("nan"), dtype=v.dtype,
+                          device="cuda")
+        o = v.storage_offset()
+        wide[..., o:o + v.shape[2]] = v.cuda()
+        return wide[..., o:o + v.shape[2]]
+    return v.cuda()
+
+
+def mag(x, w, bias, init, cu):
+    """S = |bias| + sum |w| |in| per token and channel."""
+    ab = lambda v: None if v is None else v.abs()  # noqa: E731
+    return layer.conv_fwd(ab(x), ab(w), ab(bias), ab(init), cu, silu=False)[0]
+
+
+def out_bound(pre, S, K, silu, dtype):
+    e = (K + 2) * U * S
+    if not silu:
+        return e + RND[dtype] * (np.abs(pre) + e) + TINY
+    s = np.abs(pre) / (1.0 + np.exp(-pre))
+    e = 1.1 * e + s * (sigmoid_err(pre) + U)
+    return e + RND[dtype] * (s + e) + TINY
+
+
+def dpre_bound(pre, S, dout, K, silu):
+    d = np.abs(to_f64(dout))
+    if not silu:
+        return np.zeros_like(d)
+    return d * (0.5 * (K + 2) * U * S + (4 * sigmoid_err(pre) + 4 * U) * (1 + np.abs(pre))) + TINY
+
+
+CASES = {
+    # (rows, tokens, splits, K, dtype, pad, silu, bias, initial state, packed lengths)
+    "layer": (2, 300, (1536, 128, 128), 4, "bf16", 1560, True, True, True, None),
+    "one-token": (3, 1, (64, 16, 16), 4, "bf16", 0, True, True, True, None),
+    "two-tokens-no-state": (1, 2, (64, 16, 16), 4, "bf16", 0, True, False, False, None),
+    "tile-edges": (1, 65, (512, 8, 8), 3, "bf16", 0, True, True, False, None),
+    "odd-splits": (2, 130, (33, 7, 5), 4, "bf16", 3, True, True, True, None),
+    "odd-pad": (2, 70, (64, 32, 32), 2, "bf16", 13, True, True, True, None),
+    "one-output": (1, 100, (200, 0, 0), 2, "f32", 0, True, True, True, None),
+    "b-only": (1, 40, (24, 8, 0), 3, "f32", 4, False, True, True, None),
+    "one-channel": (2, 37, (1, 0, 0), 4, "f32", 0, True, True, True, None),
+    "odd-f32": (3, 33, (129, 3, 2), 4, "f32", 1, True, False, True, None),
+    "no-act": (2, 64, (264, 16, 16), 4, "bf16", 0, False, True, True, None),
+    "packed": (1, 0, (128, 16, 16), 4, "bf16", 0, True, True, True, (100, 1, 0, 2, 3, 250, 64)),
+    "packed-short": (1, 0, (40, 8, 8), 4, "f32", 0, True, True, False, (1,) * 20 + (0, 0, 5)),
+    "packed-empty-ends": (1, 0, (40, 8, 8), 3, "f32", 8, True, True, True, (0, 70, 0)),
+    "packed-many": (1, 0, (16, 0, 0), 4, "bf16", 0, True, True, True, tuple(i % 7 for i in range(300))),
+    "packed-one": (1, 0, (33, 2, 1), 2, "bf16", 0, True, True, True, (129,)),
+}
+
+
+def setup(name):
+    b, T, splits, K, dtype, pad, silu, bias, init, lens = CASES[name]
+    cu = None
+    if lens is not None:
+        cu = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+        T = sum(lens)
+    d = draw(b, T, sum(splits), K, dtype, len(name) + T, None if lens is None else len(lens), pad, bias, init)
+    kw = dict(splits=splits, activation="silu" if silu else None)
+    dev = {k: cuda(v) for k, v in d.items()}
+    kw.update(cu_seqlens=None if cu is None else cu.cuda(), initial_states=dev["init"], bias=dev["bias"])
+    return d, dev, cu, kw, splits, K, dtype, silu
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_conv_forward(name):
+    d, dev, cu, kw, splits, K, dtype, silu = setup(name)
+    *out, final = binding.conv_fwd(dev["x"], dev["w"], **kw)
+    torch.cuda.synchronize()
+    ref, fref, pre = layer.conv_fwd(d["x"], d["w"], d["bias"], d["init"], cu, silu)
+    S = mag(d["x"], d["w"], d["bias"], d["init"], cu)
+    assert [o.shape[-1] for o in out] == list(splits) and all(o.is_contiguous() for o in out)
+    check(torch.cat(out, -1), ref, out_bound(pre, S, K, silu, dtype), "out")
+    assert np.array_equal(final.cpu().double().numpy(), fref)          # copies
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_conv_backward(name):
+    d, dev, cu, kw, splits, K, dtype, silu = setup(name)
+    douts = [o.contiguous() for o in dev["dout"].split(splits, -1)]
+    g = binding.conv_bwd(dev["x"], dev["w"], douts, dfinal_states=dev["dfinal"], **kw)
+    torch.cuda.synchronize()
+    r = layer.conv_bwd(d["x"], d["w"], d["dout"], d["bias"], d["init"], cu, silu, d["dfinal"])
+    _, _, pre = layer.conv_fwd(d["x"], d["w"], d["bias"], d["init"], cu, silu)
+    e = dpre_bound(pre, mag(d["x"], d["w"], d["bias"], d["init"], cu), d["dout"], K, silu)
+    ab = np.abs
+    # the same sums over absolute values and over the errors of dpre
+    x, w = torch.from_numpy(ab(to_f64(d["x"]))), d["w"].abs()
+    init = None if d["init"] is None else d["init"].abs()
+    sums = layer.conv_bwd(x, w, torch.from_numpy(ab(r["dpre"])), None, init, cu, False,
+                          d["dfinal"].abs())
+    errs = layer.conv_bwd(x, w, torch.from_numpy(e), None, init, cu, False)
+    for k, out in (("x", g["x"]), ("initial_states", g["initial_states"])):
+        if out is None:
+            assert k == "initial_states" and d["init"] is None
+            continue
+        tol = errs[k] + (K + 3) * U * sums[k]
+        check(out, r[k], tol + RND[dtype] * (ab(r[k]) + tol) + TINY, "d" + k)
+    check(g["weight"], r["weight"], errs["weight"] + 110 * U * sums["weight"] + TINY, "dweight")
+    if d["bias"] is None:
+        assert g["bias"] is None
+    else:
+        check(g["bias"], r["bias"], errs["bias"] + 110 * U * sums["bias"] + TINY, "dbias")
+
+
+def test_conv_backward_without_state_gradients_and_into_a_wider_tensor():
+    d, dev, cu, kw, splits, K, dtype, silu = setup("odd-pad")
+    douts = [o.contiguous() for o in dev["dout"].split(splits, -1)]
+    g = binding.conv_bwd(dev["x"], dev["w"], douts, **kw)
+    wide = torch.full((2, 70, 128 + 9), 3.0, dtype=torch.bfloat16, device="cuda")
+    h = binding.conv_bwd(dev["x"], dev["w"], douts, dx=wide[..., 5:133], **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[..., 5:133], g["x"]) and torch.equal(g["weight"], h["weight"])
+    assert (wide[..., :5] == 3).all() and (wide[..., 133:] == 3).all()
+    zero = binding.conv_bwd(dev["x"], dev["w"], douts, dfinal_states=torch.zeros_like(dev["dfinal"]), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(zero["x"], g["x"]) and torch.equal(zero["initial_states"], g["initial_states"])
+
+
+def test_conv_tokens_outside_every_sequence_are_left_alone():
+    K, C = 4, 40
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((1, 200, C), generator=g)
+    w, dout = torch.randn((C, K), generator=g), torch.randn((1, 200, C), generator=g)
+    x[:, :10] = float("nan")                       # never read into a sequence
+    x[:, 170:] = float("inf")
+    dout[:, :10] = float("nan")
+    dout[:, 170:] = float("nan")
+    cu = torch.tensor([10, 90, 90, 170], dtype=torch.int32)
+    outs = [torch.full((1, 200, n), 7.0, device="cuda") for n in (24, 8, 8)]
+    *o, fin = binding.conv_fwd(x.cuda(), w.cuda(), splits=(24, 8, 8), cu_seqlens=cu.cuda(), outs=outs)
+    dx = torch.full((1, 200, C), 7.0, device="cuda")
+    gr = binding.conv_bwd(x.cuda(), w.cuda(), [v.contiguous().cuda() for v in dout.split((24, 8, 8), -1)],
+                          splits=(24, 8, 8), cu_seqlens=cu.cuda(), dx=dx)
+    torch.cuda.synchronize()
+    for t in (*o, dx):
+        assert (t[:, :10] == 7).all() and (t[:, 170:] == 7).all()
+        assert torch.isfinite(t).all()
+    ref, _, pre = layer.conv_fwd(x, w, None, None, cu)
+    check(torch.cat(o, -1), ref, out_bound(pre, mag(x, w, None, None, cu), K, True, "f32"), "out")
+    assert torch.isfinite(gr["weight"]).all()
+
+
+def test_conv_nothing_crosses_a_sequence():
+    """NaN in one sequence (tokens, state, output gradient) stays in it."""
+    d, dev, cu, kw, splits, K, dtype, silu = setup("packed")
+    clean = binding.conv_fwd(dev["x"], dev["w"], **kw)
+    douts = [o.contiguous() for o in dev["dout"].split(splits, -1)]
+    gclean = binding.conv_bwd(dev["x"], dev["w"], douts, dfinal_states=dev["dfinal"], **kw)
+    a, e = int(cu[3]), int(cu[4])                  # the two-token sequence
+    x, init = dev["x"].clone(), dev["init"].clone()
+    x[:, a:e] = float("nan")
+    init[3] = float("inf")
+    kw["initial_states"] = init
+    dirty = binding.conv_fwd(x, dev["w"], **kw)
+    gdirty = binding.conv_bwd(x, dev["w"], douts, dfinal_states=dev["dfinal"], **kw)
+    torch.cuda.synchronize()
+    for c, v in zip(clean[:3] + (gclean["x"],), dirty[:3] + (gdirty["x"],)):
+        assert torch.equal(c[:, :a], v[:, :a]) and torch.equal(c[:, e:], v[:, e:])
+    keep = [0, 1, 2, 4, 5, 6]
+    assert torch.equal(clean[3][keep], dirty[3][keep])
+    assert torch.equal(gclean["initial_states"][keep], gdirty["initial_states"][keep])
+
+
+def test_conv_malformed_packing_stays_in_bounds():
+    """Decreasing, negative and too large entries: clamped on the device (the
+    index arithmetic is restated and checked on the CPU in test_conv_tiles.py)."""
+    x = torch.randn((1, 150, 16), device="cuda")
+    w = torch.randn((16, 4), device="cuda")
+    for bad in ([0, 100, 50, 150], [-5, 3, 10 ** 9], [150, 0], [2 ** 31 - 1, -2 ** 31, 7, 150]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        binding.conv_fwd(x, w, cu_seqlens=cu)
+        binding.conv_bwd(x, w, [x, None, None], cu_seqlens=cu)
+    torch.cuda.synchronize()
+
+
+def test_conv_no_tokens():
+    w = torch.randn((16, 4), device="cuda")
+    init = torch.randn((2, 3, 16), device="cuda")
+    x = torch.empty((2, 0, 16), device="cuda")
+    o, _, _, fin = binding.conv_fwd(x, w, initial_states=init)
+    g = binding.conv_bwd(x, w, [x, None, None], bias=w[:, 0].contiguous(), initial_states=init,
+                         dfinal_states=init)
+    torch.cuda.synchronize()
+    assert o.numel() == 0 and torch.equal(fin, init) and torch.equal(g["initial_states"], init)
+    assert not g["weight"].any() and not g["bias"].any()
+
+
+def test_conv_is_deterministic_and_splits_resume():
+    d, dev, cu, kw, splits, K, dtype, silu = setup("layer")
+    a = binding.conv_fwd(dev["x"], dev["w"], **kw)
+    douts = [o.contiguous() for o in dev["dout"].split(splits, -1)]
+    g, h = (binding.conv_bwd(dev["x"], dev["w"], douts, dfinal_states=dev["dfinal"], **kw) for _ in range(2))
+    first = binding.conv_fwd(dev["x"][:1, :77], dev["w"], **{**kw, "initial_states": dev["init"][:1]})
+    rest = binding.conv_fwd(dev["x"][:1, 77:], dev["w"], **{**kw, "initial_states": first[3]})
+    torch.cuda.synchronize()
+    for k in ("x", "weight", "bias", "initial_states"):
+        assert torch.equal(g[k], h[k])
+    for i in range(3):
+        assert torch.equal(torch.cat([first[i], rest[i]], 1), a[i][:1])
+    assert torch.equal(rest[3], a[3][:1])
+
+
+STEPS = {
+    # (batch, nslots, splits, K, dtype, pad, slots)
+    "one": (1, 1, (1536, 128, 128), 4, "bf16", 1560, None),
+    "identity": (5, 7, (64, 16, 16), 4, "bf16", 0, None),
+    "slots": (6, 9, (64, 16, 16), 3, "bf16", 8, [8, 0, 3, 4, 7, 1]),
+    "padding": (7, 4, (33, 5, 2), 4, "bf16", 3, [2, -1, 2, 4, 0, 99, -2 ** 31]),
+    "f32": (4, 4, (300, 4, 4), 2, "f32", 1, [3, 2, 1, 0]),
+    "odd-f32": (3, 5, (257, 0, 0), 4, "f32", 0, [4, 4, 4]),
+    "many-rows": (600, 610, (16, 8, 8), 4, "bf16", 0, "shuffle"),
+}
+
+
+@pytest.mark.parametrize("name", sorted(STEPS))
+def test_conv_step(name):
+    batch, nslots, splits, K, dtype, pad, slots = STEPS[name]
+    C = sum(splits)
+    g = torch.Generator().manual_seed(len(name))
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x = r(batch, C + pad).to(DT[dtype])[:, pad:]
+    states, w, bias = r(nslots, K - 1, C).to(DT[dtype]), r(C, K), r(C)
+    if slots == "shuffle":
+        slots = torch.randperm(nslots, generator=g)[:batch].tolist()
+        slots[7], slots[333], slots[599] = -1, slots[3], slots[598]
+    st = states.cuda()
+    outs = [torch.full((batch, n), 5.0, dtype=DT[dtype], device="cuda") for n in splits]
+    wide = torch.zeros((batch, C + pad), dtype=DT[dtype], device="cuda")
+    wide[:, pad:] = x.cuda()
+    dslots = None if slots is None else torch.tensor(slots, dtype=torch.int32, device="cuda")
+    binding.conv_step(wide[:, pad:], st, w.cuda(), bias.cuda(), splits=splits, slots=dslots, outs=outs)
+    torch.cuda.synchronize()
+    ref, sref = layer.conv_step(x, states, w, bias, slots)
+    assert np.array_equal(st.cpu().double().numpy(), sref)              # moved, not computed
+    got = torch.cat(outs, -1)
+    pads = torch.tensor(layer.padding_rows(slots, batch, nslots))
+    assert (got.cpu()[pads] == 5).all()
+    src = states[[i if slots is None else min(max(slots[i], 0), nslots - 1) for i in range(batch)]]
+    full = torch.cat([src, x[:, None]], 1).double()
+    pre = (full * w.t().double()).sum(1).numpy() + bias.double().numpy()
+    S = (full.abs() * w.t().abs().double()).sum(1).numpy() + bias.abs().double().numpy()
+    check(got, ref, out_bound(pre, S, K, True, dtype), "out")
+
+
+def test_conv_prompt_then_steps():
+    d, dev, cu, kw, splits, K, dtype, silu = setup("layer")
+    whole = binding.conv_fwd(dev["x"], dev["w"], **kw)
+    *_, st = binding.conv_fwd(dev["x"][:, :290].contiguous(), dev["w"], **kw)
+    outs = [binding.conv_step(dev["x"][:, t], st, dev["w"], dev["bias"], splits=splits)
+            for t in range(290, 300)]
+    torch.cuda.synchronize()
+    for i in range(3):
+        assert torch.equal(torch.stack([o[i] for o in outs], 1), whole[i][:, 290:])
+    assert torch.equal(st, whole[3])
