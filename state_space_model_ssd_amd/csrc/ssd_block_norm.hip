@@ -78,19 +78,17 @@ __device__ __forceinline__ void bn_weights(const float* w, float mul, int t, int
 }
 
 // act(z) and its derivative.
-template <typename T>
 __device__ __forceinline__ float bn_act(int kind, float z) {
   if (kind == 0) return z;
-  const float s = sigmoid<T>(z);
+  const float s = sigmoid(z);
   return kind == 1 ? s : z * s;
 }
-template <typename T>
 __device__ __forceinline__ float bn_act_grad(int kind, float z, float& act) {
   if (kind == 0) {
     act = z;
     return 1.f;
   }
-  const float s = sigmoid<T>(z);
+  const float s = sigmoid(z);
   act = kind == 1 ? s : z * s;
   return kind == 1 ? s * (1.f - s) : s * (1.f + z * (1.f - s));
 }
@@ -147,7 +145,7 @@ __global__ __launch_bounds__(kBnThreads<W>) void block_norm_fwd_kernel(const Blo
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = h[k][e] * r1 * pw[k][e];
-        if (a.gate) u *= bn_act<T>(a.act, g[e]);
+        if (a.gate) u *= bn_act(a.act, g[e]);
         h[k][e] = q[e] + fw[k][e] * u;
         s += h[k][e] * h[k][e];
       }
@@ -228,7 +226,7 @@ __global__ __launch_bounds__(kBnThreads<W>) void block_norm_bwd_kernel(const Blo
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = x[e] * r1 * pw[k][e];
-        if (a.gate) u *= bn_act<T>(a.act, g[e]);
+        if (a.gate) u *= bn_act(a.act, g[e]);
         h[k][e] = q[e] + fw[k][e] * u;
         s += h[k][e] * h[k][e];
       }
@@ -261,7 +259,7 @@ __global__ __launch_bounds__(kBnThreads<W>) void block_norm_bwd_kernel(const Blo
         dh[e] += r2 * (d[e] * nw[k][e] - h[k][e] * mn);
         const float m = x[e] * r1, p = m * pw[k][e], du = dh[e] * fw[k][e];
         float act = 1.f, da = 0.f;
-        if (a.gate) da = bn_act_grad<T>(a.act, g[e], act);
+        if (a.gate) da = bn_act_grad(a.act, g[e], act);
         as[k][e] += dh[e] * p * act;
         dg[e] = du * p * da;
         const float dp = du * act;

@@ -81,42 +81,83 @@ __device__ __forceinline__ ConvTile conv_tile(const ConvArgs& a, int slot) {
     t.lo = t.start + (slot - t.s * per) * WT;
     t.hi = min(t.lo + WT, t.end);
   }
+  // the same in every lane already; said so, row addresses stay scalar
+  t.s = __builtin_amdgcn_readfirstlane(t.s);
+  t.start = __builtin_amdgcn_readfirstlane(t.start);
+  t.end = __builtin_amdgcn_readfirstlane(t.end);
+  t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+  t.hi = __builtin_amdgcn_readfirstlane(t.hi);
   return t;
 }
 
-// Pointer to channel c of token 0 in the output (or its gradient) that holds
-// the channel, and that output's channels.
+// The channels of a wave: tiles of 64 V channels that never straddle two of the
+// three outputs, so every row base is the same in all lanes.  An output whose
+// channels are not whole vectors (it has at least V) ends in a vector that
+// overlaps the one before it: both compute and store the same values.
+struct ConvCols {
+  int i, ld;            // output and its channels
+  int c;                // this lane's first channel, of all C (some channel if !ok)
+  int co;               // the same within the output
+  int tile;             // the tile's first channel within the output
+  bool ok;              // the lane has channels
+};
+
+template <int V>
+__host__ __device__ inline int conv_col_tiles(int n) { return (n + 64 * V - 1) / (64 * V); }
+template <int V>
+int conv_col_tiles(const ConvArgs& a) {
+  return conv_col_tiles<V>(a.n[0]) + conv_col_tiles<V>(a.n[1]) + conv_col_tiles<V>(a.n[2]);
+}
+
+// First channel of vector v of an output of n channels.
+template <int V>
+__device__ __forceinline__ int conv_vec(int v, int n) { return min(v * V, n - V); }
+
+template <int V>
+__device__ __forceinline__ ConvCols conv_cols(const ConvArgs& a, int ct) {
+  ConvCols k;
+  const int t0 = conv_col_tiles<V>(a.n[0]), t1 = t0 + conv_col_tiles<V>(a.n[1]);
+  k.i = ct < t0 ? 0 : ct < t1 ? 1 : 2;
+  k.ld = ct < t0 ? a.n[0] : ct < t1 ? a.n[1] : a.n[2];
+  const int first = ct < t0 ? 0 : ct < t1 ? a.n[0] : a.n[0] + a.n[1];
+  ct -= ct < t0 ? 0 : ct < t1 ? t0 : t1;
+  const int v = ct * 64 + (int)(threadIdx.x & 63);
+  k.tile = ct * 64 * V;
+  k.ok = v * V < k.ld;
+  k.co = conv_vec<V>(v, k.ld);
+  k.c = first + k.co;
+  return k;
+}
+
 template <typename T>
-__device__ __forceinline__ T* conv_split(const ConvArgs& a, void* const* out, int c, int& ld) {
-  if (c < a.n[0]) {
-    ld = a.n[0];
-    return static_cast<T*>(out[0]) + c;
-  }
-  c -= a.n[0];
-  if (c < a.n[1]) {
-    ld = a.n[1];
-    return static_cast<T*>(out[1]) + c;
-  }
-  ld = a.n[2];
-  return static_cast<T*>(out[2]) + (c - a.n[1]);
+__device__ __forceinline__ T* conv_pick(void* const* p, int i) {
+  return static_cast<T*>(i == 0 ? p[0] : i == 1 ? p[1] : p[2]);
 }
 
 // Row p of sequence t.s's input, for tokens from K - 1 before the sequence on
-// to its last: a token's row, a row of the initial state, or zeros.  The
-// sequence has a token.
+// to its last: a token's row or a row of the initial state.  Without an initial
+// state a row before the sequence is the tensor's first (some row that exists):
+// conv_row_is_zero says so, and the caller clears it after all its loads are
+// issued.  The tensor has a token.
+template <typename T, int K>
+__device__ __forceinline__ const T* conv_row(const ConvArgs& a, const ConvTile& t, int p) {
+  const bool before = p < t.start, state = before && a.init;
+  const T* base = static_cast<const T*>(state ? a.init : a.x);
+  const int64_t row = state ? (int64_t)t.s * (K - 1) + (p - t.start + K - 1) : before ? 0 : p;
+  return base + row * (state ? (int64_t)a.C : a.in_stride);
+}
+__device__ __forceinline__ bool conv_row_is_zero(const ConvArgs& a, const ConvTile& t, int p) {
+  return p < t.start && !a.init;
+}
+
+// One more token: `win` holds the K rows up to it, oldest first.
 template <typename T, int V, int K>
-__device__ __forceinline__ Vec<T, V> conv_row(const ConvArgs& a, const ConvTile& t, int p, int c) {
-  Vec<T, V> q;
-  const bool before = p < t.start;
-  const T* row = static_cast<const T*>(a.x) + (int64_t)p * a.in_stride;
-  if (before) {
-    // without an initial state: the sequence's first row, then cleared
-    row = a.init ? static_cast<const T*>(a.init) + ((int64_t)t.s * (K - 1) + (p - t.start + K - 1)) * a.C
-                 : static_cast<const T*>(a.x) + (int64_t)t.start * a.in_stride;
-  }
-  q.load(row + c);
-  q.clear_unless(!before || a.init);
-  return q;
+__device__ __forceinline__ void conv_slide(float (&win)[K][V], const Vec<T, V>& q) {
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) win[k][e] = win[k + 1][e];
+  q.get(win[K - 1]);
 }
 
 // The K taps and the bias of V channels.
@@ -135,19 +176,72 @@ __device__ __forceinline__ void conv_weights(const ConvArgs& a, int c, float (&w
 // workgroups after the convolution's own: V channels of one state row each.
 template <typename T, int V, int K>
 __device__ void conv_final_rows(const ConvArgs& a, int64_t i) {
-  const int nvec = a.C / V;
+  const int nvec = (a.C + V - 1) / V;
   if (i >= (int64_t)a.nstates * (K - 1) * nvec) return;
-  const int c = (int)(i % nvec) * V, r = (int)(i / nvec % (K - 1)), s = (int)(i / nvec / (K - 1));
+  const int c = conv_vec<V>((int)(i % nvec), a.C), r = (int)(i / nvec % (K - 1));
+  const int s = (int)(i / nvec / (K - 1));
   ConvTile t;
   conv_seq(a, s, t);
   const int p = t.end - (K - 1) + r;
   Vec<T, V> q;
-  if (p < t.start && !a.init) q.clear();
-  else q = conv_row<T, V, K>(a, t, p, c);
+  if (conv_row_is_zero(a, t, p)) q.clear();
+  else q.load(conv_row<T, K>(a, t, p) + c);
   q.store(static_cast<T*>(a.final_states) + ((int64_t)s * (K - 1) + r) * a.C + c);
 }
 
-template <typename T, int V, int K, int TT>
+// One run of TT tokens from t0 on.  EDGE: its rows may lie before the sequence
+// or the run may end early; the inner runs have neither test.
+template <typename T, int V, int K, int TT, bool SILU, bool EDGE>
+__device__ __forceinline__ void conv_fwd_run(const ConvArgs& a, const ConvTile& t, int t0,
+                                             const ConvCols& col, const float (&w)[K][V],
+                                             const float (&b)[V]) {
+  Vec<T, V> q[TT + K - 1];
+  const uint32_t cx = lane_offset((uint32_t)col.c * (uint32_t)sizeof(T));
+  uint32_t co = lane_offset((uint32_t)col.co * (uint32_t)sizeof(T));
+  const int64_t step = a.in_stride * (int64_t)sizeof(T);
+  RowCursor row(static_cast<const T*>(a.x) + (int64_t)(EDGE ? t0 : t0 - (K - 1)) * a.in_stride);
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      RowCursor first(conv_row<T, K>(a, t, t0 - (K - 1) + j));
+      q[j].load_at(first, cx);
+    }
+  }
+#pragma unroll
+  for (int j = EDGE ? K - 1 : 0; j < TT + K - 1; ++j) {
+    q[j].load_at(row, cx);
+    // past the run's end: its last row again
+    row.move(!EDGE || t0 + j - (K - 1) < t.hi - 1 ? step : 0);
+  }
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) q[j].clear_unless(!conv_row_is_zero(a, t, t0 - (K - 1) + j));
+  }
+  RowCursor out(conv_pick<T>(a.out, col.i) + (int64_t)t0 * col.ld);
+  float win[K][V];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) q[j].get(win[j + 1]);
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    if (EDGE && t0 + i >= t.hi) continue;
+    if (EDGE) co = lane_offset(co);
+    conv_slide<T, V, K>(win, q[i + K - 1]);
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      float pre = b[e];
+#pragma unroll
+      for (int k = 0; k < K; ++k) pre += w[k][e] * win[k][e];
+      o[e] = SILU ? pre * sigmoid(pre) : pre;
+    }
+    Vec<T, V> r;
+    r.set(o);
+    r.store_at(out, co);
+    out.move((int64_t)col.ld * (int64_t)sizeof(T));
+  }
+}
+
+template <typename T, int V, int K, int TT, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs a, int nct,
                                                                 int nslots, int nparts) {
   constexpr int WT = TT * kConvWaves;
@@ -155,43 +249,16 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs a
     conv_final_rows<T, V, K>(a, (int64_t)((int)blockIdx.x - nct * nparts) * kConvThreads + threadIdx.x);
     return;
   }
-  const int lane = threadIdx.x & 63, wv = wave_id();
-  const int nvec = a.C / V, v = (int)(blockIdx.x % nct) * 64 + lane;
-  const int c = min(v, nvec - 1) * V;
+  const int wv = wave_id();
+  const ConvCols col = conv_cols<V>(a, blockIdx.x % nct);
   float w[K][V], b[V];
-  conv_weights<V, K>(a, c, w, b);
-  int ld;
-  T* out = conv_split<T>(a, a.out, c, ld);
+  conv_weights<V, K>(a, col.c, w, b);
   for (int slot = blockIdx.x / nct; slot < nslots; slot += nparts) {
     const ConvTile t = conv_tile<WT>(a, slot);
     const int t0 = t.lo + wv * TT;
-    if (t0 >= t.hi) continue;
-    Vec<T, V> q[TT + K - 1];
-#pragma unroll
-    for (int j = 0; j < TT + K - 1; ++j)
-      q[j] = conv_row<T, V, K>(a, t, min(t0 - (K - 1) + j, t.hi - 1), c);
-    float win[K][V];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) q[j].get(win[j + 1]);
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) win[k][e] = win[k + 1][e];
-      q[i + K - 1].get(win[K - 1]);
-      float o[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float pre = b[e];
-#pragma unroll
-        for (int k = 0; k < K; ++k) pre += w[k][e] * win[k][e];
-        o[e] = a.silu ? pre * sigmoid<T>(pre) : pre;
-      }
-      Vec<T, V> r;
-      r.set(o);
-      if (t0 + i < t.hi && v < nvec) r.store(out + (int64_t)(t0 + i) * ld);
-    }
+    if (t0 >= t.hi || !col.ok) continue;
+    if (t0 - (K - 1) >= t.start && t0 + TT <= t.hi) conv_fwd_run<T, V, K, TT, SILU, false>(a, t, t0, col, w, b);
+    else conv_fwd_run<T, V, K, TT, SILU, true>(a, t, t0, col, w, b);
   }
 }
 
@@ -200,47 +267,59 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs a
 // row len + i of a sequence shorter than K - 1 is row i of the final state.
 template <typename T, int V, int K>
 __device__ void conv_dinit_rows(const ConvArgs& a, int64_t i) {
-  const int nvec = a.C / V;
+  const int v0 = (a.n[0] + V - 1) / V, v1 = v0 + (a.n[1] + V - 1) / V;
+  const int nvec = v1 + (a.n[2] + V - 1) / V;
   if (i >= (int64_t)a.nstates * nvec) return;
-  const int c = (int)(i % nvec) * V, s = (int)(i / nvec);
+  const int s = (int)(i / nvec), v = (int)(i % nvec);
+  const int o = v < v0 ? 0 : v < v1 ? 1 : 2;      // output that holds the channels
+  const int ld = o == 0 ? a.n[0] : o == 1 ? a.n[1] : a.n[2];
+  const int co = conv_vec<V>(v - (o == 0 ? 0 : o == 1 ? v0 : v1), ld);
+  const int c = co + (o == 0 ? 0 : o == 1 ? a.n[0] : a.n[0] + a.n[1]);
+  const T* dout = conv_pick<const T>(const_cast<void* const*>(a.dout), o) + co;
   ConvTile t;
   conv_seq(a, s, t);
   const int len = t.end - t.start;
   float w[K][V], b[V];
   conv_weights<V, K>(a, c, w, b);
-  int ld;
-  const T* dout = conv_split<const T>(a, const_cast<void* const*>(a.dout), c, ld);
   float acc[K - 1][V];
+  Vec<T, V> q[2 * (K - 1)], dq[K - 1], fq[K - 1];
+  const int past = max(t.end - 1, 0);             // rows of tokens there are not: any row
+  if (a.total > 0) {
+#pragma unroll
+    for (int j = 0; j < 2 * (K - 1); ++j)
+      q[j].load(conv_row<T, K>(a, t, j < K - 1 ? t.start - (K - 1) + j : min(t.start + j - (K - 1), past)) + c);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) dq[j].load(dout + (int64_t)min(t.start + j, past) * ld);
+  }
 #pragma unroll
   for (int r = 0; r < K - 1; ++r) {
+    fq[r].clear();
+    if (a.dfinal && r >= len)
+      fq[r].load(static_cast<const T*>(a.dfinal) + ((int64_t)s * (K - 1) + r - len) * a.C + c);
+  }
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[r][e] = 0.f;
-    if (a.dfinal && r >= len) {
-      Vec<T, V> q;
-      q.load(static_cast<const T*>(a.dfinal) + ((int64_t)s * (K - 1) + r - len) * a.C + c);
-      q.get(acc[r]);
-    }
+  for (int j = 0; j < K - 1; ++j) {
+    fq[j].get(acc[j]);
+    q[j].clear_unless(!conv_row_is_zero(a, t, t.start - (K - 1) + j));
   }
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     if (j >= len) continue;
     float d[V], pre[V];
-    Vec<T, V> q;
-    q.load(dout + (int64_t)(t.start + j) * ld);
-    q.get(d);
+    dq[j].get(d);
 #pragma unroll
     for (int e = 0; e < V; ++e) pre[e] = b[e];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float f[V];
-      conv_row<T, V, K>(a, t, t.start + j - (K - 1) + k, c).get(f);
+      q[j + k].get(f);
 #pragma unroll
       for (int e = 0; e < V; ++e) pre[e] += w[k][e] * f[e];
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (a.silu) {
-        const float sg = sigmoid<T>(pre[e]);
+        const float sg = sigmoid(pre[e]);
         d[e] *= sg * (1.f + pre[e] * (1.f - sg));
       }
 #pragma unroll
@@ -255,28 +334,151 @@ __device__ void conv_dinit_rows(const ConvArgs& a, int64_t i) {
   }
 }
 
-// Backward.  A run's dpre is formed for its TT tokens and the K - 1 after
-// them, in order, from a sliding window of K input rows; din of a token is
-// complete K - 1 tokens later.  dw and db accumulate in registers over the
-// workgroup's tiles, are added over its waves in LDS at the end, and leave
-// as one partial row per workgroup, [part][K + 1][C].
-template <typename T, int V, int K, int TT>
+// Backward, one run of TT = kConvBwdSteps - (K - 1) tokens.  dpre is formed for
+// them and the K - 1 tokens after, in order, from a sliding window of K input
+// rows; din of a token is complete K - 1 tokens later.  The rows are loaded a
+// group of GR tokens ahead of their use, so that the loads of one group are in
+// flight while another is computed (all rows of a run at once, as the forward
+// loads them, left memory idle while the waves computed: 25.9 us against XXX at
+// 8192 x 1792 bf16).  EDGE as in the forward; the gradient of the final state
+// reaches edge runs only.
+template <typename T, int V, int K, int STEPS, int GR, bool SILU, bool EDGE>
+__device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, const ConvTile& t, int t0,
+                                             const ConvCols& col, const float (&w)[K][V],
+                                             const float (&b)[V], float (&acc)[K + 1][V]) {
+  constexpr int TT = STEPS - (K - 1), NG = STEPS / GR;
+  static_assert(STEPS % GR == 0, "whole groups");
+  const int own = EDGE ? min(TT, t.hi - t0) : TT;     // tokens of this run
+  uint32_t co = lane_offset((uint32_t)col.co * (uint32_t)sizeof(T));
+  uint32_t cx = lane_offset((uint32_t)col.c * (uint32_t)sizeof(T));
+  const T* x = static_cast<const T*>(a.x);
+  const int64_t xstep = a.in_stride * (int64_t)sizeof(T), ostep = col.ld * (int64_t)sizeof(T);
+  RowCursor xrow(x + (int64_t)(EDGE ? t0 : t0 - (K - 1)) * a.in_stride);
+  RowCursor orow(conv_pick<const T>(const_cast<void* const*>(a.dout), col.i) + (int64_t)t0 * col.ld);
+  Vec<T, V> h[K - 1], q[2][GR], dq[2][GR], fq[K - 1];
+  // row j of the run; past the sequence's end its last row again
+  auto load = [&](int j, Vec<T, V>& xv, Vec<T, V>& dv) {
+    xv.load_at(xrow, cx);
+    dv.load_at(orow, co);
+    xrow.move(!EDGE || t0 + j < t.end - 1 ? xstep : 0);
+    orow.move(!EDGE || t0 + j < t.end - 1 ? ostep : 0);
+  };
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    if constexpr (EDGE) {
+      RowCursor first(conv_row<T, K>(a, t, t0 - (K - 1) + j));
+      h[j].load_at(first, cx);
+    } else {
+      h[j].load_at(xrow, cx);
+      xrow.move(xstep);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < GR; ++u) load(u, q[0][u], dq[0][u]);
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+      // any row that exists where there is no gradient of the final state
+      RowCursor df(a.dfinal ? static_cast<const T*>(a.dfinal) + ((int64_t)t.s * (K - 1) + k) * a.C
+                            : x + (int64_t)t.start * a.in_stride);
+      fq[k].load_at(df, cx);
+    }
+  }
+  RowCursor dx(static_cast<T*>(a.dx) + (int64_t)t0 * a.din_stride);
+  float win[K][V], dp[K][V];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    if (EDGE && g * GR >= own + K - 1) continue;
+    if constexpr (EDGE) {                           // a block of its own: see lane_offset
+      co = lane_offset(co);
+      cx = lane_offset(cx);
+    }
+    if (g + 1 < NG) {
+#pragma unroll
+      for (int u = 0; u < GR; ++u) load((g + 1) * GR + u, q[(g + 1) & 1][u], dq[(g + 1) & 1][u]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (g == 0) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        if (EDGE) h[j].clear_unless(!conv_row_is_zero(a, t, t0 - (K - 1) + j));
+        h[j].get(win[j + 1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < GR; ++u) {
+      const int j = g * GR + u;
+      if (EDGE && j >= own + K - 1) continue;
+      conv_slide<T, V, K>(win, q[g & 1][u]);
+      conv_slide<T, V, K>(dp, dq[g & 1][u]);
+      // past the sequence there is no token: whatever was loaded is dropped
+      const bool in = !EDGE || t0 + j < t.end;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if constexpr (SILU) {
+          float pre = b[e];
+#pragma unroll
+          for (int k = 0; k < K; ++k) pre += w[k][e] * win[k][e];
+          const float sg = sigmoid(pre);
+          dp[K - 1][e] *= sg * (1.f + pre * (1.f - sg));
+        }
+        if (EDGE) dp[K - 1][e] = in ? dp[K - 1][e] : 0.f;
+      }
+      if (j < TT && (!EDGE || j < own)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) acc[k][e] += dp[K - 1][e] * win[k][e];
+          acc[K][e] += dp[K - 1][e];
+        }
+      }
+      if (j < K - 1) continue;
+      float o[V];                                   // din of token t0 + j - (K - 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        o[e] = w[K - 1][e] * dp[0][e];
+#pragma unroll
+        for (int k = 1; k < K; ++k) o[e] += w[K - 1 - k][e] * dp[k][e];
+      }
+      if constexpr (EDGE) {
+        const int f = t0 + j - t.end;               // the final state's row of this token
+        if (a.dfinal && f >= 0) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) {
+            float ff[V];
+            fq[k].get(ff);
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] += f == k ? ff[e] : 0.f;
+          }
+        }
+      }
+      Vec<T, V> r;
+      r.set(o);
+      if (EDGE) cx = lane_offset(cx);
+      r.store_at(dx, cx);
+      dx.move(a.din_stride * (int64_t)sizeof(T));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// dw and db accumulate in registers over the workgroup's tiles, are added over
+// its waves in LDS at the end, and leave as one partial row per workgroup,
+// [part][K + 1][C].
+template <typename T, int V, int K, int STEPS, int GR, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a, int nct,
                                                                 int nslots, int nparts) {
-  constexpr int WT = TT * kConvWaves;
+  constexpr int TT = STEPS - (K - 1), WT = TT * kConvWaves;
   __shared__ float red[kConvWaves][K + 1][64 * V];
   if ((int)blockIdx.x >= nct * nparts) {
     conv_dinit_rows<T, V, K>(a, (int64_t)((int)blockIdx.x - nct * nparts) * kConvThreads + threadIdx.x);
     return;
   }
   const int lane = threadIdx.x & 63, wv = wave_id();
-  const int ct = blockIdx.x % nct, part = blockIdx.x / nct;
-  const int nvec = a.C / V, v = ct * 64 + lane;
-  const int c = min(v, nvec - 1) * V;
+  const int part = blockIdx.x / nct;
+  const ConvCols col = conv_cols<V>(a, blockIdx.x % nct);
   float w[K][V], b[V];
-  conv_weights<V, K>(a, c, w, b);
-  int ld;
-  const T* dout = conv_split<const T>(a, const_cast<void* const*>(a.dout), c, ld);
+  conv_weights<V, K>(a, col.c, w, b);
   float acc[K + 1][V];
 #pragma unroll
   for (int k = 0; k <= K; ++k)
@@ -285,85 +487,27 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a
   for (int slot = part; slot < nslots; slot += nparts) {
     const ConvTile t = conv_tile<WT>(a, slot);
     const int t0 = t.lo + wv * TT;
-    if (t0 >= t.hi) continue;
-    const int own = min(TT, t.hi - t0);           // tokens of this run
-    Vec<T, V> q[TT + 2 * (K - 1)], dq[TT + K - 1];
-#pragma unroll
-    for (int j = 0; j < TT + 2 * (K - 1); ++j)
-      q[j] = conv_row<T, V, K>(a, t, min(t0 - (K - 1) + j, t.end - 1), c);
-#pragma unroll
-    for (int j = 0; j < TT + K - 1; ++j) dq[j].load(dout + (int64_t)min(t0 + j, t.end - 1) * ld);
-    float win[K][V], dp[K][V];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) q[j].get(win[j + 1]);
-#pragma unroll
-    for (int j = 0; j < TT + K - 1; ++j) {
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          win[k][e] = win[k + 1][e];
-          dp[k][e] = dp[k + 1][e];
-        }
-      q[j + K - 1].get(win[K - 1]);
-      dq[j].get(dp[K - 1]);
-      const bool in = t0 + j < t.end;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (a.silu) {
-          float pre = b[e];
-#pragma unroll
-          for (int k = 0; k < K; ++k) pre += w[k][e] * win[k][e];
-          const float sg = sigmoid<T>(pre);
-          dp[K - 1][e] *= sg * (1.f + pre * (1.f - sg));
-        }
-        // past the sequence there is no token: whatever was loaded is dropped
-        dp[K - 1][e] = in ? dp[K - 1][e] : 0.f;
-      }
-      if (j < own) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-#pragma unroll
-          for (int k = 0; k < K; ++k) acc[k][e] += dp[K - 1][e] * win[k][e];
-          acc[K][e] += dp[K - 1][e];
-        }
-      }
-      const int i = j - (K - 1);                  // the token whose gradient is complete
-      if (i >= 0 && i < own) {
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          o[e] = 0.f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) o[e] += w[K - 1 - k][e] * dp[k][e];
-        }
-        const int f = t0 + i - (t.end - (K - 1));
-        if (a.dfinal && f >= 0) {
-          Vec<T, V> df;
-          float ff[V];
-          df.load(static_cast<const T*>(a.dfinal) + ((int64_t)t.s * (K - 1) + f) * a.C + c);
-          df.get(ff);
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += ff[e];
-        }
-        Vec<T, V> r;
-        r.set(o);
-        if (v < nvec) r.store(static_cast<T*>(a.dx) + (int64_t)(t0 + i) * a.din_stride + c);
-      }
-    }
+    if (t0 >= t.hi || !col.ok) continue;
+    if (t0 - (K - 1) >= t.start && t0 + TT <= t.hi && t0 + TT + K - 1 <= t.end)
+      conv_bwd_run<T, V, K, STEPS, GR, SILU, false>(a, t, t0, col, w, b, acc);
+    else
+      conv_bwd_run<T, V, K, STEPS, GR, SILU, true>(a, t, t0, col, w, b, acc);
   }
 #pragma unroll
   for (int k = 0; k <= K; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e) red[wv][k][lane * V + e] = acc[k][e];
   __syncthreads();
+  const int first = __builtin_amdgcn_readfirstlane(col.c - col.co);   // the output's first channel
   for (int i = threadIdx.x; i < (K + 1) * 64 * V; i += kConvThreads) {
-    const int k = i / (64 * V), cc = i % (64 * V), ch = ct * 64 * V + cc;
-    if (ch >= a.C) continue;
-    float t = red[0][k][cc];
+    const int k = i / (64 * V), cc = i % (64 * V), ch = col.tile + cc;
+    if (ch >= col.ld) continue;
+    // the value's place: its vector's lane, whose vector may start earlier
+    const int at = cc / V * V + ch - conv_vec<V>(ch / V, col.ld);
+    float s = red[0][k][at];
 #pragma unroll
-    for (int u = 1; u < kConvWaves; ++u) t += red[u][k][cc];
-    a.part[((int64_t)part * (K + 1) + k) * a.C + ch] = t;
+    for (int u = 1; u < kConvWaves; ++u) s += red[u][k][at];
+    a.part[((int64_t)part * (K + 1) + k) * a.C + first + ch] = s;
   }
 }
 
@@ -382,18 +526,18 @@ struct ConvGradOut {
 // slot's state, so the shift in place needs no exchange.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs a, int nblk) {
-  const int row = blockIdx.x / nblk, v = (int)(blockIdx.x % nblk) * kConvThreads + threadIdx.x;
-  int64_t slot;
-  if (step_row_is_padding(a.slots, row, a.nslots, slot)) return;
-  if (v >= a.C / V) return;
-  const int c = v * V;
-  T* st = static_cast<T*>(a.states) + slot * (K - 1) * a.C + c;
+  const int row = blockIdx.x / nblk, v = (int)(blockIdx.x % nblk) * (int)blockDim.x + threadIdx.x;
+  StepSlot slot;
+  if (!slot.begin(a.slots, row, a.nslots)) return;
+  const int c = min(v, a.C / V - 1) * V;
+  T* st = static_cast<T*>(a.states) + (int64_t)slot.mine * (K - 1) * a.C + c;
   Vec<T, V> q[K];
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) q[k].load(st + (int64_t)k * a.C);
   q[K - 1].load(static_cast<const T*>(a.x) + row * a.in_stride + c);
   float w[K][V], o[V];
   conv_weights<V, K>(a, c, w, o);
+  if (slot.repeated() || v >= a.C / V) return;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float f[V];
@@ -403,19 +547,21 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
   }
   if (a.silu) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] *= sigmoid<T>(o[e]);
+    for (int e = 0; e < V; ++e) o[e] *= sigmoid(o[e]);
   }
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) q[k + 1].store(st + (int64_t)k * a.C);
-  int ld;
-  T* out = conv_split<T>(a, a.out, c, ld);
+  const int i = c < a.n[0] ? 0 : c < a.n[0] + a.n[1] ? 1 : 2;
+  const int ld = i == 0 ? a.n[0] : i == 1 ? a.n[1] : a.n[2];
   Vec<T, V> r;
   r.set(o);
-  r.store(out + (int64_t)row * ld);
+  r.store(conv_pick<T>(a.out, i) + (int64_t)row * ld + c - (i == 0 ? 0 : i == 1 ? a.n[0] : a.n[0] + a.n[1]));
 }
 
-constexpr int kConvFwdTT = 16, kConvBwdTT = 8;
+constexpr int kConvFwdLong = 16, kConvFwdShort = 4;     // tokens per run, forward
+constexpr int kConvBwdLong = 64, kConvBwdShort = 16;    // steps per run, backward
 constexpr int kConvBwdMaxParts = 256;
+constexpr int kConvStepThreads = 128;
 constexpr int64_t kConvMaxGroups = 1 << 22;   // workgroups of one launch
 
 // Token groups of a launch: one per slot while the launch stays within
@@ -425,29 +571,29 @@ int conv_parts(int nslots, int nct, int64_t most) {
   return (int)(nslots < p ? nslots : (p > 0 ? p : 1));
 }
 
-template <typename T, int V, int K>
+template <typename T, int V, int K, int TT>
 hipError_t conv_fwd_go(const ConvArgs& a, hipStream_t s) {
-  const int nct = (a.C / V + 63) / 64;
-  const int nslots = conv_slots(a, kConvFwdTT * kConvWaves);
+  const int nct = conv_col_tiles<V>(a);
+  const int nslots = conv_slots(a, TT * kConvWaves);
   const int nparts = a.total > 0 ? conv_parts(nslots, nct, kConvMaxGroups) : 0;
-  const int64_t fin = a.final_states ? (int64_t)a.nstates * (K - 1) * (a.C / V) : 0;
+  const int64_t fin = a.final_states ? (int64_t)a.nstates * (K - 1) * ((a.C + V - 1) / V) : 0;
   const int64_t grid = (int64_t)nct * nparts + (fin + kConvThreads - 1) / kConvThreads;
   if (grid == 0) return hipSuccess;
-  hipLaunchKernelGGL((conv_fwd_kernel<T, V, K, kConvFwdTT>), dim3((unsigned)grid),
-                     dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
+  auto fn = a.silu ? &conv_fwd_kernel<T, V, K, TT, true> : &conv_fwd_kernel<T, V, K, TT, false>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
   return hipGetLastError();
 }
 
-template <typename T, int V, int K>
+template <typename T, int V, int K, int STEPS>
 hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
-  const int nct = (a.C / V + 63) / 64;
-  const int nslots = conv_slots(a, kConvBwdTT * kConvWaves);
+  const int nct = conv_col_tiles<V>(a);
+  const int nslots = conv_slots(a, (STEPS - (K - 1)) * kConvWaves);
   const int nparts = a.total > 0 ? conv_parts(nslots, 1, kConvBwdMaxParts) : 0;
-  const int64_t ini = a.dinit ? (int64_t)a.nstates * (a.C / V) : 0;
+  const int64_t ini = a.dinit ? (int64_t)a.nstates * ((a.C + 2) / V + 3) : 0;
   const int64_t grid = (int64_t)nct * nparts + (ini + kConvThreads - 1) / kConvThreads;
+  auto fn = a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true> : &conv_bwd_kernel<T, V, K, STEPS, 8, false>;
   if (grid > 0)
-    hipLaunchKernelGGL((conv_bwd_kernel<T, V, K, kConvBwdTT>), dim3((unsigned)grid),
-                       dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
+    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
   const int cols = (K + 1) * a.C;
   hipLaunchKernelGGL(colsum_kernel<ConvGradOut>, dim3((cols + 63) / 64), dim3(kColsumThreads), 0, s,
                      (const float*)a.part, nparts, cols, (ConvGradOut{a.dw, a.dbias, a.C, K}));
@@ -456,53 +602,81 @@ hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
 
 template <typename T, int V, int K>
 hipError_t conv_step_go(const ConvArgs& a, hipStream_t s) {
-  const int nblk = (a.C / V + kConvThreads - 1) / kConvThreads;
+  const int nblk = (a.C / V + kConvStepThreads - 1) / kConvStepThreads;
   hipLaunchKernelGGL((conv_step_kernel<T, V, K>), dim3((unsigned)(a.batch * nblk)),
-                     dim3(kConvThreads), 0, s, a, nblk);
+                     dim3(kConvStepThreads), 0, s, a, nblk);
   return hipGetLastError();
 }
 
-enum ConvOp { kFwd, kBwd, kStep };
-
-template <int OP, typename T, int V, int K>
-hipError_t conv_go(const ConvArgs& a, hipStream_t s) {
-  if constexpr (OP == kFwd) return conv_fwd_go<T, V, K>(a, s);
-  else if constexpr (OP == kBwd) return conv_bwd_go<T, V, K>(a, s);
-  else return conv_step_go<T, V, K>(a, s);
+// Every output has a whole vector of V channels (or none).
+bool conv_has(const ConvArgs& a, int V) {
+  return a.n[0] >= V && (a.n[1] >= V || a.n[1] == 0) && (a.n[2] >= V || a.n[2] == 0);
 }
 
-template <int OP, typename T, int V>
-hipError_t conv_width(const ConvArgs& a, hipStream_t s) {
-  switch (a.K) {
-    case 2: return conv_go<OP, T, V, 2>(a, s);
-    case 3: return conv_go<OP, T, V, 3>(a, s);
-    case 4: return conv_go<OP, T, V, 4>(a, s);
+// Long runs read fewer rows twice but leave few waves on a small problem, where
+// one run's latency is the launch's.  Measured (us, long / short runs):
+//   forward   1792 ch bf16: 256 tokens 5.0 / 3.0, 4096 8.8 / 8.1, 8192 13.2 / 12.9;
+//             6144 ch bf16: 4096 tokens 24.4 / 25.3, 32768 149 / 166
+//   backward  1792 ch bf16: 256 tokens 17.4 / 8.2, 4096 19.7 / 18.1, 8192 23.6 / 29.2;
+//             6144 ch bf16: 2048 tokens 20.6 / 22.9; 256 ch: 32768 tokens 19.0 / 17.4
+//             6144 ch fp32: 8192 tokens 127 / 119 (never long)
+// so the forward takes them from 2^24 elements on, the backward from 10 2^20
+// (bf16).  Two channels per thread in the short runs, again for more waves.
+bool conv_long(const ConvArgs& a, int64_t from) { return (int64_t)a.total * a.C >= from; }
+
+template <typename T, int K>
+hipError_t conv_fwd_k(const ConvArgs& a, hipStream_t s) {
+  if (conv_long(a, (int64_t)1 << 24) && conv_has(a, 4)) return conv_fwd_go<T, 4, K, kConvFwdLong>(a, s);
+  if (conv_has(a, 2)) return conv_fwd_go<T, 2, K, kConvFwdShort>(a, s);
+  return conv_fwd_go<T, 1, K, kConvFwdShort>(a, s);
+}
+
+template <typename T, int K>
+hipError_t conv_bwd_k(const ConvArgs& a, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (conv_long(a, (int64_t)10 << 20) && conv_has(a, 2)) return conv_bwd_go<T, 2, K, kConvBwdLong>(a, s);
   }
-  return hipErrorInvalidValue;
+  if (conv_has(a, 2)) return conv_bwd_go<T, 2, K, kConvBwdShort>(a, s);
+  return conv_bwd_go<T, 1, K, kConvBwdShort>(a, s);
 }
 
-// 16-byte vectors where every output's channels are whole vectors, else one
-// channel per thread.
-template <int OP>
-hipError_t conv_dispatch(const ConvArgs& a, hipStream_t s) {
-  const int m = a.bf16 ? 8 : 4;
-  const bool vec = a.n[0] % m == 0 && a.n[1] % m == 0 && a.n[2] % m == 0;
-  if (a.bf16) return vec ? conv_width<OP, bf16, 8>(a, s) : conv_width<OP, bf16, 1>(a, s);
-  return vec ? conv_width<OP, float, 4>(a, s) : conv_width<OP, float, 1>(a, s);
+// In place, so no two threads may share a channel: whole vectors only.
+template <typename T, int K>
+hipError_t conv_step_k(const ConvArgs& a, hipStream_t s) {
+  const bool whole = a.n[0] % 2 == 0 && a.n[1] % 2 == 0 && a.n[2] % 2 == 0;
+  return whole ? conv_step_go<T, 2, K>(a, s) : conv_step_go<T, 1, K>(a, s);
 }
+
+#define SSD_CONV_K(OP, T)                        \
+  switch (a.K) {                                 \
+    case 2: return conv_##OP##_k<T, 2>(a, s);    \
+    case 3: return conv_##OP##_k<T, 3>(a, s);    \
+    case 4: return conv_##OP##_k<T, 4>(a, s);    \
+  }                                              \
+  return hipErrorInvalidValue
 
 }  // namespace
 
+// As many partial rows as the launch with the shortest runs has.
 int64_t conv_bwd_floats(int64_t tokens, int64_t nstates, int64_t C, int64_t K) {
-  const int64_t slots = (tokens + kConvBwdTT * kConvWaves - 1) / (kConvBwdTT * kConvWaves) + nstates;
+  const int64_t wt = (kConvBwdShort - (K - 1)) * kConvWaves;
+  const int64_t slots = (tokens + wt - 1) / wt + nstates;
   return (slots < kConvBwdMaxParts ? slots : kConvBwdMaxParts) * (K + 1) * C;
 }
 
-hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) { return conv_dispatch<kFwd>(a, s); }
-hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s) { return conv_dispatch<kBwd>(a, s); }
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) {
+  if (a.bf16) { SSD_CONV_K(fwd, bf16); }
+  SSD_CONV_K(fwd, float);
+}
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s) {
+  if (a.bf16) { SSD_CONV_K(bwd, bf16); }
+  SSD_CONV_K(bwd, float);
+}
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t s) {
   if (a.batch <= 0) return hipSuccess;
-  return conv_dispatch<kStep>(a, s);
+  if (a.bf16) { SSD_CONV_K(step, bf16); }
+  SSD_CONV_K(step, float);
 }
+#undef SSD_CONV_K
 
 }  // namespace ssd

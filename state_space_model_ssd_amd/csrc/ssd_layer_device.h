@@ -26,6 +26,30 @@ SSD_RAW(4, 4, unsigned)
 SSD_RAW(2, 2, unsigned short)
 #undef SSD_RAW
 
+// Accesses as a scalar base plus a 32-bit lane offset, which the memory unit adds.
+// Left alone, the compiler adds the lane's offset to the tensor's base first, so
+// that every row costs each lane a 64-bit addition and two registers, and forms
+// the bases of all of an unrolled loop's rows up front, more than the scalar
+// registers hold.  Two empty asm statements keep the form: one on the lane's
+// offset, in the block of the access, and one on the base at each use, after
+// which the next row's base can only be formed from it.
+__device__ __forceinline__ uint32_t lane_offset(uint32_t off) {
+  asm("" : "+v"(off));
+  return off;
+}
+
+// The row a wave is at in a tensor: an address that is the same in every lane.
+struct RowCursor {
+  uint64_t at;
+  template <typename T>
+  __device__ __forceinline__ explicit RowCursor(const T* p) : at(reinterpret_cast<uint64_t>(p)) {}
+  __device__ __forceinline__ __attribute__((address_space(1))) char* here() {
+    asm("" : "+s"(at));
+    return reinterpret_cast<__attribute__((address_space(1))) char*>(at);
+  }
+  __device__ __forceinline__ void move(int64_t bytes) { at += bytes; }
+};
+
 template <typename T, int V> struct Vec {
   static constexpr int B = (int)sizeof(T) * V;         // bytes
   static constexpr int NP = B > 16 ? B / 16 : 1;       // accesses
@@ -40,6 +64,19 @@ template <typename T, int V> struct Vec {
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
     for (int i = 0; i < NP; ++i) *reinterpret_cast<typename raw::mem*>(p + i * PV) = q[i];
+  }
+  // `off` (a lane_offset) bytes into the cursor's row.
+  __device__ __forceinline__ void load_at(RowCursor& row, uint32_t off) {
+    const __attribute__((address_space(1))) char* p = row.here() + off;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      q[i] = *reinterpret_cast<const __attribute__((address_space(1))) typename raw::mem*>(p + i * PB);
+  }
+  __device__ __forceinline__ void store_at(RowCursor& row, uint32_t off) const {
+    __attribute__((address_space(1))) char* p = row.here() + off;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      *reinterpret_cast<__attribute__((address_space(1))) typename raw::mem*>(p + i * PB) = q[i];
   }
   // The first n elements only (n < V: a row's end), zeros after them.
   __device__ __forceinline__ void load_some(const T* p, int n) {
@@ -74,30 +111,51 @@ template <typename T, int V> struct Vec {
   }
 };
 
-// sigmoid(z) = 1 / (1 + e^-z).  fp32 tensors take the accurate exponential and
-// division; bf16 ones the hardware's (a few units in the last place of fp32,
-// far below one rounding to bf16).  e^-z may overflow to infinity: sigmoid 0.
-template <typename T> __device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
-  else return 1.f / (1.f + expf(-z));
+// sigmoid(z) = 1 / (1 + e^-z) by the hardware's exponential and reciprocal, in
+// fp32 for either type: the argument's rounding puts |z| 2^-23 and the functions
+// some 2^-22 relative on e^-z, which weighs by its share of 1 + e^-z, so the
+// result is off by a few units in the last place of fp32 for z >= -4 and by
+// |z| of them below, where it is itself e^z.  e^-z may overflow to infinity:
+// sigmoid 0.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
 
-// Whether a row of a single-token batch is padding: its slot lies outside
-// the cache, or an earlier row has the same slot (the first row has it: no two
-// workgroups ever write one state).  Every thread of the workgroup calls it.
-// Costs one load per thread and 256 rows, in flight with the row's others.
-__device__ __forceinline__ bool step_row_is_padding(const int32_t* slots, int row, int64_t nslots,
-                                                    int64_t& slot) {
-  if (!slots) {
-    slot = row;
-    return false;
+// The slot of a row of a single-token batch.  A row is padding if its slot lies
+// outside the cache, or if an earlier row has the same slot (the first row has
+// it: no two rows ever write one state).  Every wave looks through the earlier
+// rows by itself, 64 at a time, so no barrier is needed: begin() issues the
+// loads of the nearest 256 without waiting for them, and the caller issues its
+// own loads before repeated() uses them.
+struct StepSlot {
+  static constexpr int kAhead = 4;
+  const int32_t* slots;
+  int row, mine;
+  int32_t near[kAhead];
+
+  // False: outside the cache.  Uniform over the workgroup.
+  __device__ __forceinline__ bool begin(const int32_t* s, int r, int64_t nslots) {
+    slots = s;
+    row = r;
+    mine = s ? s[r] : r;
+    if (mine < 0 || mine >= nslots) return false;
+    if (s) {
+      const int lane = threadIdx.x & 63;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) near[i] = s[max(row - 1 - lane - 64 * i, 0)];
+    }
+    return true;
   }
-  const int32_t mine = slots[row];
-  slot = mine;
-  int seen = 0;
-  for (int i = threadIdx.x; i < row; i += blockDim.x) seen |= slots[i] == mine;
-  return __syncthreads_or(seen) || mine < 0 || mine >= nslots;
-}
+  __device__ __forceinline__ bool repeated() const {
+    if (!slots) return false;
+    const int lane = threadIdx.x & 63;
+    bool seen = false;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) seen |= lane + 64 * i < row && near[i] == mine;
+    for (int i = row - 1 - lane - 64 * kAhead; i >= 0; i -= 64) seen |= slots[i] == mine;
+    return __any(seen);
+  }
+};
 
 // Sums over the rows of part[nparts][cols]: OUT::put(column, sum).  One
 // workgroup of 16 waves per 64 columns; wave w adds rows w, w + 16, ... in

@@ -5,11 +5,14 @@
 //
 // What bounds it: the state, read and written once (8 P N H bytes a row);
 // everything else is under a percent.  So a workgroup streams whole rows of
-// one head's state: a row of N values lies over LPR lanes, V consecutive
+// one head's state: a row of N values lies over LPR lanes, four consecutive
 // values (16 bytes) per lane, a wave covers 64 / LPR rows, and each thread has
 // the R rows it owns in flight at once.  B and C are the same for all of a
 // thread's rows and stay in its registers; a row's sum over n is a butterfly
-// over its LPR lanes.
+// over its LPR lanes.  Where N is not a multiple of four, a row's last vector
+// starts early enough to end with the row: it overlaps the vector before it, in
+// the same wave, so both have loaded before either stores, store the same
+// values, and the sum takes the shared ones once.
 #include "ssd_device.h"
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
@@ -19,51 +22,32 @@ namespace ssd {
 
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 256;   // most threads of a workgroup
 
-// V: values per access (4, or 1 where N is not a multiple of 4); NK: accesses
-// of a lane per row; R: rows per thread.
-template <typename T, typename DT, int V, int NK, int R>
+// V: values per access (4, or 1 for N < 4); R: rows per thread.
+template <typename T, typename DT, int V, int R>
 __global__ __launch_bounds__(kStepThreads) void step_kernel(const StepArgs a, int lpr, int nblk) {
   const int blk = blockIdx.x % nblk;              // block of rows of the head's state
   const int hb = blockIdx.x / nblk;
   const int h = hb % a.H, b = hb / a.H;
   const int g = h / (a.H / a.G);
-  int64_t slot;
-  if (step_row_is_padding(a.slots, b, a.nslots, slot)) return;
+  StepSlot slot;
+  if (!slot.begin(a.slots, b, a.nslots)) return;
   const int ln = threadIdx.x & (lpr - 1);         // lane within the row
-  const int rows = kStepThreads / lpr;            // rows per pass
+  const int rows = blockDim.x / lpr;              // rows per pass
   const int p0 = blk * rows * R + threadIdx.x / lpr;
-  float* st = a.states + (slot * a.H + h) * (int64_t)a.P * a.N;
+  const bool in = ln * V < a.N;
+  const int n = min(ln * V, a.N - V);             // the lane's first value
+  float* st = a.states + ((int64_t)slot.mine * a.H + h) * a.P * a.N + n;
 
-  Vec<float, V> s[R][NK];
+  Vec<float, V> s[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int p = min(p0 + r * rows, a.P - 1);
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const int n = (ln + k * lpr) * V;
-      s[r][k].load(st + (int64_t)p * a.N + (n < a.N ? n : 0));
-    }
-  }
+  for (int r = 0; r < R; ++r) s[r].load(st + (int64_t)min(p0 + r * rows, a.P - 1) * a.N);
   const T* x = static_cast<const T*>(a.x) + b * a.x_stride + (int64_t)h * a.P;
-  const T* Bp = static_cast<const T*>(a.B) + b * a.b_stride + (int64_t)g * a.N;
-  const T* Cp = static_cast<const T*>(a.C) + b * a.c_stride + (int64_t)g * a.N;
-  float Bv[NK][V], Cv[NK][V], xv[R];
-#pragma unroll
-  for (int k = 0; k < NK; ++k) {
-    const int n = (ln + k * lpr) * V;
-    Vec<T, V> q;
-    q.load(Bp + (n < a.N ? n : 0));
-    q.get(Bv[k]);
-    q.load(Cp + (n < a.N ? n : 0));
-    q.get(Cv[k]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      Bv[k][e] = n < a.N ? Bv[k][e] : 0.f;
-      Cv[k][e] = n < a.N ? Cv[k][e] : 0.f;
-    }
-  }
+  Vec<T, V> Bq, Cq;
+  Bq.load(static_cast<const T*>(a.B) + b * a.b_stride + (int64_t)g * a.N + n);
+  Cq.load(static_cast<const T*>(a.C) + b * a.c_stride + (int64_t)g * a.N + n);
+  float Bv[V], Cv[V], xv[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) xv[r] = to_f32(x[min(p0 + r * rows, a.P - 1)]);
   const float u = to_f32(static_cast<const DT*>(a.dt)[b * a.dt_stride + h]) +
@@ -72,63 +56,70 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const StepArgs a, in
   const float decay = expf(delta * a.A[h]);
   const float D = a.D ? a.D[h] : 0.f;
   T* out = static_cast<T*>(a.out) + ((int64_t)b * a.H + h) * a.P;
+  if (slot.repeated()) return;
+  Bq.get(Bv);
+  Cq.get(Cv);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int p = p0 + r * rows;
     const float dx = delta * xv[r];
-    float y = 0.f;
+    float y = 0.f, f[V];
+    s[r].get(f);
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const int n = (ln + k * lpr) * V;
-      float f[V];
-      s[r][k].get(f);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        f[e] = f[e] * decay + dx * Bv[k][e];
-        // a lane past the row's end holds another value's copy: it adds nothing
-        y += n < a.N ? f[e] * Cv[k][e] : 0.f;
-      }
-      s[r][k].set(f);
-      if (p < a.P && n < a.N) s[r][k].store(st + (int64_t)p * a.N + n);
+    for (int e = 0; e < V; ++e) {
+      f[e] = f[e] * decay + dx * Bv[e];
+      // values before the lane's own place belong to the lane before it, and
+      // lanes past the row's end have none
+      y += n + e >= ln * V && in ? f[e] * Cv[e] : 0.f;
     }
+    s[r].set(f);
+    if (p < a.P && in) s[r].store(st + (int64_t)p * a.N);
     y = run_sum_dpp(y, lpr);
     if (ln == 0 && p < a.P) out[p] = from_f32<T>(a.D ? y + D * xv[r] : y);
   }
 }
 
 // Lanes per row: N's accesses rounded up to a power of two, at most a wave.
-int step_lpr(int N, int V) {
+int step_lpr(int N) {
+  const int V = N >= 4 ? 4 : 1;
   int l = 1;
-  while (l < 64 && l * V < N) l *= 2;
+  while (l * V < N) l *= 2;
   return l;
 }
 
-template <typename T, typename DT, int V, int NK, int R>
+template <typename T, typename DT, int V, int R>
 hipError_t step_go(const StepArgs& a, int lpr, hipStream_t s) {
-  const int rows = kStepThreads / lpr * R;
+  // one wave where a head's rows fill no more
+  int threads = kStepThreads;
+  while (threads > 64 && threads / 2 * R >= a.P * lpr) threads /= 2;
+  const int rows = threads / lpr * R;
   const int nblk = (a.P + rows - 1) / rows;
-  hipLaunchKernelGGL((step_kernel<T, DT, V, NK, R>), dim3((unsigned)(a.batch * (int64_t)a.H * nblk)),
-                     dim3(kStepThreads), 0, s, a, lpr, nblk);
+  hipLaunchKernelGGL((step_kernel<T, DT, V, R>), dim3((unsigned)(a.batch * (int64_t)a.H * nblk)),
+                     dim3(threads), 0, s, a, lpr, nblk);
   return hipGetLastError();
 }
 
+// Rows per thread: more rows are more bytes in flight per wave and fewer
+// workgroups to start, fewer rows more waves.  Measured (us, R = 1 / 2 / 4; P 64,
+// N 128): one sequence of 24 heads 3.16 / 3.35 / 3.83, four 4.58 / 4.17 / 4.33, 32 18.0
+// / 12.6 / 11.3; 64 sequences of 32 heads 38.9 / 24.6 / 23.4; 256, whose states pass
+// the last-level cache, 156 / 103 / 106 (5.1 TB/s, a large copy's rate).  So four
+// rows from one workgroup per CU on, two from half a one, and two again for
+// states larger than the cache (256 MB).
 template <typename T, typename DT>
 hipError_t step_type(const StepArgs& a, hipStream_t s) {
-  if (a.N % 4 == 0) return step_go<T, DT, 4, 1, 1>(a, step_lpr(a.N, 4), s);
-  const int lpr = step_lpr(a.N, 1);
-  switch ((a.N + lpr - 1) / lpr) {
-    case 1: return step_go<T, DT, 1, 1, 1>(a, lpr, s);
-    case 2: return step_go<T, DT, 1, 2, 1>(a, lpr, s);
-    case 3: return step_go<T, DT, 1, 3, 1>(a, lpr, s);
-    case 4: return step_go<T, DT, 1, 4, 1>(a, lpr, s);
-  }
-  return hipErrorInvalidValue;
+  const int lpr = step_lpr(a.N);
+  if (a.N < 4) return step_go<T, DT, 1, 1>(a, lpr, s);
+  const int64_t lanes = (int64_t)a.batch * a.H * a.P * lpr;
+  if (lanes < 2 * 128 * kStepThreads) return step_go<T, DT, 4, 1>(a, lpr, s);
+  if (lanes < 4 * 256 * kStepThreads || lanes >= 1 << 24) return step_go<T, DT, 4, 2>(a, lpr, s);
+  return step_go<T, DT, 4, 4>(a, lpr, s);
 }
 
 }  // namespace
 
 int64_t step_row_blocks(int64_t P, int64_t N) {
-  const int rows = kStepThreads / step_lpr((int)N, N % 4 == 0 ? 4 : 1);
+  const int rows = kStepThreads / step_lpr((int)N);
   return (P + rows - 1) / rows;
 }
 
