@@ -220,6 +220,8 @@ def _ptr(t: Optional[torch.Tensor]):
 def _need(t, name, dtype, shape, device):
     if t is None:
         return
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -509,13 +511,19 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without making a torch.cuda.Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(dev, fn, *args):
     """fn(*args, stream) with `dev` current, on its current stream."""
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            code = fn(*args, _raw_stream(index))
     if code != SSD_OK:
         _check(code)
 
@@ -533,6 +541,8 @@ def _row_stride(t, name, rows):
     """Elements from one row to the next of a tensor whose last axes are
     contiguous and whose first `rows` axes lie evenly behind one another."""
     st, sh = t.stride(), t.shape
+    if t.is_contiguous():
+        return math.prod(sh[rows:])
     inner = 1
     for i in range(len(sh) - 1, rows - 1, -1):
         if sh[i] != 1 and st[i] != inner:
@@ -591,9 +601,10 @@ def _conv_prompt(what, x, weight, bias, splits, activation, initial_states, cu_s
     return dev, b, T, C, splits, sshape, prob
 
 
-def _conv_outs(outs, splits, lead, dtype, dev, name):
+def _conv_outs(outs, splits, lead, like, name):
+    dtype, dev = like.dtype, like.device
     if outs is None:
-        return [torch.empty(lead + (n,), dtype=dtype, device=dev) for n in splits]
+        return [like.new_empty(lead + (n,)) for n in splits]
     if len(outs) != 3:
         raise ValueError(f"{name} are three tensors")
     for o, n in zip(outs, splits):
@@ -621,11 +632,11 @@ def conv_fwd(x, weight, bias=None, splits=None, initial_states=None, cu_seqlens=
     return_final_states)."""
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_fwd", x, weight, bias, splits,
                                                       activation, initial_states, cu_seqlens)
-    outs = _conv_outs(outs, splits, (b, T), x.dtype, dev, "outs")
+    outs = _conv_outs(outs, splits, (b, T), x, "outs")
     if final_states is not None:
         _need(final_states, "final_states", x.dtype, sshape, dev)
     elif return_final_states:
-        final_states = torch.empty(sshape, dtype=x.dtype, device=dev)
+        final_states = x.new_empty(sshape)
     _launch(dev, load_library().ssd_conv_fwd, prob[1], x.data_ptr(), weight.data_ptr(), _addr(bias),
             _addr(initial_states), _addr(cu_seqlens), _addr(outs[0]), _addr(outs[1]),
             _addr(outs[2]), _addr(final_states))
@@ -650,14 +661,14 @@ def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_s
         stride = _row_stride(dx, "dx", 2)
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_bwd", x, weight, bias, splits,
                                                       activation, initial_states, cu_seqlens, stride)
-    douts = _conv_outs(douts, splits, (b, T), x.dtype, dev, "douts")
+    douts = _conv_outs(douts, splits, (b, T), x, "douts")
     _need(dfinal_states, "dfinal_states", x.dtype, sshape, dev)
     f32 = torch.float32
     if dx is None:
-        dx = torch.empty((b, T, C), dtype=x.dtype, device=dev)
-    g = {"x": dx, "weight": torch.empty(weight.shape, dtype=f32, device=dev),
-         "bias": torch.empty((C,), dtype=f32, device=dev) if bias is not None else None,
-         "initial_states": torch.empty_like(initial_states) if initial_states is not None else None}
+        dx = x.new_empty((b, T, C))
+    g = {"x": dx, "weight": weight.new_empty(weight.shape),
+         "bias": weight.new_empty((C,)) if bias is not None else None,
+         "initial_states": x.new_empty(sshape) if initial_states is not None else None}
     if workspace is None:
         workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
     _launch(dev, load_library().ssd_conv_bwd, prob[1], x.data_ptr(), weight.data_ptr(), _addr(bias),
@@ -688,7 +699,7 @@ def conv_step(x, conv_states, weight, bias=None, splits=None, slots=None, activa
     if outs is None and slots is not None:
         outs = [torch.zeros((b, n), dtype=x.dtype, device=dev) for n in splits]
     else:
-        outs = _conv_outs(outs, splits, (b,), x.dtype, dev, "outs")
+        outs = _conv_outs(outs, splits, (b,), x, "outs")
     prob = _conv_problem(b, 1, 0, *splits, K, _row_stride(x, "x", 1), 0, _DT[x.dtype], act)
     _launch(dev, load_library().ssd_conv_step, prob[1], x.data_ptr(), weight.data_ptr(),
             _addr(bias), conv_states.data_ptr(), nslots, _addr(slots), _addr(outs[0]),
@@ -711,8 +722,9 @@ def ssd_step(x, dt, A, B, C, states, D=None, dt_bias=None, slots=None, dt_min=0.
     b, H, P = x.shape
     G, N = B.shape[1], B.shape[2]
     f32 = torch.float32
-    for t, name, dtp, shape in ((dt, "dt", dt.dtype, (b, H)), (B, "B", x.dtype, (b, G, N)),
-                                (C, "C", x.dtype, (b, G, N))):
+    bc = (b, G, N)
+    for t, name, dtp, shape in ((dt, "dt", dt.dtype, (b, H)), (B, "B", x.dtype, bc),
+                                (C, "C", x.dtype, bc)):
         if t.device != dev or t.dtype != dtp or t.shape != shape:
             raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
                              f"{dtp} {shape} on {dev}")
@@ -776,11 +788,11 @@ def block_norm_fwd(x, residual, pre_weight, gate=None, gate_activation="sigmoid"
         "block_norm_fwd", x, residual, gate, post_weight, scale, pre_weight, gate_activation,
         residual_scale, eps, residual_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
     else:
         _need(out, "out", x.dtype, shape, dev)
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=rdt, device=dev)
+        residual_out = x.new_empty(shape, dtype=rdt)
     else:
         _need(residual_out, "residual_out", rdt, shape, dev)
     _launch(dev, load_library().ssd_block_norm_fwd, prob[1], x.data_ptr(), _addr(residual),
@@ -801,13 +813,12 @@ def block_norm_bwd(x, residual, pre_weight, dout, dresidual_out=None, gate=None,
         residual_scale, eps, residual_dtype)
     _need(dout, "dout", x.dtype, shape, dev)
     _need(dresidual_out, "dresidual_out", rdt, shape, dev)
-    f32 = torch.float32
-    g = {"x": torch.empty(shape, dtype=x.dtype, device=dev),
-         "residual": torch.empty(shape, dtype=rdt, device=dev) if residual is not None else None,
-         "gate": torch.empty(shape, dtype=x.dtype, device=dev) if gate is not None else None,
-         "post_weight": torch.empty((C,), dtype=f32, device=dev) if post_weight is not None else None,
-         "scale": torch.empty((C,), dtype=f32, device=dev) if scale is not None else None,
-         "pre_weight": torch.empty((C,), dtype=f32, device=dev)}
+    g = {"x": x.new_empty(shape),
+         "residual": x.new_empty(shape, dtype=rdt) if residual is not None else None,
+         "gate": x.new_empty(shape) if gate is not None else None,
+         "post_weight": pre_weight.new_empty((C,)) if post_weight is not None else None,
+         "scale": pre_weight.new_empty((C,)) if scale is not None else None,
+         "pre_weight": pre_weight.new_empty((C,))}
     if workspace is None:
         workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
     _launch(dev, load_library().ssd_block_norm_bwd, prob[1], x.data_ptr(), _addr(residual),

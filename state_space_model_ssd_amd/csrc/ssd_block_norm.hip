@@ -8,11 +8,18 @@
 //   dpre_w = sum dout n,  dscale = sum dh alpha u,  dpost_w = sum dp m
 //
 // What bounds it: memory; each input is read and each output written once.  A
-// row stays in registers from its loads to its stores: it lies over W waves,
-// KT vectors of V channels (16 bytes of x) per lane, and its sums (up to two
-// forward, four backward, each needed before the next) are butterflies in
-// registers, joined over the W waves in LDS.  W is the fewest waves that hold a
-// row with KT = 2, so a row of up to 128 vectors needs no barrier at all.
+// row lies over W waves, one vector of four channels per lane (KT vectors in rows
+// wider than 2048 channels), and stays in registers from its loads to its
+// stores.  Its sums are butterflies in registers, joined over the W waves in LDS
+// with one barrier: two exchanges forward (the norm after the block, then the
+// one before the next), and two backward, whose later sums are arranged to need
+// nothing that the second exchange computes.  Four channels per lane rather
+// than eight: fewer registers, more rows in flight (forward at 8192 x 768 with an
+// fp32 residual 23.5 -> 19.4 us, 4.5 TB/s; backward 82 -> 38 us, 3.6 TB/s).
+//
+// The forward keeps the next row's loads in flight; the backward, with twice
+// the registers, does better with more waves (8192 x 768: 43 us with the next
+// row in flight, 38 without).
 //
 // Weight gradients accumulate in registers over the rows a workgroup walks,
 // leave as one partial row per workgroup and are added in workgroup order by a
@@ -26,23 +33,29 @@ namespace ssd {
 
 namespace {
 
-template <typename T> constexpr int kBnV = 16 / (int)sizeof(T);
-
-// Sum of v over the W waves of a row, the same in every lane.  `buf`: two
-// buffers of W floats used in turn (`par`), so the barrier of one sum also
-// frees the buffer of the sum before.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float (*buf)[W], int& par) {
-  v = run_sum_dpp(v, 64);
-  if constexpr (W > 1) {
-    if ((threadIdx.x & 63) == 0) buf[par][threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = buf[par][0];
+// Sums of s[0..M) over the W waves of a row, the same in every lane.  `buf` holds
+// two sets of W floats per sum and row, used in turn (`par`), so the barrier of
+// one call also frees the set of the call before.  Every thread of the workgroup
+// calls it.
+template <int W, int RG, int M, int MAXM>
+__device__ __forceinline__ void row_sums(float (&s)[M], float (*buf)[MAXM][RG][W], int rg, int& par) {
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += buf[par][w];
+  for (int i = 0; i < M; ++i) s[i] = run_sum_dpp(s[i], 64);
+  if constexpr (W > 1) {
+    const int w = wave_id() - rg * W;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) buf[par][i][rg][w] = s[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      s[i] = buf[par][i][rg][0];
+#pragma unroll
+      for (int j = 1; j < W; ++j) s[i] += buf[par][i][rg][j];
+    }
     par ^= 1;
   }
-  return v;
 }
 
 // The channels [c, c + V) of a row of C channels, zeros past its end.
@@ -63,18 +76,22 @@ __device__ __forceinline__ void bn_store(const Vec<E, V>& q, E* row, int c, int 
   else if (TAIL && c < C) q.store_some(row + c, C - c);
 }
 
-// Weights of the thread's channels: `one` where there is no weight, 0 past the
-// row's end.
-template <int KT, int V, int LANES>
+// Weights of the thread's channels, times `mul`; `mul` where there is no weight,
+// 0 past the row's end.
+template <bool TAIL, int KT, int V, int LANES>
 __device__ __forceinline__ void bn_weights(const float* w, float mul, int t, int C,
                                            float (&out)[KT][V]) {
 #pragma unroll
-  for (int k = 0; k < KT; ++k)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = (t + k * LANES) * V + e;
-      out[k][e] = c < C ? (w ? mul * w[c] : mul) : 0.f;
+  for (int k = 0; k < KT; ++k) {
+    const int c = (t + k * LANES) * V;
+    Vec<float, V> q;
+    if (w) {
+      bn_load<TAIL>(q, w, c, C);
+      q.get(out[k]);
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[k][e] = c + e < C ? (w ? mul * out[k][e] : mul) : 0.f;
+  }
 }
 
 // act(z) and its derivative.
@@ -93,102 +110,148 @@ __device__ __forceinline__ float bn_act_grad(int kind, float z, float& act) {
   return kind == 1 ? s * (1.f - s) : s * (1.f + z * (1.f - s));
 }
 
-// Threads of a workgroup: one row of W waves, or four rows of one wave.
-template <int W> constexpr int kBnThreads = W > 1 ? W * 64 : 256;
-template <int W> constexpr int kBnRows = kBnThreads<W> / (W * 64);
+// The row of row group rg in the pass from row r0 on: past the last row, the last
+// one again; past the last pass, the row of the pass before (whose lines are
+// near; one row for all workgroups would be a hot spot).
+__device__ __forceinline__ int64_t bn_row(int64_t r0, int rg, int64_t rows) {
+  return min(r0 + rg, rows - 1);
+}
+__device__ __forceinline__ int64_t bn_next(int64_t r0, int64_t step, int rg, int64_t rows) {
+  return bn_row(r0 + step < rows ? r0 + step : r0, rg, rows);
+}
 
-template <typename T, typename R, int W, int KT, bool TAIL>
-__global__ __launch_bounds__(kBnThreads<W>) void block_norm_fwd_kernel(const BlockNormArgs a) {
-  constexpr int V = kBnV<T>, LANES = W * 64, ROWS = kBnRows<W>;
-  __shared__ float buf[2][W];
+// A workgroup holds RG rows of W waves each and walks over rows with a stride of
+// the grid; the next row's loads are in flight while a row is worked on.
+template <typename T, typename R, int V, int W, int KT, int RG, bool TAIL>
+__global__ __launch_bounds__(64 * W * RG) void block_norm_fwd_kernel(const BlockNormArgs a) {
+  constexpr int LANES = W * 64;
+  __shared__ float buf[2][1][RG][W];
   int par = 0;
-  const int t = threadIdx.x % LANES, C = a.C;
+  const int rg = RG > 1 ? wave_id() / W : 0, t = threadIdx.x - rg * LANES, C = a.C;
   const float inv = 1.f / (float)C;
   float pw[KT][V], fw[KT][V], nw[KT][V];
-  bn_weights<KT, V, LANES>(a.post_w, 1.f, t, C, pw);
-  bn_weights<KT, V, LANES>(a.scale, a.alpha, t, C, fw);
-  bn_weights<KT, V, LANES>(a.pre_w, 1.f, t, C, nw);
-  for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; r < a.rows;
-       r += (int64_t)gridDim.x * ROWS) {
-    const T* x = static_cast<const T*>(a.x) + r * C;
-    const T* gate = static_cast<const T*>(a.gate) + r * C;
-    const R* res = static_cast<const R*>(a.residual) + r * C;
-    Vec<T, V> xq[KT], gq[KT];
-    Vec<R, V> rq[KT];
+  Vec<T, V> xq[KT], gq[KT], nx[KT], ng[KT];
+  Vec<R, V> rq[KT], nr[KT];
+  auto load = [&](int64_t r, Vec<T, V>(&x)[KT], Vec<T, V>(&g)[KT], Vec<R, V>(&q)[KT]) {
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const int c = (t + k * LANES) * V;
-      bn_load<TAIL>(xq[k], x, c, C);
-      if (a.gate) bn_load<TAIL>(gq[k], gate, c, C);
-      if (a.residual) bn_load<TAIL>(rq[k], res, c, C);
-      else rq[k].clear();
+      bn_load<TAIL>(x[k], static_cast<const T*>(a.x) + r * C, c, C);
+      // where there is no gate or residual, x's row again: loaded, never used
+      bn_load<TAIL>(g[k], static_cast<const T*>(a.gate ? a.gate : a.x) + r * C, c, C);
+      if (a.residual) bn_load<TAIL>(q[k], static_cast<const R*>(a.residual) + r * C, c, C);
+      else q[k].clear();
     }
-    float h[KT][V];
-    float s = 0.f;
+  };
+  load(bn_row((int64_t)blockIdx.x * RG, rg, a.rows), xq, gq, rq);
+  bn_weights<TAIL, KT, V, LANES>(a.post_w, 1.f, t, C, pw);
+  bn_weights<TAIL, KT, V, LANES>(a.scale, a.alpha, t, C, fw);
+  bn_weights<TAIL, KT, V, LANES>(a.pre_w, 1.f, t, C, nw);
+#pragma unroll 1
+  for (int64_t r0 = (int64_t)blockIdx.x * RG; r0 < a.rows; r0 += (int64_t)gridDim.x * RG) {
+    load(bn_next(r0, (int64_t)gridDim.x * RG, rg, a.rows), nx, ng, nr);
+    float h[KT][V], s[1] = {0.f};
+    float r1 = 1.f;
     if (a.post_w) {
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
         xq[k].get(h[k]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += h[k][e] * h[k][e];
+        for (int e = 0; e < V; ++e) s[0] += h[k][e] * h[k][e];
       }
-      s = rsqrtf(row_sum<W>(s, buf, par) * inv + a.eps);
+      row_sums<W, RG>(s, buf, rg, par);
+      r1 = rsqrtf(s[0] * inv + a.eps);
+      s[0] = 0.f;
     }
-    const float r1 = a.post_w ? s : 1.f;
-    s = 0.f;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       float g[V], q[V];
       xq[k].get(h[k]);
       rq[k].get(q);
-      if (a.gate) gq[k].get(g);
+      gq[k].get(g);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = h[k][e] * r1 * pw[k][e];
         if (a.gate) u *= bn_act(a.act, g[e]);
         h[k][e] = q[e] + fw[k][e] * u;
-        s += h[k][e] * h[k][e];
+        s[0] += h[k][e] * h[k][e];
       }
     }
-    const float r2 = rsqrtf(row_sum<W>(s, buf, par) * inv + a.eps);
+    row_sums<W, RG>(s, buf, rg, par);
+    const float r2 = rsqrtf(s[0] * inv + a.eps);
+    const int64_t o = (r0 + rg) * C;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const int c = (t + k * LANES) * V;
-      float o[V];
+      if (r0 + rg < a.rows) {
+        float out[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = h[k][e] * r2 * nw[k][e];
-      Vec<T, V> oq;
-      oq.set(o);
-      bn_store<TAIL>(oq, static_cast<T*>(a.out) + r * C, c, C);
-      if (a.res_out) {
-        rq[k].set(h[k]);
-        bn_store<TAIL>(rq[k], static_cast<R*>(a.res_out) + r * C, c, C);
+        for (int e = 0; e < V; ++e) out[e] = h[k][e] * r2 * nw[k][e];
+        Vec<T, V> oq;
+        oq.set(out);
+        bn_store<TAIL>(oq, static_cast<T*>(a.out) + o, c, C);
+        if (a.res_out) {
+          rq[k].set(h[k]);
+          bn_store<TAIL>(rq[k], static_cast<R*>(a.res_out) + o, c, C);
+        }
       }
+      xq[k] = nx[k];
+      gq[k] = ng[k];
+      rq[k] = nr[k];
     }
   }
 }
 
-template <typename T, typename R, int W, int KT, bool TAIL>
-__global__ __launch_bounds__(kBnThreads<W>) void block_norm_bwd_kernel(const BlockNormArgs a,
-                                                                       int sec_scale, int sec_pre,
-                                                                       int nsec) {
-  constexpr int V = kBnV<T>, LANES = W * 64, ROWS = kBnRows<W>;
-  __shared__ float buf[2][W];
-  __shared__ float red[ROWS > 1 ? ROWS : 1][ROWS > 1 ? KT * LANES * V : 1];
+// Backward.  With y = f act post_w m (what dh is multiplied by on its way to
+// m), every sum after r1 is linear in quantities known before r2, so one
+// exchange serves them all: mean(dn n) = r2 mean(dn h), and mean(dm m) =
+// mean(y dh) = r2 mean(y dn) - r2^3 mean(dn h) mean(y h) + mean(y dh_out).
+//
+// The gate's factors are formed twice, and with several vectors per lane the
+// weights wait in LDS, to keep the registers for rows in flight.
+template <typename T, typename R, int V, int W, int KT, int RG, bool TAIL>
+__global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const BlockNormArgs a,
+                                                                     int sec_scale, int sec_pre,
+                                                                     int nsec) {
+  constexpr int LANES = W * 64, CC = LANES * KT * V;
+  constexpr bool kLds = KT > 1;                   // weights in LDS
+  static_assert(W == 1 || RG == 1, "rows of several waves do not share a workgroup's barriers");
+  static_assert(!kLds || RG == 1, "one row per workgroup with the weights in LDS");
+  __shared__ float buf[2][5][RG][W];
+  __shared__ __align__(16) float wt[kLds ? 3 : 1][kLds || RG > 1 ? CC : 1];
   int par = 0;
-  const int t = threadIdx.x % LANES, C = a.C;
+  const int rg = RG > 1 ? wave_id() : 0, t = threadIdx.x - rg * LANES, C = a.C;
   const float inv = 1.f / (float)C;
-  float pw[KT][V], fw[KT][V], nw[KT][V];
-  bn_weights<KT, V, LANES>(a.post_w, 1.f, t, C, pw);
-  bn_weights<KT, V, LANES>(a.scale, a.alpha, t, C, fw);
-  bn_weights<KT, V, LANES>(a.pre_w, 1.f, t, C, nw);
+  float wr[3][KT][V];
+  if constexpr (kLds) {
+    for (int c = threadIdx.x; c < CC; c += LANES) {
+      wt[0][c] = c < C ? (a.post_w ? a.post_w[c] : 1.f) : 0.f;
+      wt[1][c] = c < C ? a.alpha * (a.scale ? a.scale[c] : 1.f) : 0.f;
+      wt[2][c] = c < C ? a.pre_w[c] : 0.f;
+    }
+    __syncthreads();
+  } else {
+    bn_weights<TAIL, KT, V, LANES>(a.post_w, 1.f, t, C, wr[0]);
+    bn_weights<TAIL, KT, V, LANES>(a.scale, a.alpha, t, C, wr[1]);
+    bn_weights<TAIL, KT, V, LANES>(a.pre_w, 1.f, t, C, wr[2]);
+  }
+  auto weights = [&](int k, int i, float(&w)[V]) {
+    if constexpr (kLds) {
+      Vec<float, V> q;
+      q.load(&wt[i][(t + k * LANES) * V]);
+      q.get(w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = wr[i][k][e];
+    }
+  };
   float ap[KT][V], as[KT][V], an[KT][V];
 #pragma unroll
   for (int k = 0; k < KT; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e) ap[k][e] = as[k][e] = an[k][e] = 0.f;
-  for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; r < a.rows;
-       r += (int64_t)gridDim.x * ROWS) {
+#pragma unroll 1
+  for (int64_t r = (int64_t)blockIdx.x * RG + rg; r < a.rows; r += (int64_t)gridDim.x * RG) {
     const int64_t o = r * C;
     Vec<T, V> xq[KT], gq[KT], dq[KT];
     Vec<R, V> rq[KT], hq[KT];
@@ -196,77 +259,81 @@ __global__ __launch_bounds__(kBnThreads<W>) void block_norm_bwd_kernel(const Blo
     for (int k = 0; k < KT; ++k) {
       const int c = (t + k * LANES) * V;
       bn_load<TAIL>(xq[k], static_cast<const T*>(a.x) + o, c, C);
+      // where there is no gate, x's row again: loaded, never used
+      bn_load<TAIL>(gq[k], static_cast<const T*>(a.gate ? a.gate : a.x) + o, c, C);
       bn_load<TAIL>(dq[k], static_cast<const T*>(a.dout) + o, c, C);
-      if (a.gate) bn_load<TAIL>(gq[k], static_cast<const T*>(a.gate) + o, c, C);
       if (a.residual) bn_load<TAIL>(rq[k], static_cast<const R*>(a.residual) + o, c, C);
       else rq[k].clear();
       if (a.dres_out) bn_load<TAIL>(hq[k], static_cast<const R*>(a.dres_out) + o, c, C);
       else hq[k].clear();
     }
-    float s = 0.f;
+    float r1 = 1.f;
     if (a.post_w) {
+      float s[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
         float x[V];
         xq[k].get(x);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += x[e] * x[e];
+        for (int e = 0; e < V; ++e) s[0] += x[e] * x[e];
       }
-      s = rsqrtf(row_sum<W>(s, buf, par) * inv + a.eps);
+      row_sums<W, RG>(s, buf, rg, par);
+      r1 = rsqrtf(s[0] * inv + a.eps);
     }
-    const float r1 = a.post_w ? s : 1.f;
-    float h[KT][V];
-    s = 0.f;
+    // sums of h^2, dn h, and with a norm of y dn, y h, y dh_out
+    float h[KT][V], s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-      float x[V], g[V], q[V];
+      float x[V], g[V], q[V], d[V], ho[V], pw[V], fw[V], nw[V];
       xq[k].get(x);
       rq[k].get(q);
-      if (a.gate) gq[k].get(g);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float u = x[e] * r1 * pw[k][e];
-        if (a.gate) u *= bn_act(a.act, g[e]);
-        h[k][e] = q[e] + fw[k][e] * u;
-        s += h[k][e] * h[k][e];
-      }
-    }
-    const float r2 = rsqrtf(row_sum<W>(s, buf, par) * inv + a.eps);
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      float d[V];
       dq[k].get(d);
+      gq[k].get(g);
+      hq[k].get(ho);
+      weights(k, 0, pw);
+      weights(k, 1, fw);
+      weights(k, 2, nw);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        h[k][e] *= r2;                            // n
-        s += d[e] * nw[k][e] * h[k][e];
-        an[k][e] += d[e] * h[k][e];
+        const float act = a.gate ? bn_act(a.act, g[e]) : 1.f;
+        const float y = x[e] * r1 * pw[e] * act * fw[e], dn = d[e] * nw[e];
+        h[k][e] = q[e] + y;
+        s[0] += h[k][e] * h[k][e];
+        s[1] += dn * h[k][e];
+        s[2] += y * dn;
+        s[3] += y * h[k][e];
+        s[4] += y * ho[e];
       }
     }
-    const float mn = row_sum<W>(s, buf, par) * inv;
-    s = 0.f;
+    row_sums<W, RG>(s, buf, rg, par);
+    const float r2 = rsqrtf(s[0] * inv + a.eps);
+    const float hk = r2 * r2 * r2 * (s[1] * inv);   // dh = r2 dn - hk h + dh_out
+    const float mm = a.post_w ? (r2 * s[2] - hk * s[3] + s[4]) * inv : 0.f;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const int c = (t + k * LANES) * V;
-      float x[V], g[V], d[V], dh[V], dg[V];
+      float x[V], g[V], d[V], dh[V], dg[V], pw[V], fw[V], nw[V];
       xq[k].get(x);
       dq[k].get(d);
+      gq[k].get(g);
       hq[k].get(dh);
-      if (a.gate) gq[k].get(g);
+      weights(k, 0, pw);
+      weights(k, 1, fw);
+      weights(k, 2, nw);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        dh[e] += r2 * (d[e] * nw[k][e] - h[k][e] * mn);
-        const float m = x[e] * r1, p = m * pw[k][e], du = dh[e] * fw[k][e];
         float act = 1.f, da = 0.f;
         if (a.gate) da = bn_act_grad(a.act, g[e], act);
-        as[k][e] += dh[e] * p * act;
+        an[k][e] += d[e] * (h[k][e] * r2);
+        dh[e] += r2 * (d[e] * nw[e]) - hk * h[k][e];
+        const float m = x[e] * r1, p = m * pw[e], du = dh[e] * fw[e], dp = du * act;
+        as[k][e] += dh[e] * (p * act);
         dg[e] = du * p * da;
-        const float dp = du * act;
         ap[k][e] += dp * m;
-        h[k][e] = dp * pw[k][e];                  // dm, or dp without a norm
-        s += h[k][e] * m;
+        x[e] = r1 * (dp * pw[e] - m * mm);
       }
+      xq[k].set(x);
+      bn_store<TAIL>(xq[k], static_cast<T*>(a.dx) + o, c, C);
       if (a.dres) {
         hq[k].set(dh);
         bn_store<TAIL>(hq[k], static_cast<R*>(a.dres) + o, c, C);
@@ -276,44 +343,37 @@ __global__ __launch_bounds__(kBnThreads<W>) void block_norm_bwd_kernel(const Blo
         bn_store<TAIL>(gq[k], static_cast<T*>(a.dgate) + o, c, C);
       }
     }
-    const float mm = a.post_w ? row_sum<W>(s, buf, par) * inv : 0.f;
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const int c = (t + k * LANES) * V;
-      float x[V];
-      xq[k].get(x);
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[e] = r1 * (h[k][e] - x[e] * r1 * mm);
-      xq[k].set(x);
-      bn_store<TAIL>(xq[k], static_cast<T*>(a.dx) + o, c, C);
-    }
   }
-  // one partial row per workgroup and weight; four rows at a time are added
-  // in LDS first
+  // one partial row per workgroup and weight.  Rows of one wave are added in LDS
+  // first, in the order of the waves.
   float* part = a.part + (int64_t)blockIdx.x * nsec * C;
   auto put = [&](float(&v)[KT][V], int sec, float mul) {
-    if constexpr (ROWS > 1) {
-      const int row = threadIdx.x / LANES;
-      __syncthreads();
+    if constexpr (RG > 1) {
+      float* red = wt[0];
+#pragma unroll 1
+      for (int g = 0; g < RG; ++g) {
+        __syncthreads();
+        if (rg == g) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
+          for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[row][(t + k * LANES) * V + e] = v[k][e];
-      __syncthreads();
-      for (int c = threadIdx.x; c < C; c += kBnThreads<W>) {
-        float u = red[0][c];
-#pragma unroll
-        for (int q = 1; q < ROWS; ++q) u += red[q][c];
-        part[(int64_t)sec * C + c] = u * mul;
+            for (int e = 0; e < V; ++e) {
+              float* to = red + (t + k * LANES) * V + e;
+              *to = g == 0 ? v[k][e] : *to + v[k][e];
+            }
+        }
       }
+      __syncthreads();
+      for (int c = threadIdx.x; c < C; c += LANES * RG) part[(int64_t)sec * C + c] = red[c] * mul;
     } else {
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
+      for (int k = 0; k < KT; ++k) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int c = (t + k * LANES) * V + e;
-          if (c < C) part[(int64_t)sec * C + c] = v[k][e] * mul;
-        }
+        for (int e = 0; e < V; ++e) v[k][e] *= mul;
+        Vec<float, V> q;
+        q.set(v[k]);
+        bn_store<TAIL>(q, part + (int64_t)sec * C, (t + k * LANES) * V, C);
+      }
     }
   };
   if (a.post_w) put(ap, 0, 1.f);
@@ -332,7 +392,7 @@ struct BlockNormOut {
   }
 };
 
-constexpr int kBnMaxParts = 1024;        // partial rows the workspace holds
+constexpr int kBnMaxParts = 2048;        // partial rows the workspace holds
 int bn_grid(int64_t rows, int rows_per_group, int per_cu, int most) {
   const int cus = device_cu_count();
   int64_t want = (int64_t)(cus > 0 ? cus : 256) * per_cu;
@@ -341,12 +401,20 @@ int bn_grid(int64_t rows, int rows_per_group, int per_cu, int most) {
   return (int)(groups < want ? groups : want);
 }
 
+// Workgroups per CU: as many as are resident, so that each walks over rows to the
+// end of the launch.  A forward wave needs about 50 registers (six waves per
+// SIMD and more), a backward one about 100 (four per SIMD); with several vectors
+// per lane the backward's LDS and registers leave one workgroup.  More than are
+// resident costs a second, part-filled round: the backward at 8192 x 1536 took
+// 91 us with three workgroups of six waves per CU, 73 with two.
 template <bool BWD, typename T, typename R, int W, int KT, bool TAIL>
 hipError_t bn_go(const BlockNormArgs& a, hipStream_t s) {
+  constexpr int V = 4, RG = W == 1 ? 4 : 1;
   if constexpr (!BWD) {
-    const int grid = bn_grid(a.rows, kBnRows<W>, 8, 1 << 20);
-    hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, W, KT, TAIL>), dim3(grid),
-                       dim3(kBnThreads<W>), 0, s, a);
+    const int grid = bn_grid(a.rows, RG, 24 / (W * RG) > 1 ? 24 / (W * RG) : 1, 1 << 20);
+    hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, V, W, KT, RG, TAIL>), dim3(grid),
+                       dim3(64 * W * RG), 0, s, a);
+    return hipGetLastError();
   } else {
     const int nsec = 1 + (a.post_w ? 1 : 0) + (a.scale ? 1 : 0);
     const int sec_scale = a.post_w ? 1 : 0, sec_pre = nsec - 1;
@@ -355,32 +423,33 @@ hipError_t bn_go(const BlockNormArgs& a, hipStream_t s) {
     out.w[0] = out.w[1] = out.w[2] = a.dpre_w;
     if (a.post_w) out.w[0] = a.dpost_w;
     if (a.scale) out.w[sec_scale] = a.dscale;
-    const int grid = bn_grid(a.rows, kBnRows<W>, 4, kBnMaxParts);
+    const int grid = bn_grid(a.rows, RG, KT == 1 ? 16 / (W * RG) : 1, kBnMaxParts);
     if (grid > 0)
-      hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, W, KT, TAIL>), dim3(grid),
-                         dim3(kBnThreads<W>), 0, s, a, sec_scale, sec_pre, nsec);
-    const int cols = nsec * a.C;
-    hipLaunchKernelGGL(colsum_kernel<BlockNormOut>, dim3((cols + 63) / 64), dim3(kColsumThreads), 0,
-                       s, (const float*)a.part, grid, cols, out);
+      hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, V, W, KT, RG, TAIL>), dim3(grid),
+                         dim3(64 * W * RG), 0, s, a, sec_scale, sec_pre, nsec);
+    return colsum(a.part, grid, nsec * a.C, out, s);
   }
-  return hipGetLastError();
 }
 
 template <bool BWD, typename T, typename R, bool TAIL>
 hipError_t bn_rows(const BlockNormArgs& a, hipStream_t s) {
-  const int nvec = (a.C + kBnV<T> - 1) / kBnV<T>;
-  if (nvec <= 64) return bn_go<BWD, T, R, 1, 1, TAIL>(a, s);
-  if (nvec <= 128) return bn_go<BWD, T, R, 1, 2, TAIL>(a, s);
-  if (nvec <= 256) return bn_go<BWD, T, R, 2, 2, TAIL>(a, s);
-  if (nvec <= 512) return bn_go<BWD, T, R, 4, 2, TAIL>(a, s);
-  if (nvec <= 1024) return bn_go<BWD, T, R, 8, 2, TAIL>(a, s);
-  if constexpr (sizeof(T) == 4) return bn_go<BWD, T, R, 16, 2, TAIL>(a, s);
-  return hipErrorInvalidValue;
+  const int nw = (a.C + 255) / 256;         // waves a row fills with one vector per lane
+  switch (nw) {
+#define SSD_BN(w) case w: return bn_go<BWD, T, R, w, 1, TAIL>(a, s);
+    SSD_BN(1) SSD_BN(2) SSD_BN(3) SSD_BN(4) SSD_BN(5) SSD_BN(6) SSD_BN(7) SSD_BN(8)
+#undef SSD_BN
+  }
+  // wider rows: sixteen waves forward; backward eight with more vectors per
+  // lane, as 1024 threads leave too few registers (4096 x 4096 bf16: 208 us
+  // against 115)
+  constexpr int W = BWD ? 8 : 16;
+  if (nw <= 16) return bn_go<BWD, T, R, W, 16 / W, TAIL>(a, s);
+  return bn_go<BWD, T, R, W, 32 / W, TAIL>(a, s);
 }
 
 template <bool BWD, typename T, typename R>
 hipError_t bn_tail(const BlockNormArgs& a, hipStream_t s) {
-  return a.C % kBnV<T> ? bn_rows<BWD, T, R, true>(a, s) : bn_rows<BWD, T, R, false>(a, s);
+  return a.C % 4 ? bn_rows<BWD, T, R, true>(a, s) : bn_rows<BWD, T, R, false>(a, s);
 }
 
 template <bool BWD>

@@ -158,33 +158,51 @@ struct StepSlot {
 };
 
 // Sums over the rows of part[nparts][cols]: OUT::put(column, sum).  One
-// workgroup of 16 waves per 64 columns; wave w adds rows w, w + 16, ... in
-// order, eight loads in flight, then the wave sums are added in wave order.
-// No atomics: the order never changes.
-constexpr int kColsumThreads = 1024;
+// workgroup per 16 columns: 64 groups of 16 lanes, group g adding rows g, g + 64,
+// ... in order with eight loads in flight, then the groups' sums are added in a
+// fixed order.  No atomics: the order never changes.  Narrow workgroups, because
+// a sum's time is the latency of its rows' loads: 1024 rows of 2304 columns take
+// 64 rows per thread with one thread per column and wave, 16 here.
+constexpr int kColsumThreads = 1024, kColsumCols = 16;
 template <typename OUT>
 __global__ __launch_bounds__(kColsumThreads) void colsum_kernel(const float* __restrict__ part,
                                                                 int nparts, int cols, OUT out) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  constexpr int NG = kColsumThreads / kColsumCols;
+  __shared__ float sums[NG][kColsumCols];
+  const int lane = threadIdx.x % kColsumCols, g = threadIdx.x / kColsumCols;
+  const int col = blockIdx.x * kColsumCols + lane;
   const int c = col < cols ? col : cols - 1;
   float t = 0.f;
-  int r = w;
-  for (; r + 7 * 16 < nparts; r += 8 * 16) {
+  int r = g;
+  for (; r + 7 * NG < nparts; r += 8 * NG) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)(r + 16 * i) * cols + c];
+    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)(r + NG * i) * cols + c];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += v[i];
   }
-  for (; r < nparts; r += 16) t += part[(int64_t)r * cols + c];
-  sums[w][lane] = t;
-  __syncthreads();
-  if (w > 0 || col >= cols) return;
+  if (r < nparts) {
+    float v[8];                                   // rows past the last: the last again, unused
 #pragma unroll
-  for (int q = 1; q < 16; ++q) t += sums[q][lane];
-  out.put(col, t);
+    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)min(r + NG * i, nparts - 1) * cols + c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += r + NG * i < nparts ? v[i] : 0.f;
+  }
+  sums[g][lane] = t;
+  __syncthreads();
+  if (g >= 4) return;
+  t = 0.f;
+#pragma unroll
+  for (int q = 0; q < NG / 4; ++q) t += sums[g * (NG / 4) + q][lane];
+  t += __shfl_xor(t, 16);
+  t += __shfl_xor(t, 32);
+  if (g == 0 && col < cols) out.put(col, t);
+}
+template <typename OUT>
+inline hipError_t colsum(const float* part, int nparts, int cols, const OUT& out, hipStream_t s) {
+  hipLaunchKernelGGL(colsum_kernel<OUT>, dim3((cols + kColsumCols - 1) / kColsumCols),
+                     dim3(kColsumThreads), 0, s, part, nparts, cols, out);
+  return hipGetLastError();
 }
 
 }  // namespace ssd

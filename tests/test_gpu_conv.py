@@ -7,8 +7,8 @@ bound of tests/layer_bounds.py's count of operations:
         sigmoid's and 4 U of (1 + |pre|)
   dx    sum |w| err(dpre) + (K + 2) U sum |w dpre|
   dw    sum |in| err(dpre) + n U sum |dpre in|, n the additions a term passes:
-        at most 64 in a thread's run (8 tokens a tile, up to 8 tiles here), 4
-        waves, 16 + 16 over the partial rows, so 110 covers them
+        at most 64 in a thread's runs here, 4 waves, 8 partial rows per thread,
+        16 + 2 over the threads of a column, so 110 covers them
 """
 import numpy as np
 import pytest
@@ -84,6 +84,10 @@ CASES = {
     "packed-short": (1, 0, (40, 8, 8), 4, "f32", 0, True, True, False, (1,) * 20 + (0, 0, 5)),
     "packed-empty-ends": (1, 0, (40, 8, 8), 3, "f32", 8, True, True, True, (0, 70, 0)),
     "packed-many": (1, 0, (16, 0, 0), 4, "bf16", 0, True, True, True, tuple(i % 7 for i in range(300))),
+    # long enough for the long runs of either direction
+    "long": (2, 5600, (1500, 20, 17), 4, "bf16", 3, True, True, True, None),
+    "long-packed": (1, 0, (1792, 128, 128), 3, "bf16", 0, True, True, True, (8000, 1, 0, 3, 300)),
+    "long-f32": (1, 8200, (2048, 0, 0), 2, "f32", 0, True, False, False, None),
     "packed-one": (1, 0, (33, 2, 1), 2, "bf16", 0, True, True, True, (129,)),
 }
 
