@@ -487,8 +487,9 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_problem_t* p, const void* xbc, const fl
  *   dinitial_states         like initial_states (nullable: not computed)
  * pre is computed again from xbc.  Tokens outside every sequence add nothing
  * and their rows of dxbc are not written.  The workspace (no initial contents)
- * is ssd_conv_bwd_workspace_size bytes, 256-byte aligned.  No atomics:
- * results are deterministic.
+ * is ssd_conv_bwd_workspace_size bytes, 256-byte aligned; calls that may overlap
+ * (on different streams, or in graphs replayed side by side) need one each.  No
+ * atomics: results are deterministic.
  */
 size_t ssd_conv_bwd_workspace_size(const ssd_conv_problem_t* p);
 
@@ -614,8 +615,9 @@ ssd_status_t ssd_block_norm_fwd(const ssd_block_norm_problem_t* p, const void* x
  * residual, dx and dgate like x; dgate is required with a gate, dscale with a
  * scale, dpost_weight with a post_weight, and NULL otherwise; dpre_weight is
  * required.  h is computed again from the inputs.  The workspace (no initial
- * contents) is ssd_block_norm_bwd_workspace_size bytes, 256-byte aligned.  No
- * atomics: results are deterministic.
+ * contents) is ssd_block_norm_bwd_workspace_size bytes, 256-byte aligned; calls
+ * that may overlap (on different streams, or in graphs replayed side by side)
+ * need one each.  No atomics: results are deterministic.
  */
 size_t ssd_block_norm_bwd_workspace_size(const ssd_block_norm_problem_t* p);
 

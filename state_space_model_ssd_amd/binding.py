@@ -528,6 +528,16 @@ def _launch(dev, fn, *args):
         _check(code)
 
 
+def _workspace(workspace, need, dev):
+    """The caller's workspace (its size and alignment are the library's to
+    check), or one made for this call."""
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    return workspace
+
+
 def _on_gpu(t, name, what):
     dev = t.device
     if dev.type != "cuda":
@@ -669,8 +679,7 @@ def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_s
     g = {"x": dx, "weight": weight.new_empty(weight.shape),
          "bias": weight.new_empty((C,)) if bias is not None else None,
          "initial_states": x.new_empty(sshape) if initial_states is not None else None}
-    if workspace is None:
-        workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, prob[2], dev)
     _launch(dev, load_library().ssd_conv_bwd, prob[1], x.data_ptr(), weight.data_ptr(), _addr(bias),
             _addr(initial_states), _addr(cu_seqlens), _addr(douts[0]), _addr(douts[1]),
             _addr(douts[2]), _addr(dfinal_states), dx.data_ptr(), g["weight"].data_ptr(),
@@ -819,8 +828,7 @@ def block_norm_bwd(x, residual, pre_weight, dout, dresidual_out=None, gate=None,
          "post_weight": pre_weight.new_empty((C,)) if post_weight is not None else None,
          "scale": pre_weight.new_empty((C,)) if scale is not None else None,
          "pre_weight": pre_weight.new_empty((C,))}
-    if workspace is None:
-        workspace = torch.empty(max(prob[2], 256), dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, prob[2], dev)
     _launch(dev, load_library().ssd_block_norm_bwd, prob[1], x.data_ptr(), _addr(residual),
             _addr(gate), _addr(post_weight), _addr(scale), pre_weight.data_ptr(), dout.data_ptr(),
             _addr(dresidual_out), g["x"].data_ptr(), _addr(g["residual"]), _addr(g["gate"]),

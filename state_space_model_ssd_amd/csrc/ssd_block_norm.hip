@@ -29,6 +29,10 @@
 #include "ssd_layer_device.h"
 #include "ssd_rowsum.h"
 
+// Multiply-adds are fused only inside one expression, so every variant of a kernel
+// rounds a value alike.
+#pragma clang fp contract(on)
+
 namespace ssd {
 
 namespace {

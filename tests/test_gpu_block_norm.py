@@ -179,6 +179,39 @@ def test_block_norm_in_place_and_deterministic():
             assert torch.equal(g[n], k[n])
 
 
+@pytest.mark.parametrize("C", [64, 300, 2048, 5000])
+def test_block_norm_in_place_over_many_rows(C):
+    """In place where a workgroup walks over several rows with the next row's
+    loads in flight."""
+    g = torch.Generator(device="cuda").manual_seed(C)
+    x = torch.randn((6001, C), generator=g, device="cuda", dtype=torch.bfloat16)
+    res, w = torch.randn((6001, C), generator=g, device="cuda"), torch.rand(C, generator=g, device="cuda")
+    kw = dict(post_weight=w, scale=w, residual_scale=0.5)
+    out, h = binding.block_norm_fwd(x, res, w, **kw)
+    binding.block_norm_fwd(x, res, w, out=x, residual_out=res, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(x, out) and torch.equal(res, h)
+
+
+def test_block_norm_far_rows():
+    """Elements past 2^32: the last rows equal a run on those rows alone."""
+    C = 8192
+    T = 2 ** 32 // C + 3000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.full((T, C), 0.25, dtype=torch.bfloat16, device="cuda")
+    x[-2000:] = torch.randn((2000, C), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand(C, generator=g, device="cuda")
+    out, h = binding.block_norm_fwd(x, x, w, post_weight=w)
+    o2, h2 = binding.block_norm_fwd(x[-2000:], x[-2000:], w, post_weight=w)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-2000:], o2) and torch.equal(h[-2000:], h2)
+    del out
+    gr = binding.block_norm_bwd(x, x, w, h, post_weight=w)
+    wg = binding.block_norm_bwd(x[-2000:], x[-2000:], w, h[-2000:], post_weight=w)
+    torch.cuda.synchronize()
+    assert torch.equal(gr["x"][-2000:], wg["x"]) and torch.equal(gr["residual"][-2000:], wg["residual"])
+
+
 def test_block_norm_rows_are_independent():
     """Infinity, NaN and zeros in some rows leave the others as they were."""
     d, kw, dtype, rdt = draw("sigmoid")

@@ -296,3 +296,71 @@ def test_conv_prompt_then_steps():
     for i in range(3):
         assert torch.equal(torch.stack([o[i] for o in outs], 1), whole[i][:, 290:])
     assert torch.equal(st, whole[3])
+
+
+def test_conv_far_tokens():
+    """Elements past 2^32: the last tokens of a long row equal a run on a slice
+    of it behind the state there, forward and backward."""
+    C, K = 6144, 4
+    T = 2 ** 32 // C + 2000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x, dout = torch.empty((1, T, C), dtype=torch.bfloat16, device="cuda"), r(1, 1000, C)
+    x[:, :1000] = r(1, 1000, C)
+    x[:, 1000:-3000] = 0.5
+    x[:, -3000:] = r(1, 3000, C)
+    w, bias = torch.randn((C, K), generator=g, device="cuda") * 0.5, torch.randn(C, generator=g, device="cuda")
+    out, _, _, fin = binding.conv_fwd(x, w, bias)
+    tail = x[:, -1000:].contiguous()
+    want, _, _, wfin = binding.conv_fwd(tail, w, bias, initial_states=x[:, -1003:-1000].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, -1000:], want) and torch.equal(fin, wfin)
+    big = out                                       # its storage serves as the output gradient
+    big.zero_()
+    big[:, -1000:] = dout
+    gr = binding.conv_bwd(x, w, [big, None, None], bias)
+    wg = binding.conv_bwd(tail, w, [dout, None, None], bias, initial_states=x[:, -1003:-1000].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(gr["x"][:, -1000:], wg["x"])
+    assert torch.equal(gr["x"][:, -1003:-1000], wg["initial_states"])
+    assert not gr["x"][:, :-1003].any()
+
+
+def test_conv_workspace_checked():
+    x, w = torch.randn((1, 8, 16), device="cuda"), torch.randn((16, 4), device="cuda")
+    for bad in (torch.empty(1 << 20, dtype=torch.uint8),
+                torch.empty((1 << 20, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            binding.conv_bwd(x, w, [x, None, None], workspace=bad)
+    with pytest.raises(binding.SsdError) as e:
+        binding.conv_bwd(x, w, [x, None, None], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == binding.SSD_ERR_WORKSPACE
+
+
+def test_conv_argument_checks():
+    x, w = torch.randn((2, 8, 16), device="cuda"), torch.randn((16, 4), device="cuda")
+    st = torch.zeros((2, 3, 16), device="cuda")
+    for bad in (dict(x=x.half()), dict(x=x[0]), dict(x=x[..., ::2]), dict(x=x[:, :6]), dict(weight=w.bfloat16()),
+                dict(weight=w[:8]), dict(bias=w), dict(splits=(8, 4, 2)), dict(splits=(16,)),
+                dict(activation="gelu"), dict(initial_states=st[:1]), dict(initial_states=st.cpu()),
+                dict(cu_seqlens=torch.tensor([0, 8], device="cuda")), dict(outs=[x, x]),
+                dict(outs=[x.bfloat16(), None, None]), dict(final_states=st[:, :2])):
+        with pytest.raises(ValueError):
+            binding.conv_fwd(**{**dict(x=x, weight=w), **bad})
+    with pytest.raises(ValueError):
+        binding.conv_bwd(x, w, [x, None, None], dx=x.bfloat16())
+    for K in (1, 5):
+        with pytest.raises(binding.SsdError) as e:
+            binding.conv_fwd(x, torch.randn((16, K), device="cuda"))
+        assert e.value.code == binding.SSD_ERR_UNSUPPORTED
+    with pytest.raises(binding.SsdError) as e:      # a packed batch is one row
+        binding.conv_fwd(x, w, cu_seqlens=torch.tensor([0, 8], dtype=torch.int32, device="cuda"))
+    assert e.value.code == binding.SSD_ERR_INVALID_ARG
+    s = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in (dict(x=x), dict(conv_states=st.bfloat16()), dict(slots=s.long()), dict(slots=s[:1]),
+                dict(conv_states=st[:, :, :8]), dict(outs=[x[:, 0], None])):
+        with pytest.raises(ValueError):
+            binding.conv_step(**{**dict(x=x[:, 0], conv_states=st, weight=w), **bad})
+    with pytest.raises(binding.SsdError) as e:      # fewer states than rows, and no slots
+        binding.conv_step(x[:, 0], st[:1], w)
+    assert e.value.code == binding.SSD_ERR_INVALID_ARG
