@@ -158,43 +158,33 @@ struct StepSlot {
 };
 
 // Sums over the rows of part[nparts][cols]: OUT::put(column, sum).  One
-// workgroup per 16 columns: 64 groups of 16 lanes, group g adding rows g, g + 64,
-// ... in order with eight loads in flight, then the groups' sums are added in a
-// fixed order.  No atomics: the order never changes.  Narrow workgroups, because
-// a sum's time is the latency of its rows' loads: 1024 rows of 2304 columns take
-// 64 rows per thread with one thread per column and wave, 16 here.
-constexpr int kColsumThreads = 1024, kColsumCols = 16;
+// workgroup per 32 columns (whole lines of the partial rows): 32 groups of 32
+// lanes, group g adding rows g, g + 32, ... in order with sixteen loads in
+// flight, then the groups' sums are added in a fixed order.  No atomics: the
+// order never changes.
+constexpr int kColsumThreads = 1024, kColsumCols = 32;
 template <typename OUT>
 __global__ __launch_bounds__(kColsumThreads) void colsum_kernel(const float* __restrict__ part,
                                                                 int nparts, int cols, OUT out) {
-  constexpr int NG = kColsumThreads / kColsumCols;
+  constexpr int NG = kColsumThreads / kColsumCols, NL = 16;
   __shared__ float sums[NG][kColsumCols];
   const int lane = threadIdx.x % kColsumCols, g = threadIdx.x / kColsumCols;
   const int col = blockIdx.x * kColsumCols + lane;
   const int c = col < cols ? col : cols - 1;
   float t = 0.f;
-  int r = g;
-  for (; r + 7 * NG < nparts; r += 8 * NG) {
-    float v[8];
+  for (int r = g; r < nparts; r += NL * NG) {
+    float v[NL];                                  // rows past the last: the last again, unused
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)(r + NG * i) * cols + c];
+    for (int i = 0; i < NL; ++i) v[i] = part[(int64_t)min(r + NG * i, nparts - 1) * cols + c];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += v[i];
-  }
-  if (r < nparts) {
-    float v[8];                                   // rows past the last: the last again, unused
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)min(r + NG * i, nparts - 1) * cols + c];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += r + NG * i < nparts ? v[i] : 0.f;
+    for (int i = 0; i < NL; ++i) t += r + NG * i < nparts ? v[i] : 0.f;
   }
   sums[g][lane] = t;
   __syncthreads();
-  if (g >= 4) return;
+  if (g >= 2) return;                             // the first wave: half the groups each
   t = 0.f;
 #pragma unroll
-  for (int q = 0; q < NG / 4; ++q) t += sums[g * (NG / 4) + q][lane];
-  t += __shfl_xor(t, 16);
+  for (int q = 0; q < NG / 2; ++q) t += sums[g * (NG / 2) + q][lane];
   t += __shfl_xor(t, 32);
   if (g == 0 && col < cols) out.put(col, t);
 }
