@@ -62,7 +62,9 @@ __device__ __forceinline__ void row_sums(float (&s)[M], float (*buf)[MAXM][RG][W
   }
 }
 
-// The channels [c, c + V) of a row of C channels, zeros past its end.
+// The channels [c, c + V) of a row of C channels, zeros past its end: with TAIL
+// from the load itself, else after bn_trim, which the caller leaves until the
+// values are needed (so that it does not wait for them any earlier).
 template <bool TAIL, typename E, int V>
 __device__ __forceinline__ void bn_load(Vec<E, V>& q, const E* row, int c, int C) {
   if constexpr (TAIL) {
@@ -70,8 +72,11 @@ __device__ __forceinline__ void bn_load(Vec<E, V>& q, const E* row, int c, int C
     else q.load_some(row + c, C - c);
   } else {
     q.load(row + (c < C ? c : 0));
-    q.clear_unless(c < C);
   }
+}
+template <bool TAIL, typename E, int V>
+__device__ __forceinline__ void bn_trim(Vec<E, V>& q, int c, int C) {
+  if constexpr (!TAIL) q.clear_unless(c < C);
 }
 
 template <bool TAIL, typename E, int V>
@@ -154,6 +159,12 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_fwd_kernel(const Block
 #pragma unroll 1
   for (int64_t r0 = (int64_t)blockIdx.x * RG; r0 < a.rows; r0 += (int64_t)gridDim.x * RG) {
     load(bn_next(r0, (int64_t)gridDim.x * RG, rg, a.rows), nx, ng, nr);
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      bn_trim<TAIL>(xq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(gq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(rq[k], (t + k * LANES) * V, C);
+    }
     float h[KT][V], s[1] = {0.f};
     float r1 = 1.f;
     if (a.post_w) {
@@ -270,6 +281,14 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
       else rq[k].clear();
       if (a.dres_out) bn_load<TAIL>(hq[k], static_cast<const R*>(a.dres_out) + o, c, C);
       else hq[k].clear();
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      bn_trim<TAIL>(xq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(rq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(gq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(dq[k], (t + k * LANES) * V, C);
+      bn_trim<TAIL>(hq[k], (t + k * LANES) * V, C);
     }
     float r1 = 1.f;
     if (a.post_w) {

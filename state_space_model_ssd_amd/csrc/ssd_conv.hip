@@ -569,7 +569,7 @@ constexpr int kConvFwdLong = 16, kConvFwdShort = 4;     // tokens per run, forwa
 constexpr int kConvBwdLong = 64, kConvBwdShort = 16;    // steps per run, backward
 constexpr int kConvBwdMaxParts = 256;
 constexpr int kConvStepThreads = 128;
-constexpr int64_t kConvMaxGroups = 1 << 22;   // workgroups of one launch
+constexpr int64_t kConvMaxGroups = 1 << 21;   // workgroups of one launch
 
 // Token groups of a launch: one per slot while the launch stays within
 // `most` workgroups, each walking several slots beyond that.

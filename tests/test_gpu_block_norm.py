@@ -230,6 +230,30 @@ def test_block_norm_rows_are_independent():
     assert not o2[11].any() and torch.isfinite(g2["x"][11]).all()    # a row of zeros: eps holds
 
 
+@pytest.mark.parametrize("C", [700, 701, 2300])
+def test_block_norm_infinite_values_as_the_formula(C):
+    """Rows that do not fill their waves: infinity at one channel reaches the
+    others exactly as the formula says (here h's sum is infinite, so every other
+    output is zero)."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, res, gate, w = r(8, C), r(8, C), r(8, C).abs() + 0.1, torch.ones(C, device="cuda")
+    for row, t in ((0, x), (1, res), (2, gate)):
+        t[row, 0] = float("inf")
+    x[3, C - 1] = float("inf")
+    for post in (None, w):
+        out, h = binding.block_norm_fwd(x, res, w, gate=gate, gate_activation="linear", post_weight=post)
+        xs = x if post is None else x * torch.rsqrt((x * x).mean(1, keepdim=True) + 1e-5)
+        hr = res + xs * gate
+        ref = hr * torch.rsqrt((hr * hr).mean(1, keepdim=True) + 1e-5)
+        torch.cuda.synchronize()
+        for got, want in ((out, ref), (h, hr)):
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.equal(torch.isinf(got), torch.isinf(want))
+            fin = torch.isfinite(want)
+            assert torch.allclose(got[fin], want[fin], rtol=1e-5, atol=1e-6)
+
+
 def test_block_norm_no_rows():
     x = torch.empty((0, 512), dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, device="cuda")
