@@ -15,11 +15,12 @@
 // one before the next), and two backward, whose later sums are arranged to need
 // nothing that the second exchange computes.  Four channels per lane rather
 // than eight: fewer registers, more rows in flight (forward at 8192 x 768 with an
-// fp32 residual 23.5 -> 19.4 us, 4.5 TB/s; backward 82 -> 38 us, 3.6 TB/s).
+// fp32 residual 23.5 -> 15.7 us, 5.6 TB/s; backward 82 -> 37 us, 3.7 TB/s with its
+// second launch).
 //
 // The forward keeps the next row's loads in flight; the backward, with twice
-// the registers, does better with more waves (8192 x 768: 43 us with the next
-// row in flight, 38 without).
+// the registers, gains nothing from that at 8192 x 768 (37.3 / 37.4 us with /
+// without) and loses a wave in wider rows (8192 x 2048: 83 / 76 us).
 //
 // Weight gradients accumulate in registers over the rows a workgroup walks,
 // leave as one partial row per workgroup and are added in workgroup order by a
