@@ -20,7 +20,8 @@
 //
 // The forward keeps the next row's loads in flight; the backward, with twice
 // the registers, gains nothing from that at 8192 x 768 (37.3 / 37.4 us with /
-// without) and loses a wave in wider rows (8192 x 2048: 83 / 76 us).
+// without) and loses a wave in wider rows (8192 x 2048: 83 / 76 us).  Rows of one
+// wave with three vectors per lane need no barrier, but 226 registers: 44 us.
 //
 // Weight gradients accumulate in registers over the rows a workgroup walks,
 // leave as one partial row per workgroup and are added in workgroup order by a
@@ -465,7 +466,7 @@ hipError_t bn_rows(const BlockNormArgs& a, hipStream_t s) {
   }
   // wider rows: sixteen waves forward; backward eight with more vectors per
   // lane, as 1024 threads leave too few registers (4096 x 4096 bf16: 208 us
-  // against 115)
+  // against 93; 2048 x 8192: 306 against 135)
   constexpr int W = BWD ? 8 : 16;
   if (nw <= 16) return bn_go<BWD, T, R, W, 16 / W, TAIL>(a, s);
   return bn_go<BWD, T, R, W, 32 / W, TAIL>(a, s);
