@@ -228,8 +228,7 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_fwd_kernel(const Block
 // weights wait in LDS, to keep the registers for rows in flight.
 template <typename T, typename R, int V, int W, int KT, int RG, bool TAIL>
 __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const BlockNormArgs a,
-                                                                     int sec_scale, int sec_pre,
-                                                                     int nsec) {
+                                                                     int sec_scale, int sec_pre) {
   constexpr int LANES = W * 64, CC = LANES * KT * V;
   constexpr bool kLds = KT > 1;                   // weights in LDS
   static_assert(W == 1 || RG == 1, "rows of several waves do not share a workgroup's barriers");
@@ -371,7 +370,7 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
   }
   // one partial row per workgroup and weight.  Rows of one wave are added in LDS
   // first, in the order of the waves.
-  float* part = a.part + (int64_t)blockIdx.x * nsec * C;
+  const int cp = (int)part_cols(C);
   auto put = [&](float(&v)[KT][V], int sec, float mul) {
     if constexpr (RG > 1) {
       float* red = wt[0];
@@ -389,7 +388,8 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
         }
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < C; c += LANES * RG) part[(int64_t)sec * C + c] = red[c] * mul;
+      for (int c = threadIdx.x; c < C; c += LANES * RG)
+        *part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c) = red[c] * mul;
     } else {
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
@@ -397,7 +397,9 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
         for (int e = 0; e < V; ++e) v[k][e] *= mul;
         Vec<float, V> q;
         q.set(v[k]);
-        bn_store<TAIL>(q, part + (int64_t)sec * C, (t + k * LANES) * V, C);
+        // a whole vector: its section's columns go to the end of a block
+        const int c = (t + k * LANES) * V;
+        if (c < C) q.store(part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c));
       }
     }
   };
@@ -406,14 +408,15 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
   put(an, sec_pre, 1.f);
 }
 
-// Column sec C + c of the partial sums.
+// Column c of section sec of the partial sums.
 struct BlockNormOut {
   float* w[3];
-  int C;
+  int C, cp;
   __device__ __forceinline__ void put(int col, float v) const {
-    const int sec = col / C;
+    const int sec = col / cp, c = col - sec * cp;
+    if (c >= C) return;
     float* o = sec == 0 ? w[0] : sec == 1 ? w[1] : w[2];
-    o[col - sec * C] = v;
+    o[c] = v;
   }
 };
 
@@ -445,14 +448,15 @@ hipError_t bn_go(const BlockNormArgs& a, hipStream_t s) {
     const int sec_scale = a.post_w ? 1 : 0, sec_pre = nsec - 1;
     BlockNormOut out;
     out.C = a.C;
+    out.cp = (int)part_cols(a.C);
     out.w[0] = out.w[1] = out.w[2] = a.dpre_w;
     if (a.post_w) out.w[0] = a.dpost_w;
     if (a.scale) out.w[sec_scale] = a.dscale;
     const int grid = bn_grid(a.rows, RG, KT == 1 ? 16 / (W * RG) : 1, kBnMaxParts);
     if (grid > 0)
       hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, V, W, KT, RG, TAIL>), dim3(grid),
-                         dim3(64 * W * RG), 0, s, a, sec_scale, sec_pre, nsec);
-    return colsum(a.part, grid, nsec * a.C, out, s);
+                         dim3(64 * W * RG), 0, s, a, sec_scale, sec_pre);
+    return colsum(a.part, grid, nsec * part_cols(a.C), out, s);
   }
 }
 
@@ -486,7 +490,7 @@ hipError_t bn_type(const BlockNormArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t block_norm_bwd_floats(int64_t rows, int64_t C) {
-  return (rows < kBnMaxParts ? rows : kBnMaxParts) * 3 * C;
+  return (rows < kBnMaxParts ? rows : kBnMaxParts) * 3 * part_cols(C);
 }
 
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, hipStream_t s) {

@@ -471,7 +471,7 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, const ConvTile& 
 
 // dw and db accumulate in registers over the workgroup's tiles, are added over
 // its waves in LDS at the end, and leave as one partial row per workgroup,
-// [part][K + 1][C].
+// K + 1 sections of part_cols(C) columns.
 template <typename T, int V, int K, int STEPS, int GR, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a, int nct,
                                                                 int nslots, int nparts) {
@@ -506,6 +506,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a
     for (int e = 0; e < V; ++e) red[wv][k][lane * V + e] = acc[k][e];
   __syncthreads();
   const int first = __builtin_amdgcn_readfirstlane(col.c - col.co);   // the output's first channel
+  const int cp = (int)part_cols(a.C);
   for (int i = threadIdx.x; i < (K + 1) * 64 * V; i += kConvThreads) {
     const int k = i / (64 * V), cc = i % (64 * V), ch = col.tile + cc;
     if (ch >= col.ld) continue;
@@ -514,16 +515,17 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a
     float s = red[0][k][at];
 #pragma unroll
     for (int u = 1; u < kConvWaves; ++u) s += red[u][k][at];
-    a.part[((int64_t)part * (K + 1) + k) * a.C + first + ch] = s;
+    *part_at(a.part, part, nparts, k * cp + first + ch) = s;
   }
 }
 
-// Column k C + c of the partial sums: dweight[c][k], or dbias[c] for k = K.
+// Column c of section k of the partial sums: dweight[c][k], or dbias[c] for k = K.
 struct ConvGradOut {
   float *dw, *db;
-  int C, K;
+  int C, cp, K;
   __device__ __forceinline__ void put(int col, float v) const {
-    const int k = col / C, c = col - k * C;
+    const int k = col / cp, c = col - k * cp;
+    if (c >= C) return;
     if (k < K) dw[(int64_t)c * K + k] = v;
     else if (db) db[c] = v;
   }
@@ -601,7 +603,8 @@ hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
   auto fn = a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true> : &conv_bwd_kernel<T, V, K, STEPS, 8, false>;
   if (grid > 0)
     hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
-  return colsum(a.part, nparts, (K + 1) * a.C, ConvGradOut{a.dw, a.dbias, a.C, K}, s);
+  const int64_t cp = part_cols(a.C);
+  return colsum(a.part, nparts, (K + 1) * cp, ConvGradOut{a.dw, a.dbias, a.C, (int)cp, K}, s);
 }
 
 template <typename T, int V, int K>
@@ -665,7 +668,7 @@ hipError_t conv_step_k(const ConvArgs& a, hipStream_t s) {
 int64_t conv_bwd_floats(int64_t tokens, int64_t nstates, int64_t C, int64_t K) {
   const int64_t wt = (kConvBwdShort - (K - 1)) * kConvWaves;
   const int64_t slots = (tokens + wt - 1) / wt + nstates;
-  return (slots < kConvBwdMaxParts ? slots : kConvBwdMaxParts) * (K + 1) * C;
+  return (slots < kConvBwdMaxParts ? slots : kConvBwdMaxParts) * (K + 1) * part_cols(C);
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) {
