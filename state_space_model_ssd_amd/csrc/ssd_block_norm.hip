@@ -331,8 +331,10 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
     }
     row_sums<W, RG>(s, buf, rg, par);
     const float r2 = rsqrtf(s[0] * inv + a.eps);
-    const float hk = r2 * r2 * r2 * (s[1] * inv);   // dh = r2 dn - hk h + dh_out
-    const float mm = a.post_w ? (r2 * s[2] - hk * s[3] + s[4]) * inv : 0.f;
+    // dh = r2 (dn - c n) + dh_out.  Factors r2 only beside an h: r2^3 would leave fp32's
+    // range for |h| beyond 1e12 (and under 1e-12 without eps).
+    const float c2 = r2 * (s[1] * inv);
+    const float mm = a.post_w ? (r2 * (s[2] - c2 * (r2 * s[3])) + s[4]) * inv : 0.f;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const int c = (t + k * LANES) * V;
@@ -348,8 +350,9 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
       for (int e = 0; e < V; ++e) {
         float act = 1.f, da = 0.f;
         if (a.gate) da = bn_act_grad(a.act, g[e], act);
-        an[k][e] += d[e] * (h[k][e] * r2);
-        dh[e] += r2 * (d[e] * nw[e]) - hk * h[k][e];
+        const float n = h[k][e] * r2;
+        an[k][e] += d[e] * n;
+        dh[e] += r2 * (d[e] * nw[e] - c2 * n);
         const float m = x[e] * r1, p = m * pw[e], du = dh[e] * fw[e], dp = du * act;
         as[k][e] += dh[e] * (p * act);
         dg[e] = du * p * da;

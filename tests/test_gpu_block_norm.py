@@ -254,6 +254,56 @@ def test_block_norm_infinite_values_as_the_formula(C):
             assert torch.allclose(got[fin], want[fin], rtol=1e-5, atol=1e-6)
 
 
+@pytest.mark.parametrize("k", [46, -46])
+@pytest.mark.parametrize("C,post", [(768, True), (768, False), (1025, True), (4096, True)])
+def test_block_norm_backward_holds_at_any_scale_of_the_stream(C, post, k):
+    """Without eps, a stream 2^k times as large gives the same out and the same
+    gradients, dresidual 2^-k times as large: products with powers of two are
+    exact.  Only the root of the mean may round otherwise, by 2 U on either side,
+    which enters dn's and n's terms at most four times: 16 U of the terms' sizes, and
+    of their absolute sums in the weights' gradients."""
+    g = torch.Generator(device="cuda").manual_seed(C)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, res, gate, dout, dh = (r(9, C) for _ in range(5))
+    pre, sc, pw = (1 + 0.3 * r(C) for _ in range(3))
+    f = 2.0 ** k
+
+    def run(f):
+        # with a norm after the block its output does not scale, alpha does
+        kw = dict(gate=gate, scale=sc, post_weight=pw if post else None, eps=0.0,
+                  residual_scale=f if post else 1.0)
+        xs = x if post else x * f
+        out, h = binding.block_norm_fwd(xs, res * f, pre, **kw)
+        b = binding.block_norm_bwd(xs, res * f, pre, dout, dh / f, **kw)
+        b["out"], b["residual"], b["h"] = out, b["residual"] * f, h / f
+        if not post:
+            b["x"] = b["x"] * f
+        return b
+
+    one, other = run(1.0), run(f)
+    torch.cuda.synchronize()
+    d = lambda t: t.double()  # noqa: E731
+    h = d(one["h"])
+    r2 = (h * h).mean(1, keepdim=True).rsqrt()
+    n, dn = (h * r2).abs(), (d(dout) * d(pre)).abs()
+    size = r2 * (dn + n * (dn * n).mean(1, keepdim=True)) + d(dh).abs()
+    act = torch.sigmoid(d(gate))
+    m = d(x) * (d(x) * d(x)).mean(1, keepdim=True).rsqrt() if post else d(x)
+    p = (m * d(pw) if post else m).abs()
+    dp = size * d(sc).abs() * act
+    dm = (dp * d(pw).abs()) if post else dp
+    r1 = (d(x) * d(x)).mean(1, keepdim=True).rsqrt() if post else 1.0
+    sizes = {"out": d(one["out"]).abs(), "h": h.abs(), "residual": size,
+             "gate": size * d(sc).abs() * p * act * (1 - act),
+             "x": r1 * (dm + m.abs() * (dm * m.abs()).mean(1, keepdim=True)) if post else dp,
+             "pre_weight": (d(dout).abs() * n).sum(0), "scale": (size * p * act).sum(0)}
+    if post:
+        sizes["post_weight"] = (dp * m.abs()).sum(0)
+    for name, s in sizes.items():
+        err = (d(one[name]) - d(other[name])).abs()
+        assert bool((err <= 16 * U * s).all()), (name, float((err / s).max()))
+
+
 def test_block_norm_no_rows():
     x = torch.empty((0, 512), dtype=torch.bfloat16, device="cuda")
     w = torch.ones(512, device="cuda")
