@@ -469,12 +469,14 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, const ConvTile& 
   }
 }
 
-// dw and db accumulate in registers over the workgroup's tiles, are added over
-// its waves in LDS at the end, and leave as one partial row per workgroup,
-// K + 1 sections of part_cols(C) columns.
-template <typename T, int V, int K, int STEPS, int GR, bool SILU>
+// dw and db accumulate in registers over `seg` of the workgroup's tiles, are added
+// over its waves in LDS, and go to one partial row per workgroup, K + 1 sections of
+// part_cols(C) columns, to which the next `seg` tiles are added (conv_segment).  SEG:
+// there is more than one segment (in the kernel for one, the test alone costs 0.3 of
+// the 8 us that a packed batch of 6349 tokens x 160 channels takes).
+template <typename T, int V, int K, int STEPS, int GR, bool SILU, bool SEG>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a, int nct,
-                                                                int nslots, int nparts) {
+                                                                int nslots, int nparts, int seg) {
   constexpr int TT = STEPS - (K - 1), WT = TT * kConvWaves;
   __shared__ float red[kConvWaves][K + 1][64 * V];
   if ((int)blockIdx.x >= nct * nparts) {
@@ -486,36 +488,44 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a
   const ConvCols col = conv_cols<V>(a, blockIdx.x % nct);
   float w[K][V], b[V];
   conv_weights<V, K>(a, col.c, w, b);
-  float acc[K + 1][V];
+  for (int s0 = part;;) {                           // a segment; every workgroup has a tile
+    float acc[K + 1][V];
 #pragma unroll
-  for (int k = 0; k <= K; ++k)
+    for (int k = 0; k <= K; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
-  for (int slot = part; slot < nslots; slot += nparts) {
-    const ConvTile t = conv_tile<WT>(a, slot);
-    const int t0 = t.lo + wv * TT;
-    if (t0 >= t.hi || !col.ok) continue;
-    if (t0 - (K - 1) >= t.start && t0 + TT <= t.hi && t0 + TT + K - 1 <= t.end)
-      conv_bwd_run<T, V, K, STEPS, GR, SILU, false>(a, t, t0, col, w, b, acc);
-    else
-      conv_bwd_run<T, V, K, STEPS, GR, SILU, true>(a, t, t0, col, w, b, acc);
-  }
+      for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
+    const int s1 = SEG ? min(s0 + seg * nparts, nslots) : nslots;
+    for (int slot = s0; slot < s1; slot += nparts) {
+      const ConvTile t = conv_tile<WT>(a, slot);
+      const int t0 = t.lo + wv * TT;
+      if (t0 >= t.hi || !col.ok) continue;
+      if (t0 - (K - 1) >= t.start && t0 + TT <= t.hi && t0 + TT + K - 1 <= t.end)
+        conv_bwd_run<T, V, K, STEPS, GR, SILU, false>(a, t, t0, col, w, b, acc);
+      else
+        conv_bwd_run<T, V, K, STEPS, GR, SILU, true>(a, t, t0, col, w, b, acc);
+    }
+    if (SEG && s0 != part) __syncthreads();         // the segment before has been read
 #pragma unroll
-  for (int k = 0; k <= K; ++k)
+    for (int k = 0; k <= K; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) red[wv][k][lane * V + e] = acc[k][e];
-  __syncthreads();
-  const int first = __builtin_amdgcn_readfirstlane(col.c - col.co);   // the output's first channel
-  const int cp = (int)part_cols(a.C);
-  for (int i = threadIdx.x; i < (K + 1) * 64 * V; i += kConvThreads) {
-    const int k = i / (64 * V), cc = i % (64 * V), ch = col.tile + cc;
-    if (ch >= col.ld) continue;
-    // the value's place: its vector's lane, whose vector may start earlier
-    const int at = cc / V * V + ch - conv_vec<V>(ch / V, col.ld);
-    float s = red[0][k][at];
+      for (int e = 0; e < V; ++e) red[wv][k][lane * V + e] = acc[k][e];
+    __syncthreads();
+    const int first = __builtin_amdgcn_readfirstlane(col.c - col.co);   // the output's first channel
+    const int cp = (int)part_cols(a.C);
+    for (int i = threadIdx.x; i < (K + 1) * 64 * V; i += kConvThreads) {
+      const int k = i / (64 * V), cc = i % (64 * V), ch = col.tile + cc;
+      if (ch >= col.ld) continue;
+      // the value's place: its vector's lane, whose vector may start earlier
+      const int at = cc / V * V + ch - conv_vec<V>(ch / V, col.ld);
+      float s = red[0][k][at];
 #pragma unroll
-    for (int u = 1; u < kConvWaves; ++u) s += red[u][k][at];
-    *part_at(a.part, part, nparts, k * cp + first + ch) = s;
+      for (int u = 1; u < kConvWaves; ++u) s += red[u][k][at];
+      float* to = part_at(a.part, part, nparts, k * cp + first + ch);
+      if (SEG && s0 != part) s += *to;              // the same thread in every segment
+      *to = s;
+    }
+    s0 += seg * nparts;
+    if (!SEG || s0 >= nslots) return;
   }
 }
 
@@ -580,6 +590,19 @@ int conv_parts(int nslots, int nct, int64_t most) {
   return (int)(nslots < p ? nslots : (p > 0 ? p : 1));
 }
 
+// Tiles of a workgroup whose terms of dw and db one register adds before they go to
+// the partial row: 256 tokens' worth, and the square root of the tokens a wave has
+// where that is more, so that a term passes at most about 256 + tokens / 256 or
+// 2 sqrt(tokens) additions there, not one per token.  (One register over all tiles: a sum
+// of 2^23 equal terms per channel, 8192 a wave, was off by 1354 2^-24 of its value,
+// with segments by under 50; 2^20 tokens x 160 channels of fp32 512 and 520 us.)
+int conv_segment(int nslots, int nparts, int TT) {
+  const int runs = nparts > 0 ? (nslots + nparts - 1) / nparts : 0;
+  int seg = (256 + TT - 1) / TT;
+  while ((int64_t)seg * seg * TT < runs) ++seg;
+  return seg;
+}
+
 template <typename T, int V, int K, int TT>
 hipError_t conv_fwd_go(const ConvArgs& a, hipStream_t s) {
   const int nct = conv_col_tiles<V>(a);
@@ -600,9 +623,14 @@ hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
   const int nparts = a.total > 0 ? conv_parts(nslots, 1, kConvBwdMaxParts) : 0;
   const int64_t ini = a.dinit ? (int64_t)a.nstates * ((a.C + 2) / V + 3) : 0;
   const int64_t grid = (int64_t)nct * nparts + (ini + kConvThreads - 1) / kConvThreads;
-  auto fn = a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true> : &conv_bwd_kernel<T, V, K, STEPS, 8, false>;
+  const int seg = conv_segment(nslots, nparts, STEPS - (K - 1));
+  const bool many = (int64_t)seg * nparts < nslots;
+  auto fn = many ? (a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true, true>
+                           : &conv_bwd_kernel<T, V, K, STEPS, 8, false, true>)
+                 : (a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true, false>
+                           : &conv_bwd_kernel<T, V, K, STEPS, 8, false, false>);
   if (grid > 0)
-    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
+    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts, seg);
   const int64_t cp = part_cols(a.C);
   return colsum(a.part, nparts, (K + 1) * cp, ConvGradOut{a.dw, a.dbias, a.C, (int)cp, K}, s);
 }
