@@ -23,9 +23,9 @@
 // without) and loses a wave in wider rows (8192 x 2048: 83 / 76 us).  Rows of one
 // wave with three vectors per lane need no barrier, but 226 registers: 44 us.
 //
-// Weight gradients accumulate in registers over the rows a workgroup walks,
-// leave as one partial row per workgroup and are added in workgroup order by a
-// second launch.  No atomics.
+// Weight gradients accumulate in registers over the rows a workgroup walks, in
+// segments (bn_segment), leave as one partial row per workgroup and are added in
+// workgroup order by a second launch.  No atomics.
 #include "ssd_kernels.h"
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
@@ -226,9 +226,10 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_fwd_kernel(const Block
 //
 // The gate's factors are formed twice, and with several vectors per lane the
 // weights wait in LDS, to keep the registers for rows in flight.
-template <typename T, typename R, int V, int W, int KT, int RG, bool TAIL>
+template <typename T, typename R, int V, int W, int KT, int RG, bool TAIL, bool SEG>
 __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const BlockNormArgs a,
-                                                                     int sec_scale, int sec_pre) {
+                                                                     int sec_scale, int sec_pre,
+                                                                     int64_t seg) {
   constexpr int LANES = W * 64, CC = LANES * KT * V;
   constexpr bool kLds = KT > 1;                   // weights in LDS
   static_assert(W == 1 || RG == 1, "rows of several waves do not share a workgroup's barriers");
@@ -261,120 +262,13 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
       for (int e = 0; e < V; ++e) w[e] = wr[i][k][e];
     }
   };
-  float ap[KT][V], as[KT][V], an[KT][V];
-#pragma unroll
-  for (int k = 0; k < KT; ++k)
-#pragma unroll
-    for (int e = 0; e < V; ++e) ap[k][e] = as[k][e] = an[k][e] = 0.f;
-#pragma unroll 1
-  for (int64_t r = (int64_t)blockIdx.x * RG + rg; r < a.rows; r += (int64_t)gridDim.x * RG) {
-    const int64_t o = r * C;
-    Vec<T, V> xq[KT], gq[KT], dq[KT];
-    Vec<R, V> rq[KT], hq[KT];
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const int c = (t + k * LANES) * V;
-      bn_load<TAIL>(xq[k], static_cast<const T*>(a.x) + o, c, C);
-      // where there is no gate, x's row again: loaded, never used
-      bn_load<TAIL>(gq[k], static_cast<const T*>(a.gate ? a.gate : a.x) + o, c, C);
-      bn_load<TAIL>(dq[k], static_cast<const T*>(a.dout) + o, c, C);
-      if (a.residual) bn_load<TAIL>(rq[k], static_cast<const R*>(a.residual) + o, c, C);
-      else rq[k].clear();
-      if (a.dres_out) bn_load<TAIL>(hq[k], static_cast<const R*>(a.dres_out) + o, c, C);
-      else hq[k].clear();
-    }
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      bn_trim<TAIL>(xq[k], (t + k * LANES) * V, C);
-      bn_trim<TAIL>(rq[k], (t + k * LANES) * V, C);
-      bn_trim<TAIL>(gq[k], (t + k * LANES) * V, C);
-      bn_trim<TAIL>(dq[k], (t + k * LANES) * V, C);
-      bn_trim<TAIL>(hq[k], (t + k * LANES) * V, C);
-    }
-    float r1 = 1.f;
-    if (a.post_w) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        float x[V];
-        xq[k].get(x);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] += x[e] * x[e];
-      }
-      row_sums<W, RG>(s, buf, rg, par);
-      r1 = rsqrtf(s[0] * inv + a.eps);
-    }
-    // sums of h^2, dn h, and with a norm of y dn, y h, y dh_out
-    float h[KT][V], s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      float x[V], g[V], q[V], d[V], ho[V], pw[V], fw[V], nw[V];
-      xq[k].get(x);
-      rq[k].get(q);
-      dq[k].get(d);
-      gq[k].get(g);
-      hq[k].get(ho);
-      weights(k, 0, pw);
-      weights(k, 1, fw);
-      weights(k, 2, nw);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float act = a.gate ? bn_act(a.act, g[e]) : 1.f;
-        const float y = x[e] * r1 * pw[e] * act * fw[e], dn = d[e] * nw[e];
-        h[k][e] = q[e] + y;
-        s[0] += h[k][e] * h[k][e];
-        s[1] += dn * h[k][e];
-        s[2] += y * dn;
-        s[3] += y * h[k][e];
-        s[4] += y * ho[e];
-      }
-    }
-    row_sums<W, RG>(s, buf, rg, par);
-    const float r2 = rsqrtf(s[0] * inv + a.eps);
-    // dh = r2 (dn - c n) + dh_out.  Factors r2 only beside an h: r2^3 would leave fp32's
-    // range for |h| beyond 1e12 (and under 1e-12 without eps).
-    const float c2 = r2 * (s[1] * inv);
-    const float mm = a.post_w ? (r2 * (s[2] - c2 * (r2 * s[3])) + s[4]) * inv : 0.f;
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const int c = (t + k * LANES) * V;
-      float x[V], g[V], d[V], dh[V], dg[V], pw[V], fw[V], nw[V];
-      xq[k].get(x);
-      dq[k].get(d);
-      gq[k].get(g);
-      hq[k].get(dh);
-      weights(k, 0, pw);
-      weights(k, 1, fw);
-      weights(k, 2, nw);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float act = 1.f, da = 0.f;
-        if (a.gate) da = bn_act_grad(a.act, g[e], act);
-        const float n = h[k][e] * r2;
-        an[k][e] += d[e] * n;
-        dh[e] += r2 * (d[e] * nw[e] - c2 * n);
-        const float m = x[e] * r1, p = m * pw[e], du = dh[e] * fw[e], dp = du * act;
-        as[k][e] += dh[e] * (p * act);
-        dg[e] = du * p * da;
-        ap[k][e] += dp * m;
-        x[e] = r1 * (dp * pw[e] - m * mm);
-      }
-      xq[k].set(x);
-      bn_store<TAIL>(xq[k], static_cast<T*>(a.dx) + o, c, C);
-      if (a.dres) {
-        hq[k].set(dh);
-        bn_store<TAIL>(hq[k], static_cast<R*>(a.dres) + o, c, C);
-      }
-      if (a.gate) {
-        gq[k].set(dg);
-        bn_store<TAIL>(gq[k], static_cast<T*>(a.dgate) + o, c, C);
-      }
-    }
-  }
-  // one partial row per workgroup and weight.  Rows of one wave are added in LDS
-  // first, in the order of the waves.
+  // One partial row per workgroup and weight: a segment's sums, added to those of the
+  // segments before by the same threads.  Rows of one wave are added in LDS first, in
+  // the order of the waves.
   const int cp = (int)part_cols(C);
-  auto put = [&](float(&v)[KT][V], int sec, float mul) {
+  auto put = [&](float(&v)[KT][V], int sec, float mul, bool add) {
+    // read again in every segment, or its addresses would be held over the rows
+    const int t = body_tid<SEG, 64 * W * RG>() - rg * LANES;
     if constexpr (RG > 1) {
       float* red = wt[0];
 #pragma unroll 1
@@ -391,24 +285,156 @@ __global__ __launch_bounds__(64 * W * RG) void block_norm_bwd_kernel(const Block
         }
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < C; c += LANES * RG)
-        *part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c) = red[c] * mul;
+      for (int c = threadIdx.x; c < C; c += LANES * RG) {
+        float* to = part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c);
+        *to = add ? *to + red[c] * mul : red[c] * mul;
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
 #pragma unroll
         for (int e = 0; e < V; ++e) v[k][e] *= mul;
-        Vec<float, V> q;
-        q.set(v[k]);
         // a whole vector: its section's columns go to the end of a block
         const int c = (t + k * LANES) * V;
-        if (c < C) q.store(part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c));
+        if (c >= C) continue;
+        float* to = part_at(a.part, (int)blockIdx.x, (int)gridDim.x, sec * cp + c);
+        Vec<float, V> q;
+        if (add) {
+          float was[V];
+          q.load(to);
+          q.get(was);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[k][e] += was[e];
+        }
+        q.set(v[k]);
+        q.store(to);
       }
     }
   };
-  if (a.post_w) put(ap, 0, 1.f);
-  if (a.scale) put(as, sec_scale, a.alpha);
-  put(an, sec_pre, 1.f);
+  const int64_t first = (int64_t)blockIdx.x * RG, step = (int64_t)gridDim.x * RG;
+#pragma unroll 1
+  for (int64_t s0 = first; s0 < a.rows; s0 += seg * step) {
+    const int64_t s1 = SEG ? min(s0 + seg * step, a.rows) : a.rows;
+    float ap[KT][V], as[KT][V], an[KT][V];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) ap[k][e] = as[k][e] = an[k][e] = 0.f;
+#pragma unroll 1
+    for (int64_t r = s0 + rg; r < s1; r += step) {
+      // with segments the row's number goes through an empty asm statement, or each lane
+      // would hold one address per tensor from row to row (up to 20 registers)
+      int64_t row = r;
+      if constexpr (SEG) asm("" : "+s"(row));
+      const int64_t o = row * C;
+      Vec<T, V> xq[KT], gq[KT], dq[KT];
+      Vec<R, V> rq[KT], hq[KT];
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int c = (t + k * LANES) * V;
+        bn_load<TAIL>(xq[k], static_cast<const T*>(a.x) + o, c, C);
+        // where there is no gate, x's row again: loaded, never used
+        bn_load<TAIL>(gq[k], static_cast<const T*>(a.gate ? a.gate : a.x) + o, c, C);
+        bn_load<TAIL>(dq[k], static_cast<const T*>(a.dout) + o, c, C);
+        if (a.residual) bn_load<TAIL>(rq[k], static_cast<const R*>(a.residual) + o, c, C);
+        else rq[k].clear();
+        if (a.dres_out) bn_load<TAIL>(hq[k], static_cast<const R*>(a.dres_out) + o, c, C);
+        else hq[k].clear();
+      }
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        bn_trim<TAIL>(xq[k], (t + k * LANES) * V, C);
+        bn_trim<TAIL>(rq[k], (t + k * LANES) * V, C);
+        bn_trim<TAIL>(gq[k], (t + k * LANES) * V, C);
+        bn_trim<TAIL>(dq[k], (t + k * LANES) * V, C);
+        bn_trim<TAIL>(hq[k], (t + k * LANES) * V, C);
+      }
+      float r1 = 1.f;
+      if (a.post_w) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          float x[V];
+          xq[k].get(x);
+#pragma unroll
+          for (int e = 0; e < V; ++e) s[0] += x[e] * x[e];
+        }
+        row_sums<W, RG>(s, buf, rg, par);
+        r1 = rsqrtf(s[0] * inv + a.eps);
+      }
+      // sums of h^2, dn h, and with a norm of y dn, y h, y dh_out
+      float h[KT][V], s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        float x[V], g[V], q[V], d[V], ho[V], pw[V], fw[V], nw[V];
+        xq[k].get(x);
+        rq[k].get(q);
+        dq[k].get(d);
+        gq[k].get(g);
+        hq[k].get(ho);
+        weights(k, 0, pw);
+        weights(k, 1, fw);
+        weights(k, 2, nw);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float act = a.gate ? bn_act(a.act, g[e]) : 1.f;
+          const float y = x[e] * r1 * pw[e] * act * fw[e], dn = d[e] * nw[e];
+          h[k][e] = q[e] + y;
+          s[0] += h[k][e] * h[k][e];
+          s[1] += dn * h[k][e];
+          s[2] += y * dn;
+          s[3] += y * h[k][e];
+          s[4] += y * ho[e];
+        }
+      }
+      row_sums<W, RG>(s, buf, rg, par);
+      const float r2 = rsqrtf(s[0] * inv + a.eps);
+      // dh = r2 (dn - c n) + dh_out.  Factors r2 only beside an h: r2^3 would leave fp32's
+      // range for |h| beyond 1e12 (and under 1e-12 without eps).
+      const float c2 = r2 * (s[1] * inv);
+      const float mm = a.post_w ? (r2 * (s[2] - c2 * (r2 * s[3])) + s[4]) * inv : 0.f;
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int c = (t + k * LANES) * V;
+        float x[V], g[V], d[V], dh[V], dg[V], pw[V], fw[V], nw[V];
+        xq[k].get(x);
+        dq[k].get(d);
+        gq[k].get(g);
+        hq[k].get(dh);
+        weights(k, 0, pw);
+        weights(k, 1, fw);
+        weights(k, 2, nw);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float act = 1.f, da = 0.f;
+          if (a.gate) da = bn_act_grad(a.act, g[e], act);
+          const float n = h[k][e] * r2;
+          an[k][e] += d[e] * n;
+          dh[e] += r2 * (d[e] * nw[e] - c2 * n);
+          const float m = x[e] * r1, p = m * pw[e], du = dh[e] * fw[e], dp = du * act;
+          as[k][e] += dh[e] * (p * act);
+          dg[e] = du * p * da;
+          ap[k][e] += dp * m;
+          x[e] = r1 * (dp * pw[e] - m * mm);
+        }
+        xq[k].set(x);
+        bn_store<TAIL>(xq[k], static_cast<T*>(a.dx) + o, c, C);
+        if (a.dres) {
+          hq[k].set(dh);
+          bn_store<TAIL>(hq[k], static_cast<R*>(a.dres) + o, c, C);
+        }
+        if (a.gate) {
+          gq[k].set(dg);
+          bn_store<TAIL>(gq[k], static_cast<T*>(a.dgate) + o, c, C);
+        }
+      }
+    }
+    const bool add = SEG && s0 > first;
+    if (a.post_w) put(ap, 0, 1.f, add);
+    if (a.scale) put(as, sec_scale, a.alpha, add);
+    put(an, sec_pre, 1.f, add);
+    if (!SEG) return;
+  }
 }
 
 // Column c of section sec of the partial sums.
@@ -430,6 +456,18 @@ int bn_grid(int64_t rows, int rows_per_group, int per_cu, int most) {
   if (want > most) want = most;
   const int64_t groups = (rows + rows_per_group - 1) / rows_per_group;
   return (int)(groups < want ? groups : want);
+}
+
+// Rows whose terms of the weight gradients one register adds before they go to the
+// partial row, of the `walk` rows that a wave walks: 64, and their square root where
+// that is more, so that a term passes at most 64 + walk / 64 or 2 sqrt(walk) additions
+// there, not one per row.  (2^23 rows of equal terms, 2048 a wave: off by 382 2^-24 in one
+// register, by 15 in segments.  262144 x 768 900 and 912 us, 65536 x 8192 1447 and 1385.)
+// Up to 64 rows a wave run the kernel without the segments' test.
+int64_t bn_segment(int64_t walk) {
+  int64_t seg = 64;
+  while (seg * seg < walk) ++seg;
+  return seg;
 }
 
 // Workgroups per CU: as many as are resident, so that each walks over rows to the
@@ -456,9 +494,12 @@ hipError_t bn_go(const BlockNormArgs& a, hipStream_t s) {
     if (a.post_w) out.w[0] = a.dpost_w;
     if (a.scale) out.w[sec_scale] = a.dscale;
     const int grid = bn_grid(a.rows, RG, KT == 1 ? 16 / (W * RG) : 1, kBnMaxParts);
+    const int64_t walk = grid > 0 ? (a.rows + (int64_t)grid * RG - 1) / ((int64_t)grid * RG) : 0;
+    const int64_t seg = bn_segment(walk);
+    auto fn = seg < walk ? &block_norm_bwd_kernel<T, R, V, W, KT, RG, TAIL, true>
+                         : &block_norm_bwd_kernel<T, R, V, W, KT, RG, TAIL, false>;
     if (grid > 0)
-      hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, V, W, KT, RG, TAIL>), dim3(grid),
-                         dim3(64 * W * RG), 0, s, a, sec_scale, sec_pre);
+      hipLaunchKernelGGL(fn, dim3(grid), dim3(64 * W * RG), 0, s, a, sec_scale, sec_pre, seg);
     return colsum(a.part, grid, nsec * part_cols(a.C), out, s);
   }
 }

@@ -595,7 +595,7 @@ int conv_parts(int nslots, int nct, int64_t most) {
 // where that is more, so that a term passes at most about 256 + tokens / 256 or
 // 2 sqrt(tokens) additions there, not one per token.  (One register over all tiles: a sum
 // of 2^23 equal terms per channel, 8192 a wave, was off by 1354 2^-24 of its value,
-// with segments by under 50; 2^20 tokens x 160 channels of fp32 512 and 520 us.)
+// with segments by 63; 2^20 tokens x 160 channels of fp32 512 and 520 us.)
 int conv_segment(int nslots, int nparts, int TT) {
   const int runs = nparts > 0 ? (nslots + nparts - 1) / nparts : 0;
   int seg = (256 + TT - 1) / TT;
