@@ -671,6 +671,8 @@ def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_s
         stride = _row_stride(dx, "dx", 2)
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_bwd", x, weight, bias, splits,
                                                       activation, initial_states, cu_seqlens, stride)
+    if douts is None:
+        raise ValueError("douts are three tensors")
     douts = _conv_outs(douts, splits, (b, T), x, "douts")
     _need(dfinal_states, "dfinal_states", x.dtype, sshape, dev)
     f32 = torch.float32
