@@ -446,7 +446,8 @@ ssd_status_t ssd_fwd_noalloc(const ssd_problem_t* p,
  * Accumulation in fp32, one rounding of each output to the dtype; final
  * states are copies.  A packed batch (nseq > 0, batch 1) takes cu_seqlens
  * (non-decreasing); tokens before its first entry and from its last entry on
- * belong to no sequence, and their rows of the outputs keep what they held.
+ * belong to no sequence, and their rows of the outputs keep what they held, or
+ * with clear_outside become zeros.
  * Malformed cu_seqlens give unspecified outputs but never an access outside
  * the given buffers.  No pointer may alias another.  Errors as for ssd_fwd;
  * width outside 2..4 is SSD_ERR_UNSUPPORTED.
@@ -463,6 +464,9 @@ typedef struct {
   int64_t din_stride;  /* the same of dxbc (ssd_conv_bwd)                   */
   int32_t dtype;       /* ssd_dtype_t of xbc, the states and the outputs    */
   int32_t activation;  /* 0: none, 1: SiLU                                  */
+  int32_t clear_outside; /* packed batch: 1 clears the rows of tokens outside */
+                       /* every sequence in what the call writes (the       */
+                       /* outputs, or dxbc); 0 leaves them                  */
 } ssd_conv_problem_t;
 
 ssd_status_t ssd_conv_fwd(const ssd_conv_problem_t* p, const void* xbc, const float* weight,
@@ -486,7 +490,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_problem_t* p, const void* xbc, const fl
  *   dweight [C][K] fp32 (required);  dbias [C] fp32 (nullable: not computed)
  *   dinitial_states         like initial_states (nullable: not computed)
  * pre is computed again from xbc.  Tokens outside every sequence add nothing
- * and their rows of dxbc are not written.  The workspace (no initial contents)
+ * and their rows of dxbc are not written (clear_outside: zeros).  The workspace (no initial contents)
  * is ssd_conv_bwd_workspace_size bytes, 256-byte aligned; calls that may overlap
  * (on different streams, or in graphs replayed side by side) need one each.  No
  * atomics: results are deterministic.

@@ -82,7 +82,8 @@ class ConvProblemC(ctypes.Structure):
                 ("channels_x", ctypes.c_int64), ("channels_b", ctypes.c_int64),
                 ("channels_c", ctypes.c_int64), ("width", ctypes.c_int64),
                 ("in_stride", ctypes.c_int64), ("din_stride", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("clear_outside", ctypes.c_int32)]
 
 
 class StepProblemC(ctypes.Structure):
@@ -593,7 +594,10 @@ def _conv_checked(what, x, weight, bias, splits, activation):
     return dev, C, tuple(splits), _CONV_ACTIVATIONS[activation]
 
 
-def _conv_prompt(what, x, weight, bias, splits, activation, initial_states, cu_seqlens, dx_stride=0):
+def _conv_prompt(what, x, weight, bias, splits, activation, initial_states, cu_seqlens, given,
+                 dx_stride=0):
+    """given: the caller's tensor for what the call writes (None: the call makes it, and
+    clears its rows of tokens outside every sequence)."""
     if x.dim() != 3:
         raise ValueError(f"x has {x.dim()} dimensions, expected (batch, seqlen, channels)")
     dev, C, splits, act = _conv_checked(what, x, weight, bias, splits, activation)
@@ -607,7 +611,7 @@ def _conv_prompt(what, x, weight, bias, splits, activation, initial_states, cu_s
     sshape = (nseq if nseq > 0 else b, weight.shape[1] - 1, C)
     _need(initial_states, "initial_states", x.dtype, sshape, dev)
     prob = _conv_problem(b, T, nseq, *splits, weight.shape[1], _row_stride(x, "x", 2), dx_stride,
-                         _DT[x.dtype], act)
+                         _DT[x.dtype], act, int(nseq > 0 and given is None))
     return dev, b, T, C, splits, sshape, prob
 
 
@@ -639,9 +643,11 @@ def conv_fwd(x, weight, bias=None, splits=None, initial_states=None, cu_seqlens=
     splits[i]) tensors, which viewed as (b, T, heads, headdim) and (b, T,
     groups, dstate) are ssd_fwd's inputs, and the states (nstates, K - 1, C)
     that conv_step and a later call's initial_states take (None without
-    return_final_states)."""
+    return_final_states).  Rows of tokens outside every sequence (before cu_seqlens'
+    first entry, from its last on) keep what they held in the caller's `outs`, and are
+    zeros in outputs that the call makes."""
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_fwd", x, weight, bias, splits,
-                                                      activation, initial_states, cu_seqlens)
+                                                      activation, initial_states, cu_seqlens, outs)
     outs = _conv_outs(outs, splits, (b, T), x, "outs")
     if final_states is not None:
         _need(final_states, "final_states", x.dtype, sshape, dev)
@@ -660,9 +666,9 @@ def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_s
     outputs (ssd_bwd's x, B and C gradients).  Returns a dict with x, weight,
     bias (None without a bias), initial_states (None without one) and the
     workspace.  dx: where x's gradient goes, a (b, T, C) tensor that may be a
-    slice of a wider one (the gradient of the projection's output).  Its rows of
-    tokens outside every sequence are not written: pass a zeroed dx where
-    cu_seqlens does not run from 0 to T."""
+    slice of a wider one (the gradient of the projection's output).  Rows of tokens
+    outside every sequence keep what they held in the caller's dx, and are zeros in
+    one that the call makes."""
     stride = 0
     if dx is not None:
         _on_gpu(dx, "dx", "conv_bwd")
@@ -670,7 +676,8 @@ def conv_bwd(x, weight, douts, bias=None, splits=None, initial_states=None, cu_s
             raise ValueError("dx must be like x")
         stride = _row_stride(dx, "dx", 2)
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_bwd", x, weight, bias, splits,
-                                                      activation, initial_states, cu_seqlens, stride)
+                                                      activation, initial_states, cu_seqlens, dx,
+                                                      stride)
     if douts is None:
         raise ValueError("douts are three tensors")
     douts = _conv_outs(douts, splits, (b, T), x, "douts")
@@ -711,7 +718,7 @@ def conv_step(x, conv_states, weight, bias=None, splits=None, slots=None, activa
         outs = [torch.zeros((b, n), dtype=x.dtype, device=dev) for n in splits]
     else:
         outs = _conv_outs(outs, splits, (b,), x, "outs")
-    prob = _conv_problem(b, 1, 0, *splits, K, _row_stride(x, "x", 1), 0, _DT[x.dtype], act)
+    prob = _conv_problem(b, 1, 0, *splits, K, _row_stride(x, "x", 1), 0, _DT[x.dtype], act, 0)
     _launch(dev, load_library().ssd_conv_step, prob[1], x.data_ptr(), weight.data_ptr(),
             _addr(bias), conv_states.data_ptr(), nslots, _addr(slots), _addr(outs[0]),
             _addr(outs[1]), _addr(outs[2]))

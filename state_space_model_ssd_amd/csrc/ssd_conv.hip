@@ -195,6 +195,23 @@ __device__ void conv_final_rows(const ConvArgs& a, int64_t i) {
   q.store(static_cast<T*>(a.final_states) + ((int64_t)s * (K - 1) + r) * a.C + c);
 }
 
+// Zeros in the rows of tokens outside every sequence (before the first entry of
+// cu_seqlens and from its last on): vectors i, i + step, ... of n channels of rows `stride`
+// apart.
+template <typename T, int V>
+__device__ void conv_clear_rows(const ConvArgs& a, T* out, int n, int64_t stride, int64_t i,
+                                int64_t step) {
+  const int lo = clamp_cu(a.cu, 0, a.total), hi = max(lo, clamp_cu(a.cu, a.nstates, a.total));
+  const int nvec = (n + V - 1) / V;
+  const int64_t items = (int64_t)(lo + a.total - hi) * nvec;
+  Vec<T, V> zero;
+  zero.clear();
+  for (; i < items; i += step) {
+    const int64_t r = i / nvec;
+    zero.store(out + (r < lo ? r : r - lo + hi) * stride + conv_vec<V>((int)(i - r * nvec), n));
+  }
+}
+
 // One run of TT tokens from t0 on.  EDGE: its rows may lie before the sequence
 // or the run may end early; the inner runs have neither test.
 template <typename T, int V, int K, int TT, bool SILU, bool EDGE>
@@ -247,12 +264,25 @@ __device__ __forceinline__ void conv_fwd_run(const ConvArgs& a, const ConvTile& 
   }
 }
 
+// Workgroups after the nct * nparts of the convolution: nside for the final states,
+// the rest for the rows to clear.
 template <typename T, int V, int K, int TT, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs a, int nct,
-                                                                int nslots, int nparts) {
+                                                                int nslots, int nparts, int nside) {
   constexpr int WT = TT * kConvWaves;
   if ((int)blockIdx.x >= nct * nparts) {
-    conv_final_rows<T, V, K>(a, (int64_t)((int)blockIdx.x - nct * nparts) * kConvThreads + threadIdx.x);
+    const int side = (int)blockIdx.x - nct * nparts;
+    if (side < nside) {
+      conv_final_rows<T, V, K>(a, (int64_t)side * kConvThreads + threadIdx.x);
+    } else {
+      const int64_t i = (int64_t)(side - nside) * kConvThreads + threadIdx.x;
+      const int64_t step = (int64_t)((int)gridDim.x - nct * nparts - nside) * kConvThreads;
+#pragma unroll 1
+      for (int o = 0; o < 3; ++o) {
+        const int n = o == 0 ? a.n[0] : o == 1 ? a.n[1] : a.n[2];
+        if (n > 0) conv_clear_rows<T, V>(a, conv_pick<T>(a.out, o), n, n, i, step);
+      }
+    }
     return;
   }
   const int wv = wave_id();
@@ -476,11 +506,18 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, const ConvTile& 
 // the 8 us that a packed batch of 6349 tokens x 160 channels takes).
 template <typename T, int V, int K, int STEPS, int GR, bool SILU, bool SEG>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvArgs a, int nct,
-                                                                int nslots, int nparts, int seg) {
+                                                                int nslots, int nparts, int seg,
+                                                                int nside) {
   constexpr int TT = STEPS - (K - 1), WT = TT * kConvWaves;
   __shared__ float red[kConvWaves][K + 1][64 * V];
   if ((int)blockIdx.x >= nct * nparts) {
-    conv_dinit_rows<T, V, K>(a, (int64_t)((int)blockIdx.x - nct * nparts) * kConvThreads + threadIdx.x);
+    const int side = (int)blockIdx.x - nct * nparts;
+    if (side < nside)
+      conv_dinit_rows<T, V, K>(a, (int64_t)side * kConvThreads + threadIdx.x);
+    else
+      conv_clear_rows<T, V>(a, static_cast<T*>(a.dx), a.C, a.din_stride,
+                            (int64_t)(side - nside) * kConvThreads + threadIdx.x,
+                            (int64_t)((int)gridDim.x - nct * nparts - nside) * kConvThreads);
     return;
   }
   const int lane = threadIdx.x & 63, wv = wave_id();
@@ -590,6 +627,13 @@ int conv_parts(int nslots, int nct, int64_t most) {
   return (int)(nslots < p ? nslots : (p > 0 ? p : 1));
 }
 
+// Workgroups for the rows to clear, which only the device can count: one per 16 tokens
+// up to one per CU, idle where there are none.
+int conv_clear_groups(const ConvArgs& a) {
+  if (!a.clear || !a.cu || a.total == 0) return 0;
+  return a.total < 16 * 256 ? (a.total + 15) / 16 : 256;
+}
+
 // Tiles of a workgroup whose terms of dw and db one register adds before they go to
 // the partial row: 256 tokens' worth, and the square root of the tokens a wave has
 // where that is more, so that a term passes at most about 256 + tokens / 256 or
@@ -609,10 +653,12 @@ hipError_t conv_fwd_go(const ConvArgs& a, hipStream_t s) {
   const int nslots = conv_slots(a, TT * kConvWaves);
   const int nparts = a.total > 0 ? conv_parts(nslots, nct, kConvMaxGroups) : 0;
   const int64_t fin = a.final_states ? (int64_t)a.nstates * (K - 1) * ((a.C + V - 1) / V) : 0;
-  const int64_t grid = (int64_t)nct * nparts + (fin + kConvThreads - 1) / kConvThreads;
+  const int64_t nside = (fin + kConvThreads - 1) / kConvThreads;
+  const int64_t grid = (int64_t)nct * nparts + nside + conv_clear_groups(a);
   if (grid == 0) return hipSuccess;
   auto fn = a.silu ? &conv_fwd_kernel<T, V, K, TT, true> : &conv_fwd_kernel<T, V, K, TT, false>;
-  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts);
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts,
+                     (int)nside);
   return hipGetLastError();
 }
 
@@ -622,7 +668,8 @@ hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
   const int nslots = conv_slots(a, (STEPS - (K - 1)) * kConvWaves);
   const int nparts = a.total > 0 ? conv_parts(nslots, 1, kConvBwdMaxParts) : 0;
   const int64_t ini = a.dinit ? (int64_t)a.nstates * ((a.C + 2) / V + 3) : 0;
-  const int64_t grid = (int64_t)nct * nparts + (ini + kConvThreads - 1) / kConvThreads;
+  const int64_t nside = (ini + kConvThreads - 1) / kConvThreads;
+  const int64_t grid = (int64_t)nct * nparts + nside + conv_clear_groups(a);
   const int seg = conv_segment(nslots, nparts, STEPS - (K - 1));
   const bool many = (int64_t)seg * nparts < nslots;
   auto fn = many ? (a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true, true>
@@ -630,7 +677,8 @@ hipError_t conv_bwd_go(const ConvArgs& a, hipStream_t s) {
                  : (a.silu ? &conv_bwd_kernel<T, V, K, STEPS, 8, true, false>
                            : &conv_bwd_kernel<T, V, K, STEPS, 8, false, false>);
   if (grid > 0)
-    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts, seg);
+    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nct, nslots, nparts, seg,
+                       (int)nside);
   const int64_t cp = part_cols(a.C);
   return colsum(a.part, nparts, (K + 1) * cp, ConvGradOut{a.dw, a.dbias, a.C, (int)cp, K}, s);
 }

@@ -18,6 +18,7 @@ struct ConvArgs {
   int C;                  // their sum
   int64_t in_stride, din_stride;
   bool bf16, silu;
+  bool clear;             // rows outside every sequence become zeros
   const void* x;
   const float* w;
   const float* bias;      // nullable

@@ -32,6 +32,7 @@ ssd_status_t check_conv(const ssd_conv_problem_t* p) {
       p->channels_c < 0 || p->width < 1)
     return SSD_ERR_INVALID_ARG;
   if (!dtype_ok(p->dtype) || p->activation < 0 || p->activation > 1) return SSD_ERR_INVALID_ARG;
+  if (p->clear_outside < 0 || p->clear_outside > 1) return SSD_ERR_INVALID_ARG;
   if (p->nseq > 0 && p->batch != 1) return SSD_ERR_INVALID_ARG;
   if (p->width < 2 || p->width > 4) return SSD_ERR_UNSUPPORTED;
   const int64_t most = (int64_t)1 << 20;
@@ -62,6 +63,7 @@ ConvArgs conv_args(const ssd_conv_problem_t* p) {
   a.din_stride = p->din_stride ? p->din_stride : a.C;
   a.bf16 = p->dtype == SSD_BF16;
   a.silu = p->activation == 1;
+  a.clear = p->clear_outside == 1;
   a.batch = (int)p->batch;
   return a;
 }

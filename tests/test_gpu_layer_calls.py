@@ -1,5 +1,7 @@
 """Calls of the operators around the SSD that are easy to make by mistake, or that leave
 something out (GPU): refused, or answered as documented."""
+import ctypes
+
 import pytest
 import torch
 
@@ -18,3 +20,54 @@ def test_conv_backward_without_output_gradients_is_refused():
     x, w = conv_args()
     with pytest.raises(ValueError, match="douts"):
         binding.conv_bwd(x, w, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,splits,cu", [
+    (200, (24, 8, 8), [10, 90, 90, 170]),
+    (200, (33, 2, 5), [0, 120]),                    # behind the last sequence only
+    (9000, (1500, 20, 17), [4000, 4100, 8999]),     # long runs, rows that are not whole vectors
+    (70, (1, 0, 0), [70, 70, 70]),                  # no token lies in a sequence
+    (70, (40, 0, 0), [3, 3, 69]),
+])
+def test_conv_rows_outside_every_sequence_are_zeros_where_the_call_makes_them(T, splits, cu, dtype):
+    x, w = conv_args(T, sum(splits), dtype=dtype)
+    douts = [o.contiguous() for o in x.split(splits, -1)]
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kw = dict(splits=splits, cu_seqlens=cu)
+    lo, hi = int(cu[0]), int(cu[-1])
+    outs = [torch.full_like(o, 7.0) for o in douts]
+    dx = torch.full_like(x, 7.0)
+    *want, _ = binding.conv_fwd(x, w, outs=outs, **kw)
+    gwant = binding.conv_bwd(x, w, douts, dx=dx, **kw)
+    # memory that the next call's tensors are likely to be made from
+    stale = [torch.full_like(t, float("nan")) for t in (*douts, x, x, x) for _ in range(2)]
+    del stale
+    *got, _ = binding.conv_fwd(x, w, **kw)
+    stale = [torch.full_like(x, float("nan")) for _ in range(4)]
+    del stale
+    g = binding.conv_bwd(x, w, douts, **kw)
+    torch.cuda.synchronize()
+    for a, b in zip((*got, g["x"]), (*want, gwant["x"])):
+        assert torch.equal(a[:, lo:hi], b[:, lo:hi])
+        assert not a[:, :lo].any() and not a[:, hi:].any()
+        assert (b[:, :lo] == 7).all() and (b[:, hi:] == 7).all()
+    assert torch.equal(g["weight"], gwant["weight"])
+
+
+def test_conv_malformed_packing_with_rows_to_clear_stays_in_bounds():
+    """Entries are clamped to the tensor before a row is counted, so every row cleared is
+    one of the tensor's; guard rows around it keep what they held."""
+    wide = torch.full((1, 154, 16), 3.0, device="cuda")
+    w = torch.randn((16, 4), device="cuda")
+    x = wide[:, 2:152]
+    p = binding.ConvProblemC(1, 150, 1, 16, 0, 0, 4, 0, 0, binding.SSD_F32, 1, 1)
+    out = torch.full((154, 16), 5.0, device="cuda")
+    for bad in ([100, 50], [-5, 10 ** 9], [150, 0], [2 ** 31 - 1, -2 ** 31], [-9, -3]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        code = binding.load_library().ssd_conv_fwd(
+            ctypes.byref(p), x.data_ptr(), w.data_ptr(), None, None, cu.data_ptr(),
+            out[2:].data_ptr(), None, None, None, torch.cuda.current_stream().cuda_stream)
+        assert code == binding.SSD_OK
+        torch.cuda.synchronize()
+        assert (out[:2] == 5).all() and (out[152:] == 5).all()
