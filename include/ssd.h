@@ -449,8 +449,11 @@ ssd_status_t ssd_fwd_noalloc(const ssd_problem_t* p,
  * belong to no sequence, and their rows of the outputs keep what they held, or
  * with clear_outside become zeros.
  * Malformed cu_seqlens give unspecified outputs but never an access outside
- * the given buffers.  No pointer may alias another.  Errors as for ssd_fwd;
- * width outside 2..4 is SSD_ERR_UNSUPPORTED.
+ * the given buffers.  No buffer that a call writes may share memory with another
+ * of its buffers (SSD_ERR_INVALID_ARG; final_states are not updated in place),
+ * but strided rows may lie beside other rows of the same stride, as columns of one
+ * wider tensor.  Errors as for ssd_fwd; width outside 2..4 is
+ * SSD_ERR_UNSUPPORTED.
  */
 typedef struct {
   int64_t batch;       /* rows; must be 1 for a packed batch               */
@@ -544,7 +547,8 @@ ssd_status_t ssd_conv_step(const ssd_conv_problem_t* p, const void* xbc, const f
  * Any headdim, and any dstate up to 256 (else SSD_ERR_UNSUPPORTED): the
  * compiled chunk configurations do not matter here.  The state is held and
  * updated in fp32; out is rounded once.  No workspace; `states` is the only
- * buffer that is both read and written, and no pointer may alias another.
+ * buffer that is both read and written, and neither it nor out may share memory
+ * with another buffer (SSD_ERR_INVALID_ARG).
  */
 typedef struct {
   int64_t batch;      /* rows; >= 0                                         */
@@ -585,8 +589,8 @@ ssd_status_t ssd_step(const ssd_step_problem_t* p, const void* x, const void* dt
  *   its rounding to residual_dtype.
  * Any channel count up to 8192.  Accumulation in fp32, one rounding of each
  * output.  residual_out may be residual, and out may be x (each element is
- * read before it is written, by the same thread); else no pointer may alias
- * another.  Errors as for ssd_fwd.
+ * read before it is written, by the same thread); else no buffer that is written
+ * may share memory with another (SSD_ERR_INVALID_ARG).  Errors as for ssd_fwd.
  */
 typedef struct {
   int64_t tokens;          /* rows                                          */

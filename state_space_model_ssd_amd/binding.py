@@ -485,7 +485,9 @@ def ssd_fwd_gated(x, dt, A, B, C, chunk_size, z, norm_weight, group_size, eps=1e
 # The operators around the scan: short convolution, single-token step, block
 # norms.  A decoding step is a few microseconds of GPU time, so these calls
 # keep the host's part small: problem structs and workspace sizes are made
-# once per set of sizes, and pointers go to ctypes as plain integers.
+# once per set of sizes, and pointers go to ctypes as plain integers.  A tensor
+# that a call writes may not share memory with another of its tensors, except
+# where a call says so: the library refuses it.
 # ---------------------------------------------------------------------------
 _DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 

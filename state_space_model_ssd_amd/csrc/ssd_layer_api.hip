@@ -4,6 +4,7 @@
 
 #include "ssd.h"
 #include "ssd_layer.h"
+#include "ssd_span.h"
 
 namespace ssd {
 namespace {
@@ -127,6 +128,26 @@ BlockNormArgs block_norm_args(const ssd_block_norm_problem_t* p) {
   return a;
 }
 
+size_t elem_size(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+
+// The buffers of a convolution call.
+struct ConvSpans {
+  uint64_t e, C, K, tokens;
+  const ssd_conv_problem_t* p;
+  explicit ConvSpans(const ssd_conv_problem_t* q, const ConvArgs& a)
+      : e(elem_size(q->dtype)), C((uint64_t)a.C), K((uint64_t)a.K), tokens((uint64_t)a.total), p(q) {}
+  Span xbc(const void* x, int64_t stride) const {
+    return rows_of(x, (int64_t)tokens, (int64_t)C, stride, e);
+  }
+  Span part(const void* o, int64_t channels) const {
+    return bytes_of(o, tokens * (uint64_t)channels * e);
+  }
+  Span weight(const void* w) const { return bytes_of(w, C * K * 4); }
+  Span bias(const void* b) const { return bytes_of(b, C * 4); }
+  Span states(const void* s, int64_t n) const { return bytes_of(s, (uint64_t)n * (K - 1) * C * e); }
+  Span packing(const void* cu) const { return bytes_of(cu, (uint64_t)(p->nseq + 1) * 4); }
+};
+
 ssd_status_t status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
 }  // namespace
@@ -146,6 +167,12 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_problem_t* p, const void* xbc, const fl
     return SSD_ERR_INVALID_ARG;
   if (!ssd::aligned_to(xbc, p->dtype) || !ssd::aligned_to(initial_states, p->dtype) ||
       !ssd::aligned_to(final_states, p->dtype))
+    return SSD_ERR_INVALID_ARG;
+  const ssd::ConvSpans m(p, a);
+  if (ssd::aliased({m.part(out_x, p->channels_x), m.part(out_b, p->channels_b),
+                    m.part(out_c, p->channels_c), m.states(final_states, a.nstates)},
+                   {m.xbc(xbc, a.in_stride), m.weight(weight), m.bias(bias),
+                    m.states(initial_states, a.nstates), m.packing(cu_seqlens)}))
     return SSD_ERR_INVALID_ARG;
   a.x = xbc; a.w = weight; a.bias = bias; a.init = initial_states; a.cu = cu_seqlens;
   a.out[0] = out_x; a.out[1] = out_b; a.out[2] = out_c;
@@ -181,6 +208,15 @@ ssd_status_t ssd_conv_bwd(const ssd_conv_problem_t* p, const void* xbc, const fl
   if (dinitial_states && !weight) return SSD_ERR_INVALID_ARG;
   if (!ssd::workspace_ok(workspace, workspace_bytes, ssd_conv_bwd_workspace_size(p)))
     return SSD_ERR_WORKSPACE;
+  const ssd::ConvSpans m(p, a);
+  if (ssd::aliased({m.xbc(dxbc, a.din_stride), m.weight(dweight), m.bias(dbias),
+                    m.states(dinitial_states, a.nstates),
+                    ssd::bytes_of(workspace, ssd_conv_bwd_workspace_size(p))},
+                   {m.xbc(xbc, a.in_stride), m.weight(weight), m.bias(bias),
+                    m.states(initial_states, a.nstates), m.packing(cu_seqlens),
+                    m.part(dout_x, p->channels_x), m.part(dout_b, p->channels_b),
+                    m.part(dout_c, p->channels_c), m.states(dfinal_states, a.nstates)}))
+    return SSD_ERR_INVALID_ARG;
   a.x = xbc; a.w = weight; a.bias = bias; a.init = initial_states; a.cu = cu_seqlens;
   a.dout[0] = dout_x; a.dout[1] = dout_b; a.dout[2] = dout_c;
   a.dfinal = dfinal_states;
@@ -203,6 +239,12 @@ ssd_status_t ssd_conv_step(const ssd_conv_problem_t* p, const void* xbc, const f
                       (nslots > 0 && !conv_states)))
     return SSD_ERR_INVALID_ARG;
   if (!ssd::aligned_to(xbc, p->dtype) || !ssd::aligned_to(conv_states, p->dtype))
+    return SSD_ERR_INVALID_ARG;
+  const ssd::ConvSpans m(p, a);
+  if (ssd::aliased({m.states(conv_states, nslots), m.part(out_x, p->channels_x),
+                    m.part(out_b, p->channels_b), m.part(out_c, p->channels_c)},
+                   {m.xbc(xbc, a.in_stride), m.weight(weight), m.bias(bias),
+                    ssd::bytes_of(slots, (uint64_t)p->batch * 4)}))
     return SSD_ERR_INVALID_ARG;
   a.x = xbc; a.w = weight; a.bias = bias;
   a.states = conv_states; a.nslots = nslots; a.slots = slots;
@@ -234,6 +276,17 @@ ssd_status_t ssd_step(const ssd_step_problem_t* p, const void* x, const void* dt
   a.bf16 = p->dtype == SSD_BF16;
   a.dt_bf16 = p->dt_dtype == SSD_BF16;
   a.dt_min = p->dt_min; a.dt_max = p->dt_max;
+  const int64_t HP = p->nheads * p->headdim, GN = p->ngroups * p->dstate;
+  const uint64_t e = ssd::elem_size(p->dtype), H4 = (uint64_t)p->nheads * 4;
+  if (ssd::aliased({ssd::bytes_of(states, ssd::capped(p->nslots, HP * p->dstate * 4)),
+                    ssd::bytes_of(out, (uint64_t)p->batch * HP * e)},
+                   {ssd::rows_of(x, p->batch, HP, a.x_stride, e),
+                    ssd::rows_of(dt, p->batch, p->nheads, a.dt_stride, ssd::elem_size(p->dt_dtype)),
+                    ssd::rows_of(B, p->batch, GN, a.b_stride, e),
+                    ssd::rows_of(C, p->batch, GN, a.c_stride, e), ssd::bytes_of(dt_bias, H4),
+                    ssd::bytes_of(A, H4), ssd::bytes_of(D, H4),
+                    ssd::bytes_of(slots, (uint64_t)p->batch * 4)}))
+    return SSD_ERR_INVALID_ARG;
   a.x = x; a.dt = dt; a.dt_bias = dt_bias; a.A = A; a.B = B; a.C = C; a.D = D;
   a.states = states; a.slots = slots; a.out = out;
   return ssd::status_of(ssd::launch_step(a, static_cast<hipStream_t>(stream)));
@@ -250,6 +303,20 @@ ssd_status_t ssd_block_norm_fwd(const ssd_block_norm_problem_t* p, const void* x
   if (!ssd::aligned_to(x, p->dtype) || !ssd::aligned_to(gate, p->dtype) ||
       !ssd::aligned_to(out, p->dtype) || !ssd::aligned_to(residual, p->residual_dtype) ||
       !ssd::aligned_to(residual_out, p->residual_dtype))
+    return SSD_ERR_INVALID_ARG;
+  const uint64_t n = (uint64_t)(p->tokens * p->channels), c4 = (uint64_t)p->channels * 4;
+  const uint64_t xb = n * ssd::elem_size(p->dtype), rb = n * ssd::elem_size(p->residual_dtype);
+  // in place: the elements of out may be x's, those of residual_out residual's
+  if (ssd::aliased({ssd::bytes_of(out, xb), ssd::bytes_of(residual_out, rb)},
+                   {ssd::bytes_of(gate, xb), ssd::bytes_of(post_weight, c4),
+                    ssd::bytes_of(scale, c4), ssd::bytes_of(pre_weight, c4)}) ||
+      (out != x && ssd::overlap(ssd::bytes_of(out, xb), ssd::bytes_of(x, xb))) ||
+      (residual_out != residual &&
+       ssd::overlap(ssd::bytes_of(residual_out, rb), ssd::bytes_of(residual, rb))) ||
+      ((residual != x || rb != xb) &&
+       ssd::overlap(ssd::bytes_of(out, xb), ssd::bytes_of(residual, rb))) ||
+      ((residual != x || rb != xb) &&
+       ssd::overlap(ssd::bytes_of(residual_out, rb), ssd::bytes_of(x, xb))))
     return SSD_ERR_INVALID_ARG;
   ssd::BlockNormArgs a = ssd::block_norm_args(p);
   a.x = x; a.residual = residual; a.gate = gate;
@@ -285,6 +352,17 @@ ssd_status_t ssd_block_norm_bwd(const ssd_block_norm_problem_t* p, const void* x
     return SSD_ERR_INVALID_ARG;
   if (!ssd::workspace_ok(workspace, workspace_bytes, ssd_block_norm_bwd_workspace_size(p)))
     return SSD_ERR_WORKSPACE;
+  const uint64_t n = (uint64_t)(p->tokens * p->channels), c4 = (uint64_t)p->channels * 4;
+  const uint64_t xb = n * ssd::elem_size(p->dtype), rb = n * ssd::elem_size(p->residual_dtype);
+  if (ssd::aliased({ssd::bytes_of(dx, xb), ssd::bytes_of(dresidual, rb), ssd::bytes_of(dgate, xb),
+                    ssd::bytes_of(dpost_weight, c4), ssd::bytes_of(dscale, c4),
+                    ssd::bytes_of(dpre_weight, c4),
+                    ssd::bytes_of(workspace, ssd_block_norm_bwd_workspace_size(p))},
+                   {ssd::bytes_of(x, xb), ssd::bytes_of(residual, rb), ssd::bytes_of(gate, xb),
+                    ssd::bytes_of(post_weight, c4), ssd::bytes_of(scale, c4),
+                    ssd::bytes_of(pre_weight, c4), ssd::bytes_of(dout, xb),
+                    ssd::bytes_of(dresidual_out, rb)}))
+    return SSD_ERR_INVALID_ARG;
   ssd::BlockNormArgs a = ssd::block_norm_args(p);
   a.x = x; a.residual = residual; a.gate = gate;
   a.post_w = post_weight; a.scale = scale; a.pre_w = pre_weight;

@@ -71,3 +71,49 @@ def test_conv_malformed_packing_with_rows_to_clear_stays_in_bounds():
         assert code == binding.SSD_OK
         torch.cuda.synchronize()
         assert (out[:2] == 5).all() and (out[152:] == 5).all()
+
+
+def test_shared_memory_is_refused():
+    """Calls that would read what they write: in place where nothing says so."""
+    x, w = conv_args(b=2)
+    st = torch.zeros((2, 3, 24), device="cuda")
+    steps = x[:, 0].contiguous()
+    h, n = x.clone(), torch.ones(24, device="cuda")
+    heads = steps.view(2, 3, 8)
+    states = torch.zeros((2, 3, 8, 8), device="cuda")
+    v = torch.ones(3, device="cuda")
+    for call in (lambda: binding.conv_fwd(x, w, initial_states=st, final_states=st),
+                 lambda: binding.conv_fwd(x, w, outs=[x, None, None]),
+                 lambda: binding.conv_bwd(x, w, [h, None, None], dx=h),
+                 lambda: binding.conv_bwd(x, w, [h, None, None], dx=x),
+                 lambda: binding.conv_step(steps, st, w, outs=[steps, None, None]),
+                 lambda: binding.ssd_step(heads, steps[:, :3], v, heads[:, :1], heads[:, 1:2], states,
+                                          out=heads),
+                 lambda: binding.block_norm_fwd(x, h, n, out=h),
+                 lambda: binding.block_norm_fwd(x, h, n, residual_out=x),
+                 lambda: binding.block_norm_fwd(x, x, n, out=x, residual_out=x)):
+        with pytest.raises(binding.SsdError) as e:
+            call()
+        assert e.value.code == binding.SSD_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert not st.any() and not states.any()
+
+
+def test_columns_of_one_tensor_are_taken():
+    """x and its gradient as columns of one wider tensor; a stream that is also the
+    block's output, normed in place."""
+    x, w = conv_args(T=130, b=2)
+    dout = torch.randn_like(x)
+    want = binding.conv_bwd(x, w, [dout, None, None])
+    wide = torch.full((2, 130, 60), 3.0, device="cuda")
+    wide[..., 2:26] = x
+    g = binding.conv_bwd(wide[..., 2:26], w, [dout, None, None], dx=wide[..., 30:54])
+    n = torch.rand(24, device="cuda")
+    o1, h1 = binding.block_norm_fwd(x, x, n)
+    y = x.clone()
+    o2, h2 = binding.block_norm_fwd(y, y, n, out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[..., 30:54], want["x"]) and torch.equal(g["weight"], want["weight"])
+    assert torch.equal(wide[..., 2:26], x)
+    assert all((wide[..., s] == 3).all() for s in (slice(0, 2), slice(26, 30), slice(54, 60)))
+    assert torch.equal(o1, y) and torch.equal(h1, h2)
