@@ -73,7 +73,8 @@ typedef enum {
   SSD_OK = 0,
   SSD_ERR_INVALID_ARG = 1,  /* a size, pointer or combination is invalid   */
   SSD_ERR_UNSUPPORTED = 2,  /* valid, but (dtype, headdim, dstate, chunk)  */
-                            /* has no compiled kernel                      */
+                            /* has no compiled kernel, or a size is beyond */
+                            /* the limits stated at its problem struct     */
   SSD_ERR_WORKSPACE = 3,    /* workspace NULL or smaller than required     */
   SSD_ERR_HIP = 4,          /* a HIP launch or device query failed         */
   SSD_ERR_TOO_LARGE = 5     /* ssd_fwd_noalloc: the problem's workspace is */
@@ -442,7 +443,11 @@ ssd_status_t ssd_fwd_noalloc(const ssd_problem_t* p,
  *   initial_states, final_states  [nstates][K-1][C] dtype (nullable)
  *   out_x, out_b, out_c  [batch][seqlen][channels_*] dtype, each contiguous:
  *            ssd_fwd's x, B and C.  An output with no channels may be NULL.
- * Any channel counts and any alignment of the dtype's size are taken.
+ * Any channel counts and any alignment of the dtype's size are taken, within
+ * these limits (beyond them SSD_ERR_UNSUPPORTED): width 2 to 4, C up to 2^20,
+ * sequences (batch, or nseq) up to 65535, tokens (batch * seqlen) up to 2^30,
+ * tokens * C up to 2^40, sequences * C up to 2^30, slots (ssd_conv_step) below
+ * 2^31.  Strides of up to 2^31 elements (else SSD_ERR_INVALID_ARG).
  * Accumulation in fp32, one rounding of each output to the dtype; final
  * states are copies.  A packed batch (nseq > 0, batch 1) takes cu_seqlens
  * (non-decreasing); tokens before its first entry and from its last entry on
@@ -452,13 +457,13 @@ ssd_status_t ssd_fwd_noalloc(const ssd_problem_t* p,
  * the given buffers.  No buffer that a call writes may share memory with another
  * of its buffers (SSD_ERR_INVALID_ARG; final_states are not updated in place),
  * but strided rows may lie beside other rows of the same stride, as columns of one
- * wider tensor.  Errors as for ssd_fwd; width outside 2..4 is
- * SSD_ERR_UNSUPPORTED.
+ * wider tensor.  Errors as for ssd_fwd.
  */
 typedef struct {
-  int64_t batch;       /* rows; must be 1 for a packed batch               */
+  int64_t batch;       /* rows, up to 65535; 1 for a packed batch           */
   int64_t seqlen;      /* tokens per row (packed batch: total tokens); >= 0 */
-  int64_t nseq;        /* 0: rows are the sequences; > 0: packed batch      */
+  int64_t nseq;        /* 0: rows are the sequences; > 0: packed batch, up  */
+                       /* to 65535 sequences                                */
   int64_t channels_x;  /* nheads * headdim of the SSD that follows; >= 1    */
   int64_t channels_b;  /* ngroups * dstate; >= 0                            */
   int64_t channels_c;  /* ngroups * dstate; >= 0                            */
@@ -544,16 +549,22 @@ ssd_status_t ssd_conv_step(const ssd_conv_problem_t* p, const void* xbc, const f
  *   slots   [batch] int32 (nullable: row b has slot b, nslots >= batch);
  *           padding and repeated slots as for ssd_conv_step
  *   out     [batch][nheads][headdim] dtype, contiguous
- * Any headdim, and any dstate up to 256 (else SSD_ERR_UNSUPPORTED): the
- * compiled chunk configurations do not matter here.  The state is held and
+ * Any headdim and dstate within these limits (beyond them
+ * SSD_ERR_UNSUPPORTED), whatever chunk configurations are compiled: dstate up
+ * to 256; batch, nheads and headdim up to 65535 each; nslots below 2^31; and
+ * batch * nheads * ceil(headdim / r) up to 2^23 with r = 256 / l, l the least
+ * power of two of lanes that hold a row of dstate values, four (dstate below
+ * four: one) each.  At dstate 128 r is 8, and the last limit 2^26 rows of
+ * states, 32 GiB: larger batches take several calls.  Strides as for the
+ * convolution.  The state is held and
  * updated in fp32; out is rounded once.  No workspace; `states` is the only
  * buffer that is both read and written, and neither it nor out may share memory
  * with another buffer (SSD_ERR_INVALID_ARG).
  */
 typedef struct {
-  int64_t batch;      /* rows; >= 0                                         */
-  int64_t nheads;     /* H >= 1                                             */
-  int64_t headdim;    /* P >= 1                                             */
+  int64_t batch;      /* rows, 0 to 65535                                   */
+  int64_t nheads;     /* H, 1 to 65535                                      */
+  int64_t headdim;    /* P, 1 to 65535                                      */
   int64_t dstate;     /* N, 1 to 256                                        */
   int64_t ngroups;    /* G >= 1, H % G == 0                                 */
   int64_t nslots;     /* states in the cache                                */
@@ -587,8 +598,8 @@ ssd_status_t ssd_step(const ssd_step_problem_t* p, const void* x, const void* dt
  *   shape in residual_dtype (the dtype or fp32);  weights [channels] fp32.
  *   residual_out receives h (nullable).  h is normalised as summed, before
  *   its rounding to residual_dtype.
- * Any channel count up to 8192.  Accumulation in fp32, one rounding of each
- * output.  residual_out may be residual, and out may be x (each element is
+ * Any channel count up to 8192 and up to 2^40 elements (beyond:
+ * SSD_ERR_UNSUPPORTED).  Accumulation in fp32, one rounding of each output.  residual_out may be residual, and out may be x (each element is
  * read before it is written, by the same thread); else no buffer that is written
  * may share memory with another (SSD_ERR_INVALID_ARG).  Errors as for ssd_fwd.
  */
