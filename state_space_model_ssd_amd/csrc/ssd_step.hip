@@ -17,6 +17,7 @@
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
 #include "ssd_rowsum.h"
+#include "ssd_step_rule.h"
 
 // Multiply-adds are fused only inside one expression, so every variant of a kernel
 // rounds a value alike.
@@ -83,14 +84,6 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const StepArgs a, in
   }
 }
 
-// Lanes per row: N's accesses rounded up to a power of two, at most a wave.
-int step_lpr(int N) {
-  const int V = N >= 4 ? 4 : 1;
-  int l = 1;
-  while (l * V < N) l *= 2;
-  return l;
-}
-
 template <typename T, typename DT, int V, int R>
 hipError_t step_go(const StepArgs& a, int lpr, hipStream_t s) {
   // one wave where a head's rows fill no more
@@ -103,21 +96,15 @@ hipError_t step_go(const StepArgs& a, int lpr, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows per thread: more rows are more bytes in flight per wave and fewer
-// workgroups to start, fewer rows more waves.  Measured (us, R = 1 / 2 / 4; P 64,
-// N 128): one sequence of 24 heads 3.16 / 3.35 / 3.83, four 4.58 / 4.17 / 4.33, 32 18.0
-// / 12.6 / 11.3; 64 sequences of 32 heads 38.9 / 24.6 / 23.4; 256, whose states pass
-// the last-level cache, 156 / 103 / 106 (5.1 TB/s, a large copy's rate).  So four
-// rows from one workgroup per CU on, two from half a one, and two again for
-// states larger than the cache (256 MB).
 template <typename T, typename DT>
 hipError_t step_type(const StepArgs& a, hipStream_t s) {
   const int lpr = step_lpr(a.N);
   if (a.N < 4) return step_go<T, DT, 1, 1>(a, lpr, s);
-  const int64_t lanes = (int64_t)a.batch * a.H * a.P * lpr;
-  if (lanes < 2 * 128 * kStepThreads) return step_go<T, DT, 4, 1>(a, lpr, s);
-  if (lanes < 4 * 256 * kStepThreads || lanes >= 1 << 24) return step_go<T, DT, 4, 2>(a, lpr, s);
-  return step_go<T, DT, 4, 4>(a, lpr, s);
+  switch (step_rows(a.batch, a.H, a.P, a.N)) {
+    case 4: return step_go<T, DT, 4, 4>(a, lpr, s);
+    case 2: return step_go<T, DT, 4, 2>(a, lpr, s);
+  }
+  return step_go<T, DT, 4, 1>(a, lpr, s);
 }
 
 }  // namespace
