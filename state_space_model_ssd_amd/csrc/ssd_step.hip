@@ -13,7 +13,6 @@
 // starts early enough to end with the row: it overlaps the vector before it, in
 // the same wave, so both have loaded before either stores, store the same
 // values, and the sum takes the shared ones once.
-#include "ssd_device.h"
 #include "ssd_layer.h"
 #include "ssd_layer_device.h"
 #include "ssd_rowsum.h"
@@ -28,6 +27,13 @@ namespace ssd {
 namespace {
 
 constexpr int kStepThreads = 256;   // most threads of a workgroup
+
+// softplus and the clamp as the scan forms them (step_from_raw in ssd_device.h), but a
+// NaN stays one: fmaxf and fminf would take the clamp's bound for it.
+__device__ __forceinline__ float step_size(float u, float dt_min, float dt_max) {
+  const float sp = fmaxf(u, 0.f) + log1pf(expf(-fabsf(u)));
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(sp, dt_min), dt_max);
+}
 
 // V: values per access (4, or 1 for N < 4); R: rows per thread.
 template <typename T, typename DT, int V, int R>
@@ -57,7 +63,7 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const StepArgs a, in
   for (int r = 0; r < R; ++r) xv[r] = to_f32(x[min(p0 + r * rows, a.P - 1)]);
   const float u = to_f32(static_cast<const DT*>(a.dt)[b * a.dt_stride + h]) +
                   (a.dt_bias ? a.dt_bias[h] : 0.f);
-  const float delta = step_from_raw(u, a.dt_min, a.dt_max);
+  const float delta = step_size(u, a.dt_min, a.dt_max);
   const float decay = expf(delta * a.A[h]);
   const float D = a.D ? a.D[h] : 0.f;
   T* out = static_cast<T*>(a.out) + ((int64_t)b * a.H + h) * a.P;

@@ -117,3 +117,27 @@ def test_columns_of_one_tensor_are_taken():
     assert torch.equal(wide[..., 2:26], x)
     assert all((wide[..., s] == 3).all() for s in (slice(0, 2), slice(26, 30), slice(54, 60)))
     assert torch.equal(o1, y) and torch.equal(h1, h2)
+
+
+@pytest.mark.parametrize("N", [3, 16, 130])
+@pytest.mark.parametrize("where", ["dt", "dt_bias", "A"])
+def test_step_keeps_a_nan_it_is_given(where, N):
+    """A step size (or decay) of NaN makes its head's state and output NaN, as the formula
+    does, and no other's; it is not clamped to a number."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    b, H, P = 3, 4, 5
+    x, dt, B, C, A, bias, st = r(b, H, P), r(b, H), r(b, 2, N), r(b, 2, N), -r(H).abs(), r(H), r(b, H, P, N)
+    clean = st.clone()
+    want = binding.ssd_step(x, dt, A, B, C, clean, dt_bias=bias, dt_min=0.01, dt_max=1.0)
+    bad = torch.zeros((b, H), dtype=torch.bool, device="cuda")
+    if where == "dt":
+        dt[1, 2] = float("nan")
+        bad[1, 2] = True
+    else:
+        (bias if where == "dt_bias" else A)[2] = float("nan")
+        bad[:, 2] = True
+    out = binding.ssd_step(x, dt, A, B, C, st, dt_bias=bias, dt_min=0.01, dt_max=1.0)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[bad]).all() and torch.isnan(st[bad]).all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(st[~bad], clean[~bad])
