@@ -15,8 +15,14 @@
 // one before the next), and two backward, whose later sums are arranged to need
 // nothing that the second exchange computes.  Four channels per lane rather
 // than eight: fewer registers, more rows in flight (forward at 8192 x 768 with an
-// fp32 residual 23.5 -> 15.7 us, 5.6 TB/s; backward 82 -> 37 us, 3.7 TB/s with its
+// fp32 residual and a gate 23.5 -> 15.7 us, 5.6 TB/s; backward 82 -> 37 us, 3.8 TB/s with its
 // second launch).
+//
+// A row that does not fill its waves pays for the last one: backward at 5003 rows of
+// fp32 31.7 us for 1024 channels, 35.8 for 1028 (a fifth wave with one lane in use), 36.0
+// for 1025; in bf16 at 8192 rows 21.9 for 768, 26.7 for 772.  Channels that are no whole
+// vectors add the tail's loads one by one, each waited for: 35.9 for 771 (forward 9.7 / 13.1
+// / 17.2).  Where rows start costs little: 1024 one element off 30.8.
 //
 // The forward keeps the next row's loads in flight; the backward, with twice
 // the registers, gains nothing from that at 8192 x 768 (37.3 / 37.4 us with /
@@ -513,8 +519,8 @@ hipError_t bn_rows(const BlockNormArgs& a, hipStream_t s) {
 #undef SSD_BN
   }
   // wider rows: sixteen waves forward; backward eight with more vectors per
-  // lane, as 1024 threads leave too few registers (4096 x 4096 bf16: 208 us
-  // against 93; 2048 x 8192: 306 against 135)
+  // lane, as 1024 threads leave too few registers (bf16 with an fp32 stream, all
+  // parts: 4096 x 4096 208 us against 93, 2048 x 8192 306 against 135; today 92 and 118)
   constexpr int W = BWD ? 8 : 16;
   if (nw <= 16) return bn_go<BWD, T, R, W, 16 / W, TAIL>(a, s);
   return bn_go<BWD, T, R, W, 32 / W, TAIL>(a, s);

@@ -9,10 +9,12 @@
 // owns V neighbouring channels and a run of tokens, a wave 64 such vectors of one
 // run, and a workgroup four runs in a row.  The forward loads all rows of a run,
 // the K - 1 before it included, at once into registers; the backward a group of
-// rows ahead.  Each element is read from memory once; the rows that two runs
-// share come from the L1 and L2.  At 6144 channels x 32768 tokens of bf16 the
-// forward takes 150 us (5.4 TB/s, a large copy's rate), at 1792 x 8192 the backward
-// 24 us with its second launch (3.7 TB/s).
+// rows ahead.  The rows that two runs share come from the L1 and L2: the forward reads
+// each element from memory once (6144 channels x 32768 tokens of bf16: 403.6 MB for
+// 402.8, 150 us, 5.4 TB/s, a large copy's rate).  The backward, in column tiles of 256
+// bytes, reads 78.2 MB for 58.7 at 1792 x 8192 out of rows of 3352 channels, which start
+// anywhere in a 128-byte line: tiles share lines, and neighbouring tiles run on
+// different XCDs.  It takes 23.3 us with its second launch (3.8 TB/s).
 //
 // Runs never straddle a sequence: a workgroup's tokens are the overlap of one
 // WT-token tile of the token axis with one sequence.  Slot i of the grid is
@@ -374,11 +376,11 @@ __device__ void conv_dinit_rows(const ConvArgs& a, int64_t i) {
 // the K - 1 tokens after, in order, from a sliding window of K input rows; din
 // of a token is complete K - 1 tokens later.  The rows are loaded a group of GR
 // tokens ahead of their use, so that the loads of one group are in flight while
-// another is computed.  About 30 vector instructions and two transcendental ones
-// per element and step make this 12 of the 17 us that the bytes take at 1792
-// channels x 8192 tokens (bf16); two channels per thread keep it at three waves
-// per SIMD (four channels: 254 registers, 31 against 24 us).  EDGE as in the
-// forward; the gradient of the final state reaches edge runs only.
+// another is computed.  About 30 vector instructions and two transcendental ones (at a
+// quarter of the rate) per element and step are 12 + 3 us at 1792 channels x 8192 tokens
+// (bf16), where the bytes take 16.3; two channels per thread keep it at three waves per
+// SIMD (four channels: 254 registers, 31 against 24 us).  EDGE as in the forward; the
+// gradient of the final state reaches edge runs only.
 template <typename T, int V, int K, int STEPS, int GR, bool SILU, bool EDGE>
 __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, const ConvTile& t, int t0,
                                              const ConvCols& col, const float (&w)[K][V],
