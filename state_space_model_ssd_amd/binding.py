@@ -647,7 +647,8 @@ def conv_fwd(x, weight, bias=None, splits=None, initial_states=None, cu_seqlens=
     that conv_step and a later call's initial_states take (None without
     return_final_states).  Rows of tokens outside every sequence (before cu_seqlens'
     first entry, from its last on) keep what they held in the caller's `outs`, and are
-    zeros in outputs that the call makes."""
+    zeros in outputs that the call makes.  final_states may not be initial_states, nor
+    any output share memory with an input."""
     dev, b, T, C, splits, sshape, prob = _conv_prompt("conv_fwd", x, weight, bias, splits,
                                                       activation, initial_states, cu_seqlens, outs)
     outs = _conv_outs(outs, splits, (b, T), x, "outs")
