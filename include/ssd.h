@@ -649,6 +649,178 @@ ssd_status_t ssd_block_norm_bwd(const ssd_block_norm_problem_t* p, const void* x
                                 float* dpre_weight, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/*
+ * The gated delta rule: the layer of a gated delta network, which hybrid models
+ * mix with Mamba-2 and attention layers (clova.ai page, "Why optimize Mamba-2?",
+ * names it; the formula is read here as the published gated delta rule).  For each
+ * sequence s, head h (q/k group i = h / (nheads / ngroups)) and token t, with the
+ * state S of headdim x dstate:
+ *
+ *   a   = exp(g[t,h])
+ *   w   = beta[t,h] * (v[t,h,:] - a * S_{t-1} k[t,i,:])
+ *   S_t = a * S_{t-1} + w (outer) k[t,i,:]
+ *   out[t,h,:] = scale * S_t q[t,i,:]
+ *   S_{-1} = initial_states[s,h] (or 0);  final_states[s,h] = S after the last token.
+ *
+ * It is the SSD's recurrence with a state that first forgets what it holds at k;
+ * x, B, C of the SSD are v, k, q here.
+ *
+ *   q, k    [batch][seqlen][ngroups][dstate] dtype (as ssd_qk_norm_fwd leaves them)
+ *   v, out  [batch][seqlen][nheads][headdim] dtype
+ *   g       [batch][seqlen][nheads] gate_dtype: log decays, at most 0 as a rule; one
+ *           below -512 (also -inf) is one of -512, after which the state is zero
+ *   beta    [batch][seqlen][nheads] gate_dtype
+ *   initial_states, final_states [nstates][nheads][headdim][dstate] fp32 (nullable)
+ * all contiguous; q, k, v, out and their gradients 16-byte aligned.  Packed batches as
+ * for ssd_conv_fwd (cu_seqlens, clear_outside; malformed entries never leave the
+ * buffers).  The state is carried in fp32; with bf16 inputs whatever enters it does so
+ * to 2^-17 or better, while the output's own products round their operands to bf16
+ * once, as the output is.  A NaN or infinity in a token's inputs may reach the outputs
+ * of earlier tokens of the same 64 (they are computed together), and no others before it.
+ * Limits (beyond them SSD_ERR_UNSUPPORTED): dstate 32, 64 or 128; headdim a multiple of
+ * 16 up to 256; nheads up to 4096; batch and nseq up to 65535; seqlen and batch * seqlen
+ * up to 2^30; tokens * nheads up to 2^34; sequences * nheads up to 2^24.
+ * The workspace (no initial contents) is ssd_delta_fwd_workspace_size bytes, 256-byte
+ * aligned; calls that may overlap need one each.  No buffer that is written may share
+ * memory with another (SSD_ERR_INVALID_ARG).  Deterministic.  Errors as for ssd_fwd.
+ */
+typedef struct {
+  int64_t batch;       /* rows, up to 65535; 1 for a packed batch           */
+  int64_t seqlen;      /* tokens per row (packed batch: total tokens); >= 0 */
+  int64_t nheads;      /* H, 1 to 4096                                      */
+  int64_t headdim;     /* P, 16 to 256 in steps of 16                       */
+  int64_t dstate;      /* N, 32, 64 or 128                                  */
+  int64_t ngroups;     /* G >= 1, H % G == 0: heads of q and k              */
+  int64_t nseq;        /* 0: rows are the sequences; > 0: packed batch      */
+  int32_t dtype;       /* ssd_dtype_t of q, k, v, out                       */
+  int32_t gate_dtype;  /* ssd_dtype_t of g, beta: fp32 or the dtype         */
+  float scale;         /* of the output; dstate^-0.5 as a rule              */
+  int32_t clear_outside; /* packed batch: 1 clears the rows of tokens outside */
+                       /* every sequence in what the call writes; 0 leaves them */
+} ssd_delta_problem_t;
+
+size_t ssd_delta_fwd_workspace_size(const ssd_delta_problem_t* p);
+
+ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta,
+                           const float* initial_states, const int32_t* cu_seqlens, void* out,
+                           float* final_states, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * The backward of ssd_delta_fwd: gradients of sum(out * dout) + sum(final_states *
+ * dfinal_states).  dq, dk, dv, dg, dbeta like q, k, v, g, beta (required);
+ * dinitial_states like initial_states (nullable: not computed, also given without an
+ * initial state); dfinal_states nullable: 0.  dq and dk sum over the heads of a group.
+ * The forward's states are computed again.  The gradient of the state is carried as the
+ * state is; with bf16 inputs the other products round their operands to bf16 once, so dg
+ * and dbeta are of that accuracy (some 3e-3 relative in the 2-norm) in fp32 too.
+ * Workspace: ssd_delta_bwd_workspace_size bytes, as for the forward.
+ */
+size_t ssd_delta_bwd_workspace_size(const ssd_delta_problem_t* p);
+
+ssd_status_t ssd_delta_bwd(const ssd_delta_problem_t* p, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta,
+                           const float* initial_states, const int32_t* cu_seqlens,
+                           const void* dout, const float* dfinal_states, void* dq, void* dk,
+                           void* dv, void* dg, void* dbeta, float* dinitial_states,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gated delta rule for one new token per sequence: the recurrence above, one update,
+ * in place on a cache of states (decoding after ssd_delta_fwd, whose final_states are the
+ * first states).  Slots, padding and repeated slots as for ssd_conv_step.
+ *
+ *   q, k    [batch][ngroups][dstate] dtype, rows q_stride and k_stride elements apart
+ *   v       [batch][nheads][headdim] dtype, rows v_stride apart
+ *   g, beta [batch][nheads] gate_dtype, rows g_stride and beta_stride apart
+ *           (a stride of 0 is a contiguous tensor's; rows may lie inside wider ones)
+ *   states  [nslots][nheads][headdim][dstate] fp32, updated in place
+ *   out     [batch][nheads][headdim] dtype, contiguous
+ * Any headdim and dstate within ssd_step's limits, which hold here too.  fp32
+ * arithmetic; out is rounded once.  No workspace; neither states nor out may share
+ * memory with another buffer (SSD_ERR_INVALID_ARG).
+ */
+typedef struct {
+  int64_t batch;      /* rows, 0 to 65535                                   */
+  int64_t nheads;     /* H, 1 to 65535                                      */
+  int64_t headdim;    /* P, 1 to 65535                                      */
+  int64_t dstate;     /* N, 1 to 256                                        */
+  int64_t ngroups;    /* G >= 1, H % G == 0                                 */
+  int64_t nslots;     /* states in the cache                                */
+  int64_t q_stride, k_stride, v_stride, g_stride, beta_stride; /* elements; 0: contiguous */
+  int32_t dtype;      /* ssd_dtype_t of q, k, v and out                     */
+  int32_t gate_dtype; /* ssd_dtype_t of g and beta: fp32 or the dtype       */
+  float scale;
+} ssd_delta_step_problem_t;
+
+ssd_status_t ssd_delta_step(const ssd_delta_step_problem_t* p, const void* q, const void* k,
+                            const void* v, const void* g, const void* beta, float* states,
+                            const int32_t* slots, void* out, void* stream);
+
+/*
+ * The norm of queries and keys in each head, and the rotation by the token's position, in
+ * one pass: what stands in front of the gated delta rule (norm 1, no rotation), of an
+ * attention layer of a hybrid model, or of an SSD whose B and C are normed and rotated.
+ * For every token t and head of `headdim` D channels, x being q or k:
+ *
+ *   n = x * r * weight,  r = 1 / sqrt(mean(x^2) + eps)   (norm 0)
+ *                          = 1 / sqrt(sum(x^2) + eps)    (norm 1)
+ *   the rotary_pairs R pairs (a, b) of n become (a cos - b sin, b cos + a sin) of the
+ *   angle positions[t] * inv_freq[i]; pair i is channels (i, i + R), or (2i, 2i + 1) with
+ *   `interleaved`; channels from 2R on stay.
+ *
+ *   q, k     [tokens][q_heads or k_heads][headdim] dtype, rows q_stride and k_stride
+ *            elements apart (0: contiguous), so they may lie inside the projection's rows
+ *   weights  [headdim] fp32, one for all heads of q and one for k's (nullable: 1)
+ *   positions [tokens] int32, inv_freq [rotary_pairs] fp32 (with rotary_pairs > 0)
+ *   q_out, k_out  contiguous, dtype
+ * Accumulation in fp32, one rounding of each output; angles are reduced in fp64, so a
+ * far position is as exact as a near one.  headdim up to 256, heads up to 4096 each,
+ * tokens up to 2^30 (beyond: SSD_ERR_UNSUPPORTED); any alignment of the dtype's size.
+ * No buffer that is written may share memory with another (SSD_ERR_INVALID_ARG), but
+ * strided rows may lie beside others of the same stride.  Errors as for ssd_fwd.
+ */
+typedef struct {
+  int64_t tokens;         /* rows                                           */
+  int64_t q_heads;        /* 1 to 4096                                      */
+  int64_t k_heads;
+  int64_t headdim;        /* D, 1 to 256                                    */
+  int64_t rotary_pairs;   /* R, 2 R <= D; 0: no rotation                    */
+  int64_t q_stride, k_stride;    /* elements between tokens; 0: contiguous  */
+  int64_t dq_stride, dk_stride;  /* the same of dq and dk (ssd_qk_norm_bwd) */
+  int32_t dtype;          /* ssd_dtype_t of q, k, the outputs and gradients */
+  int32_t norm;           /* 0: by the mean of squares, 1: by their sum     */
+  int32_t interleaved;    /* 0: pairs (i, i + R), 1: (2i, 2i + 1)           */
+  float eps;
+} ssd_qk_norm_problem_t;
+
+ssd_status_t ssd_qk_norm_fwd(const ssd_qk_norm_problem_t* p, const void* q, const void* k,
+                             const float* q_weight, const float* k_weight,
+                             const int32_t* positions, const float* inv_freq, void* q_out,
+                             void* k_out, void* stream);
+
+/*
+ * The backward of ssd_qk_norm_fwd: gradients of sum(q_out * dq_out) + sum(k_out * dk_out).
+ * With d the output's gradient turned back, n = x r and dn = d weight:
+ *
+ *   dx = r (dn - n mean(dn n))   (norm 1: sum);    dweight = sum over tokens and heads of d n
+ *
+ * dq_out, dk_out like the outputs; dq, dk like q and k, dq_stride and dk_stride elements
+ * apart (what lies between the rows is not written); dq_weight is required with a
+ * q_weight and NULL without, dk_weight likewise.  The workspace (no initial contents;
+ * not needed without weights) is ssd_qk_norm_bwd_workspace_size bytes, 256-byte aligned;
+ * calls that may overlap need one each.  No atomics: results are deterministic.
+ */
+size_t ssd_qk_norm_bwd_workspace_size(const ssd_qk_norm_problem_t* p);
+
+ssd_status_t ssd_qk_norm_bwd(const ssd_qk_norm_problem_t* p, const void* q, const void* k,
+                             const float* q_weight, const float* k_weight,
+                             const int32_t* positions, const float* inv_freq, const void* dq_out,
+                             const void* dk_out, void* dq, void* dk, float* dq_weight,
+                             float* dk_weight, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 /* Static description of a status code (library bookkeeping, not from the
  * pages). */
 const char* ssd_status_string(ssd_status_t s);

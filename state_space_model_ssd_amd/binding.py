@@ -36,7 +36,9 @@ EXPORTED = ("ssd_fwd_workspace_size", "ssd_workspace_layout", "ssd_config_suppor
             "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd", "ssd_fwd_gated",
             "ssd_conv_fwd", "ssd_conv_bwd_workspace_size", "ssd_conv_bwd", "ssd_conv_step",
             "ssd_step", "ssd_block_norm_fwd", "ssd_block_norm_bwd_workspace_size",
-            "ssd_block_norm_bwd", "ssd_status_string")
+            "ssd_block_norm_bwd", "ssd_delta_fwd_workspace_size", "ssd_delta_fwd",
+            "ssd_delta_bwd_workspace_size", "ssd_delta_bwd", "ssd_delta_step", "ssd_qk_norm_fwd",
+            "ssd_qk_norm_bwd_workspace_size", "ssd_qk_norm_bwd", "ssd_status_string")
 
 
 class SsdError(RuntimeError):
@@ -102,6 +104,35 @@ class BlockNormProblemC(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
                 ("gate_activation", ctypes.c_int32), ("residual_scale", ctypes.c_float),
                 ("eps", ctypes.c_float)]
+
+
+class DeltaProblemC(ctypes.Structure):
+    """ssd_delta_problem_t: the gated delta rule over whole prompts."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("nseq", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("clear_outside", ctypes.c_int32)]
+
+
+class DeltaStepProblemC(ctypes.Structure):
+    """ssd_delta_step_problem_t: the gated delta rule, one token per sequence."""
+    _fields_ = [("batch", ctypes.c_int64), ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("nslots", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+                ("beta_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class QkNormProblemC(ctypes.Structure):
+    """ssd_qk_norm_problem_t: the norm of queries and keys, with the rotation."""
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("rotary_pairs", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class TuningC(ctypes.Structure):
@@ -170,8 +201,21 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_block_norm_bwd_workspace_size.argtypes = [BP]
     lib.ssd_block_norm_bwd_workspace_size.restype = sz
     lib.ssd_block_norm_bwd.argtypes = [BP] + [vp] * 14 + [vp, sz, vp]
+    DP, DSP, QP = (ctypes.POINTER(s) for s in (DeltaProblemC, DeltaStepProblemC, QkNormProblemC))
+    lib.ssd_delta_fwd_workspace_size.argtypes = [DP]
+    lib.ssd_delta_fwd.argtypes = [DP] + [vp] * 9 + [vp, sz, vp]
+    lib.ssd_delta_bwd_workspace_size.argtypes = [DP]
+    lib.ssd_delta_bwd.argtypes = [DP] + [vp] * 15 + [vp, sz, vp]
+    lib.ssd_delta_step.argtypes = [DSP] + [vp] * 9
+    lib.ssd_qk_norm_fwd.argtypes = [QP] + [vp] * 9
+    lib.ssd_qk_norm_bwd_workspace_size.argtypes = [QP]
+    lib.ssd_qk_norm_bwd.argtypes = [QP] + [vp] * 12 + [vp, sz, vp]
+    for fn in (lib.ssd_delta_fwd_workspace_size, lib.ssd_delta_bwd_workspace_size,
+               lib.ssd_qk_norm_bwd_workspace_size):
+        fn.restype = sz
     for fn in (lib.ssd_conv_fwd, lib.ssd_conv_bwd, lib.ssd_conv_step, lib.ssd_step,
-               lib.ssd_block_norm_fwd, lib.ssd_block_norm_bwd):
+               lib.ssd_block_norm_fwd, lib.ssd_block_norm_bwd, lib.ssd_delta_fwd, lib.ssd_delta_bwd,
+               lib.ssd_delta_step, lib.ssd_qk_norm_fwd, lib.ssd_qk_norm_bwd):
         fn.restype = ctypes.c_int
     lib.ssd_status_string.argtypes = [ctypes.c_int]
     lib.ssd_status_string.restype = ctypes.c_char_p
@@ -846,6 +890,238 @@ def block_norm_bwd(x, residual, pre_weight, dout, dresidual_out=None, gate=None,
             _addr(dresidual_out), g["x"].data_ptr(), _addr(g["residual"]), _addr(g["gate"]),
             _addr(g["post_weight"]), _addr(g["scale"]), g["pre_weight"].data_ptr(),
             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    g["workspace"] = workspace
+    return g
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule, and the norm of queries and keys in front of it
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _delta_problem(*sizes):
+    p = DeltaProblemC(*sizes)
+    ref, lib = ctypes.byref(p), load_library()
+    return p, ref, int(lib.ssd_delta_fwd_workspace_size(ref)), int(lib.ssd_delta_bwd_workspace_size(ref))
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_step_problem(*sizes):
+    p = DeltaStepProblemC(*sizes)
+    return p, ctypes.byref(p)
+
+
+@functools.lru_cache(maxsize=1024)
+def _qk_norm_problem(*sizes):
+    p = QkNormProblemC(*sizes)
+    return p, ctypes.byref(p), int(load_library().ssd_qk_norm_bwd_workspace_size(ctypes.byref(p)))
+
+
+def _gates_checked(g, beta, shape, x_dtype, dev):
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t.device != dev or t.shape != shape or t.dtype != g.dtype:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                             f"{g.dtype} {shape} on {dev}")
+    if g.dtype != torch.float32 and g.dtype != x_dtype:
+        raise ValueError(f"g has dtype {g.dtype}, expected torch.float32 or {x_dtype}")
+
+
+def _delta_checked(what, q, k, v, g, beta, scale, initial_states, cu_seqlens, clear):
+    dev = _on_gpu(q, "q", what)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k are (batch, seqlen, groups, dstate), v (batch, seqlen, heads, headdim)")
+    b, T, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    _need(q, "q", q.dtype, (b, T, G, N), dev)
+    _need(k, "k", q.dtype, (b, T, G, N), dev)
+    _need(v, "v", q.dtype, (b, T, H, P), dev)
+    _gates_checked(g, beta, (b, T, H), q.dtype, dev)
+    _need(g, "g", g.dtype, (b, T, H), dev)
+    _need(beta, "beta", g.dtype, (b, T, H), dev)
+    nseq = 0
+    if cu_seqlens is not None:
+        nseq = cu_seqlens.numel() - 1
+        if nseq < 1:
+            raise ValueError("cu_seqlens needs at least two entries")
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
+    sshape = (nseq if nseq > 0 else b, H, P, N)
+    _need(initial_states, "initial_states", torch.float32, sshape, dev)
+    prob = _delta_problem(b, T, H, P, N, G, nseq, _DT[q.dtype], _DT[g.dtype],
+                          N ** -0.5 if scale is None else float(scale), int(nseq > 0 and clear))
+    return dev, sshape, prob
+
+
+def delta_fwd(q, k, v, g, beta, scale=None, initial_states=None, cu_seqlens=None, out=None,
+              final_states=None, return_final_states=True, workspace=None):
+    """ssd_delta_fwd: the gated delta rule over whole prompts.
+
+    q, k (b, T, G, N) and v (b, T, H, P) fp32 or bf16, q and k as qk_norm_fwd
+    leaves them; g (log decays) and beta (b, T, H) in fp32 or q's dtype; N 32, 64 or
+    128, P a multiple of 16 up to 256; scale: of the output (default N ** -0.5);
+    initial_states (nstates, H, P, N) fp32 or None; cu_seqlens (nseq + 1) int32 for a
+    packed batch (b == 1).  Returns (out, final_states, workspace): out like v, and the
+    states that delta_step and a later call's initial_states take (None without
+    return_final_states).  Rows of tokens outside every sequence keep what they held in
+    the caller's `out`, and are zeros in one that the call makes."""
+    dev, sshape, prob = _delta_checked("delta_fwd", q, k, v, g, beta, scale, initial_states,
+                                       cu_seqlens, out is None)
+    if out is None:
+        out = v.new_empty(v.shape)
+    else:
+        _need(out, "out", v.dtype, v.shape, dev)
+    if final_states is not None:
+        _need(final_states, "final_states", torch.float32, sshape, dev)
+    elif return_final_states:
+        final_states = v.new_empty(sshape, dtype=torch.float32)
+    workspace = _workspace(workspace, prob[2], dev)
+    _launch(dev, load_library().ssd_delta_fwd, prob[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), _addr(initial_states), _addr(cu_seqlens), out.data_ptr(),
+            _addr(final_states), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out, final_states, workspace
+
+
+def delta_bwd(q, k, v, g, beta, dout, dfinal_states=None, scale=None, initial_states=None,
+              cu_seqlens=None, workspace=None):
+    """ssd_delta_bwd: gradients of sum(out * dout) + sum(final_states * dfinal_states) for
+    delta_fwd's arguments.  Returns a dict with q, k, v, g, beta (each like its argument;
+    rows of tokens outside every sequence are zeros), initial_states (None without one) and
+    the workspace."""
+    dev, sshape, prob = _delta_checked("delta_bwd", q, k, v, g, beta, scale, initial_states,
+                                       cu_seqlens, True)
+    _need(dout, "dout", v.dtype, v.shape, dev)
+    _need(dfinal_states, "dfinal_states", torch.float32, sshape, dev)
+    if dout is None:
+        raise ValueError("dout is missing")
+    grads = {"q": q.new_empty(q.shape), "k": k.new_empty(k.shape), "v": v.new_empty(v.shape),
+             "g": g.new_empty(g.shape), "beta": beta.new_empty(beta.shape),
+             "initial_states": v.new_empty(sshape, dtype=torch.float32)
+             if initial_states is not None else None}
+    workspace = _workspace(workspace, prob[3], dev)
+    _launch(dev, load_library().ssd_delta_bwd, prob[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), _addr(initial_states), _addr(cu_seqlens), dout.data_ptr(),
+            _addr(dfinal_states), grads["q"].data_ptr(), grads["k"].data_ptr(),
+            grads["v"].data_ptr(), grads["g"].data_ptr(), grads["beta"].data_ptr(),
+            _addr(grads["initial_states"]), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    grads["workspace"] = workspace
+    return grads
+
+
+def delta_step(q, k, v, g, beta, states, scale=None, slots=None, out=None):
+    """ssd_delta_step: the gated delta rule for one new token per sequence, in place on a
+    cache of states.  q, k (batch, G, N) and v (batch, H, P) fp32 or bf16, g and beta
+    (batch, H) in fp32 or q's dtype; each row contiguous but possibly inside a wider one;
+    any P, N up to 256.  states (nslots, H, P, N) fp32, updated (delta_fwd's final_states
+    are such states); slots as for conv_step.  Returns out (batch, H, P); padding's rows of
+    it keep what they held (zeros where the call makes it)."""
+    dev = _on_gpu(q, "q", "delta_step")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k are (batch, groups, dstate), v (batch, heads, headdim)")
+    b, G, N = q.shape
+    H, P = v.shape[1], v.shape[2]
+    for t, name, shape in ((k, "k", (b, G, N)), (v, "v", (b, H, P))):
+        if t.device != dev or t.dtype != q.dtype or t.shape != shape:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                             f"{q.dtype} {shape} on {dev}")
+    _gates_checked(g, beta, (b, H), q.dtype, dev)
+    nslots = states.shape[0]
+    _need(states, "states", torch.float32, (nslots, H, P, N), dev)
+    _need(slots, "slots", torch.int32, (b,), dev)
+    if out is None:
+        make = torch.empty if slots is None else torch.zeros
+        out = make((b, H, P), dtype=v.dtype, device=dev)
+    _need(out, "out", v.dtype, (b, H, P), dev)
+    prob = _delta_step_problem(b, H, P, N, G, nslots, _row_stride(q, "q", 1), _row_stride(k, "k", 1),
+                               _row_stride(v, "v", 1), _row_stride(g, "g", 1),
+                               _row_stride(beta, "beta", 1), _DT[q.dtype], _DT[g.dtype],
+                               N ** -0.5 if scale is None else float(scale))
+    _launch(dev, load_library().ssd_delta_step, prob[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), states.data_ptr(), _addr(slots), out.data_ptr())
+    return out
+
+
+_QK_NORMS = {"rms": 0, "l2": 1}
+
+
+def _qk_norm_checked(what, q, k, q_weight, k_weight, norm, eps, positions, inv_freq, interleaved,
+                     dq_stride=0, dk_stride=0):
+    dev = _on_gpu(q, "q", what)
+    if q.dim() < 2 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q is (..., heads, headdim), k the same but for its heads")
+    if k.dtype != q.dtype or k.device != dev:
+        raise ValueError(f"k is {k.dtype} on {k.device}, expected {q.dtype} on {dev}")
+    lead, D = tuple(q.shape[:-2]), q.shape[-1]
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(t, name, torch.float32, (D,), dev)
+    if norm not in _QK_NORMS:
+        raise ValueError("norm is 'rms' or 'l2'")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("the rotation takes both positions and inv_freq")
+    R = 0
+    if inv_freq is not None:
+        R = inv_freq.numel()
+        if R < 1 or 2 * R > D:
+            raise ValueError(f"inv_freq has {R} entries, expected 1 to {D // 2}")
+        _need(inv_freq, "inv_freq", torch.float32, (R,), dev)
+        _need(positions, "positions", torch.int32, lead, dev)
+    rows = len(lead)
+    prob = _qk_norm_problem(math.prod(lead), q.shape[-2], k.shape[-2], D, R,
+                            _row_stride(q, "q", rows), _row_stride(k, "k", rows), dq_stride,
+                            dk_stride, _DT[q.dtype], _QK_NORMS[norm], int(bool(interleaved)),
+                            float(eps))
+    return dev, prob
+
+
+def qk_norm_fwd(q, k, q_weight=None, k_weight=None, norm="rms", eps=1e-6, positions=None,
+                inv_freq=None, interleaved=False, outs=None):
+    """ssd_qk_norm_fwd: the norm of queries and keys in each head, and the rotation by the
+    token's position, in one pass.  q (..., Hq, D), k (..., Hk, D) fp32 or bf16, each
+    token's heads contiguous but possibly inside wider rows; weights (D) fp32 or None;
+    norm 'rms' (by the mean of squares) or 'l2' (by their sum: unit length, as the gated
+    delta rule takes them); positions (...) int32 and inv_freq (R) fp32 turn the first 2 R
+    channels, as pairs (i, i + R) or, interleaved, (2i, 2i + 1); None: no rotation.
+    Returns contiguous (q, k)."""
+    dev, prob = _qk_norm_checked("qk_norm_fwd", q, k, q_weight, k_weight, norm, eps, positions,
+                                 inv_freq, interleaved)
+    if outs is None:
+        outs = (q.new_empty(q.shape), k.new_empty(k.shape))
+    else:
+        if len(outs) != 2:
+            raise ValueError("outs are two tensors")
+        for o, like in zip(outs, (q, k)):
+            _need(o, "outs", q.dtype, like.shape, dev)
+    _launch(dev, load_library().ssd_qk_norm_fwd, prob[1], q.data_ptr(), k.data_ptr(),
+            _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), outs[0].data_ptr(),
+            outs[1].data_ptr())
+    return outs[0], outs[1]
+
+
+def qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
+                positions=None, inv_freq=None, interleaved=False, dq=None, dk=None, workspace=None):
+    """ssd_qk_norm_bwd: gradients of sum(q_out * dq_out) + sum(k_out * dk_out) for
+    qk_norm_fwd's arguments.  Returns a dict with q, k, q_weight, k_weight (None without a
+    weight) and the workspace.  dq, dk: where q's and k's gradients go, tensors like q and k
+    that may be slices of a wider one (the gradient of the projection's output)."""
+    strides = []
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk")):
+        if t is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
+            raise ValueError(f"{name} must be like {name[1:]}")
+        strides.append(0 if t is None else _row_stride(t, name, t.dim() - 2))
+    dev, prob = _qk_norm_checked("qk_norm_bwd", q, k, q_weight, k_weight, norm, eps, positions,
+                                 inv_freq, interleaved, *strides)
+    if dq_out is None or dk_out is None:
+        raise ValueError("dq_out and dk_out are the outputs' gradients")
+    _need(dq_out, "dq_out", q.dtype, q.shape, dev)
+    _need(dk_out, "dk_out", q.dtype, k.shape, dev)
+    g = {"q": q.new_empty(q.shape) if dq is None else dq,
+         "k": k.new_empty(k.shape) if dk is None else dk,
+         "q_weight": torch.empty_like(q_weight) if q_weight is not None else None,
+         "k_weight": torch.empty_like(k_weight) if k_weight is not None else None}
+    need = prob[2] if q_weight is not None or k_weight is not None else 0
+    workspace = _workspace(workspace, need, dev)
+    _launch(dev, load_library().ssd_qk_norm_bwd, prob[1], q.data_ptr(), k.data_ptr(),
+            _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), dq_out.data_ptr(),
+            dk_out.data_ptr(), g["q"].data_ptr(), g["k"].data_ptr(), _addr(g["q_weight"]),
+            _addr(g["k_weight"]), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     g["workspace"] = workspace
     return g
 

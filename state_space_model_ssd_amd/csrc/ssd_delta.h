@@ -1,0 +1,122 @@
+// Host-side launch interface of the gated delta rule and of the norms of queries
+// and keys (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssd_common.h"
+
+namespace ssd {
+
+constexpr int kDeltaChunk = 64;              // tokens per chunk
+constexpr int kGateFloats = 5 * kDeltaChunk; // per (chunk, head): beta, E, D, and G in fp64
+
+// The gated delta rule over whole prompts, forward and backward.
+struct DeltaArgs {
+  int total;              // tokens over all rows
+  int seqlen;             // tokens per row
+  int nstates;            // sequences
+  int H, G, P, N;
+  int max_chunks, nc_row;
+  bool bf16, gate_bf16;
+  bool clear;             // rows outside every sequence become zeros
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* init;      // nullable
+  const int32_t* cu;      // packed batch, else nullptr
+  void* out;
+  float* final_states;    // nullable
+  // backward
+  const void* dout;
+  const float* dfinal;    // nullable
+  void* dq;
+  void* dk;
+  void* dv;
+  void* dg;
+  void* dbeta;
+  float* dinit;           // nullable
+  // workspace; C = 64 tokens, per (chunk, head) unless said otherwise
+  int4* table;            // packed batch: [max_chunks]
+  int* seq_chunks;        // packed batch: [nstates + 1]
+  float* gates;           // [kGateFloats]
+  void* T;                // [C][C] (1 + L)^-1: two bf16 planes, or fp32
+  void* A;                // [C][C] scale (D * q k^T), lower, dtype (forward)
+  void* kt;               // per (chunk, group): [N][C] k transposed, dtype
+  // backward
+  void* Tt;               // [C][C] T transposed, as T
+  void* At;               // [C][C] A transposed: two bf16 planes, or fp32
+  void* qt;               // per (chunk, group): [N][C] q transposed, dtype
+  void* S0;               // [P][N] the state entering the chunk, dtype
+  void* dS;               // [P][N] the gradient of the state leaving it, dtype
+  void* Wt;               // [P][C] the rows w, transposed, dtype
+  void* dRt;              // [P][C] their gradient before T, transposed, dtype
+
+  ChunkMap cmap() const {
+    ChunkMap m;
+    m.table = cu ? table : nullptr;
+    m.seq_chunks = cu ? seq_chunks : nullptr;
+    m.seqlen = seqlen;
+    m.nc_row = nc_row;
+    m.L = kDeltaChunk;
+    return m;
+  }
+};
+
+bool delta_dstate_ok(int64_t N);
+// Zeros in the rows that no sequence of a packed batch has, `row_bytes` each.
+hipError_t launch_delta_clear(const DeltaArgs& a, void* p, int64_t row_bytes, hipStream_t s);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s);
+// The chain of states; `keep`: for the backward, which wants S0 and Wt and no output.
+hipError_t launch_delta_chain(const DeltaArgs& a, bool keep, hipStream_t s);
+hipError_t launch_delta_chain_bwd(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_local_bwd(const DeltaArgs& a, hipStream_t s);
+
+// One token per sequence.
+struct DeltaStepArgs {
+  int batch, H, G, P, N;
+  int64_t nslots;
+  int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+  bool bf16, gate_bf16;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  float* states;
+  const int32_t* slots;   // nullable
+  void* out;
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t s);
+
+// The norm of queries and keys in each head, with the rotation.
+struct QkNormArgs {
+  int64_t tokens;
+  int heads[2];           // of q and of k
+  int D, R;               // channels of a head; pairs that are rotated
+  bool bf16, l2, interleaved;
+  float eps;
+  int64_t stride[2], dstride[2];  // elements from token to token of the inputs and of dx
+  const void* x[2];
+  const float* w[2];      // nullable
+  const int32_t* pos;     // with R > 0
+  const float* freq;
+  void* out[2];
+  // backward
+  const void* dout[2];
+  void* dx[2];
+  float* dw[2];           // with w
+  float* part;
+};
+constexpr int kQkNormMaxD = 256;
+hipError_t launch_qk_norm_fwd(const QkNormArgs& a, hipStream_t s);
+hipError_t launch_qk_norm_bwd(const QkNormArgs& a, hipStream_t s);
+// Floats of the backward's workspace: does not depend on the device.
+int64_t qk_norm_bwd_floats(int64_t tokens, int64_t D);
+
+}  // namespace ssd

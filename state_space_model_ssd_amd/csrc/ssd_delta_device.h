@@ -1,0 +1,142 @@
+// Device-side building blocks of the gated delta rule (internal): operands of 16x16
+// matrix instructions over 32 values of the contracted axis, exact or as pairs.
+//
+// Every product here contracts 32 values per step.  Lane i holds eight consecutive ones,
+// 8 (i / 16) .. + 7, of row (first operand) or column (second) i % 16; bf16 takes one
+// 16x16x32 instruction, fp32 eight 16x16x4 ones, the e-th with value e of every lane.
+// Either way the operands lie alike, so one kernel text serves both types.
+//
+// Results feed the next product without leaving their registers.  A result tile's lane i
+// holds rows 4 (i / 16) .. + 3 of column i % 16.  With the rows of the two tiles of a
+// 32-row block dealt out as tile_row() does, lane i's four values of the first and four of
+// the second tile are rows 8 (i / 16) .. + 7 of the block: the second operand (or, turned,
+// the first) of a product that contracts these rows.
+//
+// With bf16 inputs a value that is not an input goes into a product either rounded once
+// (2^-9 of it, where the result is rounded to bf16 itself), or as the sum of two bf16
+// (2^-18 of it, where it is part of a state, whose error would last): the products of two
+// such pairs leave out the two low parts' product.
+#pragma once
+
+#include "ssd_common.h"
+#include "ssd_delta.h"
+
+namespace ssd {
+
+struct Pair {             // hi + lo
+  bf16x8 hi, lo;
+};
+struct F8 {
+  float v[8];
+};
+
+template <typename T> struct Opnd;
+template <> struct Opnd<bf16> {
+  using X = bf16x8;                    // exact or rounded
+  using S = Pair;                      // to 2^-18
+  static constexpr int PX = 1, PS = 2; // 16-byte pieces per lane
+  __device__ __forceinline__ static X round(const float (&f)[8]) {
+    X x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = static_cast<bf16>(f[e]);
+    return x;
+  }
+  __device__ __forceinline__ static S split(const float (&f)[8]) {
+    S s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s.hi[e] = static_cast<bf16>(f[e]);
+      s.lo[e] = static_cast<bf16>(f[e] - static_cast<float>(s.hi[e]));
+    }
+    return s;
+  }
+  __device__ __forceinline__ static X hi(const S& s) { return s.hi; }
+  __device__ __forceinline__ static void get(const X& x, float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(x[e]);
+  }
+};
+template <> struct Opnd<float> {
+  using X = F8;
+  using S = F8;
+  static constexpr int PX = 2, PS = 2;
+  __device__ __forceinline__ static X round(const float (&f)[8]) {
+    X x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.v[e] = f[e];
+    return x;
+  }
+  __device__ __forceinline__ static S split(const float (&f)[8]) { return round(f); }
+  __device__ __forceinline__ static X hi(const S& s) { return s; }
+  __device__ __forceinline__ static void get(const X& x, float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = x.v[e];
+  }
+};
+
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(bf16x8 a, const Pair& b, f32x4 c) {
+  return mma(a, b.hi, mma(a, b.lo, c));
+}
+__device__ __forceinline__ f32x4 mma(const Pair& a, bf16x8 b, f32x4 c) {
+  return mma(a.hi, b, mma(a.lo, b, c));
+}
+__device__ __forceinline__ f32x4 mma(const Pair& a, const Pair& b, f32x4 c) {
+  return mma(a.hi, b.hi, mma(a.hi, b.lo, mma(a.lo, b.hi, c)));
+}
+__device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+  return c;
+}
+
+constexpr f32x4 kZero4 = {0.f, 0.f, 0.f, 0.f};
+
+// Row of result tile t (of 16) that lies in its row i of the instruction.
+__device__ __forceinline__ int tile_row(int t, int i) {
+  return 32 * (t >> 1) + 4 * (t & 1) + 8 * (i >> 2) + (i & 3);
+}
+
+// The eight values of a 32-row block's two tiles, in the order of their rows.
+__device__ __forceinline__ void block8(f32x4 t0, f32x4 t1, float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e] = t0[e];
+    f[4 + e] = t1[e];
+  }
+}
+
+// Operands from memory: 8 elements at p (16-byte aligned).
+__device__ __forceinline__ bf16x8 load_opnd(const bf16* p) {
+  return *reinterpret_cast<const bf16x8*>(p);
+}
+__device__ __forceinline__ F8 load_opnd(const float* p) {
+  F8 f;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  block8(a, b, f.v);
+  return f;
+}
+__device__ __forceinline__ bf16x8 load_opnd(__amdgpu_buffer_rsrc_t r, uint32_t off, bf16) {
+  return __builtin_bit_cast(bf16x8, buf_load16(r, off));
+}
+__device__ __forceinline__ F8 load_opnd(__amdgpu_buffer_rsrc_t r, uint32_t off, float) {
+  F8 f;
+  block8(__builtin_bit_cast(f32x4, buf_load16(r, off)), __builtin_bit_cast(f32x4, buf_load16(r, off + 16)),
+         f.v);
+  return f;
+}
+__device__ __forceinline__ void store_opnd(bf16* p, bf16x8 v) { *reinterpret_cast<bf16x8*>(p) = v; }
+__device__ __forceinline__ void store_opnd(float* p, const F8& v) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{v.v[0], v.v[1], v.v[2], v.v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v.v[4], v.v[5], v.v[6], v.v[7]};
+}
+
+// Sum over the four lanes that hold one column's rows.
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+}  // namespace ssd
