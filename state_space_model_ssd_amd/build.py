@@ -30,10 +30,17 @@ COMMON = [
     "-I", os.path.join(ROOT, "include"),
 ]
 
+# Results of matrix instructions in ordinary registers: these kernels use them with vector
+# instructions at once, and copies from accumulator registers were a sixth of the chain's
+# instructions.
+EXTRA = {name: ("-mllvm", "-amdgpu-mfma-vgpr-form=1")
+         for name in ("ssd_delta_chain",)}
+
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *COMMON, "-c", src, "-o", obj]
+    name = os.path.splitext(os.path.basename(src))[0]
+    cmd = [HIPCC, *COMMON, *EXTRA.get(name, ()), "-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), file=sys.stderr, flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -11,6 +11,11 @@ namespace ssd {
 
 constexpr int kDeltaChunk = 64;              // tokens per chunk
 constexpr int kGateFloats = 5 * kDeltaChunk; // per (chunk, head): beta, E, D, and G in fp64
+constexpr int kPiece = 1024;                 // bytes of 64 lanes' 16: operands lie in such pieces
+// Pieces of a triangular 64x64 matrix (six 16x32 tiles of eight), rounded or as pairs, and of a
+// [N][64] one.
+__host__ __device__ constexpr int triangle_pieces(bool b16, bool pair) { return b16 && !pair ? 6 : 12; }
+__host__ __device__ constexpr int transposed_pieces(bool b16, int N) { return N / 16 * 2 * (b16 ? 1 : 2); }
 
 // The gated delta rule over whole prompts, forward and backward.
 struct DeltaArgs {
@@ -40,21 +45,22 @@ struct DeltaArgs {
   void* dg;
   void* dbeta;
   float* dinit;           // nullable
-  // workspace; C = 64 tokens, per (chunk, head) unless said otherwise
+  // workspace; per (chunk, head) unless said otherwise.  Matrices that later launches
+  // multiply by lie as operands: see ssd_delta_device.h.
   int4* table;            // packed batch: [max_chunks]
   int* seq_chunks;        // packed batch: [nstates + 1]
   float* gates;           // [kGateFloats]
-  void* T;                // [C][C] (1 + L)^-1: two bf16 planes, or fp32
-  void* A;                // [C][C] scale (D * q k^T), lower, dtype (forward)
-  void* kt;               // per (chunk, group): [N][C] k transposed, dtype
+  void* T;                // (1 + L)^-1, lower, pairs
+  void* A;                // scale (D * q k^T), lower (forward)
+  void* kt;               // per (chunk, group): k transposed
   // backward
-  void* Tt;               // [C][C] T transposed, as T
-  void* At;               // [C][C] A transposed: two bf16 planes, or fp32
-  void* qt;               // per (chunk, group): [N][C] q transposed, dtype
+  void* Tt;               // T transposed, upper, pairs
+  void* At;               // A transposed, upper, pairs
+  void* qt;               // per (chunk, group): q transposed
   void* S0;               // [P][N] the state entering the chunk, dtype
   void* dS;               // [P][N] the gradient of the state leaving it, dtype
-  void* Wt;               // [P][C] the rows w, transposed, dtype
-  void* dRt;              // [P][C] their gradient before T, transposed, dtype
+  void* Wt;               // [P][64] the rows w, transposed, dtype
+  void* dRt;              // [P][64] their gradient before T, transposed, dtype
 
   ChunkMap cmap() const {
     ChunkMap m;

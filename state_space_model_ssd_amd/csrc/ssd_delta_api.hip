@@ -90,15 +90,17 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
     part(a.seq_chunks, ((size_t)a.nstates + 1) * 4);
   }
   part(a.gates, mh * kGateFloats * 4);
-  part(a.T, mh * C * C * 4);
-  part(a.kt, mg * a.N * C * e);
+  const size_t pair = (size_t)triangle_pieces(a.bf16, true) * kPiece;
+  const size_t tr = (size_t)transposed_pieces(a.bf16, a.N) * kPiece;
+  part(a.T, mh * pair);
+  part(a.kt, mg * tr);
   if (!bwd) {
-    part(a.A, mh * C * C * e);
+    part(a.A, mh * triangle_pieces(a.bf16, false) * kPiece);
     return off;
   }
-  part(a.Tt, mh * C * C * 4);
-  part(a.At, mh * C * C * 4);
-  part(a.qt, mg * a.N * C * e);
+  part(a.Tt, mh * pair);
+  part(a.At, mh * pair);
+  part(a.qt, mg * tr);
   part(a.S0, mh * a.P * a.N * e);
   part(a.dS, mh * a.P * a.N * e);
   part(a.Wt, mh * a.P * C * e);

@@ -3,13 +3,28 @@
 //   W = T (beta V - beta E K S^T)
 //   O = scale E (Q S^T) + A W
 //   S <- E_C S + (D W)^T K,     D_i = exp(G_C - G_i)
+// and backward, from the last chunk to the first, with dO the output's gradient, dS that of
+// the state leaving the chunk and dR that of beta V - beta E K S^T:
+//   dW = A^T dO + D K dS^T,   dR = T^T dW
+//   dS <- E_C dS + dO^T (scale E Q) - dR^T (beta E K)
 //
 // Rows of S (values of the head) do not meet, so a wave owns 16 of them and carries them
 // through the sequence in its registers, in fp32: S^T, W and the products between them
-// chain result to operand without LDS.  Waves of a workgroup own neighbouring rows of one
-// head and share what the chunk's products read besides: K, Q, K^T, T and A, copied to LDS
-// as operands (64 lanes of 16 bytes each, one after another) by loads that write LDS
-// directly, one chunk ahead where two chunks fit.
+// chain result to operand without LDS (ssd_delta_device.h).  What the products read besides
+// is the same for all of a head's rows and lies in LDS as operands.
+//
+// One token chunk is one step of a dependent chain, and a step is bound by the instructions
+// that one wave issues.  So a workgroup has NW state waves, which do only the chain, and four
+// helper waves, which move the operands from memory to LDS (through registers, a phase ahead)
+// and do what nothing waits for: O, or what the backward keeps.  A step has two phases with
+// a barrier after each; each half of the operands is read in one and replaced in the other,
+// so one copy in LDS is enough:
+//              state waves                         helper waves
+//   phase 1    S and W as operands to LDS;         K^T of this chunk to LDS; loads of the next
+//              W by K, T, V                        chunk's K, T, V
+//   phase 2    S by K^T                            next K, T, V to LDS; O; loads of its K^T
+//
+// 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): MEASURED.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
@@ -19,91 +34,123 @@ namespace ssd {
 namespace {
 
 constexpr int C = kDeltaChunk;
-constexpr int kPiece = 1024;              // 64 lanes of 16 bytes
-constexpr int kLdsBytes = 160 * 1024;
-typedef __attribute__((address_space(3))) void lds_void;
+constexpr int HW = 4;                     // helper waves
 
-// 16 bytes per lane from `off` (zeros past the resource) to LDS, lane after lane.
-__device__ __forceinline__ void copy_piece(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
-}
+// One helper wave's share of `COUNT` loads of 16 bytes per lane on their way from memory to
+// LDS, through registers.
+template <int COUNT> struct Pieces {
+  static constexpr int n = (COUNT + HW - 1) / HW;
+  uint4 q[n];
+  // The i-th load of helper w; the last ones may be made twice.
+  __device__ __forceinline__ static int index(int i, int w) {
+    return COUNT % HW ? min(i * HW + w, COUNT - 1) : i * HW + w;
+  }
+};
 
-// The operand at `p` in LDS: PX pieces, for pairs the high parts and then the low ones.
-__device__ __forceinline__ bf16x8 lds_x(const char* p, int lane, bf16) {
-  return *reinterpret_cast<const bf16x8*>(p + lane * 16);
+// Operands that lie in memory as they do in LDS.
+template <int COUNT> struct Copied : Pieces<COUNT> {
+  __device__ __forceinline__ void load(const char* p, int w, int lane) {
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(p, COUNT * kPiece);
+#pragma unroll
+    for (int i = 0; i < this->n; ++i) this->q[i] = buf_load16(r, this->index(i, w) * kPiece + lane * 16);
+  }
+  __device__ __forceinline__ void store(char* lds, int w, int lane) const {
+#pragma unroll
+    for (int i = 0; i < this->n; ++i)
+      *reinterpret_cast<uint4*>(lds + this->index(i, w) * kPiece + lane * 16) = this->q[i];
+  }
+};
+
+// The operands of a [C][N] matrix of T in its caller's rows, rows dealt to tiles as tile_row()
+// does.  LDS has them in the order [32-block][tile].  A load takes 128 bytes of 8 rows (64 of 16
+// where rows have no more): a lane per row, the operands' own order, takes four times as long to
+// issue.  The exclusive or in a lane's slot keeps the eight lanes that write LDS together on
+// different banks.
+template <typename T, int N> struct Rows : Pieces<4 * (N / 32) * Opnd<T>::PX> {
+  static constexpr int LR = N * (int)sizeof(T) >= 128 ? 8 : 4;    // lanes on one row
+  static constexpr int RL = 64 / LR, PR = N * (int)sizeof(T) / (16 * LR);
+  static constexpr bool FLIP = LR == 8 && sizeof(T) == 2;
+  __device__ __forceinline__ static uint32_t slot(int a, int i, int flip) {
+    return (uint32_t)(16 * a + (i ^ 2 * a ^ flip)) * 16;
+  }
+  // A reader's slot; `flip` is 1 for the second of two pieces that share 128 bytes.
+  __device__ __forceinline__ static uint32_t read(int lane, int flip) {
+    return slot(lane >> 4, lane & 15, FLIP ? flip : 0);
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t pitch, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < this->n; ++i) {
+      const int x = this->index(i, w), part = x % PR, row = x / PR * RL + lane / LR;   // tile by tile
+      this->q[i] = buf_load16(r, tile_row(row / 16, row % 16) * pitch + (part * LR + lane % LR) * 16);
+    }
+  }
+  __device__ __forceinline__ void store(char* lds, int w, int lane) const {
+#pragma unroll
+    for (int i = 0; i < this->n; ++i) {
+      const int x = this->index(i, w), part = x % PR, row = x / PR * RL + lane / LR;
+      const int b = (part * LR + lane % LR) * 16;                 // byte of the row
+      const int e = b / (int)sizeof(T), kb = e / 32, a = e % 32 / 8, px = e % 8 * (int)sizeof(T) / 16;
+      const int flip = FLIP ? b / 64 & 1 : 0;
+      const int piece = (kb * 4 + row / 16) * Opnd<T>::PX + px;
+      *reinterpret_cast<uint4*>(lds + piece * kPiece + slot(a, row % 16, flip)) = this->q[i];
+    }
+  }
+};
+
+// A [C][16 NW] block of T, as rows in LDS: the workgroup's columns of V or dO.
+template <typename T, int NW> struct Block : Pieces<NW * (int)sizeof(T)> {
+  static constexpr int LR = NW * (int)sizeof(T);                  // lanes on one row
+  static constexpr int pitch = 16 * NW + 16 / (int)sizeof(T);     // elements
+  static constexpr int bytes = C * pitch * (int)sizeof(T);
+  // `row`: bytes from token to token; `cols`: columns that there are (a multiple of 16).
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int cols, int w, int lane) {
+    const uint32_t at = lane % LR * 16;
+#pragma unroll
+    for (int i = 0; i < this->n; ++i) {
+      const int c = this->index(i, w) * (64 / LR) + lane / LR;
+      this->q[i] = buf_load16(r, at < cols * sizeof(T) ? c * row + at : 0xffffff00u);   // else zeros
+    }
+  }
+  __device__ __forceinline__ void store(char* lds, int w, int lane) const {
+#pragma unroll
+    for (int i = 0; i < this->n; ++i) {
+      const int c = this->index(i, w) * (64 / LR) + lane / LR;
+      *reinterpret_cast<uint4*>(lds + c * pitch * sizeof(T) + lane % LR * 16) = this->q[i];
+    }
+  }
+};
+// Rows 32 cb + 8 (lane / 16) .. + 7 of a block's column tile_row(s, lane % 16).
+template <int NW>
+__device__ __forceinline__ bf16x8 column_opnd(const char* lds, int s, int cb, int lane, bf16) {
+  constexpr int pitch = Block<bf16, NW>::pitch;
+  const int m = lane & 15;
+  const bf16* p = reinterpret_cast<const bf16*>(lds) + (32 * cb + 8 * (lane >> 4) + (m >> 2)) * pitch +
+                  32 * (s >> 1) + 8 * (m & 3) + 4 * (s & 1);
+  const i16x4 lo = lds_tr16_b64(p), hi = lds_tr16_b64(p + 4 * pitch);
+  typedef short i16x8v __attribute__((ext_vector_type(8)));
+  const i16x8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
 }
-__device__ __forceinline__ F8 lds_x(const char* p, int lane, float) {
+template <int NW>
+__device__ __forceinline__ F8 column_opnd(const char* lds, int s, int cb, int lane, float) {
+  constexpr int pitch = Block<float, NW>::pitch;
   F8 f;
-  block8(*reinterpret_cast<const f32x4*>(p + lane * 16),
-         *reinterpret_cast<const f32x4*>(p + kPiece + lane * 16), f.v);
+  const float* p = reinterpret_cast<const float*>(lds) + (32 * cb + 8 * (lane >> 4)) * pitch + tile_row(s, lane & 15);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.v[e] = p[e * pitch];
   return f;
 }
-__device__ __forceinline__ Pair lds_s(const char* p, int lane, bf16) {
-  return {lds_x(p, lane, bf16{}), lds_x(p + kPiece, lane, bf16{})};
-}
-__device__ __forceinline__ F8 lds_s(const char* p, int lane, float) { return lds_x(p, lane, 0.f); }
 
-// The six 16x32 tiles of a triangular [C][C] matrix that are not zero, in operand order:
-// lower (0,0) (1,0) (2,0) (3,0) (2,1) (3,1) as (tile of rows, 32-block of columns).
-__device__ __forceinline__ int2 lower_tile(int i) {
-  return i < 4 ? make_int2(i, 0) : make_int2(i - 2, 1);
-}
-__device__ __forceinline__ constexpr int lower_at(int u, int cb) { return cb == 0 ? u : u + 2; }
-// upper (0,0) (1,0) (0,1) (1,1) (2,1) (3,1)
-__device__ __forceinline__ int2 upper_tile(int i) {
-  return i < 2 ? make_int2(i, 0) : make_int2(i - 2, 1);
-}
-__device__ __forceinline__ constexpr int upper_at(int u, int cb) { return cb == 0 ? u : u + 2; }
-
-// Copies the operands of a [rows][32 KB] matrix of T, pitch in bytes; `dealt`: tiles of
-// rows as tile_row() deals them, else as they lie.
-template <typename T, int TILES, int KB, bool DEALT, int NW>
-__device__ __forceinline__ void copy_opnds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t pitch, int w,
-                                           int lane) {
-  constexpr int PX = Opnd<T>::PX;
-  const int l16 = lane & 15;
-  const uint32_t mine = (DEALT ? tile_row(0, l16) : l16) * pitch + (lane >> 4) * 8 * sizeof(T);
-  for (int i = w; i < TILES * KB * PX; i += NW) {
-    const int px = i % PX, kb = i / PX % KB, u = i / (PX * KB);
-    const int base = DEALT ? 32 * (u >> 1) + 4 * (u & 1) : 16 * u;
-    copy_piece(r, lds + i * kPiece, mine + base * pitch + kb * 32 * (uint32_t)sizeof(T) + px * 16);
-  }
-}
-// The same of a triangular [C][C] matrix; PAIR: two bf16 planes where T is bf16.
-template <typename T, bool LOWER, bool DEALT, bool PAIR, int NW>
-__device__ __forceinline__ void copy_triangle(const void* m, char* lds, int w, int lane) {
-  constexpr int PC = sizeof(T) == 4 || PAIR ? 2 : 1;
-  constexpr uint32_t pitch = C * sizeof(T), step = sizeof(T) == 4 ? 16 : C * C * 2;
-  const __amdgpu_buffer_rsrc_t r = buf_rsrc(m, C * C * (sizeof(T) == 4 ? 4 : 2 * PC));
-  const int l16 = lane & 15;
-  const uint32_t mine = (DEALT ? tile_row(0, l16) : l16) * pitch + (lane >> 4) * 8 * sizeof(T);
-  for (int i = w; i < 6 * PC; i += NW) {
-    const int2 t = LOWER ? lower_tile(i / PC) : upper_tile(i / PC);
-    const int base = DEALT ? 32 * (t.x >> 1) + 4 * (t.x & 1) : 16 * t.x;
-    copy_piece(r, lds + i * kPiece, mine + base * pitch + t.y * 32 * (uint32_t)sizeof(T) + i % PC * step);
-  }
-}
-
-// A [C][16] tile of T, rows of the tile one after another: a wave's own columns.
-template <typename T>
-__device__ __forceinline__ void copy_columns(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t pitch,
-                                             int lane) {
-  constexpr int LR = sizeof(T);                   // lanes per row of 16 values
-  constexpr int RW = 64 / LR;                     // rows per piece
+// M operands in a row from `p` on.
+template <int M, typename T>
+__device__ __forceinline__ void lds_xs(const char* p, uint32_t slot, typename Opnd<T>::X (&x)[M]) {
 #pragma unroll
-  for (int i = 0; i < C / RW; ++i)
-    copy_piece(r, lds + i * kPiece, (i * RW + lane / LR) * pitch + lane % LR * 16);
+  for (int m = 0; m < M; ++m) x[m] = piece_x(p + m * Opnd<T>::PX * kPiece, slot, T{});
 }
-// Rows 32 cb + 8 (lane / 16) .. + 7 of column lane % 16.
-__device__ __forceinline__ bf16x8 column_opnd(const bf16* t, int cb, int lane) {
-  return lds_operand_kmajor(t, 16, 32 * cb, 0, lane);
-}
-__device__ __forceinline__ F8 column_opnd(const float* t, int cb, int lane) {
-  F8 f;
-  const float* p = t + (32 * cb + 8 * (lane >> 4)) * 16 + (lane & 15);
+template <int M, typename T>
+__device__ __forceinline__ void lds_ss(const char* p, uint32_t slot, typename Opnd<T>::S (&x)[M]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = p[e * 16];
-  return f;
+  for (int m = 0; m < M; ++m) x[m] = piece_s(p + m * Opnd<T>::PS * kPiece, slot, T{});
 }
 
 // Values 32 cb + 8 (lane / 16) .. + 7 of a row of C floats.
@@ -120,35 +167,51 @@ __device__ __forceinline__ uint32_t rows_bytes(int n, uint32_t pitch, uint32_t r
 // Workgroup -> (sequence, head) and its block of P: the blocks of one head, which read the
 // same operands, run on the same XCD.
 struct ChainTask {
-  int seq, h, block;
+  int seq, h, g, block;
   bool none;
+  int first, tokens;      // the sequence's tokens
+  int c0, chunks;         // and chunks
+  __device__ __forceinline__ ChainTask(const DeltaArgs& a, const ChunkMap& cm, int b, int blocks) {
+    const int x8 = b & 7, rest = b >> 3, unit = rest / blocks * 8 + x8;
+    seq = unit / a.H;
+    h = unit % a.H;
+    g = h / (a.H / a.G);
+    block = rest % blocks;
+    none = unit >= a.nstates * a.H;
+    if (none) return;
+    const int2 r = cm.seq_range(seq);
+    c0 = r.x;
+    chunks = r.y - r.x;
+    if (a.cu) {           // as the chunk table's launch reads them
+      first = min(max(a.cu[seq], 0), a.total);
+      tokens = min(max(a.cu[seq + 1], first), a.total) - first;
+    } else {
+      first = seq * a.seqlen;
+      tokens = a.seqlen;
+    }
+  }
+  __device__ __forceinline__ int start(int i) const { return first + i * C; }
+  __device__ __forceinline__ int len(int i) const { return min(C, tokens - i * C); }
 };
-__device__ __forceinline__ ChainTask chain_task(int b, int nstates, int H, int blocks) {
-  const int x8 = b & 7, rest = b >> 3, unit = rest / blocks * 8 + x8;
-  return {unit / H, unit % H, rest % blocks, unit >= nstates * H};
-}
-unsigned chain_grid(const DeltaArgs& a, int blocks) {
-  return (unsigned)(((int64_t)a.nstates * a.H + 7) / 8 * 8 * blocks);
-}
 
-// S^T in its tiles from a state's rows, and back.
+// S^T in its tiles from row p of a state, zeros where there is none; and back.
 template <int N>
-__device__ __forceinline__ void load_state(const float* p, int lane, f32x4 (&S)[N / 16]) {
+__device__ __forceinline__ void load_state(const float* row, bool in, int lane, f32x4 (&S)[N / 16]) {
 #pragma unroll
   for (int kb = 0; kb < N / 32; ++kb) {
-    const float* r = p + (int64_t)(lane & 15) * N + 32 * kb + 8 * (lane >> 4);
+    const float* r = row + 32 * kb + 8 * (lane >> 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      S[2 * kb][e] = r[e];
-      S[2 * kb + 1][e] = r[4 + e];
+      S[2 * kb][e] = in ? r[e] : 0.f;
+      S[2 * kb + 1][e] = in ? r[4 + e] : 0.f;
     }
   }
 }
 template <int N>
-__device__ __forceinline__ void store_state(float* p, int lane, const f32x4 (&S)[N / 16]) {
+__device__ __forceinline__ void store_state(float* row, int lane, const f32x4 (&S)[N / 16]) {
 #pragma unroll
   for (int kb = 0; kb < N / 32; ++kb) {
-    float* r = p + (int64_t)(lane & 15) * N + 32 * kb + 8 * (lane >> 4);
+    float* r = row + 32 * kb + 8 * (lane >> 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       r[e] = S[2 * kb][e];
@@ -157,302 +220,380 @@ __device__ __forceinline__ void store_state(float* p, int lane, const f32x4 (&S)
   }
 }
 
-// KEEP: for the backward, S and W are kept (as operands there: rounded) and O is not made.
-template <typename T, int N, int NW, bool KEEP>
-__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(const DeltaArgs a, const ChunkMap cm,
-                                                              int blocks) {
-  using O = Opnd<T>;
-  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS;
-  constexpr int oK = 0, oT = oK + 4 * NK * PX, oKt = oT + 6 * PS, oQ = oKt + NT * 2 * PX;
-  constexpr int oA = oQ + (KEEP ? 0 : 4 * NK * PX), oG = oA + (KEEP ? 0 : 6 * PX), oV = oG + 1;
-  constexpr int VP = (int)sizeof(T);              // pieces of a wave's columns of V
-  constexpr int SLOT = (oV + NW * VP) * kPiece;
-  constexpr int NBUF = 2 * SLOT <= kLdsBytes ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) char lds[NBUF * SLOT];
-
-  const ChainTask t = chain_task(blockIdx.x, a.nstates, a.H, blocks);
-  if (t.none) return;
-  const int w = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
-  const int h = t.h, g = h / (a.H / a.G);
-  const bool live = (t.block * NW + w) * 16 < a.P;
-  const int p0 = live ? (t.block * NW + w) * 16 : 0;
-  const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0) * N;
-  const uint32_t qrow = (uint32_t)a.G * N * sizeof(T), vrow = (uint32_t)a.H * a.P * sizeof(T);
-
-  f32x4 S[NT];
-  if (a.init) {
-    load_state<N>(a.init + srow, lane, S);
-  } else {
+// Operands that the state waves left in LDS ([wave][EX of them], from the `from`-th on, each 32
+// columns of 16 dealt rows) to rows of a [P][COLS] matrix of T.
+template <typename T, int NW, int EX, int COLS>
+__device__ __forceinline__ void store_rows(const char* x, int from, T* dst, int rows, int w, int lane) {
+  constexpr int PX = Opnd<T>::PX, V = 16 / (int)sizeof(T), PR = COLS / V, all = 16 * NW * PR;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) S[i] = kZero4;
+  for (int i = 0; i < (all + 64 * HW - 1) / (64 * HW); ++i) {
+    const int at = (i * HW + w) * 64 + lane, p = at / PR, c = at % PR * V;
+    if (all % (64 * HW) && at >= all) break;
+    const int s = 2 * (p / 32) + (p / 4 & 1), l16 = p % 32 / 8 * 4 + p % 4;
+    const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
+    const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX + px) * kPiece + (16 * a + l16) * 16);
+    if (p < rows) *reinterpret_cast<uint4*>(dst + (int64_t)p * COLS + c) = v;
   }
-
-  auto stage = [&](int j, char* b) {
-    const ChunkDesc d = cm.desc(j);
-    const int64_t jh = (int64_t)j * a.H + h, jg = (int64_t)j * a.G + g;
-    const uint32_t qb = rows_bytes(d.len, qrow, N * sizeof(T));
-    const int64_t qo = ((int64_t)d.start * a.G + g) * N;
-    copy_opnds<T, 4, NK, true, NW>(buf_rsrc(static_cast<const T*>(a.k) + qo, qb), b + oK * kPiece, qrow, w, lane);
-    copy_triangle<T, true, true, true, NW>(static_cast<const char*>(a.T) + jh * (C * C * 4), b + oT * kPiece, w, lane);
-    copy_opnds<T, NT, 2, true, NW>(buf_rsrc(static_cast<const T*>(a.kt) + jg * N * C, N * C * sizeof(T)),
-                                   b + oKt * kPiece, C * sizeof(T), w, lane);
-    if constexpr (!KEEP) {
-      copy_opnds<T, 4, NK, false, NW>(buf_rsrc(static_cast<const T*>(a.q) + qo, qb), b + oQ * kPiece, qrow, w, lane);
-      copy_triangle<T, true, false, false, NW>(static_cast<const T*>(a.A) + jh * (C * C), b + oA * kPiece, w, lane);
-    }
-    if (w == 0) copy_piece(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), b + oG * kPiece, lane * 16);
-    const uint32_t vb = rows_bytes(d.len, vrow, 16 * sizeof(T));
-    copy_columns<T>(buf_rsrc(static_cast<const T*>(a.v) + ((int64_t)d.start * a.H + h) * a.P + p0, vb),
-                    b + (oV + w * VP) * kPiece, vrow, lane);
-  };
-
-  const int2 range = cm.seq_range(t.seq);
-  if constexpr (NBUF == 2) {
-    if (range.x < range.y) stage(range.x, lds);
-  }
-  for (int j = range.x; j < range.y; ++j) {
-    char* b = lds + (NBUF == 2 ? ((j - range.x) & 1) * SLOT : 0);
-    if constexpr (NBUF == 2) {
-      __syncthreads();                            // chunk j is there, and chunk j - 1's slot free
-      if (j + 1 < range.y) stage(j + 1, lds + ((j + 1 - range.x) & 1) * SLOT);
-    } else {
-      __syncthreads();
-      stage(j, b);
-      __syncthreads();
-    }
-    const ChunkDesc d = cm.desc(j);
-    const int64_t jh = (int64_t)j * a.H + h;
-    const float* gt = reinterpret_cast<const float*>(b + oG * kPiece);
-
-    typename O::S sf[NK];
-#pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-      float f[8];
-      block8(S[2 * kb], S[2 * kb + 1], f);
-      sf[kb] = O::split(f);
-    }
-    f32x4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u] = kZero4;
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb) x[u] = mma(lds_x(b + (oK + (u * NK + kb) * PX) * kPiece, lane, T{}), sf[kb], x[u]);
-    }
-    typename O::S rf[2];
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      float f[8], v[8], be[8], E[8];
-      block8(x[2 * cb], x[2 * cb + 1], f);
-      O::get(column_opnd(reinterpret_cast<const T*>(b + (oV + w * VP) * kPiece), cb, lane), v);
-      row8(gt, cb, lane, be);
-      row8(gt + C, cb, lane, E);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = be[e] * (v[e] - E[e] * f[e]);
-      rf[cb] = O::split(f);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u] = kZero4;
-#pragma unroll
-      for (int cb = 0; cb <= u / 2; ++cb)
-        x[u] = mma(lds_s(b + (oT + lower_at(u, cb) * PS) * kPiece, lane, T{}), rf[cb], x[u]);
-    }
-    typename O::X wf[2];
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      float f[8], D[8];
-      block8(x[2 * cb], x[2 * cb + 1], f);
-      wf[cb] = O::round(f);
-      row8(gt + 2 * C, cb, lane, D);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= D[e];
-      rf[cb] = O::split(f);
-    }
-    const float EC = gt[2 * C - 1];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      S[i] *= EC;
-#pragma unroll
-      for (int cb = 0; cb < 2; ++cb) S[i] = mma(lds_x(b + (oKt + (i * 2 + cb) * PX) * kPiece, lane, T{}), rf[cb], S[i]);
-    }
-    if constexpr (KEEP) {
-      if (live) {
-        T* s0 = static_cast<T*>(a.S0) + (jh * a.P + p0 + l16) * N + 8 * la;
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) store_opnd(s0 + 32 * kb, O::hi(sf[kb]));
-        T* wt = static_cast<T*>(a.Wt) + (jh * a.P + p0 + l16) * C + 8 * la;
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) store_opnd(wt + 32 * cb, wf[cb]);
-      }
-    } else {
-      // O with the state as first operand: rows are values, lane's column is a token
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f32x4 o = kZero4;
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) o = mma(O::hi(sf[kb]), lds_x(b + (oQ + (u * NK + kb) * PX) * kPiece, lane, T{}), o);
-        o *= a.scale * gt[C + 16 * u + l16];
-#pragma unroll
-        for (int cb = 0; cb <= u / 2; ++cb)
-          o = mma(wf[cb], lds_x(b + (oA + lower_at(u, cb) * PX) * kPiece, lane, T{}), o);
-        const int c = 16 * u + l16;
-        if (live && c < d.len) {
-          T* out = static_cast<T*>(a.out) + ((int64_t)(d.start + c) * a.H + h) * a.P + p0 + 4 * la;
-          T f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = from_f32<T>(o[e]);
-          __builtin_memcpy(out, f, sizeof(f));
-        }
-      }
-    }
-  }
-  if (!KEEP && a.final_states && live) store_state<N>(a.final_states + srow, lane, S);
 }
 
-// The chain backward: dS, the gradient of the state leaving the chunk, from the last chunk
-// to the first.  With dO the output's gradient,
-//   dW = A^T dO + D K dS^T,   dR = T^T dW       (dR: the gradient of beta V - beta E K S^T)
-//   dS <- E_C dS + dO^T (scale E Q) - dR^T (beta E K)
-// dS (before the update) and dR are kept for ssd_delta_local.hip.
-template <typename T, int N, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_chain_bwd_kernel(const DeltaArgs a, const ChunkMap cm,
-                                                                  int blocks) {
+// KEEP: for the backward, S and W are kept (as operands there: rounded) and O is not made.
+template <typename T, int N, int NW, bool KEEP>
+__global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const DeltaArgs a, const ChunkMap cm,
+                                                                      int blocks) {
   using O = Opnd<T>;
-  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS;
-  constexpr int oK = 0, oA = oK + 4 * NK * PX, oT = oA + 6 * PS, oQt = oT + 6 * PS;
-  constexpr int oKt = oQt + NT * 2 * PX, oG = oKt + NT * 2 * PX, oV = oG + 1;
-  constexpr int VP = (int)sizeof(T);
-  constexpr int SLOT = (oV + NW * VP) * kPiece;
-  constexpr int NBUF = 2 * SLOT <= kLdsBytes ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) char lds[NBUF * SLOT];
+  using KR = Rows<T, N>;
+  using VB = Block<T, NW>;
+  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
+  constexpr int oK = 0, oT = oK + 4 * NK * PX * kPiece, oG = oT + 6 * PS * kPiece, oV = oG + kPiece;
+  constexpr int oKt = oV + VB::bytes, oX = oKt + TP * kPiece, oQ = oX + NW * EX * PX * kPiece;
+  constexpr int kBytes = oQ + (KEEP ? 0 : HW * PX * kPiece);
+  __shared__ __attribute__((aligned(16))) char lds[kBytes];
 
-  const ChainTask t = chain_task(blockIdx.x, a.nstates, a.H, blocks);
+  const ChainTask t(a, cm, blockIdx.x, blocks);
   if (t.none) return;
-  const int w = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
-  const int h = t.h, g = h / (a.H / a.G);
-  const bool live = (t.block * NW + w) * 16 < a.P;
-  const int p0 = live ? (t.block * NW + w) * 16 : 0;
-  const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0) * N;
-  const uint32_t qrow = (uint32_t)a.G * N * sizeof(T), vrow = (uint32_t)a.H * a.P * sizeof(T);
+  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
+  const int h = t.h, p0 = t.block * 16 * NW, rows = min(16 * NW, a.P - p0);
+  const float* gt = reinterpret_cast<const float*>(lds + oG);
 
-  f32x4 S[NT];
-  if (a.dfinal) {
-    load_state<N>(a.dfinal + srow, lane, S);
-  } else {
+  if (wave < NW) {
+    const int p = tile_row(wave, l16);
+    const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0 + p) * N;
+    const uint32_t rs = lane * 16, rk[2] = {KR::read(lane, 0), KR::read(lane, 1)};
+    f32x4 S[NT];
+    load_state<N>(a.init + srow, a.init && p < rows, lane, S);
+    __syncthreads();
+    for (int j = 0; j < t.chunks; ++j) {
+      // phase 1
+      typename O::S sf[NK], rf[2];
+      char* x = lds + oX + wave * EX * PX * kPiece;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) S[i] = kZero4;
-  }
-
-  auto stage = [&](int j, char* b) {
-    const ChunkDesc d = cm.desc(j);
-    const int64_t jh = (int64_t)j * a.H + h, jg = (int64_t)j * a.G + g;
-    const uint32_t qb = rows_bytes(d.len, qrow, N * sizeof(T));
-    const int64_t qo = ((int64_t)d.start * a.G + g) * N;
-    copy_opnds<T, 4, NK, true, NW>(buf_rsrc(static_cast<const T*>(a.k) + qo, qb), b + oK * kPiece, qrow, w, lane);
-    copy_triangle<T, false, true, true, NW>(static_cast<const char*>(a.At) + jh * (C * C * 4), b + oA * kPiece, w, lane);
-    copy_triangle<T, false, true, true, NW>(static_cast<const char*>(a.Tt) + jh * (C * C * 4), b + oT * kPiece, w, lane);
-    copy_opnds<T, NT, 2, true, NW>(buf_rsrc(static_cast<const T*>(a.qt) + jg * N * C, N * C * sizeof(T)),
-                                   b + oQt * kPiece, C * sizeof(T), w, lane);
-    copy_opnds<T, NT, 2, true, NW>(buf_rsrc(static_cast<const T*>(a.kt) + jg * N * C, N * C * sizeof(T)),
-                                   b + oKt * kPiece, C * sizeof(T), w, lane);
-    if (w == 0) copy_piece(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), b + oG * kPiece, lane * 16);
-    const uint32_t vb = rows_bytes(d.len, vrow, 16 * sizeof(T));
-    copy_columns<T>(buf_rsrc(static_cast<const T*>(a.dout) + ((int64_t)d.start * a.H + h) * a.P + p0, vb),
-                    b + (oV + w * VP) * kPiece, vrow, lane);
-  };
-
-  const int2 range = cm.seq_range(t.seq);
-  const int last = range.y - 1;
-  if constexpr (NBUF == 2) {
-    if (range.x < range.y) stage(last, lds);
-  }
-  for (int j = last; j >= range.x; --j) {
-    char* b = lds + (NBUF == 2 ? ((last - j) & 1) * SLOT : 0);
-    if constexpr (NBUF == 2) {
-      __syncthreads();
-      if (j > range.x) stage(j - 1, lds + ((last - j + 1) & 1) * SLOT);
-    } else {
-      __syncthreads();
-      stage(j, b);
-      __syncthreads();
-    }
-    const int64_t jh = (int64_t)j * a.H + h;
-    const float* gt = reinterpret_cast<const float*>(b + oG * kPiece);
-
-    typename O::S sf[NK];
-#pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-      float f[8];
-      block8(S[2 * kb], S[2 * kb + 1], f);
-      sf[kb] = O::split(f);
-    }
-    typename O::X of[2];
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) of[cb] = column_opnd(reinterpret_cast<const T*>(b + (oV + w * VP) * kPiece), cb, lane);
-    f32x4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u] = kZero4;
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb) x[u] = mma(lds_x(b + (oK + (u * NK + kb) * PX) * kPiece, lane, T{}), sf[kb], x[u]);
-    }
-    typename O::S rf[2];
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      float D[8];
-      row8(gt + 2 * C, cb, lane, D);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int u = 2 * cb + i;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[u][e] *= D[4 * i + e];
-#pragma unroll
-        for (int k = cb; k < 2; ++k) x[u] = mma(lds_s(b + (oA + upper_at(u, k) * PS) * kPiece, lane, T{}), of[k], x[u]);
+      for (int kb = 0; kb < NK; ++kb) {
+        float f[8];
+        block8(S[2 * kb], S[2 * kb + 1], f);
+        sf[kb] = O::split(f);
+        put_piece(x + kb * PX * kPiece, rs, O::hi(sf[kb]));
       }
-      float f[8];
-      block8(x[2 * cb], x[2 * cb + 1], f);
-      rf[cb] = O::split(f);
-    }
+      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u] = kZero4;
-#pragma unroll
-      for (int k = u / 2; k < 2; ++k) x[u] = mma(lds_s(b + (oT + upper_at(u, k) * PS) * kPiece, lane, T{}), rf[k], x[u]);
-    }
-    typename O::S qf[2];
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      float f[8], be[8], E[8], o[8];
-      block8(x[2 * cb], x[2 * cb + 1], f);
-      if (live) store_opnd(static_cast<T*>(a.dRt) + (jh * a.P + p0 + l16) * C + 32 * cb + 8 * la, O::round(f));
-      row8(gt, cb, lane, be);
-      row8(gt + C, cb, lane, E);
-      O::get(of[cb], o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[e] *= -be[e] * E[e];
-        o[e] *= a.scale * E[e];
+      for (int kb = 0; kb < NK; ++kb) {
+        typename O::X kf[4];
+        lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf);
+        mma_rows(kf, sf[kb], y);
       }
-      rf[cb] = O::split(f);
-      qf[cb] = O::split(o);
-    }
-    if (live) {
-      T* ds = static_cast<T*>(a.dS) + (jh * a.P + p0 + l16) * N + 8 * la;
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb) store_opnd(ds + 32 * kb, O::hi(sf[kb]));
-    }
-    const float EC = gt[2 * C - 1];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      S[i] *= EC;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        S[i] = mma(lds_x(b + (oQt + (i * 2 + cb) * PX) * kPiece, lane, T{}), qf[cb], S[i]);
-        S[i] = mma(lds_x(b + (oKt + (i * 2 + cb) * PX) * kPiece, lane, T{}), rf[cb], S[i]);
+        float f[8], v[8], be[8], E[8];
+        block8(y[2 * cb], y[2 * cb + 1], f);
+        O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v);
+        row8(gt, cb, lane, be);
+        row8(gt + C, cb, lane, E);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = be[e] * (v[e] - E[e] * f[e]);
+        rf[cb] = O::split(f);
+      }
+      {
+        typename O::S t0[4], t1[2];
+        lds_ss<4, T>(lds + oT, rs, t0);
+        lds_ss<2, T>(lds + oT + 4 * PS * kPiece, rs, t1);
+        y[0] = y[1] = y[2] = y[3] = kZero4;
+        mma_rows(t0, rf[0], y);
+        mma_rows(t1, rf[1], y + 2);
+      }
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        float f[8], D[8];
+        block8(y[2 * cb], y[2 * cb + 1], f);
+        put_piece(x + (NK + cb) * PX * kPiece, rs, O::round(f));
+        row8(gt + 2 * C, cb, lane, D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= D[e];
+        rf[cb] = O::split(f);
+      }
+      const float EC = gt[2 * C - 1];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) S[i] *= EC;
+      __syncthreads();
+      // phase 2
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        typename O::X kf[NT];
+        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, kf);
+        mma_rows(kf, rf[cb], S);
+      }
+      __syncthreads();
+    }
+    if (!KEEP && a.final_states && p < rows) store_state<N>(a.final_states + srow, lane, S);
+    return;
+  }
+
+  const int w = wave - NW;                        // helper
+  const uint32_t qrow = (uint32_t)a.G * N * sizeof(T), vrow = (uint32_t)a.H * a.P * sizeof(T);
+  KR cK;
+  Copied<6 * PS> cT;
+  VB cV;
+  uint4 cG;
+  Copied<TP> cKt;
+  auto fetch1 = [&](int j) {
+    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, qo = ((int64_t)t.start(j) * a.G + t.g) * N;
+    cK.load(buf_rsrc(static_cast<const T*>(a.k) + qo, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
+    cT.load(static_cast<const char*>(a.T) + jh * (6 * PS * kPiece), w, lane);
+    cV.load(buf_rsrc(static_cast<const T*>(a.v) + ((int64_t)t.start(j) * a.H + h) * a.P + p0,
+                     rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cG = buf_load16(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), lane * 16);
+  };
+  auto put1 = [&]() {
+    cK.store(lds + oK, w, lane);
+    cT.store(lds + oT, w, lane);
+    cV.store(lds + oV, w, lane);
+    if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
+  };
+  // helper w makes the outputs of tokens 16 w ..; their rows of Q, four lanes on 64 bytes, and
+  // of A, as operands
+  uint4 cQ[NK * PX];
+  typename O::X af[2];
+  auto fetch2 = [&](int j) {
+    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, jg = (int64_t)(t.c0 + j) * a.G + t.g;
+    cKt.load(static_cast<const char*>(a.kt) + jg * (TP * kPiece), w, lane);
+    if constexpr (!KEEP) {
+      const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + ((int64_t)t.start(j) * a.G + t.g) * N,
+                                                 rows_bytes(t.len(j), qrow, N * sizeof(T)));
+#pragma unroll
+      for (int i = 0; i < NK * PX; ++i) cQ[i] = buf_load16(qr, (16 * w + lane / 4) * qrow + (4 * i + lane % 4) * 16);
+      const char* A = static_cast<const char*>(a.A) + jh * (6 * PX * kPiece);
+      af[0] = piece_x(A + lower_index(w, 0) * PX * kPiece, lane * 16, T{});
+      if (w >= 2) af[1] = piece_x(A + lower_index(w, 1) * PX * kPiece, lane * 16, T{});
+    }
+  };
+  if (t.chunks > 0) {
+    fetch1(0);
+    put1();
+    fetch2(0);
+  }
+  __syncthreads();
+  for (int j = 0; j < t.chunks; ++j) {
+    // phase 1
+    const float E = gt[C + 16 * w + l16];
+    if (j + 1 < t.chunks) fetch1(j + 1);
+    cKt.store(lds + oKt, w, lane);
+    typename O::X qf[NK];
+    if constexpr (!KEEP) {
+      // to operand order, 32 values a row at a time, in the wave's own corner of LDS (the exclusive
+      // or as for Rows)
+      char* q = lds + oQ + w * PX * kPiece;
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) {
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+          const int e = (4 * i + lane % 4) * 16 / (int)sizeof(T), px = e % 8 * (int)sizeof(T) / 16;
+          *reinterpret_cast<uint4*>(q + px * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[kb * PX + i];
+        }
+        __builtin_amdgcn_wave_barrier();
+        qf[kb] = piece_x(q, KR::slot(la, l16, 0), T{});
+        __builtin_amdgcn_wave_barrier();
       }
     }
+    __syncthreads();
+    // phase 2
+    if (j + 1 < t.chunks) put1();
+    const char* x = lds + oX;
+    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h;
+    if constexpr (KEEP) {
+      store_rows<T, NW, EX, N>(x, 0, static_cast<T*>(a.S0) + (jh * a.P + p0) * N, rows, w, lane);
+      store_rows<T, NW, EX, C>(x, NK, static_cast<T*>(a.Wt) + (jh * a.P + p0) * C, rows, w, lane);
+    } else {
+      // O with S and W as first operands: rows are values, the lane's column is a token
+      f32x4 o[NW];
+#pragma unroll
+      for (int s = 0; s < NW; ++s) o[s] = kZero4;
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) {
+        typename O::X f[NW];
+#pragma unroll
+        for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + kb) * PX * kPiece, lane * 16, T{});
+        mma_rows(f, qf[kb], o);
+      }
+#pragma unroll
+      for (int s = 0; s < NW; ++s) o[s] *= a.scale * E;
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        if (cb == 0 || w >= 2) {
+          typename O::X f[NW];
+#pragma unroll
+          for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + NK + cb) * PX * kPiece, lane * 16, T{});
+          mma_rows(f, af[cb], o);
+        }
+      }
+      const int c = 16 * w + l16;
+      T* out = static_cast<T*>(a.out) + ((int64_t)(t.start(j) + c) * a.H + h) * a.P + p0 + 8 * la;
+#pragma unroll
+      for (int s = 0; s < NW; s += 2) {
+        float f[8];
+        block8(o[s], o[s + 1], f);
+        if (c < t.len(j) && 16 * s + 8 * la < rows) store_opnd(out + 16 * s, O::round(f));
+      }
+    }
+    if (j + 1 < t.chunks) fetch2(j + 1);
+    __syncthreads();
   }
-  if (a.dinit && live) store_state<N>(a.dinit + srow, lane, S);
+}
+
+// Backward: dS (before the update) and dR are kept for ssd_delta_local.hip.
+template <typename T, int N, int NW>
+__global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const DeltaArgs a, const ChunkMap cm,
+                                                                          int blocks) {
+  using O = Opnd<T>;
+  using KR = Rows<T, N>;
+  using VB = Block<T, NW>;
+  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
+  constexpr int oK = 0, oA = oK + 4 * NK * PX * kPiece, oT = oA + 6 * PS * kPiece, oG = oT + 6 * PS * kPiece;
+  constexpr int oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece, oX = oKt + TP * kPiece;
+  __shared__ __attribute__((aligned(16))) char lds[oX + NW * EX * PX * kPiece];
+
+  const ChainTask t(a, cm, blockIdx.x, blocks);
+  if (t.none) return;
+  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15;
+  const int h = t.h, p0 = t.block * 16 * NW, rows = min(16 * NW, a.P - p0);
+  const float* gt = reinterpret_cast<const float*>(lds + oG);
+
+  if (wave < NW) {
+    const int p = tile_row(wave, l16);
+    const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0 + p) * N;
+    const uint32_t rs = lane * 16, rk[2] = {KR::read(lane, 0), KR::read(lane, 1)};
+    f32x4 S[NT];
+    load_state<N>(a.dfinal + srow, a.dfinal && p < rows, lane, S);
+    __syncthreads();
+    for (int j = t.chunks - 1; j >= 0; --j) {
+      // phase 1
+      typename O::S sf[NK], rf[2], qf[2];
+      typename O::X of[2];
+      char* x = lds + oX + wave * EX * PX * kPiece;
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) {
+        float f[8];
+        block8(S[2 * kb], S[2 * kb + 1], f);
+        sf[kb] = O::split(f);
+        put_piece(x + kb * PX * kPiece, rs, O::hi(sf[kb]));
+      }
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) of[cb] = column_opnd<NW>(lds + oV, wave, cb, lane, T{});
+      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) {
+        typename O::X kf[4];
+        lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf);
+        mma_rows(kf, sf[kb], y);
+      }
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        float D[8];
+        row8(gt + 2 * C, cb, lane, D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[2 * cb][e] *= D[e];
+          y[2 * cb + 1][e] *= D[4 + e];
+        }
+      }
+      {
+        typename O::S t0[2], t1[4];               // the upper triangle's tiles of cb 0, of cb 1
+        lds_ss<2, T>(lds + oA, rs, t0);
+        lds_ss<4, T>(lds + oA + 2 * PS * kPiece, rs, t1);
+        mma_rows(t0, of[0], y);
+        mma_rows(t1, of[1], y);
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) {
+          float f[8];
+          block8(y[2 * cb], y[2 * cb + 1], f);
+          rf[cb] = O::split(f);
+        }
+        lds_ss<2, T>(lds + oT, rs, t0);
+        lds_ss<4, T>(lds + oT + 2 * PS * kPiece, rs, t1);
+        y[0] = y[1] = y[2] = y[3] = kZero4;
+        mma_rows(t0, rf[0], y);
+        mma_rows(t1, rf[1], y);
+      }
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        float f[8], be[8], E[8], o[8];
+        block8(y[2 * cb], y[2 * cb + 1], f);
+        put_piece(x + (NK + cb) * PX * kPiece, rs, O::round(f));
+        row8(gt, cb, lane, be);
+        row8(gt + C, cb, lane, E);
+        O::get(of[cb], o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] *= -be[e] * E[e];
+          o[e] *= a.scale * E[e];
+        }
+        rf[cb] = O::split(f);
+        qf[cb] = O::split(o);
+      }
+      const float EC = gt[2 * C - 1];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) S[i] *= EC;
+      __syncthreads();
+      // phase 2
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        typename O::X f[NT];
+        lds_xs<NT, T>(lds + oQt + cb * NT * PX * kPiece, rs, f);
+        mma_rows(f, qf[cb], S);
+        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, f);
+        mma_rows(f, rf[cb], S);
+      }
+      __syncthreads();
+    }
+    if (a.dinit && p < rows) store_state<N>(a.dinit + srow, lane, S);
+    return;
+  }
+
+  const int w = wave - NW;                        // helper
+  const uint32_t qrow = (uint32_t)a.G * N * sizeof(T), vrow = (uint32_t)a.H * a.P * sizeof(T);
+  KR cK;
+  Copied<6 * PS> cA, cT;
+  VB cV;
+  uint4 cG;
+  Copied<TP> cQt, cKt;
+  auto fetch1 = [&](int j) {
+    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, qo = ((int64_t)t.start(j) * a.G + t.g) * N;
+    cK.load(buf_rsrc(static_cast<const T*>(a.k) + qo, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
+    cA.load(static_cast<const char*>(a.At) + jh * (6 * PS * kPiece), w, lane);
+    cT.load(static_cast<const char*>(a.Tt) + jh * (6 * PS * kPiece), w, lane);
+    cV.load(buf_rsrc(static_cast<const T*>(a.dout) + ((int64_t)t.start(j) * a.H + h) * a.P + p0,
+                     rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cG = buf_load16(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), lane * 16);
+  };
+  auto put1 = [&]() {
+    cK.store(lds + oK, w, lane);
+    cA.store(lds + oA, w, lane);
+    cT.store(lds + oT, w, lane);
+    cV.store(lds + oV, w, lane);
+    if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
+  };
+  auto fetch2 = [&](int j) {
+    const int64_t jg = (int64_t)(t.c0 + j) * a.G + t.g;
+    cQt.load(static_cast<const char*>(a.qt) + jg * (TP * kPiece), w, lane);
+    cKt.load(static_cast<const char*>(a.kt) + jg * (TP * kPiece), w, lane);
+  };
+  if (t.chunks > 0) {
+    fetch1(t.chunks - 1);
+    put1();
+    fetch2(t.chunks - 1);
+  }
+  __syncthreads();
+  for (int j = t.chunks - 1; j >= 0; --j) {
+    // phase 1
+    if (j > 0) fetch1(j - 1);
+    cQt.store(lds + oQt, w, lane);
+    cKt.store(lds + oKt, w, lane);
+    __syncthreads();
+    // phase 2
+    if (j > 0) put1();
+    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h;
+    store_rows<T, NW, EX, N>(lds + oX, 0, static_cast<T*>(a.dS) + (jh * a.P + p0) * N, rows, w, lane);
+    store_rows<T, NW, EX, C>(lds + oX, NK, static_cast<T*>(a.dRt) + (jh * a.P + p0) * C, rows, w, lane);
+    if (j > 0) fetch2(j - 1);
+    __syncthreads();
+  }
 }
 
 enum class Chain { fwd, keep, bwd };
@@ -460,7 +601,7 @@ enum class Chain { fwd, keep, bwd };
 template <Chain K, typename T, int N, int NW>
 hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
   const int blocks = (a.P + 16 * NW - 1) / (16 * NW);
-  const dim3 grid(chain_grid(a, blocks)), th(64 * NW);
+  const dim3 grid((unsigned)(((int64_t)a.nstates * a.H + 7) / 8 * 8 * blocks)), th(64 * (NW + HW));
   if constexpr (K == Chain::bwd)
     hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW>), grid, th, 0, s, a, a.cmap(), blocks);
   else
@@ -470,10 +611,19 @@ hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
 
 template <Chain K, typename T>
 hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
+  // fp32 operands of 128 x 128 heads leave LDS for two state waves backward
+  constexpr int most = sizeof(T) == 4 && K == Chain::bwd ? 2 : 4;
+  if (a.P <= 32) {
+    switch (a.N) {
+      case 32: return chain_go<K, T, 32, 2>(a, s);
+      case 64: return chain_go<K, T, 64, 2>(a, s);
+      case 128: return chain_go<K, T, 128, 2>(a, s);
+    }
+  }
   switch (a.N) {
-    case 32: return chain_go<K, T, 32, 2>(a, s);
-    case 64: return chain_go<K, T, 64, 2>(a, s);
-    case 128: return chain_go<K, T, 128, K == Chain::bwd ? 2 : 4>(a, s);
+    case 32: return chain_go<K, T, 32, 4>(a, s);
+    case 64: return chain_go<K, T, 64, 4>(a, s);
+    case 128: return chain_go<K, T, 128, most>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -74,22 +74,61 @@ template <> struct Opnd<float> {
   }
 };
 
-__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+// A product's instructions one by one: step i of `steps`.  Low parts come first.
+__device__ __forceinline__ f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mma(bf16x8 a, const Pair& b, f32x4 c) {
-  return mma(a, b.hi, mma(a, b.lo, c));
-}
-__device__ __forceinline__ f32x4 mma(const Pair& a, bf16x8 b, f32x4 c) {
-  return mma(a.hi, b, mma(a.lo, b, c));
-}
-__device__ __forceinline__ f32x4 mma(const Pair& a, const Pair& b, f32x4 c) {
-  return mma(a.hi, b.hi, mma(a.hi, b.lo, mma(a.lo, b.hi, c)));
-}
-__device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
+template <typename A, typename B> struct Steps;
+template <> struct Steps<bf16x8, bf16x8> {
+  static constexpr int n = 1;
+  __device__ __forceinline__ static f32x4 step(int, bf16x8 a, bf16x8 b, f32x4 c) { return mma16(a, b, c); }
+};
+template <> struct Steps<bf16x8, Pair> {
+  static constexpr int n = 2;
+  __device__ __forceinline__ static f32x4 step(int i, bf16x8 a, const Pair& b, f32x4 c) {
+    return mma16(a, i ? b.hi : b.lo, c);
+  }
+};
+template <> struct Steps<Pair, bf16x8> {
+  static constexpr int n = 2;
+  __device__ __forceinline__ static f32x4 step(int i, const Pair& a, bf16x8 b, f32x4 c) {
+    return mma16(i ? a.hi : a.lo, b, c);
+  }
+};
+template <> struct Steps<Pair, Pair> {
+  static constexpr int n = 3;
+  __device__ __forceinline__ static f32x4 step(int i, const Pair& a, const Pair& b, f32x4 c) {
+    return mma16(i == 0 ? a.lo : a.hi, i == 1 ? b.lo : b.hi, c);
+  }
+};
+template <> struct Steps<F8, F8> {
+  static constexpr int n = 8;
+  __device__ __forceinline__ static f32x4 step(int i, const F8& a, const F8& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+  }
+};
+
+template <typename A, typename B>
+__device__ __forceinline__ f32x4 mma(const A& a, const B& b, f32x4 c) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+  for (int i = 0; i < Steps<A, B>::n; ++i) c = Steps<A, B>::step(i, a, b, c);
   return c;
+}
+// c[m] += a[m] b, or a b[m], for M results: an instruction that adds to the result of the
+// one before waits for it, so the results take turns.
+template <int M, typename A, typename B>
+__device__ __forceinline__ void mma_rows(const A (&a)[M], const B& b, f32x4* c) {
+#pragma unroll
+  for (int i = 0; i < Steps<A, B>::n; ++i)
+#pragma unroll
+    for (int m = 0; m < M; ++m) c[m] = Steps<A, B>::step(i, a[m], b, c[m]);
+}
+template <int M, typename A, typename B>
+__device__ __forceinline__ void mma_cols(const A& a, const B (&b)[M], f32x4* c) {
+#pragma unroll
+  for (int i = 0; i < Steps<A, B>::n; ++i)
+#pragma unroll
+    for (int m = 0; m < M; ++m) c[m] = Steps<A, B>::step(i, a, b[m], c[m]);
 }
 
 constexpr f32x4 kZero4 = {0.f, 0.f, 0.f, 0.f};
@@ -131,6 +170,42 @@ __device__ __forceinline__ void store_opnd(bf16* p, bf16x8 v) { *reinterpret_cas
 __device__ __forceinline__ void store_opnd(float* p, const F8& v) {
   *reinterpret_cast<f32x4*>(p) = f32x4{v.v[0], v.v[1], v.v[2], v.v[3]};
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{v.v[4], v.v[5], v.v[6], v.v[7]};
+}
+
+// Operands in memory and LDS: pieces of 64 lanes' 16 bytes, one lane after another, each a
+// 16x32 tile of rounded bf16; a pair takes two (high parts, low parts), as does fp32 (values
+// 0 to 3, 4 to 7).  A [N][64] matrix is in the order [32-block of columns][tile of rows].  Of a
+// triangular [64][64] one the tiles that are not zero follow in the order (tile of rows,
+// block of columns): lower (0,0) (1,0) (2,0) (3,0) (2,1) (3,1), upper (0,0) (1,0) (0,1) (1,1)
+// (2,1) (3,1).
+__host__ __device__ constexpr int lower_index(int u, int cb) { return cb == 0 ? u : u + 2; }
+__host__ __device__ constexpr int upper_index(int u, int cb) { return cb == 0 ? u : u + 2; }
+__device__ __forceinline__ int2 lower_tile(int i) { return i < 4 ? make_int2(i, 0) : make_int2(i - 2, 1); }
+__device__ __forceinline__ int2 upper_tile(int i) { return i < 2 ? make_int2(i, 0) : make_int2(i - 2, 1); }
+
+// The operand at `p`; `slot`: the lane's place in a piece.
+__device__ __forceinline__ bf16x8 piece_x(const char* p, uint32_t slot, bf16) {
+  return *reinterpret_cast<const bf16x8*>(p + slot);
+}
+__device__ __forceinline__ F8 piece_x(const char* p, uint32_t slot, float) {
+  F8 f;
+  block8(*reinterpret_cast<const f32x4*>(p + slot), *reinterpret_cast<const f32x4*>(p + kPiece + slot), f.v);
+  return f;
+}
+__device__ __forceinline__ Pair piece_s(const char* p, uint32_t slot, bf16) {
+  return {piece_x(p, slot, bf16{}), piece_x(p + kPiece, slot, bf16{})};
+}
+__device__ __forceinline__ F8 piece_s(const char* p, uint32_t slot, float) { return piece_x(p, slot, 0.f); }
+__device__ __forceinline__ void put_piece(char* p, uint32_t slot, bf16x8 v) {
+  *reinterpret_cast<bf16x8*>(p + slot) = v;
+}
+__device__ __forceinline__ void put_piece(char* p, uint32_t slot, const F8& v) {
+  *reinterpret_cast<f32x4*>(p + slot) = f32x4{v.v[0], v.v[1], v.v[2], v.v[3]};
+  *reinterpret_cast<f32x4*>(p + kPiece + slot) = f32x4{v.v[4], v.v[5], v.v[6], v.v[7]};
+}
+__device__ __forceinline__ void put_piece(char* p, uint32_t slot, const Pair& v) {
+  put_piece(p, slot, v.hi);
+  put_piece(p + kPiece, slot, v.lo);
 }
 
 // Sum over the four lanes that hold one column's rows.

@@ -132,8 +132,9 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   const uint32_t qbytes = (uint32_t)(d.len - 1) * qrow + N * sizeof(T);
   const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + qo, qbytes);
   const __amdgpu_buffer_rsrc_t kr = buf_rsrc(static_cast<const T*>(a.k) + qo, qbytes);
-  const T* kt = static_cast<const T*>(a.kt) + ((int64_t)j * a.G + g) * N * C;
-  const T* qt = static_cast<const T*>(a.qt) + ((int64_t)j * a.G + g) * N * C;
+  const int64_t tr = ((int64_t)j * a.G + g) * (NT * 2) * O::PX * kPiece;
+  const char* kt = static_cast<const char*>(a.kt) + tr;
+  const char* qt = static_cast<const char*>(a.qt) + tr;
 
   X ko[NK], qn[NK];                               // the token's k and q
 #pragma unroll
@@ -273,8 +274,8 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       f32x4 q = yq[i] * E, x = yx[i] * -E, k = yd[i] * Dc;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        const int64_t at = (int64_t)tile_row(i, l16) * C + 32 * cb + 8 * la;
-        const X kf = load_opnd(kt + at), qf = load_opnd(qt + at);
+        const int at = (cb * NT + i) * O::PX * kPiece;
+        const X kf = piece_x(kt + at, lane * 16, T{}), qf = piece_x(qt + at, lane * 16, T{});
         q = mma(kf, pr[cb], q);
         x = mma(kf, mr[cb], x);
         k = mma(qf, pc[cb], k);

@@ -33,14 +33,22 @@ __device__ __forceinline__ float load_gate(const void* p, bool b16, int64_t i) {
   return b16 ? to_f32(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// One row of a matrix that later launches read as operands: as two bf16 planes, or fp32.
-__device__ __forceinline__ void store_pair(bf16* m, int at, const float (&f)[8]) {
-  const Pair s = Opnd<bf16>::split(f);
-  store_opnd(m + at, s.hi);
-  store_opnd(m + C * C + at, s.lo);
+// Columns 32 cb + 8 (lane / 16) .. + 7 of rows that are a [C][pitch] tile's columns, dealt tile
+// u of them: the transposed tile's operand.
+__device__ __forceinline__ bf16x8 transposed_opnd(const bf16* t, int pitch, int u, int cb, int lane) {
+  const int m = lane & 15;
+  const bf16* p = t + (32 * cb + 8 * (lane >> 4) + (m >> 2)) * pitch + 32 * (u >> 1) + 8 * (m & 3) + 4 * (u & 1);
+  const i16x4 lo = lds_tr16_b64(p), hi = lds_tr16_b64(p + 4 * pitch);
+  typedef short i16x8v __attribute__((ext_vector_type(8)));
+  const i16x8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
 }
-__device__ __forceinline__ void store_pair(float* m, int at, const float (&f)[8]) {
-  store_opnd(m + at, Opnd<float>::round(f));
+__device__ __forceinline__ F8 transposed_opnd(const float* t, int pitch, int u, int cb, int lane) {
+  F8 f;
+  const float* p = t + (32 * cb + 8 * (lane >> 4)) * pitch + tile_row(u, lane & 15);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.v[e] = p[e * pitch];
+  return f;
 }
 
 template <typename T, int N, bool BWD>
@@ -124,8 +132,8 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prep_kernel(const DeltaArg
         Ls[i * LP + c] = c < i ? bs[i] * fexp<T>((float)(Gs[i] - Gs[c])) * kk[r] : 0.f;
       }
     }
-    // A[i][c] forward: lane's row i = 16 w + l16, columns c = 16 u + 4 la + r; backward its
-    // transpose At[c][i]: lane's row c = 16 w + l16, columns i.  Zero above the diagonal.
+    // A forward: lane's row i = 16 w + l16, columns c = 16 u + 4 la + r; backward its transpose:
+    // lane's row c = 16 w + l16, columns i.  Zero above the diagonal.
     const int mine = 16 * w + l16;
     float f[4];
 #pragma unroll
@@ -134,21 +142,29 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prep_kernel(const DeltaArg
       const bool in = lo <= hi && hi < d.len;
       f[r] = in ? a.scale * fexp<T>((float)(Gs[hi] - Gs[lo])) * qk[r] : 0.f;
     }
-    const int at = mine * C + 16 * u + 4 * la;
-    if constexpr (sizeof(T) == 4) {
-      float* m = static_cast<float*>(BWD ? a.At : a.A) + jhi * C * C;
-      *reinterpret_cast<f32x4*>(m + at) = f32x4{f[0], f[1], f[2], f[3]};
-    } else {
-      bf16* m = static_cast<bf16*>(BWD ? a.At : a.A) + jhi * C * C * (BWD ? 2 : 1);
-      bf16x4 hi;
+    // four of the eight values of a lane: forward rows as they lie, backward dealt
+    const int cb = u / 2, t = BWD ? 2 * (mine / 32) + (mine / 4 & 1) : w;
+    const int i = BWD ? mine % 32 / 8 * 4 + mine % 4 : l16;
+    const uint32_t slot = 16u * (16 * (2 * (u & 1) + (la >> 1)) + i);
+    const bool kept = BWD ? cb == 1 || t < 2 : cb == 0 || t >= 2;
+    if (kept) {
+      if constexpr (sizeof(T) == 4) {
+        char* p = static_cast<char*>(BWD ? a.At : a.A) + (jhi * 12 + (BWD ? upper_index(t, cb) : lower_index(t, cb)) * 2) * kPiece;
+        *reinterpret_cast<f32x4*>(p + (la & 1) * kPiece + slot) = f32x4{f[0], f[1], f[2], f[3]};
+      } else {
+        bf16x4 hi, lo;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) hi[r] = static_cast<bf16>(f[r]);
-      *reinterpret_cast<bf16x4*>(m + at) = hi;
-      if constexpr (BWD) {
-        bf16x4 lo;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lo[r] = static_cast<bf16>(f[r] - static_cast<float>(hi[r]));
-        *reinterpret_cast<bf16x4*>(m + C * C + at) = lo;
+        for (int r = 0; r < 4; ++r) {
+          hi[r] = static_cast<bf16>(f[r]);
+          lo[r] = static_cast<bf16>(f[r] - static_cast<float>(hi[r]));
+        }
+        if constexpr (BWD) {
+          char* p = static_cast<char*>(a.At) + (jhi * 12 + upper_index(t, cb) * 2) * kPiece + slot + 8 * (la & 1);
+          *reinterpret_cast<bf16x4*>(p) = hi;
+          *reinterpret_cast<bf16x4*>(p + kPiece) = lo;
+        } else {
+          *reinterpret_cast<bf16x4*>(static_cast<char*>(a.A) + (jhi * 6 + lower_index(t, cb)) * kPiece + slot + 8 * (la & 1)) = hi;
+        }
       }
     }
   }
@@ -202,37 +218,34 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prep_kernel(const DeltaArg
   }
   __syncthreads();
 
-  // T, and for the backward its transpose, as operands
-  constexpr int TSZ = sizeof(T) == 4 ? C * C : 2 * C * C;
-  for (int i = tid; i < C * 8; i += kPrepThreads) {
-    const int r = i / 8, c0 = i % 8 * 8;
+  // T, and for the backward its transpose
+  const uint32_t slot = lane * 16;
+  for (int x = w; x < 6; x += 4) {
+    const int2 t = lower_tile(x);
+    const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
     float f[8];
+    block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? Ts[r * LP + c0 + e] : 0.f;
-    store_pair(static_cast<T*>(a.T) + jhi * TSZ, r * C + c0, f);
+    for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] : 0.f;
+    put_piece(static_cast<char*>(a.T) + (jhi * 12 + x * 2) * kPiece, slot, O::split(f));
   }
   if constexpr (BWD) {
-    for (int i = tid; i < C * 8; i += kPrepThreads) {
-      const int r = i % C, c0 = i / C * 8;
+    for (int x = w; x < 6; x += 4) {
+      const int2 t = upper_tile(x);
+      const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = c0 + e >= r ? Ts[(c0 + e) * LP + r] : 0.f;
-      store_pair(static_cast<T*>(a.Tt) + jhi * TSZ, r * C + c0, f);
+      put_piece(static_cast<char*>(a.Tt) + (jhi * 12 + x * 2) * kPiece, slot, O::split(f));
     }
   }
   // k (and q) transposed, once per group
   if (h % rep == 0) {
-    for (int i = tid; i < N * (C / V); i += kPrepThreads) {
-      const int n = i % N, c0 = i / N * V;
-      T f[V], q[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        f[e] = Ks[(c0 + e) * XP + n];
-        if constexpr (BWD) q[e] = Qs[(c0 + e) * XP + n];
-      }
-      const int64_t at = (jgi * N + n) * C + c0;
-      __builtin_memcpy(static_cast<T*>(a.kt) + at, f, 16);
-      if constexpr (BWD) __builtin_memcpy(static_cast<T*>(a.qt) + at, q, 16);
+    for (int x = w; x < N / 16 * 2; x += 4) {
+      const int u = x % (N / 16), cb = x / (N / 16);
+      const int64_t at = (jgi * (N / 16 * 2) + x) * O::PX * kPiece;
+      put_piece(static_cast<char*>(a.kt) + at, slot, transposed_opnd(Ks, XP, u, cb, lane));
+      if constexpr (BWD) put_piece(static_cast<char*>(a.qt) + at, slot, transposed_opnd(Qs, XP, u, cb, lane));
     }
   }
 }
