@@ -10,7 +10,7 @@
 namespace ssd {
 
 constexpr int kDeltaChunk = 64;              // tokens per chunk
-constexpr int kGateFloats = 5 * kDeltaChunk; // per (chunk, head): beta, E, D, and G in fp64
+constexpr int kGateFloats = 6 * kDeltaChunk; // per (chunk, head): beta, E, D, beta E, and G in fp64
 constexpr int kPiece = 1024;                 // bytes of 64 lanes' 16: operands lie in such pieces
 // Pieces of a triangular 64x64 matrix (six 16x32 tiles of eight), rounded or as pairs, and of a
 // [N][64] one.
@@ -26,6 +26,7 @@ struct DeltaArgs {
   int max_chunks, nc_row;
   bool bf16, gate_bf16;
   bool clear;             // rows outside every sequence become zeros
+  bool pairs;             // backward: what the chains keep is kept as pairs (bf16)
   float scale;
   const void* q;
   const void* k;
@@ -57,10 +58,11 @@ struct DeltaArgs {
   void* Tt;               // T transposed, upper, pairs
   void* At;               // A transposed, upper, pairs
   void* qt;               // per (chunk, group): q transposed
-  void* S0;               // [P][N] the state entering the chunk, dtype
-  void* dS;               // [P][N] the gradient of the state leaving it, dtype
-  void* Wt;               // [P][64] the rows w, transposed, dtype
-  void* dRt;              // [P][64] their gradient before T, transposed, dtype
+  void* S0;               // [P][N] the state entering the chunk, dtype (two with pairs: high
+                          // and low parts; so the next three)
+  void* dS;               // [P][N] the gradient of the state leaving it
+  void* Wt;               // [P][64] the rows w, transposed
+  void* dRt;              // [P][64] their gradient before T, transposed
 
   ChunkMap cmap() const {
     ChunkMap m;

@@ -16,6 +16,12 @@ namespace {
 
 constexpr size_t kDeltaAlign = 256;
 
+// Backward, bf16: what the chains keep is kept as pairs where the gates' gradients are wanted in
+// fp32, and where there are few of them.  Each is a sum with cancellation of products of what is
+// kept, rounded to 2^-9: over many their errors average (2.6e-3 in the 2-norm), a handful may be
+// off by several times that.
+constexpr int64_t kDeltaFewGates = 65536;
+
 bool dtype_ok(int32_t d) { return d == SSD_F32 || d == SSD_BF16; }
 size_t elem_size(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -73,6 +79,7 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   a.gate_bf16 = p->gate_dtype == SSD_BF16;
   a.clear = p->nseq > 0 && p->clear_outside == 1;
   a.scale = p->scale;
+  a.pairs = a.bf16 && (!a.gate_bf16 || (int64_t)a.total * a.H < kDeltaFewGates);
   return a;
 }
 
@@ -101,10 +108,11 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
   part(a.Tt, mh * pair);
   part(a.At, mh * pair);
   part(a.qt, mg * tr);
-  part(a.S0, mh * a.P * a.N * e);
-  part(a.dS, mh * a.P * a.N * e);
-  part(a.Wt, mh * a.P * C * e);
-  part(a.dRt, mh * a.P * C * e);
+  const size_t ke = a.pairs ? 4 : e;
+  part(a.S0, mh * a.P * a.N * ke);
+  part(a.dS, mh * a.P * a.N * ke);
+  part(a.Wt, mh * a.P * C * ke);
+  part(a.dRt, mh * a.P * C * ke);
   return off;
 }
 

@@ -20,9 +20,9 @@
 // a barrier after each; each half of the operands is read in one and replaced in the other,
 // so one copy in LDS is enough:
 //              state waves                         helper waves
-//   phase 1    S and W as operands to LDS;         K^T of this chunk to LDS; loads of the next
-//              W by K, T, V                        chunk's K, T, V
-//   phase 2    S by K^T                            next K, T, V to LDS; O; loads of its K^T
+//   phase 1    W by K, T, V; S and W as operands   loads of the next chunk's operands; K^T of
+//              to LDS                              this one to LDS; O of the chunk before
+//   phase 2    S by K^T                            next K, T, V to LDS
 //
 // 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): MEASURED.
 #include "ssd_delta_device.h"
@@ -35,6 +35,7 @@ namespace {
 
 constexpr int C = kDeltaChunk;
 constexpr int HW = 4;                     // helper waves
+constexpr int kLdsBytes = 160 * 1024;
 
 // One helper wave's share of `COUNT` loads of 16 bytes per lane on their way from memory to
 // LDS, through registers.
@@ -221,33 +222,39 @@ __device__ __forceinline__ void store_state(float* row, int lane, const f32x4 (&
 }
 
 // Operands that the state waves left in LDS ([wave][EX of them], from the `from`-th on, each 32
-// columns of 16 dealt rows) to rows of a [P][COLS] matrix of T.
-template <typename T, int NW, int EX, int COLS>
-__device__ __forceinline__ void store_rows(const char* x, int from, T* dst, int rows, int w, int lane) {
-  constexpr int PX = Opnd<T>::PX, V = 16 / (int)sizeof(T), PR = COLS / V, all = 16 * NW * PR;
+// columns of 16 dealt rows) to rows of a [P][COLS] matrix of T, or of two, one behind the other.
+template <typename T, int NW, int EX, int COLS, bool PAIR>
+__device__ __forceinline__ void store_rows(const char* x, int from, T* dst, int64_t plane, int rows, int w, int lane) {
+  constexpr int PX = Opnd<T>::PX, PL = kPlanes<T, PAIR>, V = 16 / (int)sizeof(T), PR = COLS / V, all = 16 * NW * PR;
 #pragma unroll
   for (int i = 0; i < (all + 64 * HW - 1) / (64 * HW); ++i) {
     const int at = (i * HW + w) * 64 + lane, p = at / PR, c = at % PR * V;
     if (all % (64 * HW) && at >= all) break;
     const int s = 2 * (p / 32) + (p / 4 & 1), l16 = p % 32 / 8 * 4 + p % 4;
     const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
-    const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX + px) * kPiece + (16 * a + l16) * 16);
-    if (p < rows) *reinterpret_cast<uint4*>(dst + (int64_t)p * COLS + c) = v;
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) {
+      const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + (16 * a + l16) * 16);
+      if (p < rows) *reinterpret_cast<uint4*>(dst + pl * plane + (int64_t)p * COLS + c) = v;
+    }
   }
 }
 
-// KEEP: for the backward, S and W are kept (as operands there: rounded) and O is not made.
-template <typename T, int N, int NW, bool KEEP>
+// KEEP: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
+template <typename T, int N, int NW, bool KEEP, bool PAIR>
 __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const DeltaArgs a, const ChunkMap cm,
                                                                       int blocks) {
   using O = Opnd<T>;
   using KR = Rows<T, N>;
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
+  constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
   constexpr int oK = 0, oT = oK + 4 * NK * PX * kPiece, oG = oT + 6 * PS * kPiece, oV = oG + kPiece;
-  constexpr int oKt = oV + VB::bytes, oX = oKt + TP * kPiece, oQ = oX + NW * EX * PX * kPiece;
-  constexpr int kBytes = oQ + (KEEP ? 0 : HW * PX * kPiece);
-  __shared__ __attribute__((aligned(16))) char lds[kBytes];
+  constexpr int QS = sizeof(T) == 2 ? NK : 1;     // 32-blocks of Q that a helper's corner takes
+  constexpr int oKt = oV + VB::bytes, oQ = oKt + TP * kPiece;
+  constexpr int oX = oQ + (KEEP ? 0 : HW * QS * PX * kPiece), kX = NW * EX * PE * kPiece;
+  constexpr bool DX = oX + 2 * kX <= kLdsBytes;   // two copies of what the state waves leave
+  __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
   const ChainTask t(a, cm, blockIdx.x, blocks);
   if (t.none) return;
@@ -265,60 +272,61 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     for (int j = 0; j < t.chunks; ++j) {
       // phase 1
       typename O::S sf[NK], rf[2];
-      char* x = lds + oX + wave * EX * PX * kPiece;
+      typename O::X kf[NK][4];
+      float v[2][8], be[2][8], bE[2][8], D[2][8];
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v[cb]);
+        row8(gt, cb, lane, be[cb]);
+        row8(gt + 3 * C, cb, lane, bE[cb]);
+        row8(gt + 2 * C, cb, lane, D[cb]);
+      }
+      const float EC = gt[2 * C - 1];
+      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb) {
         float f[8];
         block8(S[2 * kb], S[2 * kb + 1], f);
         sf[kb] = O::split(f);
-        put_piece(x + kb * PX * kPiece, rs, O::hi(sf[kb]));
+        mma_rows(kf[kb], sf[kb], y);
       }
-      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb) {
-        typename O::X kf[4];
-        lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf);
-        mma_rows(kf, sf[kb], y);
-      }
+      typename O::S t0[4], t1[2];
+      lds_ss<4, T>(lds + oT, rs, t0);
+      lds_ss<2, T>(lds + oT + 4 * PS * kPiece, rs, t1);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        float f[8], v[8], be[8], E[8];
+        float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v);
-        row8(gt, cb, lane, be);
-        row8(gt + C, cb, lane, E);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = be[e] * (v[e] - E[e] * f[e]);
+        for (int e = 0; e < 8; ++e) f[e] = be[cb][e] * v[cb][e] - bE[cb][e] * f[e];
         rf[cb] = O::split(f);
       }
-      {
-        typename O::S t0[4], t1[2];
-        lds_ss<4, T>(lds + oT, rs, t0);
-        lds_ss<2, T>(lds + oT + 4 * PS * kPiece, rs, t1);
-        y[0] = y[1] = y[2] = y[3] = kZero4;
-        mma_rows(t0, rf[0], y);
-        mma_rows(t1, rf[1], y + 2);
-      }
+      y[0] = y[1] = y[2] = y[3] = kZero4;
+      mma_rows(t0, rf[0], y);
+      mma_rows(t1, rf[1], y + 2);
+      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, rs, keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        float f[8], D[8];
+        float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PX * kPiece, rs, O::round(f));
-        row8(gt + 2 * C, cb, lane, D);
+        put_piece(x + (NK + cb) * PE * kPiece, rs, keep<T, PAIR>(f));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= D[e];
+        for (int e = 0; e < 8; ++e) f[e] *= D[cb][e];
         rf[cb] = O::split(f);
       }
-      const float EC = gt[2 * C - 1];
 #pragma unroll
       for (int i = 0; i < NT; ++i) S[i] *= EC;
       __syncthreads();
       // phase 2
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        typename O::X kf[NT];
-        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, kf);
-        mma_rows(kf, rf[cb], S);
+        typename O::X f[NT];
+        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, f);
+        mma_rows(f, rf[cb], S);
       }
       __syncthreads();
     }
@@ -333,13 +341,24 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   VB cV;
   uint4 cG;
   Copied<TP> cKt;
+  // the next chunk's in memory
+  const int64_t jh0 = (int64_t)t.c0 * a.H + h, jg0 = (int64_t)t.c0 * a.G + t.g;
+  const char* kp = static_cast<const char*>(a.k) + ((int64_t)t.first * a.G + t.g) * N * sizeof(T);
+  const char* qp = static_cast<const char*>(a.q) + ((int64_t)t.first * a.G + t.g) * N * sizeof(T);
+  const char* vp = static_cast<const char*>(a.v) + (((int64_t)t.first * a.H + h) * a.P + p0) * sizeof(T);
+  const char* Tp = static_cast<const char*>(a.T) + jh0 * (6 * PS * kPiece);
+  const char* Ap = static_cast<const char*>(a.A) + jh0 * (6 * PX * kPiece);
+  const char* gp = reinterpret_cast<const char*>(a.gates + jh0 * kGateFloats);
+  const char* tp = static_cast<const char*>(a.kt) + jg0 * (TP * kPiece);
   auto fetch1 = [&](int j) {
-    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, qo = ((int64_t)t.start(j) * a.G + t.g) * N;
-    cK.load(buf_rsrc(static_cast<const T*>(a.k) + qo, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
-    cT.load(static_cast<const char*>(a.T) + jh * (6 * PS * kPiece), w, lane);
-    cV.load(buf_rsrc(static_cast<const T*>(a.v) + ((int64_t)t.start(j) * a.H + h) * a.P + p0,
-                     rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
-    cG = buf_load16(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), lane * 16);
+    cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
+    cT.load(Tp, w, lane);
+    cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cG = buf_load16(buf_rsrc(gp, kGateFloats * 4), lane * 16);
+    kp += C * (int64_t)qrow;
+    vp += C * (int64_t)vrow;
+    Tp += a.H * (6 * PS * kPiece);
+    gp += a.H * (kGateFloats * 4);
   };
   auto put1 = [&]() {
     cK.store(lds + oK, w, lane);
@@ -347,59 +366,56 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     cV.store(lds + oV, w, lane);
     if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
   };
-  // helper w makes the outputs of tokens 16 w ..; their rows of Q, four lanes on 64 bytes, and
+  // helper w makes the outputs of tokens 16 w ..: their rows of Q, four lanes on 64 bytes, and
   // of A, as operands
   uint4 cQ[NK * PX];
-  typename O::X af[2];
+  typename O::X cA[2];
   auto fetch2 = [&](int j) {
-    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, jg = (int64_t)(t.c0 + j) * a.G + t.g;
-    cKt.load(static_cast<const char*>(a.kt) + jg * (TP * kPiece), w, lane);
+    cKt.load(tp, w, lane);
+    tp += a.G * (TP * kPiece);
     if constexpr (!KEEP) {
-      const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + ((int64_t)t.start(j) * a.G + t.g) * N,
-                                                 rows_bytes(t.len(j), qrow, N * sizeof(T)));
+      const __amdgpu_buffer_rsrc_t qr = buf_rsrc(qp, rows_bytes(t.len(j), qrow, N * sizeof(T)));
 #pragma unroll
       for (int i = 0; i < NK * PX; ++i) cQ[i] = buf_load16(qr, (16 * w + lane / 4) * qrow + (4 * i + lane % 4) * 16);
-      const char* A = static_cast<const char*>(a.A) + jh * (6 * PX * kPiece);
-      af[0] = piece_x(A + lower_index(w, 0) * PX * kPiece, lane * 16, T{});
-      if (w >= 2) af[1] = piece_x(A + lower_index(w, 1) * PX * kPiece, lane * 16, T{});
+      cA[0] = piece_x(Ap + lower_index(w, 0) * PX * kPiece, lane * 16, T{});
+      if (w >= 2) cA[1] = piece_x(Ap + lower_index(w, 1) * PX * kPiece, lane * 16, T{});
+      qp += C * (int64_t)qrow;
+      Ap += a.H * (6 * PX * kPiece);
     }
   };
-  if (t.chunks > 0) {
-    fetch1(0);
-    put1();
-    fetch2(0);
-  }
-  __syncthreads();
-  for (int j = 0; j < t.chunks; ++j) {
-    // phase 1
-    const float E = gt[C + 16 * w + l16];
-    if (j + 1 < t.chunks) fetch1(j + 1);
-    cKt.store(lds + oKt, w, lane);
-    typename O::X qf[NK];
+  typename O::X qf[NK], af[2];
+  float sE = 0.f;
+  // what chunk j's products with Q need besides S and W; the rows of Q to operand order in the
+  // wave's own corner of LDS (the exclusive or as for Rows)
+  auto ready = [&]() {
     if constexpr (!KEEP) {
-      // to operand order, 32 values a row at a time, in the wave's own corner of LDS (the exclusive
-      // or as for Rows)
-      char* q = lds + oQ + w * PX * kPiece;
+      sE = a.scale * gt[C + 16 * w + l16];
+      char* q = lds + oQ + w * QS * PX * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) {
+      for (int k0 = 0; k0 < NK; k0 += QS) {
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < PX; ++i) {
-          const int e = (4 * i + lane % 4) * 16 / (int)sizeof(T), px = e % 8 * (int)sizeof(T) / 16;
-          *reinterpret_cast<uint4*>(q + px * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[kb * PX + i];
-        }
+        for (int kb = k0; kb < k0 + QS; ++kb)
+#pragma unroll
+          for (int i = 0; i < PX; ++i) {
+            const int e = (4 * i + lane % 4) * 16 / (int)sizeof(T), px = e % 8 * (int)sizeof(T) / 16;
+            *reinterpret_cast<uint4*>(q + ((kb - k0) * PX + px) * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[kb * PX + i];
+          }
         __builtin_amdgcn_wave_barrier();
-        qf[kb] = piece_x(q, KR::slot(la, l16, 0), T{});
-        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int kb = k0; kb < k0 + QS; ++kb) qf[kb] = piece_x(q + (kb - k0) * PX * kPiece, KR::slot(la, l16, 0), T{});
       }
+      af[0] = cA[0];
+      af[1] = cA[1];
     }
-    __syncthreads();
-    // phase 2
-    if (j + 1 < t.chunks) put1();
-    const char* x = lds + oX;
-    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h;
+  };
+  auto finish = [&](int j) {
+    const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
     if constexpr (KEEP) {
-      store_rows<T, NW, EX, N>(x, 0, static_cast<T*>(a.S0) + (jh * a.P + p0) * N, rows, w, lane);
-      store_rows<T, NW, EX, C>(x, NK, static_cast<T*>(a.Wt) + (jh * a.P + p0) * C, rows, w, lane);
+      const int64_t jh = jh0 + (int64_t)j * a.H;
+      constexpr int PL = kPlanes<T, PAIR>;
+      store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+      store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
     } else {
       // O with S and W as first operands: rows are values, the lane's column is a token
       f32x4 o[NW];
@@ -413,7 +429,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
         mma_rows(f, qf[kb], o);
       }
 #pragma unroll
-      for (int s = 0; s < NW; ++s) o[s] *= a.scale * E;
+      for (int s = 0; s < NW; ++s) o[s] *= sE;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         if (cb == 0 || w >= 2) {
@@ -432,22 +448,44 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
         if (c < t.len(j) && 16 * s + 8 * la < rows) store_opnd(out + 16 * s, O::round(f));
       }
     }
-    if (j + 1 < t.chunks) fetch2(j + 1);
+  };
+  if (t.chunks > 0) {
+    fetch1(0);
+    put1();
+    fetch2(0);
+  }
+  __syncthreads();
+  for (int j = 0; j < t.chunks; ++j) {
+    const bool more = j + 1 < t.chunks;
+    // phase 1
+    if (more) fetch1(j + 1);
+    cKt.store(lds + oKt, w, lane);
+    if (DX && j > 0) finish(j - 1);
+    ready();
+    if (more) fetch2(j + 1);
+    __syncthreads();
+    // phase 2
+    if constexpr (!DX) finish(j);
+    if (more) put1();
     __syncthreads();
   }
+  if (DX && t.chunks > 0) finish(t.chunks - 1);
 }
 
-// Backward: dS (before the update) and dR are kept for ssd_delta_local.hip.
-template <typename T, int N, int NW>
+// Backward: dS (before the update) and dR are kept for ssd_delta_local.hip (PAIR: as pairs).
+template <typename T, int N, int NW, bool PAIR>
 __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const DeltaArgs a, const ChunkMap cm,
                                                                           int blocks) {
   using O = Opnd<T>;
   using KR = Rows<T, N>;
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
+  constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
   constexpr int oK = 0, oA = oK + 4 * NK * PX * kPiece, oT = oA + 6 * PS * kPiece, oG = oT + 6 * PS * kPiece;
   constexpr int oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece, oX = oKt + TP * kPiece;
-  __shared__ __attribute__((aligned(16))) char lds[oX + NW * EX * PX * kPiece];
+  constexpr int kX = NW * EX * PE * kPiece;
+  constexpr bool DX = oX + 2 * kX <= kLdsBytes;
+  __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
   const ChainTask t(a, cm, blockIdx.x, blocks);
   if (t.none) return;
@@ -464,70 +502,67 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     __syncthreads();
     for (int j = t.chunks - 1; j >= 0; --j) {
       // phase 1
-      typename O::S sf[NK], rf[2], qf[2];
-      typename O::X of[2];
-      char* x = lds + oX + wave * EX * PX * kPiece;
+      typename O::S sf[NK], rf[2], qf[2], t0[2], t1[4];   // t: the upper triangle's tiles of cb 0, of cb 1
+      typename O::X kf[NK][4], of[2];
+      float D[2][8], E[2][8], bE[2][8];
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        of[cb] = column_opnd<NW>(lds + oV, wave, cb, lane, T{});
+        row8(gt + 2 * C, cb, lane, D[cb]);
+        row8(gt + C, cb, lane, E[cb]);
+        row8(gt + 3 * C, cb, lane, bE[cb]);
+      }
+      const float EC = gt[2 * C - 1];
+      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb) {
         float f[8];
         block8(S[2 * kb], S[2 * kb + 1], f);
         sf[kb] = O::split(f);
-        put_piece(x + kb * PX * kPiece, rs, O::hi(sf[kb]));
+        mma_rows(kf[kb], sf[kb], y);
       }
-#pragma unroll
-      for (int cb = 0; cb < 2; ++cb) of[cb] = column_opnd<NW>(lds + oV, wave, cb, lane, T{});
-      f32x4 y[4] = {kZero4, kZero4, kZero4, kZero4};
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb) {
-        typename O::X kf[4];
-        lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf);
-        mma_rows(kf, sf[kb], y);
-      }
+      lds_ss<2, T>(lds + oA, rs, t0);
+      lds_ss<4, T>(lds + oA + 2 * PS * kPiece, rs, t1);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        float D[8];
-        row8(gt + 2 * C, cb, lane, D);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * cb][e] *= D[e];
-          y[2 * cb + 1][e] *= D[4 + e];
-        }
-      }
-      {
-        typename O::S t0[2], t1[4];               // the upper triangle's tiles of cb 0, of cb 1
-        lds_ss<2, T>(lds + oA, rs, t0);
-        lds_ss<4, T>(lds + oA + 2 * PS * kPiece, rs, t1);
-        mma_rows(t0, of[0], y);
-        mma_rows(t1, of[1], y);
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          float f[8];
-          block8(y[2 * cb], y[2 * cb + 1], f);
-          rf[cb] = O::split(f);
-        }
-        lds_ss<2, T>(lds + oT, rs, t0);
-        lds_ss<4, T>(lds + oT + 2 * PS * kPiece, rs, t1);
-        y[0] = y[1] = y[2] = y[3] = kZero4;
-        mma_rows(t0, rf[0], y);
-        mma_rows(t1, rf[1], y);
-      }
-#pragma unroll
-      for (int cb = 0; cb < 2; ++cb) {
-        float f[8], be[8], E[8], o[8];
-        block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PX * kPiece, rs, O::round(f));
-        row8(gt, cb, lane, be);
-        row8(gt + C, cb, lane, E);
+        float o[8];
         O::get(of[cb], o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] *= -be[e] * E[e];
-          o[e] *= a.scale * E[e];
-        }
-        rf[cb] = O::split(f);
+        for (int e = 0; e < 8; ++e) o[e] *= a.scale * E[cb][e];
         qf[cb] = O::split(o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[2 * cb][e] *= D[cb][e];
+          y[2 * cb + 1][e] *= D[cb][4 + e];
+        }
       }
-      const float EC = gt[2 * C - 1];
+      mma_rows(t0, of[0], y);
+      mma_rows(t1, of[1], y);
+      lds_ss<2, T>(lds + oT, rs, t0);
+      lds_ss<4, T>(lds + oT + 2 * PS * kPiece, rs, t1);
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        float f[8];
+        block8(y[2 * cb], y[2 * cb + 1], f);
+        rf[cb] = O::split(f);
+      }
+      y[0] = y[1] = y[2] = y[3] = kZero4;
+      mma_rows(t0, rf[0], y);
+      mma_rows(t1, rf[1], y);
+      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, rs, keep<T, PAIR>(sf[kb]));
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        float f[8];
+        block8(y[2 * cb], y[2 * cb + 1], f);
+        put_piece(x + (NK + cb) * PE * kPiece, rs, keep<T, PAIR>(f));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= -bE[cb][e];
+        rf[cb] = O::split(f);
+      }
 #pragma unroll
       for (int i = 0; i < NT; ++i) S[i] *= EC;
       __syncthreads();
@@ -553,14 +588,27 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   VB cV;
   uint4 cG;
   Copied<TP> cQt, cKt;
+  // the next chunk's in memory (the first one's is the last)
+  const int last = t.chunks - 1;
+  const int64_t jh0 = (int64_t)t.c0 * a.H + h, jh1 = jh0 + (int64_t)last * a.H;
+  const int64_t jg1 = ((int64_t)t.c0 + last) * a.G + t.g, tok = t.first + (int64_t)last * C;
+  const char* kp = static_cast<const char*>(a.k) + (tok * a.G + t.g) * N * sizeof(T);
+  const char* vp = static_cast<const char*>(a.dout) + ((tok * a.H + h) * a.P + p0) * sizeof(T);
+  const char* Ap = static_cast<const char*>(a.At) + jh1 * (6 * PS * kPiece);
+  const char* Tp = static_cast<const char*>(a.Tt) + jh1 * (6 * PS * kPiece);
+  const char* gp = reinterpret_cast<const char*>(a.gates + jh1 * kGateFloats);
+  int64_t tp = jg1 * (TP * kPiece);
   auto fetch1 = [&](int j) {
-    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h, qo = ((int64_t)t.start(j) * a.G + t.g) * N;
-    cK.load(buf_rsrc(static_cast<const T*>(a.k) + qo, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
-    cA.load(static_cast<const char*>(a.At) + jh * (6 * PS * kPiece), w, lane);
-    cT.load(static_cast<const char*>(a.Tt) + jh * (6 * PS * kPiece), w, lane);
-    cV.load(buf_rsrc(static_cast<const T*>(a.dout) + ((int64_t)t.start(j) * a.H + h) * a.P + p0,
-                     rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
-    cG = buf_load16(buf_rsrc(a.gates + jh * kGateFloats, kGateFloats * 4), lane * 16);
+    cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
+    cA.load(Ap, w, lane);
+    cT.load(Tp, w, lane);
+    cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cG = buf_load16(buf_rsrc(gp, kGateFloats * 4), lane * 16);
+    kp -= C * (int64_t)qrow;
+    vp -= C * (int64_t)vrow;
+    Ap -= a.H * (6 * PS * kPiece);
+    Tp -= a.H * (6 * PS * kPiece);
+    gp -= a.H * (kGateFloats * 4);
   };
   auto put1 = [&]() {
     cK.store(lds + oK, w, lane);
@@ -569,61 +617,68 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     cV.store(lds + oV, w, lane);
     if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
   };
-  auto fetch2 = [&](int j) {
-    const int64_t jg = (int64_t)(t.c0 + j) * a.G + t.g;
-    cQt.load(static_cast<const char*>(a.qt) + jg * (TP * kPiece), w, lane);
-    cKt.load(static_cast<const char*>(a.kt) + jg * (TP * kPiece), w, lane);
+  auto fetch2 = [&]() {
+    cQt.load(static_cast<const char*>(a.qt) + tp, w, lane);
+    cKt.load(static_cast<const char*>(a.kt) + tp, w, lane);
+    tp -= a.G * (TP * kPiece);
+  };
+  auto finish = [&](int j) {
+    const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
+    const int64_t jh = jh0 + (int64_t)j * a.H;
+    constexpr int PL = kPlanes<T, PAIR>;
+    store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.dS) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+    store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.dRt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
   };
   if (t.chunks > 0) {
-    fetch1(t.chunks - 1);
+    fetch1(last);
     put1();
-    fetch2(t.chunks - 1);
+    fetch2();
   }
   __syncthreads();
-  for (int j = t.chunks - 1; j >= 0; --j) {
+  for (int j = last; j >= 0; --j) {
     // phase 1
     if (j > 0) fetch1(j - 1);
     cQt.store(lds + oQt, w, lane);
     cKt.store(lds + oKt, w, lane);
+    if (DX && j < last) finish(j + 1);
+    if (j > 0) fetch2();
     __syncthreads();
     // phase 2
+    if constexpr (!DX) finish(j);
     if (j > 0) put1();
-    const int64_t jh = (int64_t)(t.c0 + j) * a.H + h;
-    store_rows<T, NW, EX, N>(lds + oX, 0, static_cast<T*>(a.dS) + (jh * a.P + p0) * N, rows, w, lane);
-    store_rows<T, NW, EX, C>(lds + oX, NK, static_cast<T*>(a.dRt) + (jh * a.P + p0) * C, rows, w, lane);
-    if (j > 0) fetch2(j - 1);
     __syncthreads();
   }
+  if (DX && t.chunks > 0) finish(0);
 }
 
 enum class Chain { fwd, keep, bwd };
 
-template <Chain K, typename T, int N, int NW>
+template <Chain K, typename T, int N, int NW, bool PAIR>
 hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
   const int blocks = (a.P + 16 * NW - 1) / (16 * NW);
   const dim3 grid((unsigned)(((int64_t)a.nstates * a.H + 7) / 8 * 8 * blocks)), th(64 * (NW + HW));
   if constexpr (K == Chain::bwd)
-    hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW>), grid, th, 0, s, a, a.cmap(), blocks);
+    hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   else
-    hipLaunchKernelGGL((delta_chain_kernel<T, N, NW, K == Chain::keep>), grid, th, 0, s, a, a.cmap(), blocks);
+    hipLaunchKernelGGL((delta_chain_kernel<T, N, NW, K == Chain::keep, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   return hipGetLastError();
 }
 
-template <Chain K, typename T>
+template <Chain K, typename T, bool PAIR>
 hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
-  // fp32 operands of 128 x 128 heads leave LDS for two state waves backward
-  constexpr int most = sizeof(T) == 4 && K == Chain::bwd ? 2 : 4;
+  // fp32 operands of dstate 128 leave LDS for two state waves
+  constexpr int most = sizeof(T) == 4 ? 2 : 4;
   if (a.P <= 32) {
     switch (a.N) {
-      case 32: return chain_go<K, T, 32, 2>(a, s);
-      case 64: return chain_go<K, T, 64, 2>(a, s);
-      case 128: return chain_go<K, T, 128, 2>(a, s);
+      case 32: return chain_go<K, T, 32, 2, PAIR>(a, s);
+      case 64: return chain_go<K, T, 64, 2, PAIR>(a, s);
+      case 128: return chain_go<K, T, 128, 2, PAIR>(a, s);
     }
   }
   switch (a.N) {
-    case 32: return chain_go<K, T, 32, 4>(a, s);
-    case 64: return chain_go<K, T, 64, 4>(a, s);
-    case 128: return chain_go<K, T, 128, most>(a, s);
+    case 32: return chain_go<K, T, 32, 4, PAIR>(a, s);
+    case 64: return chain_go<K, T, 64, 4, PAIR>(a, s);
+    case 128: return chain_go<K, T, 128, most, PAIR>(a, s);
   }
   return hipErrorInvalidValue;
 }
@@ -631,7 +686,10 @@ hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
 template <Chain K>
 hipError_t chain_type(const DeltaArgs& a, hipStream_t s) {
   if (a.nstates <= 0) return hipSuccess;
-  return a.bf16 ? chain_n<K, bf16>(a, s) : chain_n<K, float>(a, s);
+  if (!a.bf16) return chain_n<K, float, false>(a, s);
+  if constexpr (K != Chain::fwd)
+    if (a.pairs) return chain_n<K, bf16, true>(a, s);
+  return chain_n<K, bf16, false>(a, s);
 }
 
 }  // namespace

@@ -35,20 +35,26 @@ template <> struct Opnd<bf16> {
   using X = bf16x8;                    // exact or rounded
   using S = Pair;                      // to 2^-18
   static constexpr int PX = 1, PS = 2; // 16-byte pieces per lane
+  // Two values at a time, as the conversion takes them.
   __device__ __forceinline__ static X round(const float (&f)[8]) {
-    X x;
+    u32x4 x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = static_cast<bf16>(f[e]);
-    return x;
+    for (int e = 0; e < 4; ++e) x[e] = pack(f[2 * e], f[2 * e + 1]);
+    return __builtin_bit_cast(X, x);
   }
   __device__ __forceinline__ static S split(const float (&f)[8]) {
-    S s;
+    u32x4 hi, lo;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s.hi[e] = static_cast<bf16>(f[e]);
-      s.lo[e] = static_cast<bf16>(f[e] - static_cast<float>(s.hi[e]));
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = pack(f[2 * e], f[2 * e + 1]);
+      lo[e] = pack(f[2 * e] - __builtin_bit_cast(float, hi[e] << 16),
+                   f[2 * e + 1] - __builtin_bit_cast(float, hi[e] & 0xffff0000u));
     }
-    return s;
+    return {__builtin_bit_cast(X, hi), __builtin_bit_cast(X, lo)};
+  }
+  __device__ __forceinline__ static uint32_t pack(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
   }
   __device__ __forceinline__ static X hi(const S& s) { return s.hi; }
   __device__ __forceinline__ static void get(const X& x, float (&f)[8]) {
@@ -78,6 +84,10 @@ template <> struct Opnd<float> {
 __device__ __forceinline__ f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+// What is kept of a value for a later product: a pair, or rounded.
+template <typename T, bool PAIR> struct Kept { using V = typename Opnd<T>::X; };
+template <typename T> struct Kept<T, true> { using V = typename Opnd<T>::S; };
+
 template <typename A, typename B> struct Steps;
 template <> struct Steps<bf16x8, bf16x8> {
   static constexpr int n = 1;
@@ -132,6 +142,19 @@ __device__ __forceinline__ void mma_cols(const A& a, const B (&b)[M], f32x4* c) 
 }
 
 constexpr f32x4 kZero4 = {0.f, 0.f, 0.f, 0.f};
+
+template <typename T, bool PAIR>
+__device__ __forceinline__ typename Kept<T, PAIR>::V keep(const float (&f)[8]) {
+  if constexpr (PAIR) return Opnd<T>::split(f);
+  else return Opnd<T>::round(f);
+}
+template <typename T, bool PAIR>
+__device__ __forceinline__ typename Kept<T, PAIR>::V keep(const typename Opnd<T>::S& s) {
+  if constexpr (PAIR) return s;
+  else return Opnd<T>::hi(s);
+}
+// Arrays of T that hold it: a pair's high and low parts.
+template <typename T, bool PAIR> constexpr int kPlanes = PAIR && sizeof(T) == 2 ? 2 : 1;
 
 // Row of result tile t (of 16) that lies in its row i of the instruction.
 __device__ __forceinline__ int tile_row(int t, int i) {

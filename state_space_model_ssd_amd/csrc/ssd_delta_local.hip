@@ -4,7 +4,7 @@
 //   P = tril(dO W^T) * D,   M = -tril(dR W^T, -1) * D   (the gradients of q k^T and, per beta, k k^T)
 // the gradients are
 //   dq = scale (E dO S + P K)
-//   X  = M K - E dR S,    dbeta = dR.v + k.X,    dv = beta dR
+//   X  = M K - E dR S,    dbeta = dR.v + k.X (rows of M * k k^T, and k.(E dR S)),    dv = beta dR
 //   dk = beta X + scale P^T Q + D_C W dS + (beta M)^T K
 // and that of the log decay of token i sums what crosses it:
 //   dg_i = sum over pairs c >= i > c' of (P scale q k^T + M beta k k^T)_cc'
@@ -14,11 +14,14 @@
 // gradients it would be shorter, but those cancel: a first token's is exactly zero.
 //
 // One workgroup per chunk and group; it walks over the group's heads, so dq and dk are
-// summed over them in registers.  Wave w has tokens 16 w .. as the second operand's columns
-// throughout: its results are columns of its own tokens, dot products with q and k are sums
-// over a lane's rows, and P and M go into the next product as they lie.  P^T and M^T of its
-// tokens are products of their own, not exchanged.  The axis of values is walked in slabs
-// of 32, whose W, dR, S and dS lie in LDS with the values as rows (read transposed).
+// summed over them in registers.  Waves w and w + 4 have tokens 16 w .. as the second operand's
+// columns throughout: their results are columns of their own tokens, dot products with q and k
+// are sums over a lane's rows, and P and M go into the next product as they lie.  The first of
+// the two makes P and M of its tokens' rows, the second P^T and M^T (products of their own, not
+// exchanged over tokens); they swap these through LDS, and each has half of dq's and dk's
+// channels.  The axis of values is walked in slabs of 32, whose W, dR, S and dS lie in LDS with
+// the values as rows (read transposed) and whose dO as operands; the next slab's loads are in
+// flight meanwhile.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
@@ -28,7 +31,7 @@ namespace ssd {
 namespace {
 
 constexpr int C = kDeltaChunk;
-constexpr int kLocalThreads = 256;
+constexpr int kLocalThreads = 512;
 constexpr int kSlab = 32;
 
 // [kSlab][COLS] tiles in LDS and the operands that contract their rows.
@@ -70,15 +73,6 @@ template <int COLS> struct Tile<float, COLS> {
   }
 };
 
-// Copies `rows` rows (zeros up to kSlab) that lie one after another.
-template <typename T, int COLS>
-__device__ __forceinline__ void fill(T* t, const T* src, int rows) {
-  constexpr int V = 16 / (int)sizeof(T), PR = COLS / V;
-  for (int i = threadIdx.x; i < kSlab * PR; i += kLocalThreads) {
-    const int r = i / PR, c = i % PR * V;
-    *reinterpret_cast<uint4*>(Tile<T, COLS>::piece(t, r, c)) = load16(src + r * COLS + c, r < rows);
-  }
-}
 __device__ __forceinline__ float dot16(uint4 x, uint4 y, bf16) {
   const bf16x8 a = __builtin_bit_cast(bf16x8, x), b = __builtin_bit_cast(bf16x8, y);
   float s = 0.f;
@@ -90,217 +84,376 @@ __device__ __forceinline__ float dot16(uint4 x, uint4 y, float) {
   const f32x4 a = __builtin_bit_cast(f32x4, x), b = __builtin_bit_cast(f32x4, y);
   return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
-// Two such copies, and the sum of their values' products.
-template <typename T, int COLS>
-__device__ __forceinline__ float fill_dot(T* t0, T* t1, const T* s0, const T* s1, int rows) {
-  constexpr int V = 16 / (int)sizeof(T), PR = COLS / V;
-  float s = 0.f;
-  for (int i = threadIdx.x; i < kSlab * PR; i += kLocalThreads) {
-    const int r = i / PR, c = i % PR * V;
-    const uint4 x = load16(s0 + r * COLS + c, r < rows), y = load16(s1 + r * COLS + c, r < rows);
-    s += dot16(x, y, T{});
-    *reinterpret_cast<uint4*>(Tile<T, COLS>::piece(t0, r, c)) = x;
-    *reinterpret_cast<uint4*>(Tile<T, COLS>::piece(t1, r, c)) = y;
-  }
-  return s;
+// The same of a tile kept as two, high parts and low parts.
+template <typename T, int COLS, bool PAIR>
+__device__ __forceinline__ typename Kept<T, PAIR>::V kept_dealt(const T* t, int u, int lane) {
+  using TT = Tile<T, COLS>;
+  if constexpr (PAIR) return {TT::dealt(t, u, lane), TT::dealt(t + TT::size, u, lane)};
+  else return TT::dealt(t, u, lane);
 }
+template <typename T, int COLS, bool PAIR>
+__device__ __forceinline__ typename Kept<T, PAIR>::V kept_plain(const T* t, int c0, int lane) {
+  using TT = Tile<T, COLS>;
+  if constexpr (PAIR) return {TT::plain(t, c0, lane), TT::plain(t + TT::size, c0, lane)};
+  else return TT::plain(t, c0, lane);
+}
+template <typename T, bool PAIR>
+__device__ __forceinline__ void kept_get(const typename Kept<T, PAIR>::V& v, float (&f)[8]) {
+  if constexpr (PAIR) {
+    float lo[8];
+    Opnd<T>::get(v.hi, f);
+    Opnd<T>::get(v.lo, lo);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] += lo[e];
+  } else {
+    Opnd<T>::get(v, f);
+  }
+}
+
+// A [kSlab][COLS] tile on its way from memory to LDS, through registers; zeros in rows that
+// there are not.
+template <typename T, int COLS> struct Slab {
+  static constexpr int V = 16 / (int)sizeof(T), PR = COLS / V, all = kSlab * PR;
+  static constexpr int n = (all + kLocalThreads - 1) / kLocalThreads;
+  uint4 q[n];
+  __device__ __forceinline__ void load(const T* src, int rows, int tid) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int at = i * kLocalThreads + tid, r = at / PR;
+      q[i] = load16(src + (int64_t)at * V, (all % kLocalThreads == 0 || at < all) && r < rows);
+    }
+  }
+  __device__ __forceinline__ void store(T* t, int tid) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int at = i * kLocalThreads + tid;
+      if (all % kLocalThreads == 0 || at < all)
+        *reinterpret_cast<uint4*>(Tile<T, COLS>::piece(t, at / PR, at % PR * V)) = q[i];
+    }
+  }
+};
+
+// Tokens' [C][COLS] values as operands: the four dealt tiles of rows of each 32 columns, in
+// Opnd<T>::PX pieces; the exclusive or keeps lanes that write together on different banks.
+template <typename T, int COLS> struct Tokens {
+  static constexpr int PX = Opnd<T>::PX, PR = COLS / 8 * PX, all = C * PR;
+  static constexpr int n = (all + kLocalThreads - 1) / kLocalThreads;
+  static constexpr int bytes = COLS / 32 * 4 * PX * kPiece;
+  uint4 q[n];
+  __device__ __forceinline__ static uint32_t slot(int a, int i) { return (uint32_t)(16 * a + (i ^ 2 * a)) * 16; }
+  // Columns from `col` bytes on, of `cols` bytes that a row has.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t pitch, uint32_t col, uint32_t cols, int tid) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int at = i * kLocalThreads + tid, c = at / PR;
+      const uint32_t b = col + at % PR * 16;
+      q[i] = buf_load16(r, (all % kLocalThreads == 0 || at < all) && b < cols ? c * pitch + b : 0xffffff00u);
+    }
+  }
+  __device__ __forceinline__ void store(char* t, int tid) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int at = i * kLocalThreads + tid, c = at / PR, x = at % PR, y = x % (4 * PX);
+      if (all % kLocalThreads == 0 || at < all)
+        *reinterpret_cast<uint4*>(t + ((x / (4 * PX) * 4 + tile_of(c)) * PX + y % PX) * kPiece + slot(y / PX, row_of(c))) = q[i];
+    }
+  }
+  __device__ __forceinline__ static int tile_of(int c) { return 2 * (c / 32) + (c / 4 & 1); }
+  __device__ __forceinline__ static int row_of(int c) { return c % 32 / 8 * 4 + c % 4; }
+  // 32 columns kb of dealt tile u's rows, or of token c (lane % 16 of 16 neighbours).
+  __device__ __forceinline__ static typename Opnd<T>::X dealt(const char* t, int kb, int u, int lane) {
+    return piece_x(t + (kb * 4 + u) * PX * kPiece, slot(lane >> 4, lane & 15), T{});
+  }
+  __device__ __forceinline__ static typename Opnd<T>::X token(const char* t, int kb, int c, int lane) {
+    return piece_x(t + (kb * 4 + tile_of(c)) * PX * kPiece, slot(lane >> 4, row_of(c)), T{});
+  }
+};
 
 __device__ __forceinline__ void store_gate(void* p, bool b16, int64_t i, float v) {
   if (b16) static_cast<bf16*>(p)[i] = static_cast<bf16>(v);
   else static_cast<float*>(p)[i] = v;
 }
 
+// A token's channels (its operands x over all of them) at the rows of tile half N / 32 + i.
 template <typename T, int N>
+__device__ __forceinline__ void channels4(const typename Opnd<T>::X (&x)[N / 32], int half, int i, float (&f)[4]) {
+  constexpr int NH = N / 32;
+  float a[8], b[8];
+  if constexpr (NH >= 2) {
+    Opnd<T>::get(x[i / 2], a);
+    Opnd<T>::get(x[NH / 2 + i / 2], b);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = half ? b[4 * (i % 2) + r] : a[4 * (i % 2) + r];
+  } else {
+    Opnd<T>::get(x[0], a);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = half ? a[4 + r] : a[r];
+  }
+}
+
+// PAIR: what the chains kept comes as pairs.
+template <typename T, int N, bool PAIR>
 __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const DeltaArgs a, const ChunkMap cm) {
   using O = Opnd<T>;
   using X = typename O::X;
   using TC = Tile<T, C>;
   using TN = Tile<T, N>;
-  constexpr int NK = N / 32, NT = N / 16;
-  __shared__ __attribute__((aligned(16))) T Ws[TC::size], Rs[TC::size], Ss[TN::size], Ds[TN::size];
+  using TS = Tokens<T, kSlab>;
+  using TK = Tokens<T, N>;
+  constexpr int NK = N / 32, NH = N / 32, PX = O::PX;   // NH: a wave's tiles of dq and dk
+  using KV = typename Kept<T, PAIR>::V;
+  constexpr int PL = kPlanes<T, PAIR>;
+  constexpr int BUF = sizeof(T) == 2 && !PAIR ? 2 : 1;  // slabs in LDS
+  // k and q of the chunk lie there too, where the slabs leave room
+  constexpr bool KQ = sizeof(T) == 2 || N < 128;
+  __shared__ __attribute__((aligned(16))) T Ws[BUF][PL * TC::size], Rs[BUF][PL * TC::size];
+  __shared__ __attribute__((aligned(16))) T Ss[BUF][PL * TN::size], Ds[BUF][PL * TN::size];
+  __shared__ __attribute__((aligned(16))) char dOs[BUF][TS::bytes], swap[4 * 8 * PX * kPiece];
+  __shared__ __attribute__((aligned(16))) char kqs[KQ ? 2 * TK::bytes : 16];
   __shared__ double Gs[C];
-  __shared__ float bs[C], left[C], mid[C], sdots[kLocalThreads / 64];
+  __shared__ float bs[C], left[2][C], mid[2][C], dbs[2][C], sdots[kLocalThreads / 64];
   const int2 jg = xcd_chunk_head(blockIdx.x, a.G);
   const int j = jg.x, g = jg.y, rep = a.H / a.G;
   if (j >= a.max_chunks) return;
   const ChunkDesc d = cm.desc(j);
   if (d.len <= 0) return;
-  const int w = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
-  const int c = 16 * w + l16;                     // the lane's token
+  const int wave = wave_id(), w = wave & 3, half = wave >> 2;
   const uint32_t qrow = (uint32_t)a.G * N * sizeof(T), vrow = (uint32_t)a.H * a.P * sizeof(T);
   const int64_t qo = ((int64_t)d.start * a.G + g) * N;
   const uint32_t qbytes = (uint32_t)(d.len - 1) * qrow + N * sizeof(T);
   const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + qo, qbytes);
   const __amdgpu_buffer_rsrc_t kr = buf_rsrc(static_cast<const T*>(a.k) + qo, qbytes);
-  const int64_t tr = ((int64_t)j * a.G + g) * (NT * 2) * O::PX * kPiece;
+  const int64_t tr = ((int64_t)j * a.G + g) * (N / 16 * 2) * PX * kPiece;
   const char* kt = static_cast<const char*>(a.kt) + tr;
   const char* qt = static_cast<const char*>(a.qt) + tr;
 
-  X ko[NK], qn[NK];                               // the token's k and q
-#pragma unroll
-  for (int kb = 0; kb < NK; ++kb) {
-    const uint32_t off = c * qrow + (32 * kb + 8 * la) * (uint32_t)sizeof(T);
-    ko[kb] = load_opnd(kr, off, T{});
-    qn[kb] = load_opnd(qr, off, T{});
+  if constexpr (KQ) {
+    TK sk, sq;
+    sk.load(kr, qrow, 0, N * sizeof(T), threadIdx.x);
+    sq.load(qr, qrow, 0, N * sizeof(T), threadIdx.x);
+    sk.store(kqs, threadIdx.x);
+    sq.store(kqs + TK::bytes, threadIdx.x);       // read after the slabs' barriers
   }
-  f32x4 dq[NT], dk[NT];
+  f32x4 dq[NH], dk[NH];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) dq[i] = dk[i] = kZero4;
+  for (int i = 0; i < NH; ++i) dq[i] = dk[i] = kZero4;
+  Slab<T, C> sW[PL], sR[PL];
+  Slab<T, N> sS[PL], sD[PL];
+  TS sO;
+  X vv;
 
   for (int h = g * rep; h < (g + 1) * rep; ++h) {
+    // through opaque_tid, or every address below would be kept from head to head
+    const int tid = opaque_tid(), lane = tid & 63, l16 = lane & 15, la = lane >> 4;
+    const int c = 16 * w + l16;                   // the lane's token
+    // 32 channels kb of dealt tile u's or of the lane's token's k or q
+    auto dealt = [&](bool q, int kb, int u) {
+      if constexpr (KQ) return TK::dealt(kqs + (q ? TK::bytes : 0), kb, u, lane);
+      else return load_opnd(q ? qr : kr, tile_row(u, l16) * qrow + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
+    };
+    auto token = [&](bool q, int kb) {
+      if constexpr (KQ) return TK::token(kqs + (q ? TK::bytes : 0), kb, c, lane);
+      else return load_opnd(q ? qr : kr, c * qrow + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
+    };
     const int64_t jh = (int64_t)j * a.H + h;
     const float* gt = a.gates + jh * kGateFloats;
-    if (threadIdx.x < C) {
-      Gs[threadIdx.x] = reinterpret_cast<const double*>(gt + 3 * C)[threadIdx.x];
-      bs[threadIdx.x] = gt[threadIdx.x];
-    }
-    const float be = gt[c], E = gt[C + c], Dc = gt[2 * C + c], EC = gt[2 * C - 1];
     const int64_t vo = ((int64_t)d.start * a.H + h) * a.P;
     const uint32_t vbytes = (uint32_t)(d.len - 1) * vrow + a.P * (uint32_t)sizeof(T);
     const __amdgpu_buffer_rsrc_t vr = buf_rsrc(static_cast<const T*>(a.v) + vo, vbytes);
     const __amdgpu_buffer_rsrc_t dor = buf_rsrc(static_cast<const T*>(a.dout) + vo, vbytes);
-
-    f32x4 Pr[4], Lr[4], Pc[4], Lc[4];             // [c'][c]: c the query or k's reader (r), or the key (c)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) Pr[u] = Lr[u] = Pc[u] = Lc[u] = kZero4;
-    f32x4 yq[NT], yx[NT], yd[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) yq[i] = yx[i] = yd[i] = kZero4;
-    float sdot = 0.f, rv = 0.f;
-    for (int p0 = 0; p0 < a.P; p0 += kSlab) {
+    auto fetch = [&](int p0) {
       const int rows = min(kSlab, a.P - p0);
-      const int64_t at = jh * a.P + p0;
-      __syncthreads();                            // the slab before is read
-      fill<T, C>(Ws, static_cast<const T*>(a.Wt) + at * C, rows);
-      fill<T, C>(Rs, static_cast<const T*>(a.dRt) + at * C, rows);
-      sdot += fill_dot<T, N>(Ss, Ds, static_cast<const T*>(a.S0) + at * N, static_cast<const T*>(a.dS) + at * N, rows);
-      const bool in = 8 * la < rows;              // values past P: none, whatever lies there
-      const uint32_t vc = (uint32_t)(p0 + 8 * la) * sizeof(T);
-      const X od = load_opnd(dor, in ? c * vrow + vc : 0xfffffff0u - 16u, T{});
-      const X vv = load_opnd(vr, in ? c * vrow + vc : 0xfffffff0u - 16u, T{});
-      X da[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        da[u] = load_opnd(dor, in ? tile_row(u, l16) * vrow + vc : 0xfffffff0u - 16u, T{});
+      for (int i = 0; i < PL; ++i) {
+        const int64_t at = (jh * PL + i) * a.P + p0;
+        sW[i].load(static_cast<const T*>(a.Wt) + at * C, rows, tid);
+        sR[i].load(static_cast<const T*>(a.dRt) + at * C, rows, tid);
+        sS[i].load(static_cast<const T*>(a.S0) + at * N, rows, tid);
+        sD[i].load(static_cast<const T*>(a.dS) + at * N, rows, tid);
+      }
+      sO.load(dor, vrow, p0 * (uint32_t)sizeof(T), a.P * (uint32_t)sizeof(T), tid);
+    };
+    auto put = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        sW[i].store(Ws[b] + i * TC::size, tid);
+        sR[i].store(Rs[b] + i * TC::size, tid);
+        sS[i].store(Ss[b] + i * TN::size, tid);
+        sD[i].store(Ds[b] + i * TN::size, tid);
+      }
+      sO.store(dOs[b], tid);
+    };
+    fetch(0);
+    if (tid < C) {
+      Gs[tid] = reinterpret_cast<const double*>(gt + 4 * C)[tid];
+      bs[tid] = gt[tid];
+    }
+    const float be = gt[c], E = gt[C + c], Dc = gt[2 * C + c], EC = gt[2 * C - 1];
+
+    f32x4 Px[4], Lx[4];                           // [c'][c] of P's and M's sources, or of their transposes
+#pragma unroll
+    for (int u = 0; u < 4; ++u) Px[u] = Lx[u] = kZero4;
+    f32x4 yq[NH], yx[NH], yd[NH];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) yq[i] = yx[i] = yd[i] = kZero4;
+    float sdot = 0.f, rv = 0.f;
+    for (int p0 = 0, b = 0; p0 < a.P; p0 += kSlab, b = BUF - 1 - b) {
+      const bool in = p0 + 8 * la < a.P;          // values past P: none
+      const uint32_t vc = (uint32_t)(p0 + 8 * la) * sizeof(T);
+      if constexpr (BUF == 1) __syncthreads();    // the slab before is read
+      put(b);
+#pragma unroll
+      for (int i = 0; i < Slab<T, N>::n; ++i) {
+        sdot += dot16(sS[0].q[i], sD[0].q[i], T{});
+        if constexpr (PL == 2) sdot += dot16(sS[0].q[i], sD[1].q[i], T{}) + dot16(sS[1].q[i], sD[0].q[i], T{});
+      }
+      if (half == 0) vv = load_opnd(vr, in ? c * vrow + vc : 0xffffff00u, T{});
       __syncthreads();
-      const X wo = TC::plain(Ws, 16 * w, lane), ro = TC::plain(Rs, 16 * w, lane);
+      if (p0 + kSlab < a.P) fetch(p0 + kSlab);
+      const KV wo = kept_plain<T, C, PAIR>(Ws[b], 16 * w, lane), ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane);
+      const X od = TS::token(dOs[b], 0, c, lane);
+      // all four tiles, also those with no pair of the wave's tokens: no branch
+      if (half) {
+        X f[4];
+        KV r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[u] = TS::dealt(dOs[b], 0, u, lane);
+          r[u] = kept_dealt<T, C, PAIR>(Rs[b], u, lane);
+        }
+        mma_rows(f, wo, Px);
+        mma_rows(r, wo, Lx);
+      } else {
+        KV r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) r[u] = kept_dealt<T, C, PAIR>(Ws[b], u, lane);
+        mma_rows(r, od, Px);
+        mma_rows(r, ro, Lx);
+      }
       {
-        float r8[8], v8[8];
-        O::get(ro, r8);
+        KV f[NH];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ss[b], half * NH + i, lane);
+        mma_rows(f, od, yq);
+        mma_rows(f, ro, yx);
+#pragma unroll
+        for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ds[b], half * NH + i, lane);
+        mma_rows(f, wo, yd);
+      }
+      float r8[8];
+      kept_get<T, PAIR>(ro, r8);
+      if (half == 0) {
+        float v8[8];
         O::get(vv, v8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          rv += r8[e] * v8[e];
-          r8[e] *= be;
-        }
+        for (int e = 0; e < 8; ++e) rv += r8[e] * v8[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r8[e] *= be;
         if (in && c < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)c * a.H * a.P + p0 + 8 * la, O::round(r8));
       }
+    }
+    __builtin_amdgcn_sched_barrier(0);            // what follows needs the registers of the slabs' loads
+    X ko[NK], qn[NK];                             // the token's k and q
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (u < 2 || w >= 2) {                    // c' in the token's 32-block or before
-          const X f = TC::dealt(Ws, u, lane);
-          Pr[u] = mma(f, od, Pr[u]);
-          Lr[u] = mma(f, ro, Lr[u]);
-        }
-        if (u >= 2 || w < 2) {                    // or after
-          Pc[u] = mma(da[u], wo, Pc[u]);
-          Lc[u] = mma(TC::dealt(Rs, u, lane), wo, Lc[u]);
-        }
-      }
+    for (int kb = 0; kb < NK; ++kb) {
+      ko[kb] = token(false, kb);
+      qn[kb] = token(true, kb);
+    }
+    // P and M, or their transposes, and their part of the pairs' sums.  A pair's term is the same
+    // number as row and as column, so that what crosses no token cancels.
+    float pairs = 0.f, mk = 0.f;                  // mk: k's reader's sum of M k k^T
+    {
+      char* x = swap + (w * 8 + half * 4) * PX * kPiece;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const X s = TN::dealt(Ss, i, lane);
-        yq[i] = mma(s, od, yq[i]);
-        yx[i] = mma(s, ro, yx[i]);
-        yd[i] = mma(TN::dealt(Ds, i, lane), wo, yd[i]);
+      for (int cb = 0; cb < 2; ++cb) {
+        float p8[8], m8[8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int u = 2 * cb + t;
+          f32x4 qk = kZero4, kk = kZero4;
+#pragma unroll
+          for (int kb = 0; kb < NK; ++kb) {
+            const X k = dealt(false, kb, u), f = half ? dealt(true, kb, u) : k;
+            kk = mma(k, ko[kb], kk);
+            qk = mma(f, half ? ko[kb] : qn[kb], qk);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int e = 4 * t + r, o = 32 * cb + 8 * la + e;
+            const int hi = half ? o : c, lo = half ? c : o;       // the pair's later and earlier token
+            const float D = fexp<T>((float)(Gs[hi] - Gs[lo]));    // of use where lo <= hi
+            const float p = lo <= hi ? Px[u][r] * D * a.scale : 0.f;
+            const float m = lo < hi ? -Lx[u][r] * D : 0.f, mb = m * (half ? bs[o] : be);
+            const float term = lo < hi ? p * qk[r] + mb * kk[r] : 0.f;
+            pairs += half ? term : -term;
+            if (!half) mk += m * kk[r];
+            p8[e] = p;
+            m8[e] = half ? mb : m;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        put_piece(x + cb * PX * kPiece, lane * 16, O::round(p8));
+        put_piece(x + (2 + cb) * PX * kPiece, lane * 16, O::round(m8));
       }
     }
     // the row sums that need the states' products alone
     float ql = 0.f, kx = 0.f, kd = 0.f;
 #pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-      float k8[8], q8[8];
-      O::get(ko[kb], k8);
-      O::get(qn[kb], q8);
+    for (int i = 0; i < NH; ++i) {
+      float k4[4], q4[4];
+      channels4<T, N>(ko, half, i, k4);
+      channels4<T, N>(qn, half, i, q4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = 2 * kb + e / 4, r = e % 4;
-        ql += q8[e] * yq[i][r];
-        kx += k8[e] * yx[i][r];
-        kd += k8[e] * yd[i][r];
+      for (int r = 0; r < 4; ++r) {
+        ql += q4[r] * yq[i][r];
+        kx += k4[r] * yx[i][r];
+        kd += k4[r] * yd[i][r];
       }
     }
-    // P and M, their transposes, and the pairs' sums
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
     X pr[2], mr[2], pc[2], mc[2];
-    float pairs = 0.f;
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      float p8[8], m8[8], pt[8], mt[8];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int u = 2 * cb + t;
-        f32x4 qkr = kZero4, qkc = kZero4, kk = kZero4;
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-          const uint32_t off = tile_row(u, l16) * qrow + (32 * kb + 8 * la) * (uint32_t)sizeof(T);
-          const X kf = load_opnd(kr, off, T{});
-          kk = mma(kf, ko[kb], kk);
-          if (u < 2 || w >= 2) qkr = mma(kf, qn[kb], qkr);
-          if (u >= 2 || w < 2) qkc = mma(load_opnd(qr, off, T{}), ko[kb], qkc);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int e = 4 * t + r, o = 32 * cb + 8 * la + e;
-          const float D = fexp<T>((float)(o > c ? Gs[o] - Gs[c] : Gs[c] - Gs[o]));
-          const float bo = bs[o];
-          p8[e] = o <= c ? Pr[u][r] * D : 0.f;
-          m8[e] = o < c ? -Lr[u][r] * D : 0.f;
-          pt[e] = o >= c ? Pc[u][r] * D * a.scale : 0.f;
-          mt[e] = o > c ? -Lc[u][r] * D * bo : 0.f;
-          // a pair's term is the same number as row and as column: what crosses no token cancels
-          const float row = (Pr[u][r] * D * a.scale) * qkr[r] + (-Lr[u][r] * D * be) * kk[r];
-          const float col = pt[e] * qkc[r] + mt[e] * kk[r];
-          pairs += o > c ? col : o < c ? -row : 0.f;
-        }
-      }
-      pr[cb] = O::round(p8);
-      mr[cb] = O::round(m8);
-      pc[cb] = O::round(pt);
-      mc[cb] = O::round(mt);
-    }
-    float kX = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      f32x4 q = yq[i] * E, x = yx[i] * -E, k = yd[i] * Dc;
+    {
+      const char* x = swap + w * 8 * PX * kPiece;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        const int at = (cb * NT + i) * O::PX * kPiece;
+        pr[cb] = piece_x(x + cb * PX * kPiece, lane * 16, T{});
+        mr[cb] = piece_x(x + (2 + cb) * PX * kPiece, lane * 16, T{});
+        pc[cb] = piece_x(x + (4 + cb) * PX * kPiece, lane * 16, T{});
+        mc[cb] = piece_x(x + (6 + cb) * PX * kPiece, lane * 16, T{});
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      f32x4 q = yq[i] * (a.scale * E), x = yx[i] * -E, k = yd[i] * Dc;
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        const int at = (cb * (N / 16) + half * NH + i) * PX * kPiece;
         const X kf = piece_x(kt + at, lane * 16, T{}), qf = piece_x(qt + at, lane * 16, T{});
         q = mma(kf, pr[cb], q);
         x = mma(kf, mr[cb], x);
         k = mma(qf, pc[cb], k);
         k = mma(kf, mc[cb], k);
       }
-      float k8[8];
-      O::get(ko[i / 2], k8);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) kX += k8[4 * (i % 2) + r] * x[r];
-      dq[i] += q * a.scale;
+      dq[i] += q;
       dk[i] += k + x * be;
+      if (i % 2) __builtin_amdgcn_sched_barrier(0);
     }
-    const float db = column_sum(rv + kX);
+    const float db = column_sum(rv + mk - E * kx);
     const float lf = column_sum(a.scale * E * ql - be * E * kx), md = column_sum(Dc * kd + pairs);
+#pragma unroll
     for (int off = 1; off < 64; off <<= 1) sdot += __shfl_xor(sdot, off);
     if (la == 0) {
-      left[c] = lf;
-      mid[c] = md;
-      if (c < d.len) store_gate(a.dbeta, a.gate_bf16, (int64_t)(d.start + c) * a.H + h, db);
+      left[half][c] = lf;
+      mid[half][c] = md;
+      dbs[half][c] = db;
     }
-    if (lane == 0) sdots[w] = sdot;
+    if (lane == 0) sdots[wave] = sdot;
     __syncthreads();
-    if (w == 0) {
+    if (wave == 0) {
       // sums over the tokens from this one on, and over those before it
-      double s = left[63 - lane], b = mid[lane];
+      double s = (double)left[0][63 - lane] + left[1][63 - lane], b = (double)mid[0][lane] + mid[1][lane];
       const double own = b;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -311,31 +464,52 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         }
       }
       s = __shfl(s, 63 - lane);
-      const double sd = (double)EC * ((double)sdots[0] + sdots[1] + sdots[2] + sdots[3]);
-      if (lane < d.len)
-        store_gate(a.dg, a.gate_bf16, (int64_t)(d.start + lane) * a.H + h, (float)(s + (b - own) + sd));
+      double sd = 0.0;
+#pragma unroll
+      for (int i = 0; i < kLocalThreads / 64; ++i) sd += sdots[i];
+      if (lane < d.len) {
+        const int64_t at = (int64_t)(d.start + lane) * a.H + h;
+        store_gate(a.dg, a.gate_bf16, at, (float)(s + (b - own) + EC * sd));
+        store_gate(a.dbeta, a.gate_bf16, at, dbs[0][lane] + dbs[1][lane]);
+      }
     }
   }
+  const int la = (threadIdx.x & 63) >> 4, c = 16 * w + (threadIdx.x & 15);
   if (c < d.len) {
+    // a lane has channels 8 la .. of a 32-block: all eight in two tiles, or four (dstate 32)
+    const int64_t at = qo + (int64_t)c * a.G * N;
+    T* pq = static_cast<T*>(a.dq) + at;
+    T* pk = static_cast<T*>(a.dk) + at;
+    if constexpr (NH >= 2) {
 #pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-      float f[8];
-      const int64_t at = qo + (int64_t)c * a.G * N + 32 * kb + 8 * la;
-      block8(dq[2 * kb], dq[2 * kb + 1], f);
-      store_opnd(static_cast<T*>(a.dq) + at, O::round(f));
-      block8(dk[2 * kb], dk[2 * kb + 1], f);
-      store_opnd(static_cast<T*>(a.dk) + at, O::round(f));
+      for (int i = 0; i < NH; i += 2) {
+        float f[8];
+        const int n = 32 * ((half * NH + i) / 2) + 8 * la;
+        block8(dq[i], dq[i + 1], f);
+        store_opnd(pq + n, O::round(f));
+        block8(dk[i], dk[i + 1], f);
+        store_opnd(pk + n, O::round(f));
+      }
+    } else {
+      T f[4], e[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f[r] = from_f32<T>(dq[0][r]);
+        e[r] = from_f32<T>(dk[0][r]);
+      }
+      __builtin_memcpy(pq + 8 * la + 4 * half, f, sizeof(f));
+      __builtin_memcpy(pk + 8 * la + 4 * half, e, sizeof(e));
     }
   }
 }
 
-template <typename T>
+template <typename T, bool PAIR>
 hipError_t local_type(const DeltaArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)xcd_grid(a.max_chunks, a.G)), th(kLocalThreads);
   switch (a.N) {
-    case 32: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 32>), grid, th, 0, s, a, a.cmap()); break;
-    case 64: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 64>), grid, th, 0, s, a, a.cmap()); break;
-    case 128: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 128>), grid, th, 0, s, a, a.cmap()); break;
+    case 32: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 32, PAIR>), grid, th, 0, s, a, a.cmap()); break;
+    case 64: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 64, PAIR>), grid, th, 0, s, a, a.cmap()); break;
+    case 128: hipLaunchKernelGGL((delta_local_bwd_kernel<T, 128, PAIR>), grid, th, 0, s, a, a.cmap()); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -345,7 +519,8 @@ hipError_t local_type(const DeltaArgs& a, hipStream_t s) {
 
 hipError_t launch_delta_local_bwd(const DeltaArgs& a, hipStream_t s) {
   if (a.max_chunks <= 0) return hipSuccess;
-  return a.bf16 ? local_type<bf16>(a, s) : local_type<float>(a, s);
+  if (!a.bf16) return local_type<float, false>(a, s);
+  return a.pairs ? local_type<bf16, true>(a, s) : local_type<bf16, false>(a, s);
 }
 
 }  // namespace ssd

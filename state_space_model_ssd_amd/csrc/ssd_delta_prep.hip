@@ -94,9 +94,11 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prep_kernel(const DeltaArg
     bs[lane] = b;
     float* gt = a.gates + jhi * kGateFloats;
     gt[lane] = b;
-    gt[C + lane] = (float)exp(s);
+    const float E = (float)exp(s);
+    gt[C + lane] = E;
+    gt[3 * C + lane] = b * E;
     gt[2 * C + lane] = (float)exp(__shfl(s, 63) - s);
-    reinterpret_cast<double*>(gt + 3 * C)[lane] = s;
+    reinterpret_cast<double*>(gt + 4 * C)[lane] = s;
   }
   __syncthreads();
 
