@@ -34,7 +34,7 @@ COMMON = [
 # instructions at once, and copies from accumulator registers were a sixth of the chain's
 # instructions.
 EXTRA = {name: ("-mllvm", "-amdgpu-mfma-vgpr-form=1")
-         for name in ("ssd_delta_chain",)}
+         for name in ("ssd_delta_chain", "ssd_delta_prep")}
 
 
 def _compile(src: str, verbose: bool) -> str:

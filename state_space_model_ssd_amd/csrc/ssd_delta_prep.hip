@@ -6,11 +6,18 @@
 //
 // G is summed in fp64: its differences are what counts, and a chunk's sum may be large
 // beside them.  T is inverted in fp32: the four 16x16 blocks of the diagonal by
-// substitution, one wave each, a column per lane; then, one wave per block column,
+// substitution, a column per lane, then
 //   T_ij = -T_ii sum_{j <= k < i} L_ik T_kj
 // by fp32 matrix instructions, whose results are the next product's second operand as they
-// lie.  (Powers of L, which would need no substitution, cancel: nearly equal keys give
-// powers with entries of thousands for an inverse whose entries are at most one.)
+// lie, and whose first operand L is as k k^T leaves it (which is symmetric).  (Powers of L,
+// which would need no substitution, cancel: nearly equal keys give powers with entries of
+// thousands for an inverse whose entries are at most one.)
+//
+// One wave per chunk and group, which walks over the group's heads: k k^T and q k^T are
+// theirs in common.  A wave shares nothing with the others of its workgroup and waits for
+// none; its LDS holds k's rows first, then each head's T.
+//
+// 4x8192 tokens, 32 heads in 16 groups of 128 x 128, bf16: MEASURED.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
@@ -20,8 +27,8 @@ namespace ssd {
 namespace {
 
 constexpr int C = kDeltaChunk;
-constexpr int kPrepThreads = 256;
-constexpr int LP = C + 4;                 // pitch of the fp32 matrices in LDS
+constexpr int kPrepWaves = 4;
+constexpr int LP = C + 4;                 // pitch of T in LDS
 
 // A log decay below -512 is one of -512: exp is zero either way, and G stays finite, so
 // that G_i - G_j of tokens after a reset (-inf) is a number.  A NaN stays one.
@@ -51,203 +58,274 @@ __device__ __forceinline__ F8 transposed_opnd(const float* t, int pitch, int u, 
   return f;
 }
 
+// Four of a lane's eight values of an operand (`half`: the first or the last four) at `slot`.
+template <typename T>
+__device__ __forceinline__ void put_half(char* p, uint32_t slot, int half, f32x4 f) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<f32x4*>(p + half * kPiece + slot) = f;
+  } else {
+    const uint2 v = {Opnd<bf16>::pack(f[0], f[1]), Opnd<bf16>::pack(f[2], f[3])};
+    *reinterpret_cast<uint2*>(p + slot + 8 * half) = v;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put_half_pair(char* p, uint32_t slot, int half, f32x4 f) {
+  put_half<T>(p, slot, half, f);
+  if constexpr (sizeof(T) == 2) {
+    f32x4 lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lo[e] = f[e] - static_cast<float>(static_cast<bf16>(f[e]));
+    put_half<T>(p + kPiece, slot, half, lo);
+  }
+}
+
+// Orders a wave's accesses to its LDS: what other lanes wrote before is read after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The [C][N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.
+template <typename T, int N>
+__device__ __forceinline__ void stage_rows(T* lds, __amdgpu_buffer_rsrc_t r, uint32_t row, int pitch, int lane) {
+  constexpr int PR = N * (int)sizeof(T) / 16, PL = 64 / PR > 0 ? 64 / PR : 1;   // lanes a row, rows a load
+  static_assert(PR <= 64, "a row is at most a wave's load");
+  uint4 v[C / PL];
+#pragma unroll
+  for (int i = 0; i < C / PL; ++i) v[i] = buf_load16(r, (i * PL + lane / PR) * row + lane % PR * 16);
+#pragma unroll
+  for (int i = 0; i < C / PL; ++i)
+    *reinterpret_cast<uint4*>(lds + (i * PL + lane / PR) * pitch + lane % PR * (16 / (int)sizeof(T))) = v[i];
+}
+
+// The tile (block of rows i, block of columns j), j <= i, of a lower triangle of 16x16 blocks.
+__device__ __forceinline__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
+
 template <typename T, int N, bool BWD>
-__global__ __launch_bounds__(kPrepThreads) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm) {
+__global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm) {
   using O = Opnd<T>;
-  constexpr int V = 16 / (int)sizeof(T), XP = N + V, NK = N / 32;
-  __shared__ T Ks[C * XP];
-  __shared__ T Qs[BWD ? C * XP : 1];
-  __shared__ float Ls[C * LP];
-  __shared__ float Ts[C * LP];
-  __shared__ double Gs[C];
-  __shared__ float bs[C];
-  const int2 jh = xcd_chunk_head(blockIdx.x, a.H);
-  const int j = jh.x, h = jh.y, rep = a.H / a.G, g = h / rep;
+  using X = typename O::X;
+  constexpr int V = 16 / (int)sizeof(T), XP = N + V, NK = N / 32, TP = N / 16 * 2;
+  constexpr int kOwn = C * XP * (int)sizeof(T) > C * LP * 4 ? C * XP * (int)sizeof(T) : C * LP * 4;
+  __shared__ __attribute__((aligned(16))) char own[kPrepWaves][kOwn];
+  __shared__ double Gw[kPrepWaves][C];
+  __shared__ float bw[kPrepWaves][C];
+  const int wave = wave_id();
+  const int64_t item = (int64_t)blockIdx.x * kPrepWaves + wave;
+  const int j = (int)(item / a.G), g = (int)(item % a.G), rep = a.H / a.G;
   if (j >= a.max_chunks) return;
   const ChunkDesc d = cm.desc(j);
   if (d.len <= 0) return;
-  const int tid = threadIdx.x, w = wave_id(), lane = tid & 63, l16 = lane & 15, la = lane >> 4;
-  const int64_t jhi = (int64_t)j * a.H + h, jgi = (int64_t)j * a.G + g;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
+  const uint32_t slot = lane * 16;
+  T* Ks = reinterpret_cast<T*>(own[wave]);
+  float* Ts = reinterpret_cast<float*>(own[wave]);
+  double* Gs = Gw[wave];
+  float* bs = bw[wave];
 
-  const int64_t row = (int64_t)a.G * N;
-  const T* kp = static_cast<const T*>(a.k) + d.start * row + (int64_t)g * N;
-  const T* qp = static_cast<const T*>(a.q) + d.start * row + (int64_t)g * N;
-  for (int i = tid; i < C * (N / V); i += kPrepThreads) {
-    const int r = i / (N / V), c = i % (N / V) * V;
-    *reinterpret_cast<uint4*>(&Ks[r * XP + c]) = load16(kp + r * row + c, r < d.len);
-    if constexpr (BWD) *reinterpret_cast<uint4*>(&Qs[r * XP + c]) = load16(qp + r * row + c, r < d.len);
-  }
-  if (w == 0) {
-    double s = 0.0;
-    float b = 0.f;
-    if (lane < d.len) {
-      const int64_t t = (int64_t)(d.start + lane) * a.H + h;
-      s = log_decay(load_gate(a.g, a.gate_bf16, t));
-      b = load_gate(a.beta, a.gate_bf16, t);
-    }
+  const uint32_t row = (uint32_t)a.G * N * sizeof(T), bytes = (uint32_t)(d.len - 1) * row + N * sizeof(T);
+  const int64_t at0 = ((int64_t)d.start * a.G + g) * N, jg = (int64_t)j * a.G + g;
+  const __amdgpu_buffer_rsrc_t kr = buf_rsrc(static_cast<const T*>(a.k) + at0, bytes);
+  const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + at0, bytes);
+  stage_rows<T, N>(Ks, kr, row, XP, lane);
+  // the first head's gates on their way
+  const int64_t t0 = (int64_t)(d.start + lane) * a.H + g * rep;
+  const bool in = lane < d.len;
+  float gate = in ? load_gate(a.g, a.gate_bf16, t0) : 0.f, step = in ? load_gate(a.beta, a.gate_bf16, t0) : 0.f;
+  wave_sync();
+
+  // k_c.k_c' with the lane's row c = 16 i + l16 and columns c' = 16 j + 4 la + r; q_c.k_c' likewise,
+  // or backward its transpose: the lane's key c = 16 j + l16 and queries 16 i + 4 la + r
+  f32x4 kk[10], qk[10];
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double o = __shfl_up(s, off);
-      if (lane >= off) s += o;
-    }
-    Gs[lane] = s;
-    bs[lane] = b;
-    float* gt = a.gates + jhi * kGateFloats;
-    gt[lane] = b;
-    const float E = (float)exp(s);
-    gt[C + lane] = E;
-    gt[3 * C + lane] = b * E;
-    gt[2 * C + lane] = (float)exp(__shfl(s, 63) - s);
-    reinterpret_cast<double*>(gt + 4 * C)[lane] = s;
-  }
-  __syncthreads();
-
-  // wave w's 16 rows of L (columns up to its own), and its columns of A or A's transpose
-  typename O::X own[NK], oth[NK];
+  for (int i = 0; i < 10; ++i) kk[i] = qk[i] = kZero4;
 #pragma unroll
   for (int kb = 0; kb < NK; ++kb) {
-    const int at = (16 * w + l16) * XP + 32 * kb + 8 * la;
-    own[kb] = load_opnd(&Ks[at]);
-    if constexpr (BWD) {
-      oth[kb] = own[kb];
-    } else {
-      const bool in = 16 * w + l16 < d.len;
-      const T* p = qp + (in ? 16 * w + l16 : 0) * row + 32 * kb + 8 * la;
-      oth[kb] = load_opnd(p);                     // rows past the end: never stored
-    }
-  }
+    X kf[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    f32x4 kk = kZero4, qk = kZero4;
+    for (int i = 0; i < 4; ++i) kf[i] = load_opnd(&Ks[(16 * i + l16) * XP + 32 * kb + 8 * la]);
 #pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-      const int at = (16 * u + l16) * XP + 32 * kb + 8 * la;
-      const typename O::X kf = load_opnd(&Ks[at]);
-      if (u <= w) kk = mma(own[kb], kf, kk);
-      if constexpr (BWD) qk = mma(load_opnd(&Qs[at]), oth[kb], qk);
-      else qk = mma(kf, oth[kb], qk);
-    }
-    if (u <= w) {
+    for (int i = 0; i < 4; ++i) {
+      const X qf = load_opnd(qr, (16 * i + l16) * row + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * la + r, c = 16 * u + l16;
-        Ls[i * LP + c] = c < i ? bs[i] * fexp<T>((float)(Gs[i] - Gs[c])) * kk[r] : 0.f;
-      }
-    }
-    // A forward: lane's row i = 16 w + l16, columns c = 16 u + 4 la + r; backward its transpose:
-    // lane's row c = 16 w + l16, columns i.  Zero above the diagonal.
-    const int mine = 16 * w + l16;
-    float f[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int c = 16 * u + 4 * la + r, hi = BWD ? c : mine, lo = BWD ? mine : c;
-      const bool in = lo <= hi && hi < d.len;
-      f[r] = in ? a.scale * fexp<T>((float)(Gs[hi] - Gs[lo])) * qk[r] : 0.f;
-    }
-    // four of the eight values of a lane: forward rows as they lie, backward dealt
-    const int cb = u / 2, t = BWD ? 2 * (mine / 32) + (mine / 4 & 1) : w;
-    const int i = BWD ? mine % 32 / 8 * 4 + mine % 4 : l16;
-    const uint32_t slot = 16u * (16 * (2 * (u & 1) + (la >> 1)) + i);
-    const bool kept = BWD ? cb == 1 || t < 2 : cb == 0 || t >= 2;
-    if (kept) {
-      if constexpr (sizeof(T) == 4) {
-        char* p = static_cast<char*>(BWD ? a.At : a.A) + (jhi * 12 + (BWD ? upper_index(t, cb) : lower_index(t, cb)) * 2) * kPiece;
-        *reinterpret_cast<f32x4*>(p + (la & 1) * kPiece + slot) = f32x4{f[0], f[1], f[2], f[3]};
-      } else {
-        bf16x4 hi, lo;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          hi[r] = static_cast<bf16>(f[r]);
-          lo[r] = static_cast<bf16>(f[r] - static_cast<float>(hi[r]));
-        }
-        if constexpr (BWD) {
-          char* p = static_cast<char*>(a.At) + (jhi * 12 + upper_index(t, cb) * 2) * kPiece + slot + 8 * (la & 1);
-          *reinterpret_cast<bf16x4*>(p) = hi;
-          *reinterpret_cast<bf16x4*>(p + kPiece) = lo;
-        } else {
-          *reinterpret_cast<bf16x4*>(static_cast<char*>(a.A) + (jhi * 6 + lower_index(t, cb)) * kPiece + slot + 8 * (la & 1)) = hi;
-        }
+      for (int c = 0; c <= i; ++c) {
+        kk[tri(i, c)] = mma(kf[c], kf[i], kk[tri(i, c)]);
+        if constexpr (BWD) qk[tri(i, c)] = mma(qf, kf[c], qk[tri(i, c)]);
+        else qk[tri(i, c)] = mma(kf[c], qf, qk[tri(i, c)]);
       }
     }
   }
-  __syncthreads();
-
-  // the diagonal blocks: lane's column of block w
-  {
-    float t[16];
-    const float* L = &Ls[16 * w * LP + 16 * w];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == l16 ? 1.f : 0.f;
-#pragma unroll
-      for (int m = 0; m < i; ++m) v -= L[i * LP + m] * t[m];
-      t[i] = v;
-    }
-    if (lane < 16) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) Ts[(16 * w + i) * LP + 16 * w + l16] = t[i];
-    }
-  }
-  __syncthreads();
-  // below it: wave w has block column w
-  if (w < 3) {
-    f32x4 blk[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) blk[k] = kZero4;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) blk[0][r] = Ts[(16 * w + 4 * la + r) * LP + 16 * w + l16];
-#pragma unroll
-    for (int n = 1; n < 4; ++n) {                 // block row w + n
-      if (w + n < 4) {
-        const int i0 = 16 * (w + n) + l16;
-        f32x4 s = kZero4, o = kZero4;
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-          const f32x4 L = *reinterpret_cast<const f32x4*>(&Ls[i0 * LP + 16 * (w + k) + 4 * la]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s = __builtin_amdgcn_mfma_f32_16x16x4f32(L[r], blk[k][r], s, 0, 0, 0);
-        }
-        const f32x4 t = *reinterpret_cast<const f32x4*>(&Ts[i0 * LP + 16 * (w + n) + 4 * la]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o = __builtin_amdgcn_mfma_f32_16x16x4f32(t[r], s[r], o, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          blk[n][r] = -o[r];
-          Ts[(16 * (w + n) + 4 * la + r) * LP + 16 * w + l16] = -o[r];
-        }
-      }
-    }
-  }
-  __syncthreads();
-
-  // T, and for the backward its transpose
-  const uint32_t slot = lane * 16;
-  for (int x = w; x < 6; x += 4) {
-    const int2 t = lower_tile(x);
-    const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
-    float f[8];
-    block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] : 0.f;
-    put_piece(static_cast<char*>(a.T) + (jhi * 12 + x * 2) * kPiece, slot, O::split(f));
-  }
+  // k (and q) transposed
+#pragma unroll 4
+  for (int x = 0; x < TP; ++x)
+    put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
   if constexpr (BWD) {
-    for (int x = w; x < 6; x += 4) {
-      const int2 t = upper_tile(x);
+    wave_sync();
+    stage_rows<T, N>(Ks, qr, row, XP, lane);
+    wave_sync();
+#pragma unroll 4
+    for (int x = 0; x < TP; ++x)
+      put_piece(static_cast<char*>(a.qt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
+  }
+
+  for (int h = g * rep; h < (g + 1) * rep; ++h) {
+    const int64_t jh = (int64_t)j * a.H + h;
+    {
+      double s = log_decay(gate);
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(s, off);
+        if (lane >= off) s += o;
+      }
+      wave_sync();                                // the head before is done with G, beta and T
+      Gs[lane] = s;
+      bs[lane] = step;
+      float* gt = a.gates + jh * kGateFloats;
+      const float E = (float)exp(s);
+      gt[lane] = step;
+      gt[C + lane] = E;
+      gt[2 * C + lane] = (float)exp(__shfl(s, 63) - s);
+      gt[3 * C + lane] = step * E;
+      reinterpret_cast<double*>(gt + 4 * C)[lane] = s;
+      if (h + 1 < (g + 1) * rep && in) {
+        gate = load_gate(a.g, a.gate_bf16, t0 + h + 1 - g * rep);
+        step = load_gate(a.beta, a.gate_bf16, t0 + h + 1 - g * rep);
+      }
+      wave_sync();
+    }
+    // L as first operands, the diagonal's blocks to LDS; A (or its transpose)
+    f32x4 L[10];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 16 * i + l16;
+      const double Gc = Gs[c];
+      const float bc = bs[c];
+#pragma unroll
+      for (int x = 0; x <= i; ++x) {
+        f32x4 f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int o = 16 * x + 4 * la + r;
+          const float D = fexp<T>((float)(Gc - Gs[o]));
+          L[tri(i, x)][r] = o < c ? bc * D * kk[tri(i, x)][r] : 0.f;
+          if constexpr (!BWD) f[r] = o <= c ? a.scale * D * qk[tri(i, x)][r] : 0.f;
+        }
+        if (x == i) *reinterpret_cast<f32x4*>(&Ts[(16 * i + l16) * LP + 16 * i + 4 * la]) = L[tri(i, i)];
+        if constexpr (!BWD) {
+          // four of the eight values of a lane
+          const uint32_t at = 16u * (16 * (2 * (x & 1) + (la >> 1)) + l16);
+          char* p = static_cast<char*>(a.A) + (jh * 6 + lower_index(i, x / 2)) * O::PX * kPiece;
+          put_half<T>(p, at, la & 1, f);
+          // the block right of the diagonal's in the same 32 columns
+          if (x == i && i % 2 == 0) put_half<T>(p, 16u * (16 * (2 + (la >> 1)) + l16), la & 1, kZero4);
+        }
+      }
+    }
+    if constexpr (BWD) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int c = 16 * x + l16;               // the key
+        const double Gc = Gs[c];
+        const int t = 2 * (c / 32) + (c / 4 & 1), i16 = c % 32 / 8 * 4 + c % 4;   // its place in the dealt tiles
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i / 2 < x / 2) continue;            // a tile of zeros that is not kept
+          f32x4 f = kZero4;
+          if (i >= x) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int o = 16 * i + 4 * la + r;
+              f[r] = c <= o ? a.scale * fexp<T>((float)(Gs[o] - Gc)) * qk[tri(i, x)][r] : 0.f;
+            }
+          }
+          const uint32_t at = 16u * (16 * (2 * (i & 1) + (la >> 1)) + i16);
+          char* p = static_cast<char*>(a.At) + (jh * 6 + upper_index(t, i / 2)) * O::PS * kPiece;
+          put_half_pair<T>(p, at, la & 1, f);
+        }
+      }
+    }
+    wave_sync();
+    // the diagonal blocks: column l16 of block la
+    {
+      float t[16];
+      float* B = Ts + 16 * la * LP + 16 * la;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float s0 = i == l16 ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+        for (int m4 = 0; m4 < (i + 3) / 4; ++m4) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(B + i * LP + 4 * m4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * m4 + r < i) (r & 1 ? s1 : s0) -= v[r] * t[4 * m4 + r];
+        }
+        t[i] = s0 + s1;
+      }
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) B[i * LP + l16] = t[i];
+      wave_sync();
+    }
+    // below it, the blocks next to the diagonal first
+    {
+      f32x4 blk[10], dia[4];                      // T's blocks as second operands, the diagonal's as first
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dia[i] = *reinterpret_cast<const f32x4*>(&Ts[(16 * i + l16) * LP + 16 * i + 4 * la]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) blk[tri(i, i)][r] = Ts[(16 * i + 4 * la + r) * LP + 16 * i + l16];
+      }
+#pragma unroll
+      for (int n = 1; n < 4; ++n) {
+        f32x4 s[3], o[3];
+#pragma unroll
+        for (int c = 0; c < 4 - n; ++c) s[c] = o[c] = kZero4;
+#pragma unroll
+        for (int k = 0; k < n; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4 - n; ++c)
+              s[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(L[tri(c + n, c + k)][r], blk[tri(c + k, c)][r], s[c], 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < 4 - n; ++c)
+            o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(dia[c + n][r], s[c][r], o[c], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4 - n; ++c)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            blk[tri(c + n, c)][r] = -o[c][r];
+            Ts[(16 * (c + n) + 4 * la + r) * LP + 16 * c + l16] = -o[c][r];
+          }
+      }
+    }
+    wave_sync();
+    // T, and for the backward its transpose
+#pragma unroll
+    for (int x = 0; x < 6; ++x) {
+      const int2 t = lower_tile(x);
       const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
       float f[8];
+      block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = c0 + e >= r ? Ts[(c0 + e) * LP + r] : 0.f;
-      put_piece(static_cast<char*>(a.Tt) + (jhi * 12 + x * 2) * kPiece, slot, O::split(f));
+      for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] : 0.f;
+      put_piece(static_cast<char*>(a.T) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
     }
-  }
-  // k (and q) transposed, once per group
-  if (h % rep == 0) {
-    for (int x = w; x < N / 16 * 2; x += 4) {
-      const int u = x % (N / 16), cb = x / (N / 16);
-      const int64_t at = (jgi * (N / 16 * 2) + x) * O::PX * kPiece;
-      put_piece(static_cast<char*>(a.kt) + at, slot, transposed_opnd(Ks, XP, u, cb, lane));
-      if constexpr (BWD) put_piece(static_cast<char*>(a.qt) + at, slot, transposed_opnd(Qs, XP, u, cb, lane));
+    if constexpr (BWD) {
+#pragma unroll
+      for (int x = 0; x < 6; ++x) {
+        const int2 t = upper_tile(x);
+        const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = Ts[(c0 + e) * LP + r];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c0 + e >= r ? f[e] : 0.f;
+        put_piece(static_cast<char*>(a.Tt) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
+      }
     }
   }
 }
@@ -265,9 +343,9 @@ __global__ __launch_bounds__(256) void delta_clear_kernel(const int32_t* __restr
 
 template <typename T, int N>
 hipError_t prep_go(const DeltaArgs& a, bool bwd, hipStream_t s) {
-  const dim3 grid((unsigned)xcd_grid(a.max_chunks, a.H));
-  if (bwd) hipLaunchKernelGGL((delta_prep_kernel<T, N, true>), grid, dim3(kPrepThreads), 0, s, a, a.cmap());
-  else hipLaunchKernelGGL((delta_prep_kernel<T, N, false>), grid, dim3(kPrepThreads), 0, s, a, a.cmap());
+  const dim3 grid((unsigned)(((int64_t)a.max_chunks * a.G + kPrepWaves - 1) / kPrepWaves)), th(64 * kPrepWaves);
+  if (bwd) hipLaunchKernelGGL((delta_prep_kernel<T, N, true>), grid, th, 0, s, a, a.cmap());
+  else hipLaunchKernelGGL((delta_prep_kernel<T, N, false>), grid, th, 0, s, a, a.cmap());
   return hipGetLastError();
 }
 
