@@ -1,6 +1,6 @@
 // The gated delta rule, the chain of states.  Per sequence, head and chunk, from the
 // state S (P x N) entering the chunk and the chunk's T, A and decays (ssd_delta_prep.hip):
-//   W = T (beta V - beta E K S^T)
+//   W = (T beta) (V - E K S^T)
 //   O = scale E (Q S^T) + A W
 //   S <- E_C S + (D W)^T K,     D_i = exp(G_C - G_i)
 // and backward, from the last chunk to the first, with dO the output's gradient, dS that of
@@ -38,7 +38,9 @@ constexpr int HW = 4;                     // helper waves
 constexpr int kLdsBytes = 160 * 1024;
 
 // One helper wave's share of `COUNT` loads of 16 bytes per lane on their way from memory to
-// LDS, through registers.
+// LDS, through registers.  Loads are issued also where there is no next chunk (from an empty
+// resource: zeros, no access): behind a branch around loads the compiler does not know how many
+// are under way, and waits for all of them.
 template <int COUNT> struct Pieces {
   static constexpr int n = (COUNT + HW - 1) / HW;
   uint4 q[n];
@@ -50,8 +52,8 @@ template <int COUNT> struct Pieces {
 
 // Operands that lie in memory as they do in LDS.
 template <int COUNT> struct Copied : Pieces<COUNT> {
-  __device__ __forceinline__ void load(const char* p, int w, int lane) {
-    const __amdgpu_buffer_rsrc_t r = buf_rsrc(p, COUNT * kPiece);
+  __device__ __forceinline__ void load(const char* p, bool some, int w, int lane) {
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(p, some ? COUNT * kPiece : 0);
 #pragma unroll
     for (int i = 0; i < this->n; ++i) this->q[i] = buf_load16(r, this->index(i, w) * kPiece + lane * 16);
   }
@@ -154,6 +156,13 @@ __device__ __forceinline__ void lds_ss(const char* p, uint32_t slot, typename Op
   for (int m = 0; m < M; ++m) x[m] = piece_s(p + m * Opnd<T>::PS * kPiece, slot, T{});
 }
 
+__device__ __forceinline__ bf16x8 opnd_of(const uint4 (&q)[1], bf16) { return __builtin_bit_cast(bf16x8, q[0]); }
+__device__ __forceinline__ F8 opnd_of(const uint4 (&q)[2], float) {
+  F8 f;
+  block8(__builtin_bit_cast(f32x4, q[0]), __builtin_bit_cast(f32x4, q[1]), f.v);
+  return f;
+}
+
 // Values 32 cb + 8 (lane / 16) .. + 7 of a row of C floats.
 __device__ __forceinline__ void row8(const float* p, int cb, int lane, float (&f)[8]) {
   p += 32 * cb + 8 * (lane >> 4);
@@ -192,7 +201,7 @@ struct ChainTask {
     }
   }
   __device__ __forceinline__ int start(int i) const { return first + i * C; }
-  __device__ __forceinline__ int len(int i) const { return min(C, tokens - i * C); }
+  __device__ __forceinline__ int len(int i) const { return i < 0 ? 0 : min(C, tokens - i * C); }
 };
 
 // S^T in its tiles from row p of a state, zeros where there is none; and back.
@@ -221,6 +230,12 @@ __device__ __forceinline__ void store_state(float* row, int lane, const f32x4 (&
   }
 }
 
+// A lane's place in the kb-th operand that a state wave leaves: store_rows() reads one row's
+// pieces together, and the exclusive or puts them on different banks.
+__device__ __forceinline__ uint32_t left_slot(int a, int i, int kb) {
+  return (uint32_t)(16 * a + (i ^ ((a + 4 * kb) & 15))) * 16;
+}
+
 // Operands that the state waves left in LDS ([wave][EX of them], from the `from`-th on, each 32
 // columns of 16 dealt rows) to rows of a [P][COLS] matrix of T, or of two, one behind the other.
 template <typename T, int NW, int EX, int COLS, bool PAIR>
@@ -234,7 +249,7 @@ __device__ __forceinline__ void store_rows(const char* x, int from, T* dst, int6
     const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl) {
-      const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + (16 * a + l16) * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + left_slot(a, l16, kb));
       if (p < rows) *reinterpret_cast<uint4*>(dst + pl * plane + (int64_t)p * COLS + c) = v;
     }
   }
@@ -273,14 +288,13 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       // phase 1
       typename O::S sf[NK], rf[2];
       typename O::X kf[NK][4];
-      float v[2][8], be[2][8], bE[2][8], D[2][8];
+      float v[2][8], E[2][8], D[2][8];
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v[cb]);
-        row8(gt, cb, lane, be[cb]);
-        row8(gt + 3 * C, cb, lane, bE[cb]);
+        row8(gt + C, cb, lane, E[cb]);
         row8(gt + 2 * C, cb, lane, D[cb]);
       }
       const float EC = gt[2 * C - 1];
@@ -300,7 +314,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = be[cb][e] * v[cb][e] - bE[cb][e] * f[e];
+        for (int e = 0; e < 8; ++e) f[e] = v[cb][e] - E[cb][e] * f[e];
         rf[cb] = O::split(f);
       }
       y[0] = y[1] = y[2] = y[3] = kZero4;
@@ -308,12 +322,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       mma_rows(t1, rf[1], y + 2);
       char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, rs, keep<T, PAIR>(sf[kb]));
+      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PE * kPiece, rs, keep<T, PAIR>(f));
+        put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= D[cb][e];
         rf[cb] = O::split(f);
@@ -350,11 +364,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   const char* Ap = static_cast<const char*>(a.A) + jh0 * (6 * PX * kPiece);
   const char* gp = reinterpret_cast<const char*>(a.gates + jh0 * kGateFloats);
   const char* tp = static_cast<const char*>(a.kt) + jg0 * (TP * kPiece);
-  auto fetch1 = [&](int j) {
+  auto fetch1 = [&](int j) {                      // no row past the last chunk
+    const bool some = j < t.chunks;
     cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
-    cT.load(Tp, w, lane);
+    cT.load(Tp, some, w, lane);
     cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
-    cG = buf_load16(buf_rsrc(gp, kGateFloats * 4), lane * 16);
+    cG = buf_load16(buf_rsrc(gp, some ? kGateFloats * 4 : 0), lane * 16);
     kp += C * (int64_t)qrow;
     vp += C * (int64_t)vrow;
     Tp += a.H * (6 * PS * kPiece);
@@ -368,17 +383,22 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   };
   // helper w makes the outputs of tokens 16 w ..: their rows of Q, four lanes on 64 bytes, and
   // of A, as operands
-  uint4 cQ[NK * PX];
-  typename O::X cA[2];
+  uint4 cQ[NK * PX], cA[2][PX];
   auto fetch2 = [&](int j) {
-    cKt.load(tp, w, lane);
+    const bool some = j < t.chunks;
+    cKt.load(tp, some, w, lane);
     tp += a.G * (TP * kPiece);
     if constexpr (!KEEP) {
       const __amdgpu_buffer_rsrc_t qr = buf_rsrc(qp, rows_bytes(t.len(j), qrow, N * sizeof(T)));
+      const __amdgpu_buffer_rsrc_t ar = buf_rsrc(Ap, some ? 6 * PX * kPiece : 0);
 #pragma unroll
       for (int i = 0; i < NK * PX; ++i) cQ[i] = buf_load16(qr, (16 * w + lane / 4) * qrow + (4 * i + lane % 4) * 16);
-      cA[0] = piece_x(Ap + lower_index(w, 0) * PX * kPiece, lane * 16, T{});
-      if (w >= 2) cA[1] = piece_x(Ap + lower_index(w, 1) * PX * kPiece, lane * 16, T{});
+      // the second of tokens before 32 is none: past the resource
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+        for (int i = 0; i < PX; ++i)
+          cA[cb][i] = buf_load16(ar, cb == 0 || w >= 2 ? (lower_index(w, cb) * PX + i) * kPiece + lane * 16 : 0xffffff00u);
       qp += C * (int64_t)qrow;
       Ap += a.H * (6 * PX * kPiece);
     }
@@ -389,43 +409,38 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   // wave's own corner of LDS (the exclusive or as for Rows)
   auto ready = [&]() {
     if constexpr (!KEEP) {
-      sE = a.scale * gt[C + 16 * w + l16];
       char* q = lds + oQ + w * QS * PX * kPiece;
 #pragma unroll
       for (int k0 = 0; k0 < NK; k0 += QS) {
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int kb = k0; kb < k0 + QS; ++kb)
+        for (int kb = 0; kb < QS; ++kb)
 #pragma unroll
           for (int i = 0; i < PX; ++i) {
             const int e = (4 * i + lane % 4) * 16 / (int)sizeof(T), px = e % 8 * (int)sizeof(T) / 16;
-            *reinterpret_cast<uint4*>(q + ((kb - k0) * PX + px) * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[kb * PX + i];
+            *reinterpret_cast<uint4*>(q + (kb * PX + px) * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[(k0 + kb) * PX + i];
           }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int kb = k0; kb < k0 + QS; ++kb) qf[kb] = piece_x(q + (kb - k0) * PX * kPiece, KR::slot(la, l16, 0), T{});
+        for (int kb = 0; kb < QS; ++kb) qf[k0 + kb] = piece_x(q + kb * PX * kPiece, KR::slot(la, l16, 0), T{});
       }
-      af[0] = cA[0];
-      af[1] = cA[1];
+      sE = a.scale * gt[C + 16 * w + l16];
+      af[0] = opnd_of(cA[0], T{});
+      af[1] = opnd_of(cA[1], T{});
     }
   };
-  auto finish = [&](int j) {
-    const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
-    if constexpr (KEEP) {
-      const int64_t jh = jh0 + (int64_t)j * a.H;
-      constexpr int PL = kPlanes<T, PAIR>;
-      store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-      store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
-    } else {
-      // O with S and W as first operands: rows are values, the lane's column is a token
-      f32x4 o[NW];
+  // O with S and W as first operands: rows are values, the lane's column is a token
+  f32x4 o[NW];
+  auto product = [&](int j) {
+    if constexpr (!KEEP) {
+      const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
 #pragma unroll
       for (int s = 0; s < NW; ++s) o[s] = kZero4;
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb) {
         typename O::X f[NW];
 #pragma unroll
-        for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + kb) * PX * kPiece, lane * 16, T{});
+        for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + kb) * PX * kPiece, left_slot(la, l16, kb), T{});
         mma_rows(f, qf[kb], o);
       }
 #pragma unroll
@@ -435,10 +450,20 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
         if (cb == 0 || w >= 2) {
           typename O::X f[NW];
 #pragma unroll
-          for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + NK + cb) * PX * kPiece, lane * 16, T{});
+          for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + NK + cb) * PX * kPiece, left_slot(la, l16, cb), T{});
           mma_rows(f, af[cb], o);
         }
       }
+    }
+  };
+  auto write = [&](int j) {
+    if constexpr (KEEP) {
+      const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
+      const int64_t jh = jh0 + (int64_t)j * a.H;
+      constexpr int PL = kPlanes<T, PAIR>;
+      store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+      store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
+    } else {
       const int c = 16 * w + l16;
       T* out = static_cast<T*>(a.out) + ((int64_t)(t.start(j) + c) * a.H + h) * a.P + p0 + 8 * la;
 #pragma unroll
@@ -456,20 +481,26 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   }
   __syncthreads();
   for (int j = 0; j < t.chunks; ++j) {
-    const bool more = j + 1 < t.chunks;
-    // phase 1
-    if (more) fetch1(j + 1);
+    // phase 1; stores come last, as whoever waits for a load waits for the stores before it
+    fetch1(j + 1);
     cKt.store(lds + oKt, w, lane);
-    if (DX && j > 0) finish(j - 1);
+    if (DX && j > 0) product(j - 1);
     ready();
-    if (more) fetch2(j + 1);
+    fetch2(j + 1);
+    if (DX && j > 0) write(j - 1);
     __syncthreads();
     // phase 2
-    if constexpr (!DX) finish(j);
-    if (more) put1();
+    if constexpr (!DX) {
+      product(j);
+      write(j);
+    }
+    put1();
     __syncthreads();
   }
-  if (DX && t.chunks > 0) finish(t.chunks - 1);
+  if (DX && t.chunks > 0) {
+    product(t.chunks - 1);
+    write(t.chunks - 1);
+  }
 }
 
 // Backward: dS (before the update) and dR are kept for ssd_delta_local.hip (PAIR: as pairs).
@@ -489,7 +520,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
 
   const ChainTask t(a, cm, blockIdx.x, blocks);
   if (t.none) return;
-  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15;
+  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
   const int h = t.h, p0 = t.block * 16 * NW, rows = min(16 * NW, a.P - p0);
   const float* gt = reinterpret_cast<const float*>(lds + oG);
 
@@ -553,12 +584,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
       mma_rows(t1, rf[1], y);
       char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, rs, keep<T, PAIR>(sf[kb]));
+      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PE * kPiece, rs, keep<T, PAIR>(f));
+        put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= -bE[cb][e];
         rf[cb] = O::split(f);
@@ -599,11 +630,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   const char* gp = reinterpret_cast<const char*>(a.gates + jh1 * kGateFloats);
   int64_t tp = jg1 * (TP * kPiece);
   auto fetch1 = [&](int j) {
+    const bool some = j >= 0;
     cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
-    cA.load(Ap, w, lane);
-    cT.load(Tp, w, lane);
+    cA.load(Ap, some, w, lane);
+    cT.load(Tp, some, w, lane);
     cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
-    cG = buf_load16(buf_rsrc(gp, kGateFloats * 4), lane * 16);
+    cG = buf_load16(buf_rsrc(gp, some ? kGateFloats * 4 : 0), lane * 16);
     kp -= C * (int64_t)qrow;
     vp -= C * (int64_t)vrow;
     Ap -= a.H * (6 * PS * kPiece);
@@ -617,9 +649,9 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     cV.store(lds + oV, w, lane);
     if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
   };
-  auto fetch2 = [&]() {
-    cQt.load(static_cast<const char*>(a.qt) + tp, w, lane);
-    cKt.load(static_cast<const char*>(a.kt) + tp, w, lane);
+  auto fetch2 = [&](int j) {
+    cQt.load(static_cast<const char*>(a.qt) + tp, j >= 0, w, lane);
+    cKt.load(static_cast<const char*>(a.kt) + tp, j >= 0, w, lane);
     tp -= a.G * (TP * kPiece);
   };
   auto finish = [&](int j) {
@@ -632,20 +664,20 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   if (t.chunks > 0) {
     fetch1(last);
     put1();
-    fetch2();
+    fetch2(last);
   }
   __syncthreads();
   for (int j = last; j >= 0; --j) {
     // phase 1
-    if (j > 0) fetch1(j - 1);
+    fetch1(j - 1);
     cQt.store(lds + oQt, w, lane);
     cKt.store(lds + oKt, w, lane);
+    fetch2(j - 1);
     if (DX && j < last) finish(j + 1);
-    if (j > 0) fetch2();
     __syncthreads();
     // phase 2
     if constexpr (!DX) finish(j);
-    if (j > 0) put1();
+    put1();
     __syncthreads();
   }
   if (DX && t.chunks > 0) finish(0);

@@ -2,7 +2,7 @@
 // head, with G_i the running sum of the chunk's log decays, D_ij = exp(G_i - G_j) for
 // j <= i, E_i = exp(G_i),
 //   L_ij = beta_i D_ij k_i.k_j  (j < i),   T = (1 + L)^-1,   A_ij = scale D_ij q_i.k_j  (j <= i)
-// so that the rows w (ssd_delta_chain.hip) are W = T (beta V - beta E K S^T).
+// so that the rows w (ssd_delta_chain.hip) are W = (T beta) (V - E K S^T).
 //
 // G is summed in fp64: its differences are what counts, and a chunk's sum may be large
 // beside them.  T is inverted in fp32: the four 16x16 blocks of the diagonal by
@@ -23,6 +23,8 @@
 #pragma clang fp contract(on)
 
 namespace ssd {
+
+int device_cu_count();
 
 namespace {
 
@@ -103,7 +105,7 @@ __device__ __forceinline__ void stage_rows(T* lds, __amdgpu_buffer_rsrc_t r, uin
 __device__ __forceinline__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
 
 template <typename T, int N, bool BWD>
-__global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm) {
+__global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm, int nh) {
   using O = Opnd<T>;
   using X = typename O::X;
   constexpr int V = 16 / (int)sizeof(T), XP = N + V, NK = N / 32, TP = N / 16 * 2;
@@ -112,8 +114,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   __shared__ double Gw[kPrepWaves][C];
   __shared__ float bw[kPrepWaves][C];
   const int wave = wave_id();
+  // heads h0 .. of `nh` at a time: a group's, or part of one
   const int64_t item = (int64_t)blockIdx.x * kPrepWaves + wave;
-  const int j = (int)(item / a.G), g = (int)(item % a.G), rep = a.H / a.G;
+  const int per = a.H / nh, j = (int)(item / per), h0 = (int)(item % per) * nh, rep = a.H / a.G, g = h0 / rep;
   if (j >= a.max_chunks) return;
   const ChunkDesc d = cm.desc(j);
   if (d.len <= 0) return;
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + at0, bytes);
   stage_rows<T, N>(Ks, kr, row, XP, lane);
   // the first head's gates on their way
-  const int64_t t0 = (int64_t)(d.start + lane) * a.H + g * rep;
+  const int64_t t0 = (int64_t)(d.start + lane) * a.H + h0;
   const bool in = lane < d.len;
   float gate = in ? load_gate(a.g, a.gate_bf16, t0) : 0.f, step = in ? load_gate(a.beta, a.gate_bf16, t0) : 0.f;
   wave_sync();
@@ -156,20 +159,22 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       }
     }
   }
-  // k (and q) transposed
-#pragma unroll 4
-  for (int x = 0; x < TP; ++x)
-    put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
-  if constexpr (BWD) {
-    wave_sync();
-    stage_rows<T, N>(Ks, qr, row, XP, lane);
-    wave_sync();
+  // k (and q) transposed, once per group
+  if (h0 % rep == 0) {
 #pragma unroll 4
     for (int x = 0; x < TP; ++x)
-      put_piece(static_cast<char*>(a.qt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
+      put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
+    if constexpr (BWD) {
+      wave_sync();
+      stage_rows<T, N>(Ks, qr, row, XP, lane);
+      wave_sync();
+#pragma unroll 4
+      for (int x = 0; x < TP; ++x)
+        put_piece(static_cast<char*>(a.qt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
+    }
   }
 
-  for (int h = g * rep; h < (g + 1) * rep; ++h) {
+  for (int h = h0; h < h0 + nh; ++h) {
     const int64_t jh = (int64_t)j * a.H + h;
     {
       double s = log_decay(gate);
@@ -188,9 +193,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       gt[2 * C + lane] = (float)exp(__shfl(s, 63) - s);
       gt[3 * C + lane] = step * E;
       reinterpret_cast<double*>(gt + 4 * C)[lane] = s;
-      if (h + 1 < (g + 1) * rep && in) {
-        gate = load_gate(a.g, a.gate_bf16, t0 + h + 1 - g * rep);
-        step = load_gate(a.beta, a.gate_bf16, t0 + h + 1 - g * rep);
+      if (h + 1 < h0 + nh && in) {
+        gate = load_gate(a.g, a.gate_bf16, t0 + h + 1 - h0);
+        step = load_gate(a.beta, a.gate_bf16, t0 + h + 1 - h0);
       }
       wave_sync();
     }
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       }
     }
     wave_sync();
-    // T, and for the backward its transpose
+    // T, its columns times beta; for the backward T's transpose, without
 #pragma unroll
     for (int x = 0; x < 6; ++x) {
       const int2 t = lower_tile(x);
@@ -311,7 +316,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       float f[8];
       block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] : 0.f;
+      for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] * bs[c0 + e] : 0.f;
       put_piece(static_cast<char*>(a.T) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
     }
     if constexpr (BWD) {
@@ -343,9 +348,14 @@ __global__ __launch_bounds__(256) void delta_clear_kernel(const int32_t* __restr
 
 template <typename T, int N>
 hipError_t prep_go(const DeltaArgs& a, bool bwd, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.max_chunks * a.G + kPrepWaves - 1) / kPrepWaves)), th(64 * kPrepWaves);
-  if (bwd) hipLaunchKernelGGL((delta_prep_kernel<T, N, true>), grid, th, 0, s, a, a.cmap());
-  else hipLaunchKernelGGL((delta_prep_kernel<T, N, false>), grid, th, 0, s, a, a.cmap());
+  // a head per wave while that does not fill the device's SIMDs once (17 tokens, 32 heads in 16
+  // groups: MEASURED2)
+  const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  const int nh = (int64_t)a.max_chunks * a.G <= 4 * cus ? 1 : a.H / a.G;
+  const int64_t items = (int64_t)a.max_chunks * (a.H / nh);
+  const dim3 grid((unsigned)((items + kPrepWaves - 1) / kPrepWaves)), th(64 * kPrepWaves);
+  if (bwd) hipLaunchKernelGGL((delta_prep_kernel<T, N, true>), grid, th, 0, s, a, a.cmap(), nh);
+  else hipLaunchKernelGGL((delta_prep_kernel<T, N, false>), grid, th, 0, s, a, a.cmap(), nh);
   return hipGetLastError();
 }
 
