@@ -230,7 +230,7 @@ __device__ __forceinline__ void store_state(float* row, int lane, const f32x4 (&
   }
 }
 
-// A lane's place in the kb-th operand that a state wave leaves: store_rows() reads one row's
+// A lane's place in the kb-th operand that a state wave leaves: LeftRows reads one row's
 // pieces together, and the exclusive or puts them on different banks.
 __device__ __forceinline__ uint32_t left_slot(int a, int i, int kb) {
   return (uint32_t)(16 * a + (i ^ ((a + 4 * kb) & 15))) * 16;
@@ -238,22 +238,33 @@ __device__ __forceinline__ uint32_t left_slot(int a, int i, int kb) {
 
 // Operands that the state waves left in LDS ([wave][EX of them], from the `from`-th on, each 32
 // columns of 16 dealt rows) to rows of a [P][COLS] matrix of T, or of two, one behind the other.
-template <typename T, int NW, int EX, int COLS, bool PAIR>
-__device__ __forceinline__ void store_rows(const char* x, int from, T* dst, int64_t plane, int rows, int w, int lane) {
-  constexpr int PX = Opnd<T>::PX, PL = kPlanes<T, PAIR>, V = 16 / (int)sizeof(T), PR = COLS / V, all = 16 * NW * PR;
+template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
+  static constexpr int PX = Opnd<T>::PX, PL = kPlanes<T, PAIR>, V = 16 / (int)sizeof(T), PR = COLS / V;
+  static constexpr int all = 16 * NW * PR, n = (all + 64 * HW - 1) / (64 * HW);
+  uint4 q[n][PL];
+  __device__ __forceinline__ static int place(int i, int w, int lane) { return (i * HW + w) * 64 + lane; }
+  __device__ __forceinline__ void load(const char* x, int from, int w, int lane) {
 #pragma unroll
-  for (int i = 0; i < (all + 64 * HW - 1) / (64 * HW); ++i) {
-    const int at = (i * HW + w) * 64 + lane, p = at / PR, c = at % PR * V;
-    if (all % (64 * HW) && at >= all) break;
-    const int s = 2 * (p / 32) + (p / 4 & 1), l16 = p % 32 / 8 * 4 + p % 4;
-    const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
+    for (int i = 0; i < n; ++i) {
+      const int at = all % (64 * HW) ? min(place(i, w, lane), all - 1) : place(i, w, lane), p = at / PR, c = at % PR * V;
+      const int s = 2 * (p / 32) + (p / 4 & 1), l16 = p % 32 / 8 * 4 + p % 4;
+      const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
 #pragma unroll
-    for (int pl = 0; pl < PL; ++pl) {
-      const uint4 v = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + left_slot(a, l16, kb));
-      if (p < rows) *reinterpret_cast<uint4*>(dst + pl * plane + (int64_t)p * COLS + c) = v;
+      for (int pl = 0; pl < PL; ++pl)
+        q[i][pl] = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + left_slot(a, l16, kb));
     }
   }
-}
+  // To the first of `rows` rows at dst; planes `plane` elements apart.
+  __device__ __forceinline__ void store(T* dst, int64_t plane, int rows, int w, int lane) const {
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) {
+      const __amdgpu_buffer_rsrc_t r = buf_rsrc(dst + pl * plane, rows * COLS * sizeof(T));   // no row past the end
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (all % (64 * HW) == 0 || place(i, w, lane) < all) buf_store16(r, place(i, w, lane) * 16, q[i][pl]);
+    }
+  }
+};
 
 // KEEP: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
 template <typename T, int N, int NW, bool KEEP, bool PAIR>
@@ -436,24 +447,20 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
 #pragma unroll
       for (int s = 0; s < NW; ++s) o[s] = kZero4;
+      // all loads from LDS before their first use: one after another each would wait in its queue
+      typename O::X f[EX][NW];
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) {
-        typename O::X f[NW];
+      for (int kb = 0; kb < EX; ++kb)
 #pragma unroll
-        for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + kb) * PX * kPiece, left_slot(la, l16, kb), T{});
-        mma_rows(f, qf[kb], o);
-      }
+        for (int s = 0; s < NW; ++s)
+          f[kb][s] = piece_x(x + (s * EX + kb) * PX * kPiece, left_slot(la, l16, kb < NK ? kb : kb - NK), T{});
+      if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb) mma_rows(f[kb], qf[kb], o);
 #pragma unroll
       for (int s = 0; s < NW; ++s) o[s] *= sE;
-#pragma unroll
-      for (int cb = 0; cb < 2; ++cb) {
-        if (cb == 0 || w >= 2) {
-          typename O::X f[NW];
-#pragma unroll
-          for (int s = 0; s < NW; ++s) f[s] = piece_x(x + (s * EX + NK + cb) * PX * kPiece, left_slot(la, l16, cb), T{});
-          mma_rows(f, af[cb], o);
-        }
-      }
+      mma_rows(f[NK], af[0], o);
+      if (w >= 2) mma_rows(f[NK + 1], af[1], o);
     }
   };
   auto write = [&](int j) {
@@ -461,8 +468,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
       const int64_t jh = jh0 + (int64_t)j * a.H;
       constexpr int PL = kPlanes<T, PAIR>;
-      store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-      store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
+      LeftRows<T, NW, EX, N, PAIR> ls;
+      LeftRows<T, NW, EX, C, PAIR> lw;
+      ls.load(x, 0, w, lane);
+      lw.load(x, NK, w, lane);
+      ls.store(static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+      lw.store(static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
     } else {
       const int c = 16 * w + l16;
       T* out = static_cast<T*>(a.out) + ((int64_t)(t.start(j) + c) * a.H + h) * a.P + p0 + 8 * la;
@@ -658,8 +669,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
     const int64_t jh = jh0 + (int64_t)j * a.H;
     constexpr int PL = kPlanes<T, PAIR>;
-    store_rows<T, NW, EX, N, PAIR>(x, 0, static_cast<T*>(a.dS) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-    store_rows<T, NW, EX, C, PAIR>(x, NK, static_cast<T*>(a.dRt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
+    LeftRows<T, NW, EX, N, PAIR> ls;
+    LeftRows<T, NW, EX, C, PAIR> lr;
+    ls.load(x, 0, w, lane);
+    lr.load(x, NK, w, lane);
+    ls.store(static_cast<T*>(a.dS) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+    lr.store(static_cast<T*>(a.dRt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
   };
   if (t.chunks > 0) {
     fetch1(last);
