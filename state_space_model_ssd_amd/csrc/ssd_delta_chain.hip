@@ -31,6 +31,8 @@
 
 namespace ssd {
 
+int device_cu_count();
+
 namespace {
 
 constexpr int C = kDeltaChunk;
@@ -715,7 +717,9 @@ template <Chain K, typename T, bool PAIR>
 hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
   // fp32 operands of dstate 128 leave LDS for two state waves
   constexpr int most = sizeof(T) == 4 ? 2 : 4;
-  if (a.P <= 32) {
+  // two state waves where heads have no more rows, or four would leave half the device idle
+  const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  if (a.P <= 32 || 2 * (int64_t)a.nstates * a.H * ((a.P + 63) / 64) <= cus) {
     switch (a.N) {
       case 32: return chain_go<K, T, 32, 2, PAIR>(a, s);
       case 64: return chain_go<K, T, 64, 2, PAIR>(a, s);
