@@ -679,7 +679,8 @@ ssd_status_t ssd_block_norm_bwd(const ssd_block_norm_problem_t* p, const void* x
  * of earlier tokens of the same 64 (they are computed together), and no others before it.
  * Limits (beyond them SSD_ERR_UNSUPPORTED): dstate 32, 64 or 128; headdim a multiple of
  * 16 up to 256; nheads up to 4096; batch and nseq up to 65535; seqlen and batch * seqlen
- * up to 2^30; tokens * nheads up to 2^34; sequences * nheads up to 2^24.
+ * up to 2^30; chunks (of 64 tokens, a sequence's last one part-filled) * nheads, and
+ * sequences * nheads * ceil(headdim / 32), up to 2^22.
  * The workspace (no initial contents) is ssd_delta_fwd_workspace_size bytes, 256-byte
  * aligned; calls that may overlap need one each.  No buffer that is written may share
  * memory with another (SSD_ERR_INVALID_ARG).  Deterministic.  Errors as for ssd_fwd.
@@ -713,8 +714,10 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
  * dinitial_states like initial_states (nullable: not computed, also given without an
  * initial state); dfinal_states nullable: 0.  dq and dk sum over the heads of a group.
  * The forward's states are computed again.  The gradient of the state is carried as the
- * state is; with bf16 inputs the other products round their operands to bf16 once, so dg
- * and dbeta are of that accuracy (some 3e-3 relative in the 2-norm) in fp32 too.
+ * state is; with bf16 inputs the other products round their operands to bf16 once.  dg and
+ * dbeta in fp32 are of fp32's kind (1e-5 relative in the 2-norm): what they are summed from
+ * is then kept to 2^-17.  In bf16 they are rounded at the end only while tokens * nheads is
+ * below 65536, and summed from operands rounded to bf16 (some 3e-3) above.
  * Workspace: ssd_delta_bwd_workspace_size bytes, as for the forward.
  */
 size_t ssd_delta_bwd_workspace_size(const ssd_delta_problem_t* p);

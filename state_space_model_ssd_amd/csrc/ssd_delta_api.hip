@@ -35,6 +35,14 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 size_t align_up(size_t v) { return (v + kDeltaAlign - 1) / kDeltaAlign * kDeltaAlign; }
 ssd_status_t status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
+int64_t delta_chunks(const ssd_delta_problem_t* p) {
+  const int64_t L = kDeltaChunk;
+  if (p->nseq == 0) return p->batch * ((p->seqlen + L - 1) / L);
+  // every sequence may end in a part-filled chunk; a chunk has a token at least
+  const int64_t most = (p->seqlen + p->nseq * (L - 1)) / L;
+  return most < p->seqlen ? most : p->seqlen;
+}
+
 ssd_status_t check_delta(const ssd_delta_problem_t* p) {
   if (!p) return SSD_ERR_INVALID_ARG;
   if (p->batch < 0 || p->seqlen < 0 || p->nseq < 0 || p->nheads < 1 || p->headdim < 1 ||
@@ -47,23 +55,18 @@ ssd_status_t check_delta(const ssd_delta_problem_t* p) {
   if (p->clear_outside < 0 || p->clear_outside > 1) return SSD_ERR_INVALID_ARG;
   if (p->nseq > 0 && p->batch != 1) return SSD_ERR_INVALID_ARG;
   if (!delta_dstate_ok(p->dstate) || p->headdim % 16 != 0 || p->headdim > 256) return SSD_ERR_UNSUPPORTED;
-  // int32 token indices, 32-bit offsets inside a chunk, grid limits
+  // int32 token indices, 32-bit offsets inside a chunk
   if (p->nheads > 4096 || p->batch > 65535 || p->nseq > 65535 || p->seqlen > (int64_t)1 << 30)
     return SSD_ERR_UNSUPPORTED;
-  const int64_t tokens = p->batch * p->seqlen, nstates = p->nseq > 0 ? p->nseq : p->batch;
-  if (tokens > (int64_t)1 << 30 || tokens * p->nheads > (int64_t)1 << 34) return SSD_ERR_UNSUPPORTED;
-  if (nstates * p->nheads > (int64_t)1 << 24) return SSD_ERR_UNSUPPORTED;
+  const int64_t nstates = p->nseq > 0 ? p->nseq : p->batch;
+  if (p->batch * p->seqlen > (int64_t)1 << 30) return SSD_ERR_UNSUPPORTED;
+  // launches of at most 2^31 threads: 512 for each chunk and group, or each sequence, head and
+  // 32 rows of its state
+  if (delta_chunks(p) * p->nheads > (int64_t)1 << 22 ||
+      nstates * p->nheads * ((p->headdim + 31) / 32) > (int64_t)1 << 22)
+    return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
-
-int64_t delta_chunks(const ssd_delta_problem_t* p) {
-  const int64_t L = kDeltaChunk;
-  if (p->nseq == 0) return p->batch * ((p->seqlen + L - 1) / L);
-  // every sequence may end in a part-filled chunk; a chunk has a token at least
-  const int64_t most = (p->seqlen + p->nseq * (L - 1)) / L;
-  return most < p->seqlen ? most : p->seqlen;
-}
-
 DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   DeltaArgs a{};
   a.total = (int)(p->batch * p->seqlen);

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_seq_kernel(
       all += wave_tot[w];
     }
     if (s < nstates) seq_chunks[s] = min(carry + before + v - cnt, max_chunks);
-    carry += all;
+    carry = min(carry + all, max_chunks);   // malformed lengths may add up past 32 bits
     __syncthreads();
   }
   if (tid == 0) seq_chunks[nstates] = min(carry, max_chunks);

@@ -57,7 +57,8 @@ def bwd(lib, p, **kw):
     (dict(dstate=96), UNS), (dict(dstate=256), UNS), (dict(headdim=72), UNS), (dict(headdim=272), UNS),
     (dict(nheads=8192), UNS), (dict(batch=65536), UNS), (dict(seqlen=2 ** 30 + 1), UNS),
     (dict(batch=1024, seqlen=2 ** 20 + 1), UNS), (dict(batch=1, nseq=65536), UNS),
-    (dict(batch=1, seqlen=2 ** 23, nheads=4096), UNS), (dict(batch=8192, nheads=4096), UNS),
+    (dict(batch=1, seqlen=2 ** 25 + 1), UNS), (dict(batch=1025, nheads=4096, seqlen=1, headdim=16), UNS),
+    (dict(batch=129, nheads=4096, headdim=256, seqlen=0), UNS),
 ])
 def test_delta_problems_refused(lib, kw, code):
     p = delta(**kw)
@@ -68,8 +69,8 @@ def test_delta_problems_refused(lib, kw, code):
 
 @pytest.mark.parametrize("kw", [
     dict(dstate=32, headdim=16), dict(headdim=256, nheads=4096, ngroups=4096, batch=1),
-    dict(batch=65535, seqlen=1), dict(batch=1, nseq=65535), dict(batch=1, seqlen=2 ** 30, nheads=16),
-    dict(batch=1, seqlen=2 ** 22, nheads=4096), dict(batch=4096, nheads=4096, seqlen=1),
+    dict(batch=65535, seqlen=1), dict(batch=1, nseq=65535), dict(batch=1, seqlen=2 ** 25),
+    dict(batch=1, seqlen=2 ** 28, nheads=1, ngroups=1), dict(batch=1024, nheads=4096, seqlen=1, headdim=32),
 ])
 def test_delta_limits_taken(lib, kw):
     p = delta(**kw)
