@@ -10,8 +10,8 @@
 // channel of a pair comes from the row in LDS, any R, D and pairing alike; a wave reads
 // only rows that it wrote, so no barrier is needed there.
 //
-// Angles are taken by turns in fp64: pos freq / 2 pi less the nearest whole number, which
-// leaves them exact to 2^-25 of a turn however far the position.
+// Angles are taken by turns in fp64: pos freq / 2 pi less the nearest whole number, off by
+// 2^-52 of the turns and then, in fp32, by 2^-26 of a turn at most.
 #include "ssd_delta.h"
 #include "ssd_layer_device.h"
 #include "ssd_rowsum.h"
