@@ -76,8 +76,12 @@ struct DeltaArgs {
 };
 
 bool delta_dstate_ok(int64_t N);
-// Zeros in the rows that no sequence of a packed batch has, `row_bytes` each.
-hipError_t launch_delta_clear(const DeltaArgs& a, void* p, int64_t row_bytes, hipStream_t s);
+// Zeros in the rows that no sequence of a packed batch has, of n tensors and `row` bytes each.
+struct DeltaClear {
+  void* p[5];
+  int64_t row[5];
+};
+hipError_t launch_delta_clear(const DeltaArgs& a, const DeltaClear& c, int n, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s);
 // The chain of states; `keep`: for the backward, which wants S0 and Wt and no output.
 hipError_t launch_delta_chain(const DeltaArgs& a, bool keep, hipStream_t s);

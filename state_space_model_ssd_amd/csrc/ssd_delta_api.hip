@@ -258,7 +258,7 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = ssd::plan(a, s);
   if (e == hipSuccess && a.clear && a.cu)
-    e = ssd::launch_delta_clear(a, out, (int64_t)(m.H * m.P * m.e), s);
+    e = ssd::launch_delta_clear(a, {{out}, {(int64_t)(m.H * m.P * m.e)}}, 1, s);
   if (e == hipSuccess) e = ssd::launch_delta_prep(a, false, s);
   if (e == hipSuccess) e = ssd::launch_delta_chain(a, false, s);
   return ssd::status_of(e);
@@ -299,14 +299,9 @@ ssd_status_t ssd_delta_bwd(const ssd_delta_problem_t* p, const void* q, const vo
   ssd::delta_layout(a, p->nseq > 0, true, workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = ssd::plan(a, s);
-  if (a.clear && a.cu) {
-    const int64_t qk = (int64_t)(m.G * m.N * m.e), v_row = (int64_t)(m.H * m.P * m.e);
-    const int64_t gate = (int64_t)(m.H * m.ge);
-    if (e == hipSuccess) e = ssd::launch_delta_clear(a, dq, qk, s);
-    if (e == hipSuccess) e = ssd::launch_delta_clear(a, dk, qk, s);
-    if (e == hipSuccess) e = ssd::launch_delta_clear(a, dv, v_row, s);
-    if (e == hipSuccess) e = ssd::launch_delta_clear(a, dg, gate, s);
-    if (e == hipSuccess) e = ssd::launch_delta_clear(a, dbeta, gate, s);
+  if (e == hipSuccess && a.clear && a.cu) {
+    const int64_t qk = (int64_t)(m.G * m.N * m.e), v = (int64_t)(m.H * m.P * m.e), gate = (int64_t)(m.H * m.ge);
+    e = ssd::launch_delta_clear(a, {{dq, dk, dv, dg, dbeta}, {qk, qk, v, gate, gate}}, 5, s);
   }
   if (e == hipSuccess) e = ssd::launch_delta_prep(a, true, s);
   if (e == hipSuccess) e = ssd::launch_delta_chain(a, true, s);

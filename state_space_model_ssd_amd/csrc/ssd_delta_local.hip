@@ -110,24 +110,22 @@ __device__ __forceinline__ void kept_get(const typename Kept<T, PAIR>::V& v, flo
   }
 }
 
-// A [kSlab][COLS] tile on its way from memory to LDS, through registers; zeros in rows that
-// there are not.
-template <typename T, int COLS> struct Slab {
+// A [kSlab][COLS] tile on its way from memory to LDS, through the registers of THREADS threads;
+// zeros in rows that there are not.
+template <typename T, int COLS, int THREADS> struct Slab {
   static constexpr int V = 16 / (int)sizeof(T), PR = COLS / V, all = kSlab * PR;
-  static constexpr int n = (all + kLocalThreads - 1) / kLocalThreads;
+  static constexpr int n = (all + THREADS - 1) / THREADS;
   uint4 q[n];
   __device__ __forceinline__ void load(const T* src, int rows, int tid) {
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(src, (uint32_t)(max(rows, 0) * COLS) * (uint32_t)sizeof(T));
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int at = i * kLocalThreads + tid, r = at / PR;
-      q[i] = load16(src + (int64_t)at * V, (all % kLocalThreads == 0 || at < all) && r < rows);
-    }
+    for (int i = 0; i < n; ++i) q[i] = buf_load16(r, (i * THREADS + tid) * 16);
   }
   __device__ __forceinline__ void store(T* t, int tid) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const int at = i * kLocalThreads + tid;
-      if (all % kLocalThreads == 0 || at < all)
+      const int at = i * THREADS + tid;
+      if (all % THREADS == 0 || at < all)
         *reinterpret_cast<uint4*>(Tile<T, COLS>::piece(t, at / PR, at % PR * V)) = q[i];
     }
   }
@@ -135,26 +133,25 @@ template <typename T, int COLS> struct Slab {
 
 // Tokens' [C][COLS] values as operands: the four dealt tiles of rows of each 32 columns, in
 // Opnd<T>::PX pieces; the exclusive or keeps lanes that write together on different banks.
-template <typename T, int COLS> struct Tokens {
+template <typename T, int COLS, int THREADS> struct Tokens {
   static constexpr int PX = Opnd<T>::PX, PR = COLS / 8 * PX, all = C * PR;
-  static constexpr int n = (all + kLocalThreads - 1) / kLocalThreads;
+  static constexpr int n = (all + THREADS - 1) / THREADS;
   static constexpr int bytes = COLS / 32 * 4 * PX * kPiece;
   uint4 q[n];
   __device__ __forceinline__ static uint32_t slot(int a, int i) { return (uint32_t)(16 * a + (i ^ 2 * a)) * 16; }
-  // Columns from `col` bytes on, of `cols` bytes that a row has.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t pitch, uint32_t col, uint32_t cols, int tid) {
+  // A row's first columns, of PR * 16 bytes.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t pitch, int tid) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const int at = i * kLocalThreads + tid, c = at / PR;
-      const uint32_t b = col + at % PR * 16;
-      q[i] = buf_load16(r, (all % kLocalThreads == 0 || at < all) && b < cols ? c * pitch + b : 0xffffff00u);
+      const int at = i * THREADS + tid;
+      q[i] = buf_load16(r, all % THREADS == 0 || at < all ? at / PR * pitch + at % PR * 16 : 0xffffff00u);
     }
   }
   __device__ __forceinline__ void store(char* t, int tid) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const int at = i * kLocalThreads + tid, c = at / PR, x = at % PR, y = x % (4 * PX);
-      if (all % kLocalThreads == 0 || at < all)
+      const int at = i * THREADS + tid, c = at / PR, x = at % PR, y = x % (4 * PX);
+      if (all % THREADS == 0 || at < all)
         *reinterpret_cast<uint4*>(t + ((x / (4 * PX) * 4 + tile_of(c)) * PX + y % PX) * kPiece + slot(y / PX, row_of(c))) = q[i];
     }
   }
@@ -167,28 +164,64 @@ template <typename T, int COLS> struct Tokens {
   __device__ __forceinline__ static typename Opnd<T>::X token(const char* t, int kb, int c, int lane) {
     return piece_x(t + (kb * 4 + tile_of(c)) * PX * kPiece, slot(lane >> 4, row_of(c)), T{});
   }
+  // Tokens 32 cb + 8 (lane / 16) .. + 7 of the channels of dealt tile u: the transposed operand.
+  __device__ __forceinline__ static bf16x8 transposed(const char* t, int cb, int u, int lane) {
+    static_assert(sizeof(T) == 2, "reads that transpose are of 16 bits");
+    const int m = lane & 15, n = 8 * (m & 3) + 4 * (u & 1);   // of 32 channels u / 2
+    const uint32_t at = slot(n / 8, 4 * (lane >> 4) + (m >> 2)) + 2 * (n % 8);
+    const char* p = t + ((u >> 1) * 4 + 2 * cb) * kPiece + at;
+    const i16x4 lo = lds_tr16_b64(reinterpret_cast<const bf16*>(p));
+    const i16x4 hi = lds_tr16_b64(reinterpret_cast<const bf16*>(p + kPiece));
+    typedef short i16x8v __attribute__((ext_vector_type(8)));
+    const i16x8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+  }
 };
+
+__device__ __forceinline__ bf16x8 operand_of(const uint4 (&q)[1], bf16) { return __builtin_bit_cast(bf16x8, q[0]); }
+__device__ __forceinline__ F8 operand_of(const uint4 (&q)[2], float) {
+  F8 f;
+  block8(__builtin_bit_cast(f32x4, q[0]), __builtin_bit_cast(f32x4, q[1]), f.v);
+  return f;
+}
+
+// An operand's lanes (row l % 16, columns 8 (l / 16) ..) in the order of rows: lane l has row l / 4,
+// columns 8 (l % 4) ...
+template <typename V>
+__device__ __forceinline__ V by_rows(V v, int lane) {
+  constexpr int n = sizeof(V) / 4;
+  int q[n];
+  __builtin_memcpy(q, &v, sizeof(V));
+#pragma unroll
+  for (int i = 0; i < n; ++i) q[i] = __builtin_amdgcn_ds_bpermute(((lane & 3) * 16 + lane / 4) * 4, q[i]);
+  __builtin_memcpy(&v, q, sizeof(V));
+  return v;
+}
+
+// What a slab needs from memory.  The first waves' threads take W and their tokens' values, the
+// others dR and dO.
+template <typename T, int N, int PL> struct Loads {
+  Slab<T, C, kLocalThreads / 2> wr[PL];
+  Slab<T, N, kLocalThreads> s[PL], d[PL];
+  Tokens<T, kSlab, kLocalThreads / 2> vo;         // v: eight values of row 16 wave + lane / 4
+};
+
+__device__ __forceinline__ double buf_load_double(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(double, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
 
 __device__ __forceinline__ void store_gate(void* p, bool b16, int64_t i, float v) {
   if (b16) static_cast<bf16*>(p)[i] = static_cast<bf16>(v);
   else static_cast<float*>(p)[i] = v;
 }
 
-// A token's channels (its operands x over all of them) at the rows of tile half N / 32 + i.
-template <typename T, int N>
-__device__ __forceinline__ void channels4(const typename Opnd<T>::X (&x)[N / 32], int half, int i, float (&f)[4]) {
-  constexpr int NH = N / 32;
-  float a[8], b[8];
-  if constexpr (NH >= 2) {
-    Opnd<T>::get(x[i / 2], a);
-    Opnd<T>::get(x[NH / 2 + i / 2], b);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = half ? b[4 * (i % 2) + r] : a[4 * (i % 2) + r];
-  } else {
-    Opnd<T>::get(x[0], a);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = half ? a[4 + r] : a[r];
-  }
+// The four of an operand's eight values that lie at the rows of its first tile, or of its second.
+template <typename T>
+__device__ __forceinline__ f32x4 channels4(const typename Opnd<T>::X& x, bool second) {
+  float a[8];
+  Opnd<T>::get(x, a);
+  const f32x4 lo = {a[0], a[1], a[2], a[3]}, hi = {a[4], a[5], a[6], a[7]};
+  return second ? hi : lo;
 }
 
 // PAIR: what the chains kept comes as pairs.
@@ -198,8 +231,8 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   using X = typename O::X;
   using TC = Tile<T, C>;
   using TN = Tile<T, N>;
-  using TS = Tokens<T, kSlab>;
-  using TK = Tokens<T, N>;
+  using TS = Tokens<T, kSlab, kLocalThreads / 2>;
+  using TK = Tokens<T, N, kLocalThreads>;
   constexpr int NK = N / 32, NH = N / 32, PX = O::PX;   // NH: a wave's tiles of dq and dk
   using KV = typename Kept<T, PAIR>::V;
   constexpr int PL = kPlanes<T, PAIR>;
@@ -229,18 +262,60 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
 
   if constexpr (KQ) {
     TK sk, sq;
-    sk.load(kr, qrow, 0, N * sizeof(T), threadIdx.x);
-    sq.load(qr, qrow, 0, N * sizeof(T), threadIdx.x);
+    sk.load(kr, qrow, threadIdx.x);
+    sq.load(qr, qrow, threadIdx.x);
     sk.store(kqs, threadIdx.x);
     sq.store(kqs + TK::bytes, threadIdx.x);       // read after the slabs' barriers
   }
   f32x4 dq[NH], dk[NH];
 #pragma unroll
   for (int i = 0; i < NH; ++i) dq[i] = dk[i] = kZero4;
-  Slab<T, C> sW[PL], sR[PL];
-  Slab<T, N> sS[PL], sD[PL];
-  TS sO;
-  X vv;
+  // slabs in flight
+  constexpr int AHEAD = sizeof(T) == 2 && !PAIR ? 2 : 1;
+  Loads<T, N, PL> next[AHEAD];
+  float gates[5];
+  double Gt = 0.0;
+  float bt = 0.f;
+  // head h's slab from p0 (none past the group's last head or the last value)
+  auto fetch = [&](Loads<T, N, PL>& q, int h, int p0, int tid) {
+    const int rows = h < (g + 1) * rep ? a.P - p0 : 0;
+    const int64_t jh = (int64_t)j * a.H + h, vo = ((int64_t)d.start * a.H + h) * a.P;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int64_t at = (jh * PL + i) * a.P + p0;
+      q.wr[i].load(static_cast<const T*>(half ? a.dRt : a.Wt) + at * C, min(rows, kSlab), tid & (kLocalThreads / 2 - 1));
+      q.s[i].load(static_cast<const T*>(a.S0) + at * N, min(rows, kSlab), tid);
+      q.d[i].load(static_cast<const T*>(a.dS) + at * N, min(rows, kSlab), tid);
+    }
+    const uint32_t vbytes = rows > 0 ? (uint32_t)(d.len - 1) * vrow + a.P * (uint32_t)sizeof(T) : 0;
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(static_cast<const T*>(half ? a.dout : a.v) + vo, vbytes);
+    const uint32_t cols = a.P * (uint32_t)sizeof(T), col = p0 * (uint32_t)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < TS::n; ++i) {
+      const int at = i * (kLocalThreads / 2) + (tid & (kLocalThreads / 2 - 1));
+      const uint32_t b = col + (half ? at % TS::PR * 16 : 8 * (tid & 3) * (uint32_t)sizeof(T) + 16 * i);
+      const uint32_t tok = half ? at / TS::PR : 16 * w + (tid & 63) / 4;
+      q.vo.q[i] = buf_load16(r, b < cols ? tok * vrow + b : 0xffffff00u);
+    }
+  };
+  // head h's decays
+  auto fetch_gates = [&](int h, int tid) {
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.gates + ((int64_t)j * a.H + h) * kGateFloats, h < (g + 1) * rep ? kGateFloats * 4 : 0);
+    const uint32_t c = 16 * w + (tid & 15);
+    gates[0] = buf_load4(r, 4 * c);
+    gates[1] = buf_load4(r, 4 * (C + c));
+    gates[2] = buf_load4(r, 4 * (2 * C + c));
+    gates[3] = buf_load4(r, 4 * (2 * C - 1));
+    gates[4] = buf_load4(r, 4 * (16 * w + (tid & 63) / 4));
+    Gt = buf_load_double(r, 4 * 4 * C + 8 * (tid & (C - 1)));
+    bt = buf_load4(r, 4 * (tid & (C - 1)));
+  };
+  {
+    const int tid = opaque_tid();
+    fetch_gates(g * rep, tid);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(next[i], g * rep, i * kSlab, tid);
+  }
 
   for (int h = g * rep; h < (g + 1) * rep; ++h) {
     // through opaque_tid, or every address below would be kept from head to head
@@ -255,40 +330,12 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       if constexpr (KQ) return TK::token(kqs + (q ? TK::bytes : 0), kb, c, lane);
       else return load_opnd(q ? qr : kr, c * qrow + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
     };
-    const int64_t jh = (int64_t)j * a.H + h;
-    const float* gt = a.gates + jh * kGateFloats;
     const int64_t vo = ((int64_t)d.start * a.H + h) * a.P;
-    const uint32_t vbytes = (uint32_t)(d.len - 1) * vrow + a.P * (uint32_t)sizeof(T);
-    const __amdgpu_buffer_rsrc_t vr = buf_rsrc(static_cast<const T*>(a.v) + vo, vbytes);
-    const __amdgpu_buffer_rsrc_t dor = buf_rsrc(static_cast<const T*>(a.dout) + vo, vbytes);
-    auto fetch = [&](int p0) {
-      const int rows = min(kSlab, a.P - p0);
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const int64_t at = (jh * PL + i) * a.P + p0;
-        sW[i].load(static_cast<const T*>(a.Wt) + at * C, rows, tid);
-        sR[i].load(static_cast<const T*>(a.dRt) + at * C, rows, tid);
-        sS[i].load(static_cast<const T*>(a.S0) + at * N, rows, tid);
-        sD[i].load(static_cast<const T*>(a.dS) + at * N, rows, tid);
-      }
-      sO.load(dor, vrow, p0 * (uint32_t)sizeof(T), a.P * (uint32_t)sizeof(T), tid);
-    };
-    auto put = [&](int b) {
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        sW[i].store(Ws[b] + i * TC::size, tid);
-        sR[i].store(Rs[b] + i * TC::size, tid);
-        sS[i].store(Ss[b] + i * TN::size, tid);
-        sD[i].store(Ds[b] + i * TN::size, tid);
-      }
-      sO.store(dOs[b], tid);
-    };
-    fetch(0);
     if (tid < C) {
-      Gs[tid] = reinterpret_cast<const double*>(gt + 4 * C)[tid];
-      bs[tid] = gt[tid];
+      Gs[tid] = Gt;
+      bs[tid] = bt;
     }
-    const float be = gt[c], E = gt[C + c], Dc = gt[2 * C + c], EC = gt[2 * C - 1];
+    const float be = gates[0], E = gates[1], Dc = gates[2], EC = gates[3], br = gates[4];
 
     f32x4 Px[4], Lx[4];                           // [c'][c] of P's and M's sources, or of their transposes
 #pragma unroll
@@ -297,21 +344,39 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
 #pragma unroll
     for (int i = 0; i < NH; ++i) yq[i] = yx[i] = yd[i] = kZero4;
     float sdot = 0.f, rv = 0.f;
-    for (int p0 = 0, b = 0; p0 < a.P; p0 += kSlab, b = BUF - 1 - b) {
-      const bool in = p0 + 8 * la < a.P;          // values past P: none
-      const uint32_t vc = (uint32_t)(p0 + 8 * la) * sizeof(T);
+    auto slab = [&](Loads<T, N, PL>& q, int p0, int b) {
       if constexpr (BUF == 1) __syncthreads();    // the slab before is read
-      put(b);
 #pragma unroll
-      for (int i = 0; i < Slab<T, N>::n; ++i) {
-        sdot += dot16(sS[0].q[i], sD[0].q[i], T{});
-        if constexpr (PL == 2) sdot += dot16(sS[0].q[i], sD[1].q[i], T{}) + dot16(sS[1].q[i], sD[0].q[i], T{});
+      for (int i = 0; i < PL; ++i) {
+        q.wr[i].store((half ? Rs : Ws)[b] + i * TC::size, tid & (kLocalThreads / 2 - 1));
+        q.s[i].store(Ss[b] + i * TN::size, tid);
+        q.d[i].store(Ds[b] + i * TN::size, tid);
       }
-      if (half == 0) vv = load_opnd(vr, in ? c * vrow + vc : 0xffffff00u, T{});
+      if (half) q.vo.store(dOs[b], tid & (kLocalThreads / 2 - 1));
+#pragma unroll
+      for (int i = 0; i < Slab<T, N, kLocalThreads>::n; ++i) {
+        sdot += dot16(q.s[0].q[i], q.d[0].q[i], T{});
+        if constexpr (PL == 2) sdot += dot16(q.s[0].q[i], q.d[1].q[i], T{}) + dot16(q.s[1].q[i], q.d[0].q[i], T{});
+      }
       __syncthreads();
-      if (p0 + kSlab < a.P) fetch(p0 + kSlab);
       const KV wo = kept_plain<T, C, PAIR>(Ws[b], 16 * w, lane), ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane);
       const X od = TS::token(dOs[b], 0, c, lane);
+      if (half == 0) {
+        // dR in the order of rows, four lanes each, as v comes and dv goes: one lane a row would
+        // issue four times slower
+        float r8[8], v8[8];
+        kept_get<T, PAIR>(by_rows(ro, lane), r8);
+        O::get(operand_of(q.vo.q, T{}), v8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          rv += r8[e] * v8[e];
+          r8[e] *= br;
+        }
+        const int at = p0 + 8 * (lane & 3), tok = 16 * w + lane / 4;
+        if (at < a.P && tok < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)tok * a.H * a.P + at, O::round(r8));
+      }
+      fetch(q, h, p0 + AHEAD * kSlab, tid);
+      __builtin_amdgcn_sched_barrier(0);
       // all four tiles, also those with no pair of the wave's tokens: no branch
       if (half) {
         X f[4];
@@ -330,28 +395,23 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         mma_rows(r, od, Px);
         mma_rows(r, ro, Lx);
       }
+      __builtin_amdgcn_sched_barrier(0);
       {
         KV f[NH];
 #pragma unroll
         for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ss[b], half * NH + i, lane);
         mma_rows(f, od, yq);
         mma_rows(f, ro, yx);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ds[b], half * NH + i, lane);
         mma_rows(f, wo, yd);
       }
-      float r8[8];
-      kept_get<T, PAIR>(ro, r8);
-      if (half == 0) {
-        float v8[8];
-        O::get(vv, v8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rv += r8[e] * v8[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r8[e] *= be;
-        if (in && c < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)c * a.H * a.P + p0 + 8 * la, O::round(r8));
-      }
+    };
+    for (int p0 = 0; p0 < a.P; p0 += AHEAD * kSlab) {
+      slab(next[0], p0, 0);
+      if constexpr (AHEAD == 2)
+        if (p0 + kSlab < a.P) slab(next[1], p0 + kSlab, BUF - 1);
     }
     __builtin_amdgcn_sched_barrier(0);            // what follows needs the registers of the slabs' loads
     X ko[NK], qn[NK];                             // the token's k and q
@@ -367,7 +427,13 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       char* x = swap + (w * 8 + half * 4) * PX * kPiece;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        float p8[8], m8[8];
+        float p8[8] = {}, m8[8] = {};
+        // 32 tokens that make no pair with the wave's, later ones or earlier ones: zeros
+        if (half ? cb < w / 2 : cb > w / 2) {
+          put_piece(x + cb * PX * kPiece, lane * 16, O::round(p8));
+          put_piece(x + (2 + cb) * PX * kPiece, lane * 16, O::round(m8));
+          continue;
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int u = 2 * cb + t;
@@ -399,11 +465,15 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     }
     // the row sums that need the states' products alone
     float ql = 0.f, kx = 0.f, kd = 0.f;
+    X kh, qh;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      float k4[4], q4[4];
-      channels4<T, N>(ko, half, i, k4);
-      channels4<T, N>(qn, half, i, q4);
+      // the wave's tiles are half NH + i of the token's channels
+      if (i % 2 == 0) {
+        kh = token(false, (half * NH + i) / 2);
+        qh = token(true, (half * NH + i) / 2);
+      }
+      const f32x4 k4 = channels4<T>(kh, NH >= 2 ? i % 2 : half), q4 = channels4<T>(qh, NH >= 2 ? i % 2 : half);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         ql += q4[r] * yq[i][r];
@@ -412,6 +482,10 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    // the next head's first slabs on their way
+    fetch_gates(h + 1, tid);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(next[i], h + 1, i * kSlab, tid);
     __syncthreads();
     X pr[2], mr[2], pc[2], mc[2];
     {
@@ -429,8 +503,15 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       f32x4 q = yq[i] * (a.scale * E), x = yx[i] * -E, k = yd[i] * Dc;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
-        const int at = (cb * (N / 16) + half * NH + i) * PX * kPiece;
-        const X kf = piece_x(kt + at, lane * 16, T{}), qf = piece_x(qt + at, lane * 16, T{});
+        X kf, qf;
+        if constexpr (sizeof(T) == 2) {
+          kf = TK::transposed(kqs, cb, half * NH + i, lane);
+          qf = TK::transposed(kqs + TK::bytes, cb, half * NH + i, lane);
+        } else {
+          const int at = (cb * (N / 16) + half * NH + i) * PX * kPiece;
+          kf = piece_x(kt + at, lane * 16, T{});
+          qf = piece_x(qt + at, lane * 16, T{});
+        }
         q = mma(kf, pr[cb], q);
         x = mma(kf, mr[cb], x);
         k = mma(qf, pc[cb], k);
@@ -440,7 +521,11 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       dk[i] += k + x * be;
       if (i % 2) __builtin_amdgcn_sched_barrier(0);
     }
-    const float db = column_sum(rv + mk - E * kx);
+    // a row's sum of dR v from its four lanes to its column's
+    rv += __shfl_xor(rv, 1);
+    rv += __shfl_xor(rv, 2);
+    const float rc = __shfl(rv, 4 * l16);
+    const float db = column_sum((la == 0 ? rc : 0.f) + mk - E * kx);
     const float lf = column_sum(a.scale * E * ql - be * E * kx), md = column_sum(Dc * kd + pairs);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sdot += __shfl_xor(sdot, off);

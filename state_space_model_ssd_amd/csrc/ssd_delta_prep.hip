@@ -335,12 +335,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   }
 }
 
-// Rows [0, cu[0]) and [cu[nstates], total) of a tensor, `row` bytes each (a multiple of 2).
+// Rows [0, cu[0]) and [cu[nstates], total) of the tensors, each by its grid row.
 __global__ __launch_bounds__(256) void delta_clear_kernel(const int32_t* __restrict__ cu, int nstates,
-                                                          int total, void* p, int64_t row) {
-  const int64_t n2 = row / 2, lo = min(max(cu[0], 0), total) * n2;
+                                                          int total, const DeltaClear c) {
+  const int64_t n2 = c.row[blockIdx.y] / 2, lo = min(max(cu[0], 0), total) * n2;
   const int64_t hi = min(max(cu[nstates], 0), total) * n2, end = total * n2;
-  unsigned short* o = static_cast<unsigned short*>(p);
+  unsigned short* o = static_cast<unsigned short*>(c.p[blockIdx.y]);
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   for (int64_t i = at; i < lo; i += step) o[i] = 0;
   for (int64_t i = max(lo, hi) + at; i < end; i += step) o[i] = 0;
@@ -378,10 +378,12 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s) {
   return a.bf16 ? prep_type<bf16>(a, bwd, s) : prep_type<float>(a, bwd, s);
 }
 
-hipError_t launch_delta_clear(const DeltaArgs& a, void* p, int64_t row_bytes, hipStream_t s) {
-  const int64_t blocks = ((int64_t)a.total * row_bytes / 2 + 256 * 16 - 1) / (256 * 16);
-  hipLaunchKernelGGL(delta_clear_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, s,
-                     a.cu, a.nstates, a.total, p, row_bytes);
+hipError_t launch_delta_clear(const DeltaArgs& a, const DeltaClear& c, int n, hipStream_t s) {
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) most = c.row[i] > most ? c.row[i] : most;
+  const int64_t blocks = ((int64_t)a.total * most / 2 + 256 * 16 - 1) / (256 * 16);
+  hipLaunchKernelGGL(delta_clear_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), n), dim3(256), 0, s,
+                     a.cu, a.nstates, a.total, c);
   return hipGetLastError();
 }
 
