@@ -377,23 +377,19 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       }
       fetch(q, h, p0 + AHEAD * kSlab, tid);
       __builtin_amdgcn_sched_barrier(0);
-      // all four tiles, also those with no pair of the wave's tokens: no branch
-      if (half) {
-        X f[4];
-        KV r[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f[u] = TS::dealt(dOs[b], 0, u, lane);
-          r[u] = kept_dealt<T, C, PAIR>(Rs[b], u, lane);
+      for (int cb = 0; cb < 2; ++cb) {
+        if (half ? cb < w / 2 : cb > w / 2) continue;   // no pairs there
+        X f[2];
+        KV r[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (half) f[t] = TS::dealt(dOs[b], 0, 2 * cb + t, lane);
+          r[t] = kept_dealt<T, C, PAIR>(half ? Rs[b] : Ws[b], 2 * cb + t, lane);
         }
-        mma_rows(f, wo, Px);
-        mma_rows(r, wo, Lx);
-      } else {
-        KV r[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) r[u] = kept_dealt<T, C, PAIR>(Ws[b], u, lane);
-        mma_rows(r, od, Px);
-        mma_rows(r, ro, Lx);
+        if (half) mma_rows(f, wo, Px + 2 * cb);
+        else mma_rows(r, od, Px + 2 * cb);
+        mma_rows(r, half ? wo : ro, Lx + 2 * cb);
       }
       __builtin_amdgcn_sched_barrier(0);
       {
