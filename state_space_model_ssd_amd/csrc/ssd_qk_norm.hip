@@ -5,10 +5,11 @@
 // for the R pairs of channels (i, i + R) or (2i, 2i + 1); channels from 2R on stay.
 //
 // What bounds it: each element read and written once (backward: two reads, one write).  A
-// row lies over LPR lanes, 16 bytes each; a workgroup takes all heads of a few tokens, so
-// a token's cosines and sines are made once and lie in LDS for all of them.  The other
-// channel of a pair comes from the row in LDS, any R, D and pairing alike; a wave reads
-// only rows that it wrote, so no barrier is needed there.
+// row lies over LPR lanes, 16 bytes each.  A workgroup takes a few tokens, whose cosines and
+// sines are made once, into LDS; a lane keeps its channels' in registers for all heads of its
+// token.  The other channel of a pair is the lane's own (neighbours), or comes by a second load
+// of the row from the cache (halves, where they are whole vectors); where rows or halves are no
+// whole vectors it comes from the row in LDS.  MEASUREDQ
 //
 // Angles are taken by turns in fp64: pos freq / 2 pi less the nearest whole number, off by
 // 2^-52 of the turns and then, in fp32, by 2^-26 of a turn at most.
@@ -25,7 +26,7 @@ int device_cu_count();
 namespace {
 
 constexpr int kQnThreads = 256;
-constexpr int kQnMaxTok = 4;            // most tokens a workgroup takes at a time
+constexpr int kQnTok = 4;               // tokens a workgroup takes at a time where there are many
 constexpr int kQnMaxParts = 1024;       // partial rows the workspace holds
 constexpr int kQnSegment = 32;
 
@@ -49,39 +50,73 @@ template <int V> struct RowLane {
   }
 };
 
-// One token's rows of q and k: row i of the workgroup's tokens.
-struct RowAt {
-  int which, head, tok;
-  __device__ __forceinline__ RowAt(const QkNormArgs& a, int i) {
-    const int all = a.heads[0] + a.heads[1];
-    tok = i / all;
-    head = i - tok * all;
-    which = head >= a.heads[0];
-    if (which) head -= a.heads[0];
-  }
-};
-
-// f turned (or, BACK, turned back) by the token's angles; `row`: the row's D values in LDS.
-template <int V, bool BACK>
-__device__ __forceinline__ void rotate(const QkNormArgs& a, float* row, const float2* cs, int n, float (&f)[V]) {
-  __builtin_amdgcn_wave_barrier();
+// V weights from element n on, ones without weights: a resource of no bytes and a select, for
+// behind a branch they would be waited for at its end.
+template <int V>
+__device__ __forceinline__ void weights(const QkNormArgs& a, int k, int n, float (&w)[V]) {
+  const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.w[k], a.w[k] ? a.D * 4 : 0);
+  if constexpr (V == 1) {
+    w[0] = buf_load4(r, n * 4);
+  } else {
 #pragma unroll
-  for (int e = 0; e < V; ++e) row[n + e] = f[e];
-  __builtin_amdgcn_wave_barrier();
+    for (int e = 0; e < V; e += 4) {
+      const f32x4 v = __builtin_bit_cast(f32x4, buf_load16(r, (n + e) * 4));
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int c = n + e;
-    const bool first = a.interleaved ? !(c & 1) : c < a.R;
-    const int pair = a.interleaved ? c >> 1 : first ? c : c - a.R;
-    if (c < 2 * a.R) {
-      const float2 t = cs[pair];
-      const float o = row[a.interleaved ? c ^ 1 : first ? c + a.R : c - a.R];
-      const float s = first == BACK ? t.y : -t.y;
-      f[e] = f[e] * t.x + o * s;
+      for (int i = 0; i < 4; ++i) w[e + i] = v[i];
     }
   }
-  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int e = 0; e < V; ++e) w[e] = a.w[k] ? w[e] : 1.f;
 }
+
+// From a lane's first element to the other of its pair (halves of whole vectors); 0 from 2 R on.
+__device__ __forceinline__ int other(const QkNormArgs& a, int n) { return n < a.R ? a.R : n < 2 * a.R ? -a.R : 0; }
+
+// How the other channel of a pair is had: there is none; by a load (halves of whole vectors);
+// in the lane (neighbours, rows of whole vectors); through LDS.
+enum class Pairs { none, load, lane, lds };
+
+// A lane's channels of one token: the cosine, and the sine with its sign, by which the other
+// channel of the pair counts; (1, 0) from 2 R on.  BACK: turned back.
+template <int V, Pairs M, bool BACK> struct Turns {
+  float c[V], s[V];
+  __device__ __forceinline__ void get(const QkNormArgs& a, const float2* cs, int n) {
+    if constexpr (M == Pairs::none) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int i = n + e;
+      const bool first = a.interleaved ? !(i & 1) : i < a.R;
+      const float2 t = cs[min(a.interleaved ? i >> 1 : first ? i : i - a.R, a.R - 1)];
+      c[e] = i < 2 * a.R ? t.x : 1.f;
+      s[e] = i < 2 * a.R ? first == BACK ? t.y : -t.y : 0.f;
+    }
+  }
+  // f turned; `o`: the pairs' other values (load); `row`: the row's D values in LDS (lds)
+  __device__ __forceinline__ void turn(const QkNormArgs& a, const float (&o)[V], float* row, int n, float (&f)[V]) const {
+    if constexpr (M == Pairs::load) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = f[e] * c[e] + o[e] * s[e];
+    } else if constexpr (M == Pairs::lane) {
+#pragma unroll
+      for (int e = 0; e + 1 < V; e += 2) {
+        const float x = f[e], y = f[e + 1];
+        f[e] = x * c[e] + y * s[e];
+        f[e + 1] = y * c[e + 1] + x * s[e + 1];
+      }
+    } else if constexpr (M == Pairs::lds) {
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < V; ++e) row[n + e] = f[e];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int i = n + e;
+        if (i < 2 * a.R) f[e] = f[e] * c[e] + row[a.interleaved ? i ^ 1 : i < a.R ? i + a.R : i - a.R] * s[e];
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+};
 
 // The angles of `ntok` tokens from `tok`.
 __device__ __forceinline__ void angles(const QkNormArgs& a, float2* cs, int64_t tok, int ntok) {
@@ -91,49 +126,67 @@ __device__ __forceinline__ void angles(const QkNormArgs& a, float2* cs, int64_t 
   }
 }
 
-template <typename T, int V, int RU>
+// `per` tokens a workgroup; the row groups of a token share its heads.
+template <typename T, int V, Pairs M, int RU>
 __global__ __launch_bounds__(kQnThreads) void qk_norm_fwd_kernel(const QkNormArgs a, int lpr, int per) {
-  extern __shared__ float lds[];        // angles of `per` tokens, then a pass's rows
+  extern __shared__ float lds[];        // angles of `per` tokens, then (lds) the groups' rows
   float2* cs = reinterpret_cast<float2*>(lds);
   const RowLane<V> L(a.D, lpr);
-  const int64_t tok = (int64_t)blockIdx.x * per;
-  const int ntok = (int)min((int64_t)per, a.tokens - tok);
-  float* row = lds + 2 * per * a.R + threadIdx.x / lpr * a.D;
-  if (a.R) {
-    angles(a, cs, tok, ntok);
+  const int64_t tok0 = (int64_t)blockIdx.x * per;
+  const int ntok = (int)min((int64_t)per, a.tokens - tok0);
+  const int group = threadIdx.x / lpr, gpt = L.rows / per, t = group / gpt, h0 = group % gpt;
+  float* row = lds + 2 * per * a.R + group * a.D;
+  // the first rows are on their way while the angles are made
+  const T* src[2];
+  Vec<T, V> x[2][RU], y[2][RU];
+  float wt[2][V], wo[2][V];
+  const int pair = other(a, L.n);
+  auto load = [&](int k, int h) {
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const T* p = src[k] + (int64_t)min(h + u * gpt, a.heads[k] - 1) * a.D;
+      x[k][u].load(p);
+      if constexpr (M == Pairs::load) y[k][u].load(p + pair);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    src[k] = static_cast<const T*>(a.x[k]) + (tok0 + min(t, ntok - 1)) * a.stride[k] + L.n;
+    load(k, h0);
+    weights(a, k, L.n, wt[k]);
+    if constexpr (M == Pairs::load) weights(a, k, L.n + pair, wo[k]);
+  }
+  if constexpr (M != Pairs::none) {
+    angles(a, cs, tok0, ntok);
     __syncthreads();
   }
-  float wt[2][V];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int e = 0; e < V; ++e) wt[s][e] = a.w[s] ? a.w[s][L.n + e] : 1.f;
-  const int all = ntok * (a.heads[0] + a.heads[1]);
+  if (t >= ntok) return;
+  Turns<V, M, false> tn;
+  tn.get(a, cs + t * a.R, L.n);
   const float inv = a.l2 ? 1.f : 1.f / (float)a.D;
-  for (int i0 = threadIdx.x / lpr; i0 < all; i0 += RU * L.rows) {
-    Vec<T, V> x[RU];
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const RowAt at(a, min(i0 + u * L.rows, all - 1));
-      x[u].load(static_cast<const T*>(a.x[at.which]) + (tok + at.tok) * a.stride[at.which] +
-                (int64_t)at.head * a.D + L.n);
-    }
+  for (int k = 0; k < 2; ++k) {
+    const int heads = a.heads[k];
+    T* dst = static_cast<T*>(a.out[k]) + (tok0 + t) * heads * a.D + L.n;
+    for (int h = h0; h < heads; h += RU * gpt) {
+      if (h > h0) load(k, h);
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int i = i0 + u * L.rows;
-      const RowAt at(a, min(i, all - 1));
-      float f[V], s = 0.f;
-      x[u].get(f);
+      for (int u = 0; u < RU; ++u) {
+        float f[V], o[V], s = 0.f;
+        x[k][u].get(f);
+        if constexpr (M == Pairs::load) y[k][u].get(o);
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += L.mine[e] ? f[e] * f[e] : 0.f;
-      const float r = rsqrtf(run_sum_dpp(s, lpr) * inv + a.eps);
+        for (int e = 0; e < V; ++e) s += L.mine[e] ? f[e] * f[e] : 0.f;
+        const float r = rsqrtf(run_sum_dpp(s, lpr) * inv + a.eps);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = f[e] * r * (at.which ? wt[1][e] : wt[0][e]);
-      if (a.R) rotate<V, false>(a, row, cs + at.tok * a.R, L.n, f);
-      x[u].set(f);
-      if (i < all && L.ln * V < a.D)
-        x[u].store(static_cast<T*>(a.out[at.which]) +
-                   ((tok + at.tok) * a.heads[at.which] + at.head) * a.D + L.n);
+        for (int e = 0; e < V; ++e) {
+          f[e] = f[e] * r * wt[k][e];
+          if constexpr (M == Pairs::load) o[e] = o[e] * r * wo[k][e];
+        }
+        tn.turn(a, o, row, L.n, f);
+        x[k][u].set(f);
+        if (h + u * gpt < heads && L.ln * V < a.D) x[k][u].store(dst + (int64_t)(h + u * gpt) * a.D);
+      }
     }
   }
 }
@@ -143,71 +196,77 @@ __global__ __launch_bounds__(kQnThreads) void qk_norm_fwd_kernel(const QkNormArg
 // The sums over rows: a lane's own rows (kQnSegment of the workgroup's token tiles in one
 // register, then those sums in another, so that long inputs lose no more than short ones),
 // then the workgroup's, then the partial rows' columns (q's, then k's).
-template <typename T, int V>
-__global__ __launch_bounds__(kQnThreads) void qk_norm_bwd_kernel(const QkNormArgs a, int lpr, int per) {
+template <typename T, int V, Pairs M>
+__global__ __launch_bounds__(kQnThreads, kQnMaxParts / 256) void qk_norm_bwd_kernel(const QkNormArgs a, int lpr, int per) {
   extern __shared__ float lds[];
   float2* cs = reinterpret_cast<float2*>(lds);
   const RowLane<V> L(a.D, lpr);
-  float* row = lds + 2 * per * a.R + threadIdx.x / lpr * a.D;
+  const int group = threadIdx.x / lpr, gpt = L.rows / per, t = group / gpt, h0 = group % gpt;
+  float* row = lds + 2 * per * a.R + group * a.D;
   float wt[2][V], dw[2][V], seg[2][V];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int k = 0; k < 2; ++k) {
+    weights(a, k, L.n, wt[k]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      wt[s][e] = a.w[s] ? a.w[s][L.n + e] : 1.f;
-      dw[s][e] = seg[s][e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) dw[k][e] = seg[k][e] = 0.f;
+  }
+  const int pair = other(a, L.n);
   int until = kQnSegment;
   const float inv = a.l2 ? 1.f : 1.f / (float)a.D;
-  const int heads = a.heads[0] + a.heads[1];
-  for (int64_t tok = (int64_t)blockIdx.x * per; tok < a.tokens; tok += (int64_t)gridDim.x * per) {
-    const int ntok = (int)min((int64_t)per, a.tokens - tok);
-    if (a.R) {
+  for (int64_t tok0 = (int64_t)blockIdx.x * per; tok0 < a.tokens; tok0 += (int64_t)gridDim.x * per) {
+    const int ntok = (int)min((int64_t)per, a.tokens - tok0);
+    if constexpr (M != Pairs::none) {
       __syncthreads();
-      angles(a, cs, tok, ntok);
+      angles(a, cs, tok0, ntok);
       __syncthreads();
     }
-    const int all = ntok * heads;
-    for (int i = threadIdx.x / lpr; i < all; i += L.rows) {
-      const RowAt at(a, i);
-      Vec<T, V> xq, dq;
-      xq.load(static_cast<const T*>(a.x[at.which]) + (tok + at.tok) * a.stride[at.which] +
-              (int64_t)at.head * a.D + L.n);
-      dq.load(static_cast<const T*>(a.dout[at.which]) +
-              ((tok + at.tok) * a.heads[at.which] + at.head) * a.D + L.n);
-      float x[V], d[V], s = 0.f;
-      xq.get(x);
-      dq.get(d);
-      if (a.R) rotate<V, true>(a, row, cs + at.tok * a.R, L.n, d);
+    if (t < ntok) {
+      Turns<V, M, true> tn;
+      tn.get(a, cs + t * a.R, L.n);
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += L.mine[e] ? x[e] * x[e] : 0.f;
-      const float r = rsqrtf(run_sum_dpp(s, lpr) * inv + a.eps);
-      float m = 0.f;
+      for (int k = 0; k < 2; ++k) {
+        const int heads = a.heads[k];
+        const T* src = static_cast<const T*>(a.x[k]) + (tok0 + t) * a.stride[k] + L.n;
+        const T* dsrc = static_cast<const T*>(a.dout[k]) + (tok0 + t) * heads * a.D + L.n;
+        T* dst = static_cast<T*>(a.dx[k]) + (tok0 + t) * a.dstride[k] + L.n;
+#pragma unroll 2
+        for (int h = h0; h < heads; h += gpt) {
+          Vec<T, V> xq, dq, yq;
+          xq.load(src + (int64_t)h * a.D);
+          dq.load(dsrc + (int64_t)h * a.D);
+          if constexpr (M == Pairs::load) yq.load(dsrc + (int64_t)h * a.D + pair);
+          float x[V], d[V], o[V], s = 0.f;
+          xq.get(x);
+          dq.get(d);
+          if constexpr (M == Pairs::load) yq.get(o);
+          tn.turn(a, o, row, L.n, d);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        x[e] *= r;
-        const float t = L.mine[e] ? d[e] * x[e] : 0.f;
-        if (at.which) seg[1][e] += t;
-        else seg[0][e] += t;
-        d[e] *= at.which ? wt[1][e] : wt[0][e];
-        m += L.mine[e] ? d[e] * x[e] : 0.f;
+          for (int e = 0; e < V; ++e) s += L.mine[e] ? x[e] * x[e] : 0.f;
+          const float r = rsqrtf(run_sum_dpp(s, lpr) * inv + a.eps);
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            x[e] *= r;
+            seg[k][e] += L.mine[e] ? d[e] * x[e] : 0.f;
+            d[e] *= wt[k][e];
+            m += L.mine[e] ? d[e] * x[e] : 0.f;
+          }
+          m = run_sum_dpp(m, lpr) * inv;
+#pragma unroll
+          for (int e = 0; e < V; ++e) d[e] = r * (d[e] - x[e] * m);
+          dq.set(d);
+          if (L.ln * V < a.D) dq.store(dst + (int64_t)h * a.D);
+        }
       }
-      m = run_sum_dpp(m, lpr) * inv;
-#pragma unroll
-      for (int e = 0; e < V; ++e) d[e] = r * (d[e] - x[e] * m);
-      dq.set(d);
-      if (L.ln * V < a.D)
-        dq.store(static_cast<T*>(a.dx[at.which]) + (tok + at.tok) * a.dstride[at.which] +
-                 (int64_t)at.head * a.D + L.n);
     }
-    if (--until == 0 || tok + (int64_t)gridDim.x * per >= a.tokens) {
+    if (--until == 0 || tok0 + (int64_t)gridDim.x * per >= a.tokens) {
       until = kQnSegment;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          dw[s][e] += seg[s][e];
-          seg[s][e] = 0.f;
+          dw[k][e] += seg[k][e];
+          seg[k][e] = 0.f;
         }
     }
   }
@@ -247,24 +306,27 @@ int row_lanes(int D, int V) {
   return l;
 }
 
-template <typename T, int V>
+template <typename T, int V, Pairs M>
 hipError_t qn_go(const QkNormArgs& a, bool bwd, hipStream_t s) {
-  const int lpr = row_lanes(a.D, V);
-  // all tokens' workgroups at once where there are few, else four tokens share their angles'
-  // barrier
+  const int lpr = row_lanes(a.D, V), rows = kQnThreads / lpr;
+  // a token's row groups: no more than its heads of q; a token a workgroup where there are few
+  // tokens, else four at least, which share their angles' barrier
   const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-  const int per = a.tokens <= 4 * (int64_t)cus ? 1 : kQnMaxTok;
-  const size_t rows = (size_t)kQnThreads / lpr * a.D * 4;
-  const size_t lds = (size_t)per * a.R * 8 + (a.R || (bwd && a.part) ? rows : 0);
+  int gpt = rows;
+  while (gpt > 1 && gpt > a.heads[0]) gpt /= 2;
+  if (a.tokens > 4 * (int64_t)cus && gpt > rows / kQnTok) gpt = rows / kQnTok;
+  const int per = rows / gpt;
+  const size_t row_lds = (size_t)rows * a.D * 4;
+  const size_t lds = (size_t)per * a.R * 8 + (M == Pairs::lds || (bwd && a.part) ? row_lds : 0);
   const int64_t tiles = (a.tokens + per - 1) / per;
   if (!bwd) {
     if (tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, V, 2>), dim3((unsigned)tiles), dim3(kQnThreads), lds, s, a, lpr, per);
+    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, V, M, 2>), dim3((unsigned)tiles), dim3(kQnThreads), lds, s, a, lpr, per);
     return hipGetLastError();
   }
-  const int64_t most = a.part ? kQnMaxParts : (int64_t)1 << 24;
+  const int64_t most = a.part ? kQnMaxParts : (int64_t)1 << 22;
   const int grid = (int)(tiles < most ? tiles : most);
-  if (grid > 0) hipLaunchKernelGGL((qk_norm_bwd_kernel<T, V>), dim3(grid), dim3(kQnThreads), lds, s, a, lpr, per);
+  if (grid > 0) hipLaunchKernelGGL((qk_norm_bwd_kernel<T, V, M>), dim3(grid), dim3(kQnThreads), lds, s, a, lpr, per);
   if (!a.part) return hipGetLastError();
   QkNormOut out;
   out.w[0] = a.dw[0];
@@ -274,9 +336,19 @@ hipError_t qn_go(const QkNormArgs& a, bool bwd, hipStream_t s) {
   return colsum(a.part, grid, 2 * part_cols(a.D), out, s);
 }
 
+template <typename T, int V>
+hipError_t qn_pairs(const QkNormArgs& a, bool bwd, hipStream_t s) {
+  if (a.R == 0) return qn_go<T, V, Pairs::none>(a, bwd, s);
+  if constexpr (V > 1) {
+    if (a.D % V == 0 && a.interleaved) return qn_go<T, V, Pairs::lane>(a, bwd, s);
+    if (a.D % V == 0 && a.R % V == 0) return qn_go<T, V, Pairs::load>(a, bwd, s);
+  }
+  return qn_go<T, V, Pairs::lds>(a, bwd, s);
+}
+
 hipError_t qn_type(const QkNormArgs& a, bool bwd, hipStream_t s) {
-  if (a.bf16) return a.D >= 8 ? qn_go<bf16, 8>(a, bwd, s) : qn_go<bf16, 1>(a, bwd, s);
-  return a.D >= 4 ? qn_go<float, 4>(a, bwd, s) : qn_go<float, 1>(a, bwd, s);
+  if (a.bf16) return a.D >= 8 ? qn_pairs<bf16, 8>(a, bwd, s) : qn_pairs<bf16, 1>(a, bwd, s);
+  return a.D >= 4 ? qn_pairs<float, 4>(a, bwd, s) : qn_pairs<float, 1>(a, bwd, s);
 }
 
 }  // namespace
