@@ -12,10 +12,10 @@ namespace ssd {
 constexpr int kDeltaChunk = 64;              // tokens per chunk
 constexpr int kGateFloats = 6 * kDeltaChunk; // per (chunk, head): beta, E, D, beta E, and G in fp64
 constexpr int kPiece = 1024;                 // bytes of 64 lanes' 16: operands lie in such pieces
-// Pieces of a triangular 64x64 matrix (six 16x32 tiles of eight), rounded or as pairs, and of a
-// [N][64] one.
+// Pieces of a triangular 64x64 matrix (six 16x32 tiles of eight), rounded or as pairs, and of an
+// fp32 [N][64] one.
 __host__ __device__ constexpr int triangle_pieces(bool b16, bool pair) { return b16 && !pair ? 6 : 12; }
-__host__ __device__ constexpr int transposed_pieces(bool b16, int N) { return N / 16 * 2 * (b16 ? 1 : 2); }
+__host__ __device__ constexpr int transposed_pieces(int N) { return N / 16 * 2 * 2; }
 
 // The gated delta rule over whole prompts, forward and backward.
 struct DeltaArgs {
@@ -53,11 +53,11 @@ struct DeltaArgs {
   float* gates;           // [kGateFloats]
   void* T;                // (1 + L)^-1, lower, pairs
   void* A;                // scale (D * q k^T), lower (forward)
-  void* kt;               // per (chunk, group): k transposed
+  void* kt;               // per (chunk, group), fp32: k transposed
   // backward
   void* Tt;               // T transposed, upper, pairs
   void* At;               // A transposed, upper, pairs
-  void* qt;               // per (chunk, group): q transposed
+  void* qt;               // per (chunk, group), fp32: q transposed
   void* S0;               // [P][N] the state entering the chunk, dtype (two with pairs: high
                           // and low parts; so the next three)
   void* dS;               // [P][N] the gradient of the state leaving it

@@ -101,16 +101,16 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
   }
   part(a.gates, mh * kGateFloats * 4);
   const size_t pair = (size_t)triangle_pieces(a.bf16, true) * kPiece;
-  const size_t tr = (size_t)transposed_pieces(a.bf16, a.N) * kPiece;
+  const size_t tr = a.bf16 ? 0 : (size_t)transposed_pieces(a.N) * kPiece;
   part(a.T, mh * pair);
-  part(a.kt, mg * tr);
+  if (tr) part(a.kt, mg * tr);
   if (!bwd) {
     part(a.A, mh * triangle_pieces(a.bf16, false) * kPiece);
     return off;
   }
   part(a.Tt, mh * pair);
   part(a.At, mh * pair);
-  part(a.qt, mg * tr);
+  if (tr) part(a.qt, mg * tr);
   const size_t ke = a.pairs ? 4 : e;
   part(a.S0, mh * a.P * a.N * ke);
   part(a.dS, mh * a.P * a.N * ke);

@@ -25,6 +25,8 @@
 //   phase 2    S by K^T                            next K, T, V to LDS
 //
 // 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): MEASURED.
+#include <type_traits>
+
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
@@ -70,13 +72,13 @@ template <int COUNT> struct Copied : Pieces<COUNT> {
 // does.  LDS has them in the order [32-block][tile].  A load takes 128 bytes of 8 rows (64 of 16
 // where rows have no more): a lane per row, the operands' own order, takes four times as long to
 // issue.  The exclusive or in a lane's slot keeps the eight lanes that write LDS together on
-// different banks.
+// different banks, and the sixteen of a transposing read.
 template <typename T, int N> struct Rows : Pieces<4 * (N / 32) * Opnd<T>::PX> {
   static constexpr int LR = N * (int)sizeof(T) >= 128 ? 8 : 4;    // lanes on one row
   static constexpr int RL = 64 / LR, PR = N * (int)sizeof(T) / (16 * LR);
   static constexpr bool FLIP = LR == 8 && sizeof(T) == 2;
   __device__ __forceinline__ static uint32_t slot(int a, int i, int flip) {
-    return (uint32_t)(16 * a + (i ^ 2 * a ^ flip)) * 16;
+    return (uint32_t)(16 * a + (i ^ 4 * a ^ flip)) * 16;
   }
   // A reader's slot; `flip` is 1 for the second of two pieces that share 128 bytes.
   __device__ __forceinline__ static uint32_t read(int lane, int flip) {
@@ -101,6 +103,31 @@ template <typename T, int N> struct Rows : Pieces<4 * (N / 32) * Opnd<T>::PX> {
     }
   }
 };
+
+// The operand of the transposed matrix: rows are the channels of dealt tile u, it contracts
+// tokens 32 cb + 8 (lane / 16) ...
+template <int N>
+__device__ __forceinline__ bf16x8 transposed_opnd(const char* lds, int cb, int u, int lane) {
+  using R = Rows<bf16, N>;
+  const int m = lane & 15;
+  const char* p = lds + ((u >> 1) * 4 + 2 * cb) * kPiece +
+                  R::slot(m & 3, 4 * (lane >> 4) + (m >> 2), R::FLIP ? u >> 1 & 1 : 0) + 8 * (u & 1);
+  const i16x4 lo = lds_tr16_b64(reinterpret_cast<const bf16*>(p));
+  const i16x4 hi = lds_tr16_b64(reinterpret_cast<const bf16*>(p + kPiece));
+  typedef short i16x8v __attribute__((ext_vector_type(8)));
+  const i16x8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
+}
+// All tiles of it: out of the matrix's rows, or of pieces that are laid out so (fp32, for which no
+// transposing read is).
+template <typename T, int N>
+__device__ __forceinline__ void lds_transposed(const char* lds, int cb, int lane, typename Opnd<T>::X (&x)[N / 16]) {
+#pragma unroll
+  for (int u = 0; u < N / 16; ++u) {
+    if constexpr (sizeof(T) == 2) x[u] = transposed_opnd<N>(lds, cb, u, lane);
+    else x[u] = piece_x(lds + (cb * (N / 16) + u) * Opnd<T>::PX * kPiece, lane * 16, T{});
+  }
+}
 
 // A [C][16 NW] block of T, as rows in LDS: the workgroup's columns of V or dO.
 template <typename T, int NW> struct Block : Pieces<NW * (int)sizeof(T)> {
@@ -277,9 +304,11 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
   constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
-  constexpr int oK = 0, oT = oK + 4 * NK * PX * kPiece, oG = oT + 6 * PS * kPiece, oV = oG + kPiece;
+  // K is read in both phases where it is transposed on the way: two copies
+  constexpr bool TR = sizeof(T) == 2;
+  constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oT = oK + (TR ? 2 : 1) * kK, oG = oT + 6 * PS * kPiece;
   constexpr int QS = sizeof(T) == 2 ? NK : 1;     // 32-blocks of Q that a helper's corner takes
-  constexpr int oKt = oV + VB::bytes, oQ = oKt + TP * kPiece;
+  constexpr int oV = oG + kPiece, oKt = oV + VB::bytes, oQ = oKt + (TR ? 0 : TP * kPiece);
   constexpr int oX = oQ + (KEEP ? 0 : HW * QS * PX * kPiece), kX = NW * EX * PE * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;   // two copies of what the state waves leave
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
@@ -299,11 +328,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     __syncthreads();
     for (int j = 0; j < t.chunks; ++j) {
       // phase 1
+      const char* K = lds + oK + (TR && (j & 1) ? kK : 0);
       typename O::S sf[NK], rf[2];
       typename O::X kf[NK][4];
       float v[2][8], E[2][8], D[2][8];
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
+      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(K + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v[cb]);
@@ -352,7 +382,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         typename O::X f[NT];
-        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, f);
+        lds_transposed<T, N>(TR ? K : lds + oKt, cb, lane, f);
         mma_rows(f, rf[cb], S);
       }
       __syncthreads();
@@ -388,8 +418,8 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     Tp += a.H * (6 * PS * kPiece);
     gp += a.H * (kGateFloats * 4);
   };
-  auto put1 = [&]() {
-    cK.store(lds + oK, w, lane);
+  auto put1 = [&](int j) {
+    cK.store(lds + oK + (TR && (j & 1) ? kK : 0), w, lane);
     cT.store(lds + oT, w, lane);
     cV.store(lds + oV, w, lane);
     if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
@@ -399,8 +429,10 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   uint4 cQ[NK * PX], cA[2][PX];
   auto fetch2 = [&](int j) {
     const bool some = j < t.chunks;
-    cKt.load(tp, some, w, lane);
-    tp += a.G * (TP * kPiece);
+    if constexpr (!TR) {
+      cKt.load(tp, some, w, lane);
+      tp += a.G * (TP * kPiece);
+    }
     if constexpr (!KEEP) {
       const __amdgpu_buffer_rsrc_t qr = buf_rsrc(qp, rows_bytes(t.len(j), qrow, N * sizeof(T)));
       const __amdgpu_buffer_rsrc_t ar = buf_rsrc(Ap, some ? 6 * PX * kPiece : 0);
@@ -489,14 +521,14 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   };
   if (t.chunks > 0) {
     fetch1(0);
-    put1();
+    put1(0);
     fetch2(0);
   }
   __syncthreads();
   for (int j = 0; j < t.chunks; ++j) {
     // phase 1; stores come last, as whoever waits for a load waits for the stores before it
     fetch1(j + 1);
-    cKt.store(lds + oKt, w, lane);
+    if constexpr (!TR) cKt.store(lds + oKt, w, lane);
     if (DX && j > 0) product(j - 1);
     ready();
     fetch2(j + 1);
@@ -507,7 +539,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       product(j);
       write(j);
     }
-    put1();
+    put1(j + 1);
     __syncthreads();
   }
   if (DX && t.chunks > 0) {
@@ -525,8 +557,11 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
   constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
-  constexpr int oK = 0, oA = oK + 4 * NK * PX * kPiece, oT = oA + 6 * PS * kPiece, oG = oT + 6 * PS * kPiece;
-  constexpr int oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece, oX = oKt + TP * kPiece;
+  // as above; Q, which is read transposed only, lies in rows or transposed
+  constexpr bool TR = sizeof(T) == 2;
+  constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oA = oK + (TR ? 2 : 1) * kK, oT = oA + 6 * PS * kPiece;
+  constexpr int oG = oT + 6 * PS * kPiece, oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece;
+  constexpr int oX = oKt + (TR ? 0 : TP * kPiece);
   constexpr int kX = NW * EX * PE * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
@@ -546,11 +581,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     __syncthreads();
     for (int j = t.chunks - 1; j >= 0; --j) {
       // phase 1
+      const char* K = lds + oK + (TR && (j & 1) ? kK : 0);
       typename O::S sf[NK], rf[2], qf[2], t0[2], t1[4];   // t: the upper triangle's tiles of cb 0, of cb 1
       typename O::X kf[NK][4], of[2];
       float D[2][8], E[2][8], bE[2][8];
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(lds + oK + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
+      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(K + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         of[cb] = column_opnd<NW>(lds + oV, wave, cb, lane, T{});
@@ -614,9 +650,9 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         typename O::X f[NT];
-        lds_xs<NT, T>(lds + oQt + cb * NT * PX * kPiece, rs, f);
+        lds_transposed<T, N>(lds + oQt, cb, lane, f);
         mma_rows(f, qf[cb], S);
-        lds_xs<NT, T>(lds + oKt + cb * NT * PX * kPiece, rs, f);
+        lds_transposed<T, N>(TR ? K : lds + oKt, cb, lane, f);
         mma_rows(f, rf[cb], S);
       }
       __syncthreads();
@@ -631,12 +667,14 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   Copied<6 * PS> cA, cT;
   VB cV;
   uint4 cG;
-  Copied<TP> cQt, cKt;
+  std::conditional_t<TR, KR, Copied<TP>> cQt;
+  Copied<TP> cKt;
   // the next chunk's in memory (the first one's is the last)
   const int last = t.chunks - 1;
   const int64_t jh0 = (int64_t)t.c0 * a.H + h, jh1 = jh0 + (int64_t)last * a.H;
   const int64_t jg1 = ((int64_t)t.c0 + last) * a.G + t.g, tok = t.first + (int64_t)last * C;
   const char* kp = static_cast<const char*>(a.k) + (tok * a.G + t.g) * N * sizeof(T);
+  const char* qp = static_cast<const char*>(a.q) + (tok * a.G + t.g) * N * sizeof(T);
   const char* vp = static_cast<const char*>(a.dout) + ((tok * a.H + h) * a.P + p0) * sizeof(T);
   const char* Ap = static_cast<const char*>(a.At) + jh1 * (6 * PS * kPiece);
   const char* Tp = static_cast<const char*>(a.Tt) + jh1 * (6 * PS * kPiece);
@@ -655,17 +693,22 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     Tp -= a.H * (6 * PS * kPiece);
     gp -= a.H * (kGateFloats * 4);
   };
-  auto put1 = [&]() {
-    cK.store(lds + oK, w, lane);
+  auto put1 = [&](int j) {
+    cK.store(lds + oK + (TR && (j & 1) ? kK : 0), w, lane);
     cA.store(lds + oA, w, lane);
     cT.store(lds + oT, w, lane);
     cV.store(lds + oV, w, lane);
     if (w == 0) *reinterpret_cast<uint4*>(lds + oG + lane * 16) = cG;
   };
   auto fetch2 = [&](int j) {
-    cQt.load(static_cast<const char*>(a.qt) + tp, j >= 0, w, lane);
-    cKt.load(static_cast<const char*>(a.kt) + tp, j >= 0, w, lane);
-    tp -= a.G * (TP * kPiece);
+    if constexpr (TR) {
+      cQt.load(buf_rsrc(qp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
+      qp -= C * (int64_t)qrow;
+    } else {
+      cQt.load(static_cast<const char*>(a.qt) + tp, j >= 0, w, lane);
+      cKt.load(static_cast<const char*>(a.kt) + tp, j >= 0, w, lane);
+      tp -= a.G * (TP * kPiece);
+    }
   };
   auto finish = [&](int j) {
     const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
@@ -680,7 +723,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   };
   if (t.chunks > 0) {
     fetch1(last);
-    put1();
+    put1(last);
     fetch2(last);
   }
   __syncthreads();
@@ -688,13 +731,13 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     // phase 1
     fetch1(j - 1);
     cQt.store(lds + oQt, w, lane);
-    cKt.store(lds + oKt, w, lane);
+    if constexpr (!TR) cKt.store(lds + oKt, w, lane);
     fetch2(j - 1);
     if (DX && j < last) finish(j + 1);
     __syncthreads();
     // phase 2
     if constexpr (!DX) finish(j);
-    put1();
+    put1(j - 1);
     __syncthreads();
   }
   if (DX && t.chunks > 0) finish(0);

@@ -138,7 +138,7 @@ template <typename T, int COLS, int THREADS> struct Tokens {
   static constexpr int n = (all + THREADS - 1) / THREADS;
   static constexpr int bytes = COLS / 32 * 4 * PX * kPiece;
   uint4 q[n];
-  __device__ __forceinline__ static uint32_t slot(int a, int i) { return (uint32_t)(16 * a + (i ^ 2 * a)) * 16; }
+  __device__ __forceinline__ static uint32_t slot(int a, int i) { return (uint32_t)(16 * a + (i ^ 4 * a)) * 16; }
   // A row's first columns, of PR * 16 bytes.
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t pitch, int tid) {
 #pragma unroll
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   const uint32_t qbytes = (uint32_t)(d.len - 1) * qrow + N * sizeof(T);
   const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + qo, qbytes);
   const __amdgpu_buffer_rsrc_t kr = buf_rsrc(static_cast<const T*>(a.k) + qo, qbytes);
-  const int64_t tr = ((int64_t)j * a.G + g) * (N / 16 * 2) * PX * kPiece;
+  const int64_t tr = ((int64_t)j * a.G + g) * (N / 16 * 2) * PX * kPiece;   // fp32
   const char* kt = static_cast<const char*>(a.kt) + tr;
   const char* qt = static_cast<const char*>(a.qt) + tr;
 

@@ -44,14 +44,6 @@ __device__ __forceinline__ float load_gate(const void* p, bool b16, int64_t i) {
 
 // Columns 32 cb + 8 (lane / 16) .. + 7 of rows that are a [C][pitch] tile's columns, dealt tile
 // u of them: the transposed tile's operand.
-__device__ __forceinline__ bf16x8 transposed_opnd(const bf16* t, int pitch, int u, int cb, int lane) {
-  const int m = lane & 15;
-  const bf16* p = t + (32 * cb + 8 * (lane >> 4) + (m >> 2)) * pitch + 32 * (u >> 1) + 8 * (m & 3) + 4 * (u & 1);
-  const i16x4 lo = lds_tr16_b64(p), hi = lds_tr16_b64(p + 4 * pitch);
-  typedef short i16x8v __attribute__((ext_vector_type(8)));
-  const i16x8v v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
-}
 __device__ __forceinline__ F8 transposed_opnd(const float* t, int pitch, int u, int cb, int lane) {
   F8 f;
   const float* p = t + (32 * cb + 8 * (lane >> 4)) * pitch + tile_row(u, lane & 15);
@@ -159,8 +151,8 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       }
     }
   }
-  // k (and q) transposed, once per group
-  if (h0 % rep == 0) {
+  // fp32: k (and q) transposed, once per group; bf16's are read transposed out of LDS later
+  if constexpr (sizeof(T) == 4) if (h0 % rep == 0) {
 #pragma unroll 4
     for (int x = 0; x < TP; ++x)
       put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
