@@ -38,6 +38,12 @@ __device__ __forceinline__ double log_decay(float g) {
   return (double)__builtin_elementwise_maximum(g, -512.f);
 }
 
+// exp(x) to fp32: 2^n times 2 to a power of at most a half, of x log2(e) in fp64.
+__device__ __forceinline__ float exp_of(double x) {
+  const double t = x * 1.4426950408889634, n = rint(t);
+  return ldexpf(__builtin_amdgcn_exp2f((float)(t - n)), (int)n);
+}
+
 __device__ __forceinline__ float load_gate(const void* p, bool b16, int64_t i) {
   return b16 ? to_f32(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
@@ -80,14 +86,16 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The [C][N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.
-template <typename T, int N>
-__device__ __forceinline__ void stage_rows(T* lds, __amdgpu_buffer_rsrc_t r, uint32_t row, int pitch, int lane) {
+// The [C][N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.  `then`: what
+// is loaded behind them, before they are waited for.
+template <typename T, int N, typename F>
+__device__ __forceinline__ void stage_rows(T* lds, __amdgpu_buffer_rsrc_t r, uint32_t row, int pitch, int lane, F then) {
   constexpr int PR = N * (int)sizeof(T) / 16, PL = 64 / PR > 0 ? 64 / PR : 1;   // lanes a row, rows a load
   static_assert(PR <= 64, "a row is at most a wave's load");
   uint4 v[C / PL];
 #pragma unroll
   for (int i = 0; i < C / PL; ++i) v[i] = buf_load16(r, (i * PL + lane / PR) * row + lane % PR * 16);
+  then();
 #pragma unroll
   for (int i = 0; i < C / PL; ++i)
     *reinterpret_cast<uint4*>(lds + (i * PL + lane / PR) * pitch + lane % PR * (16 / (int)sizeof(T))) = v[i];
@@ -123,7 +131,19 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   const int64_t at0 = ((int64_t)d.start * a.G + g) * N, jg = (int64_t)j * a.G + g;
   const __amdgpu_buffer_rsrc_t kr = buf_rsrc(static_cast<const T*>(a.k) + at0, bytes);
   const __amdgpu_buffer_rsrc_t qr = buf_rsrc(static_cast<const T*>(a.q) + at0, bytes);
-  stage_rows<T, N>(Ks, kr, row, XP, lane);
+  auto q_opnd = [&](int i, int kb) {
+    return load_opnd(qr, (16 * i + l16) * row + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
+  };
+  constexpr bool QF = sizeof(T) == 2;       // all of q on its way with k; fp32's would not fit the registers
+  X qs[QF ? NK : 1][4];
+  stage_rows<T, N>(Ks, kr, row, XP, lane, [&]() {
+    if constexpr (QF) {
+#pragma unroll
+      for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs[kb][i] = q_opnd(i, kb);
+    }
+  });
   // the first head's gates on their way
   const int64_t t0 = (int64_t)(d.start + lane) * a.H + h0;
   const bool in = lane < d.len;
@@ -142,7 +162,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
     for (int i = 0; i < 4; ++i) kf[i] = load_opnd(&Ks[(16 * i + l16) * XP + 32 * kb + 8 * la]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const X qf = load_opnd(qr, (16 * i + l16) * row + (32 * kb + 8 * la) * (uint32_t)sizeof(T), T{});
+      const X qf = QF ? qs[QF ? kb : 0][i] : q_opnd(i, kb);
 #pragma unroll
       for (int c = 0; c <= i; ++c) {
         kk[tri(i, c)] = mma(kf[c], kf[i], kk[tri(i, c)]);
@@ -158,7 +178,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
     if constexpr (BWD) {
       wave_sync();
-      stage_rows<T, N>(Ks, qr, row, XP, lane);
+      stage_rows<T, N>(Ks, qr, row, XP, lane, []() {});
       wave_sync();
 #pragma unroll 4
       for (int x = 0; x < TP; ++x)
@@ -179,10 +199,10 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       Gs[lane] = s;
       bs[lane] = step;
       float* gt = a.gates + jh * kGateFloats;
-      const float E = (float)exp(s);
+      const float E = exp_of(s);
       gt[lane] = step;
       gt[C + lane] = E;
-      gt[2 * C + lane] = (float)exp(__shfl(s, 63) - s);
+      gt[2 * C + lane] = exp_of(__shfl(s, 63) - s);
       gt[3 * C + lane] = step * E;
       reinterpret_cast<double*>(gt + 4 * C)[lane] = s;
       if (h + 1 < h0 + nh && in) {
