@@ -22,6 +22,9 @@ constexpr size_t kDeltaAlign = 256;
 // off by several times that.
 constexpr int64_t kDeltaFewGates = 65536;
 
+constexpr int kDeltaLeast = 16;          // chunks of the shortest segments of a sequence
+constexpr int kDeltaCutUnits = 64;       // a quarter of the device's CUs
+
 bool dtype_ok(int32_t d) { return d == SSD_F32 || d == SSD_BF16; }
 size_t elem_size(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -82,6 +85,18 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   a.gate_bf16 = p->gate_dtype == SSD_BF16;
   a.clear = p->nseq > 0 && p->clear_outside == 1;
   a.scale = p->scale;
+  // sequences may be cut where one's heads fill at most a quarter of the device, which few
+  // sequences then do not either (a packed batch's lengths are not known here)
+  const int blocks = (a.P + 63) / 64, longest = p->nseq > 0 ? a.max_chunks : a.nc_row;
+  const int least = longest / 64 > kDeltaLeast ? (longest + 63) / 64 : kDeltaLeast;
+  const bool few = p->nseq > 0 ? a.nstates <= DeltaSplit::kSequences && a.H * blocks <= kDeltaCutUnits
+                               : (int64_t)a.nstates * a.H * blocks <= kDeltaCutUnits;
+  // what a packed batch pays to find that nothing is to be cut is 12 us: MEASUREDS
+  if (few && longest >= (p->nseq > 0 ? 4 : 2) * least) {
+    a.split.least = least;
+    a.split.per_row = a.nc_row / least + 1;
+    a.split.slots = p->nseq > 0 ? a.nstates + a.max_chunks / least : a.nstates * a.split.per_row;
+  }
   a.pairs = a.bf16 && (!a.gate_bf16 || (int64_t)a.total * a.H < kDeltaFewGates);
   return a;
 }
@@ -98,6 +113,12 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
   if (packed) {
     part(a.table, mc * sizeof(int4));
     part(a.seq_chunks, ((size_t)a.nstates + 1) * 4);
+  }
+  if (a.split.slots) {
+    const size_t n = (size_t)a.split.slots * a.H;
+    if (packed) part(a.split.chosen, 4);
+    part(a.split.ends, n * (a.P + a.N) * a.N * 4);
+    part(a.split.starts, n * a.P * a.N * 4);
   }
   part(a.gates, mh * kGateFloats * 4);
   const size_t pair = (size_t)triangle_pieces(a.bf16, true) * kPiece;
@@ -253,7 +274,7 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
   a.init = initial_states; a.cu = a.total > 0 ? cu_seqlens : nullptr;
   a.out = out; a.final_states = final_states;
-  if (a.total == 0) a.nc_row = a.max_chunks = 0;
+  if (a.total == 0) a.nc_row = a.max_chunks = a.split.slots = 0;
   ssd::delta_layout(a, p->nseq > 0, false, workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = ssd::plan(a, s);
@@ -295,7 +316,7 @@ ssd_status_t ssd_delta_bwd(const ssd_delta_problem_t* p, const void* q, const vo
   a.init = initial_states; a.cu = a.total > 0 ? cu_seqlens : nullptr;
   a.dout = dout; a.dfinal = dfinal_states;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dinit = dinitial_states;
-  if (a.total == 0) a.nc_row = a.max_chunks = 0;
+  if (a.total == 0) a.nc_row = a.max_chunks = a.split.slots = 0;
   ssd::delta_layout(a, p->nseq > 0, true, workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = ssd::plan(a, s);

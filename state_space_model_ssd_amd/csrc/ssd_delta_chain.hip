@@ -41,6 +41,8 @@ constexpr int C = kDeltaChunk;
 constexpr int HW = 4;                     // helper waves
 constexpr int kLdsBytes = 160 * 1024;
 
+int device_cus() { return device_cu_count() > 0 ? device_cu_count() : 256; }
+
 // One helper wave's share of `COUNT` loads of 16 bytes per lane on their way from memory to
 // LDS, through registers.  Loads are issued also where there is no next chunk (from an empty
 // resource: zeros, no access): behind a branch around loads the compiler does not know how many
@@ -208,16 +210,19 @@ __device__ __forceinline__ uint32_t rows_bytes(int n, uint32_t pitch, uint32_t r
 struct ChainTask {
   int seq, h, g, block;
   bool none;
-  int first, tokens;      // the sequence's tokens
+  int first, tokens;      // the tokens of the sequence, or of its segment
   int c0, chunks;         // and chunks
+  int slot, part, parts;  // the segment's slot; which of the sequence's it is, and of how many
   __device__ __forceinline__ ChainTask(const DeltaArgs& a, const ChunkMap& cm, int b, int blocks) {
     const int x8 = b & 7, rest = b >> 3, unit = rest / blocks * 8 + x8;
-    seq = unit / a.H;
+    slot = unit / a.H;
     h = unit % a.H;
     g = h / (a.H / a.G);
     block = rest % blocks;
-    none = unit >= a.nstates * a.H;
+    const DeltaSplit& sp = a.split;
+    none = unit >= (sp.slots ? sp.slots : a.nstates) * a.H;
     if (none) return;
+    seq = sp.slots ? sp.sequence(cm, a.nstates, slot) : slot;
     const int2 r = cm.seq_range(seq);
     c0 = r.x;
     chunks = r.y - r.x;
@@ -228,6 +233,17 @@ struct ChainTask {
       first = seq * a.seqlen;
       tokens = a.seqlen;
     }
+    part = 0;
+    parts = 1;
+    if (!sp.slots) return;
+    int per;
+    DeltaSplit::cut(chunks, sp.length(), parts, per);
+    part = slot - sp.base(cm, seq);
+    none = part >= parts;
+    c0 += part * per;
+    first += part * per * C;
+    tokens = part + 1 < parts ? per * C : tokens - part * per * C;
+    chunks = part + 1 < parts ? per : chunks - part * per;
   }
   __device__ __forceinline__ int start(int i) const { return first + i * C; }
   __device__ __forceinline__ int len(int i) const { return i < 0 ? 0 : min(C, tokens - i * C); }
@@ -295,10 +311,15 @@ template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
   }
 };
 
-// KEEP: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
-template <typename T, int N, int NW, bool KEEP, bool PAIR>
+enum class Chain { fwd, keep, ends, bwd };
+
+// keep: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
+// ends: neither; what a segment makes of a state of zeros (the first one of the initial state),
+// and, by rows of their own past P's, of a unit matrix without values.
+template <typename T, int N, int NW, Chain K, bool PAIR>
 __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const DeltaArgs a, const ChunkMap cm,
                                                                       int blocks) {
+  constexpr bool KEEP = K == Chain::keep, ENDS = K == Chain::ends;
   using O = Opnd<T>;
   using KR = Rows<T, N>;
   using VB = Block<T, NW>;
@@ -309,14 +330,20 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oT = oK + (TR ? 2 : 1) * kK, oG = oT + 6 * PS * kPiece;
   constexpr int QS = sizeof(T) == 2 ? NK : 1;     // 32-blocks of Q that a helper's corner takes
   constexpr int oV = oG + kPiece, oKt = oV + VB::bytes, oQ = oKt + (TR ? 0 : TP * kPiece);
-  constexpr int oX = oQ + (KEEP ? 0 : HW * QS * PX * kPiece), kX = NW * EX * PE * kPiece;
+  constexpr int oX = oQ + (K == Chain::fwd ? HW * QS * PX * kPiece : 0), kX = ENDS ? 0 : NW * EX * PE * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;   // two copies of what the state waves leave
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
+  if (ENDS && a.split.length() == 0) return;
   const ChainTask t(a, cm, blockIdx.x, blocks);
-  if (t.none) return;
+  if (t.none || (ENDS && t.part + 1 == t.parts)) return;
+  // ends: the unit matrix's rows, of all segments but the first
+  const int valued = (a.P + 16 * NW - 1) / (16 * NW);
+  const bool unit = ENDS && t.block >= valued;
+  if (unit && t.part == 0) return;
   const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
-  const int h = t.h, p0 = t.block * 16 * NW, rows = min(16 * NW, a.P - p0);
+  const int h = t.h, p0 = (unit ? t.block - valued : t.block) * 16 * NW;
+  const int rows = min(16 * NW, (unit ? N : a.P) - p0);
   const float* gt = reinterpret_cast<const float*>(lds + oG);
 
   if (wave < NW) {
@@ -324,16 +351,29 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0 + p) * N;
     const uint32_t rs = lane * 16, rk[2] = {KR::read(lane, 0), KR::read(lane, 1)};
     f32x4 S[NT];
-    load_state<N>(a.init + srow, a.init && p < rows, lane, S);
+    const float* from = a.init + srow;
+    bool some = a.init && p < rows;
+    if (ENDS && t.part > 0) some = false;
+    if (!ENDS && t.part > 0) {
+      from = a.split.starts + (((int64_t)t.slot * a.H + h) * a.P + p0 + p) * N;
+      some = p < rows;
+    }
+    load_state<N>(from, some, lane, S);
+    if (unit) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[i][e] = 32 * (i / 2) + 8 * la + 4 * (i % 2) + e == p0 + p ? 1.f : 0.f;
+    }
     __syncthreads();
     for (int j = 0; j < t.chunks; ++j) {
       // phase 1
-      const char* K = lds + oK + (TR && (j & 1) ? kK : 0);
+      const char* kl = lds + oK + (TR && (j & 1) ? kK : 0);
       typename O::S sf[NK], rf[2];
       typename O::X kf[NK][4];
       float v[2][8], E[2][8], D[2][8];
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(K + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
+      for (int kb = 0; kb < NK; ++kb) lds_xs<4, T>(kl + kb * 4 * PX * kPiece, rk[kb % 2], kf[kb]);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         O::get(column_opnd<NW>(lds + oV, wave, cb, lane, T{}), v[cb]);
@@ -365,12 +405,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       mma_rows(t1, rf[1], y + 2);
       char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
+      for (int kb = 0; kb < (ENDS ? 0 : NK); ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
+        if constexpr (!ENDS) put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= D[cb][e];
         rf[cb] = O::split(f);
@@ -382,12 +422,15 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         typename O::X f[NT];
-        lds_transposed<T, N>(TR ? K : lds + oKt, cb, lane, f);
+        lds_transposed<T, N>(TR ? kl : lds + oKt, cb, lane, f);
         mma_rows(f, rf[cb], S);
       }
       __syncthreads();
     }
-    if (!KEEP && a.final_states && p < rows) store_state<N>(a.final_states + srow, lane, S);
+    if (ENDS && p < rows)
+      store_state<N>(a.split.ends + (((int64_t)t.slot * a.H + h) * (a.P + N) + (unit ? a.P : 0) + p0 + p) * N, lane, S);
+    if (K == Chain::fwd && a.final_states && t.part + 1 == t.parts && p < rows)
+      store_state<N>(a.final_states + srow, lane, S);
     return;
   }
 
@@ -411,7 +454,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     const bool some = j < t.chunks;
     cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
     cT.load(Tp, some, w, lane);
-    cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cV.load(buf_rsrc(vp, unit ? 0 : rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
     cG = buf_load16(buf_rsrc(gp, some ? kGateFloats * 4 : 0), lane * 16);
     kp += C * (int64_t)qrow;
     vp += C * (int64_t)vrow;
@@ -433,7 +476,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       cKt.load(tp, some, w, lane);
       tp += a.G * (TP * kPiece);
     }
-    if constexpr (!KEEP) {
+    if constexpr (K == Chain::fwd) {
       const __amdgpu_buffer_rsrc_t qr = buf_rsrc(qp, rows_bytes(t.len(j), qrow, N * sizeof(T)));
       const __amdgpu_buffer_rsrc_t ar = buf_rsrc(Ap, some ? 6 * PX * kPiece : 0);
 #pragma unroll
@@ -453,7 +496,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   // what chunk j's products with Q need besides S and W; the rows of Q to operand order in the
   // wave's own corner of LDS (the exclusive or as for Rows)
   auto ready = [&]() {
-    if constexpr (!KEEP) {
+    if constexpr (K == Chain::fwd) {
       char* q = lds + oQ + w * QS * PX * kPiece;
 #pragma unroll
       for (int k0 = 0; k0 < NK; k0 += QS) {
@@ -477,7 +520,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   // O with S and W as first operands: rows are values, the lane's column is a token
   f32x4 o[NW];
   auto product = [&](int j) {
-    if constexpr (!KEEP) {
+    if constexpr (K == Chain::fwd) {
       const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
 #pragma unroll
       for (int s = 0; s < NW; ++s) o[s] = kZero4;
@@ -508,7 +551,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       lw.load(x, NK, w, lane);
       ls.store(static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
       lw.store(static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
-    } else {
+    } else if constexpr (K == Chain::fwd) {
       const int c = 16 * w + l16;
       T* out = static_cast<T*>(a.out) + ((int64_t)(t.start(j) + c) * a.H + h) * a.P + p0 + 8 * la;
 #pragma unroll
@@ -743,16 +786,95 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   if (DX && t.chunks > 0) finish(0);
 }
 
-enum class Chain { fwd, keep, bwd };
+// The states entering each segment but the first, from what the segments make of a state of zeros
+// (B) and of a unit matrix (M):  S_1 = B_0,  S_(i+1) = S_i M_i + B_i.
+//
+// A workgroup has 16 rows of a head's state, a wave 16 columns; by fp32 matrix instructions.
+// M and B of the next segment are on their way while one is used.
+template <int N>
+__global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, const ChunkMap cm) {
+  constexpr int pitch = N + 4;
+  __shared__ float row[2][16 * pitch];
+  const int length = a.split.length();
+  if (length == 0) return;
+  const int nb = a.P / 16, p0 = (int)(blockIdx.x % nb) * 16, sh = blockIdx.x / nb, h = sh % a.H, seq = sh / a.H;
+  const int2 r = cm.seq_range(seq);
+  int parts, per;
+  DeltaSplit::cut(r.y - r.x, length, parts, per);
+  if (parts < 2) return;
+  const int base = a.split.base(cm, seq);
+  const int lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4, col = 16 * wave_id() + l16;
+  struct Next {
+    float m[N / 4], b[4];
+  };
+  auto load = [&](Next& n, int i) {
+    const float* B = a.split.ends + ((int64_t)(base + i) * a.H + h) * (a.P + N) * N + col;
+    const float* M = B + (int64_t)a.P * N;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n.b[e] = B[(p0 + 4 * la + e) * N];
+    if (i == 0) return;                           // of the first one there is no M
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) n.m[k] = M[(4 * k + la) * N];
+  };
+  auto step = [&](Next& now, Next& next, int i) {
+    if (i + 2 < parts) load(next, i + 1);
+    f32x4 c = {now.b[0], now.b[1], now.b[2], now.b[3]};
+    if (i > 0) {
+      const float* x = row[i & 1] + l16 * pitch + la;
+      f32x4 c1 = kZero4;                          // two sums: a product waits for the one before it
+#pragma unroll
+      for (int k = 0; k < N / 4; k += 2) {
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[4 * k], now.m[k], c, 0, 0, 0);
+        c1 = __builtin_amdgcn_mfma_f32_16x16x4f32(x[4 * k + 4], now.m[k + 1], c1, 0, 0, 0);
+      }
+      c += c1;
+    }
+    float* to = a.split.starts + (((int64_t)(base + i + 1) * a.H + h) * a.P + p0) * N + col;
+    float* y = row[(i + 1) & 1] + col;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      to[(4 * la + e) * N] = c[e];
+      y[(4 * la + e) * pitch] = c[e];
+    }
+    __syncthreads();
+  };
+  Next even, odd;
+  load(even, 0);
+  for (int i = 0; i + 1 < parts; i += 2) {
+    step(even, odd, i);
+    if (i + 2 < parts) step(odd, even, i + 1);
+  }
+}
+
+// A packed batch's segment length, from its sequences' chunks (a lane each: DeltaSplit::kSequences
+// is a wave).
+__global__ __launch_bounds__(64) void delta_split_kernel(const DeltaArgs a, const ChunkMap cm, int cus) {
+  DeltaSplit::Sums v = {};
+  if ((int)threadIdx.x < a.nstates) {
+    const int2 r = cm.seq_range(threadIdx.x);
+    v.add(a.split, r.y - r.x, 1);
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    v.longest = max(v.longest, __shfl_xor(v.longest, off));
+#pragma unroll
+    for (int i = 0; i < DeltaSplit::kLengths; ++i) {
+      v.first[i] += __shfl_xor(v.first[i], off);
+      v.later[i] += __shfl_xor(v.later[i], off);
+    }
+  }
+  if (threadIdx.x == 0) *a.split.chosen = DeltaSplit::best(a.split, v, cm.seq_range(a.nstates - 1).y, a.H, a.P, a.N, cus);
+}
 
 template <Chain K, typename T, int N, int NW, bool PAIR>
 hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
-  const int blocks = (a.P + 16 * NW - 1) / (16 * NW);
-  const dim3 grid((unsigned)(((int64_t)a.nstates * a.H + 7) / 8 * 8 * blocks)), th(64 * (NW + HW));
+  const int blocks = (a.P + 16 * NW - 1) / (16 * NW) + (K == Chain::ends ? (N + 16 * NW - 1) / (16 * NW) : 0);
+  const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H;
+  const dim3 grid((unsigned)((units + 7) / 8 * 8 * blocks)), th(64 * (NW + HW));
   if constexpr (K == Chain::bwd)
     hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   else
-    hipLaunchKernelGGL((delta_chain_kernel<T, N, NW, K == Chain::keep, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
+    hipLaunchKernelGGL((delta_chain_kernel<T, N, NW, K, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   return hipGetLastError();
 }
 
@@ -761,8 +883,8 @@ hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
   // fp32 operands of dstate 128 leave LDS for two state waves
   constexpr int most = sizeof(T) == 4 ? 2 : 4;
   // two state waves where heads have no more rows, or four would leave half the device idle
-  const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-  if (a.P <= 32 || 2 * (int64_t)a.nstates * a.H * ((a.P + 63) / 64) <= cus) {
+  const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H * ((a.P + 63) / 64);
+  if (a.P <= 32 || 2 * units <= device_cus()) {
     switch (a.N) {
       case 32: return chain_go<K, T, 32, 2, PAIR>(a, s);
       case 64: return chain_go<K, T, 64, 2, PAIR>(a, s);
@@ -781,16 +903,49 @@ template <Chain K>
 hipError_t chain_type(const DeltaArgs& a, hipStream_t s) {
   if (a.nstates <= 0) return hipSuccess;
   if (!a.bf16) return chain_n<K, float, false>(a, s);
-  if constexpr (K != Chain::fwd)
+  if constexpr (K == Chain::keep || K == Chain::bwd)
     if (a.pairs) return chain_n<K, bf16, true>(a, s);
   return chain_n<K, bf16, false>(a, s);
 }
 
+hipError_t starts(const DeltaArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.nstates * a.H * (a.P / 16))), th(4 * a.N);
+  switch (a.N) {
+    case 32: hipLaunchKernelGGL((delta_starts_kernel<32>), grid, th, 0, s, a, a.cmap()); break;
+    case 64: hipLaunchKernelGGL((delta_starts_kernel<64>), grid, th, 0, s, a, a.cmap()); break;
+    case 128: hipLaunchKernelGGL((delta_starts_kernel<128>), grid, th, 0, s, a, a.cmap()); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_delta_chain(const DeltaArgs& a, bool keep, hipStream_t s) {
+hipError_t launch_delta_chain(const DeltaArgs& given, bool keep, hipStream_t s) {
+  DeltaArgs a = given;
+  hipError_t e = hipSuccess;
+  if (a.split.slots && !a.cu) {
+    // equal rows: the host knows the best length
+    DeltaSplit::Sums v = {};
+    v.add(a.split, a.nc_row, a.nstates);
+    a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, device_cus());
+    if (a.split.fixed == 0) a.split.slots = 0;
+  }
+  if (a.split.slots && a.cu) {
+    hipLaunchKernelGGL(delta_split_kernel, dim3(1), dim3(DeltaSplit::kSequences), 0, s, a, a.cmap(), device_cus());
+    e = hipGetLastError();
+  }
+  if (a.split.slots) {
+    if (e == hipSuccess) e = chain_type<Chain::ends>(a, s);
+    if (e == hipSuccess) e = starts(a, s);
+  }
+  if (e != hipSuccess) return e;
   return keep ? chain_type<Chain::keep>(a, s) : chain_type<Chain::fwd>(a, s);
 }
-hipError_t launch_delta_chain_bwd(const DeltaArgs& a, hipStream_t s) { return chain_type<Chain::bwd>(a, s); }
+hipError_t launch_delta_chain_bwd(const DeltaArgs& given, hipStream_t s) {
+  DeltaArgs a = given;
+  a.split.slots = 0;
+  return chain_type<Chain::bwd>(a, s);
+}
 
 }  // namespace ssd

@@ -279,6 +279,65 @@ def test_long_prompt_of_one_head():
     check_fwd(binding.delta_fwd(**dev(x)), x, 32 ** -0.5)
 
 
+# few heads and long sequences: cut into segments of 16 chunks or more (at most 64 workgroups of
+# 64 values; rows from 32 chunks, packed batches from 64 on)
+CUT = [("bf16", 32, 128, None), ("f32", 48, 32, None), ("bf16", 80, 64, [0, 3300, 3300, 3301, 4700]),
+       ("f32", 16, 128, [5, 2000, 5900, 6000]), ("bf16", 16, 32, [0, 1024, 5000])]
+
+
+@pytest.mark.parametrize("dtype,P,N,cu", CUT)
+def test_long_sequences_are_cut(dtype, P, N, cu):
+    x = draw(1, cu[-1] + 40 if cu else 3300, 2, 1, P, N, dtype, nseq=len(cu) - 1 if cu else None, decay=0.003)
+    c = torch.tensor(cu, dtype=torch.int32) if cu else None
+    kw = dict(cu_seqlens=c.cuda()) if cu else {}
+    check_fwd(binding.delta_fwd(**dev(x), **kw), x, N ** -0.5, c)
+    dout, dfin = draw_grads(x)
+    got = binding.delta_bwd(**dev(x), **kw, dout=dout.cuda(), dfinal_states=dfin.cuda())
+    check_bwd(got, x, dout, dfin, N ** -0.5, c)
+
+
+def test_rows_are_cut_alike():
+    """Two rows of equal inputs: cut at the same places, bit for bit, and as a packed pair."""
+    x = dev(draw(1, 4224, 2, 1, 32, 64, decay=0.003))
+    two = {n: torch.cat((v, v)) for n, v in x.items()}
+    out, fin, _ = binding.delta_fwd(**two)
+    assert torch.equal(out[0], out[1]) and torch.equal(fin[0], fin[1])
+    again = binding.delta_fwd(**two)
+    assert torch.equal(again[0], out) and torch.equal(again[1], fin)
+    p = {n: (v if n == "initial_states" else v.reshape(1, -1, *v.shape[2:])) for n, v in two.items()}
+    packed = binding.delta_fwd(**p, cu_seqlens=torch.tensor([0, 4224, 8448], dtype=torch.int32).cuda())
+    assert torch.equal(packed[0].view_as(out), out) and torch.equal(packed[1], fin)
+
+
+def test_cutting_in_a_graph_follows_the_lengths():
+    """Captured where nothing is cut, replayed where the lengths ask for it."""
+    d = dev(draw(1, 6400, 2, 1, 32, 64, nseq=4, decay=0.003))
+    cu = torch.tensor([0, 1600, 3200, 4800, 6400], dtype=torch.int32).cuda()
+    binding.delta_fwd(**d, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, fin, _ = binding.delta_fwd(**d, cu_seqlens=cu)
+    for lens in ([0, 1600, 3200, 4800, 6400], [0, 10, 20, 30, 6400], [0, 6400, 6400, 6400, 6400], [7, 3000, 3000, 6000, 6001]):
+        cu.copy_(torch.tensor(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = binding.delta_fwd(**d, cu_seqlens=cu)
+        assert torch.equal(out, eager[0]) and torch.equal(fin, eager[1]), lens
+
+
+@pytest.mark.parametrize("cu", [[0, 6000, 100], [0, -5, 10 ** 9], [4000, 0, 6000], [0, 6000, -1]])
+def test_bad_lengths_of_long_batches_stay_in_bounds(cu):
+    x = draw(1, 6000, 2, 1, 16, 32, nseq=2)
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    out = torch.full((1, 6128, 2, 16), 5.0, dtype=torch.bfloat16, device="cuda")
+    fin = torch.full((4, 2, 16, 32), 5.0, device="cuda")
+    binding.delta_fwd(**dev(x), cu_seqlens=c, out=out[:, 64:6064], final_states=fin[1:3])
+    torch.cuda.synchronize()
+    assert bool((out[:, :64] == 5).all()) and bool((out[:, 6064:] == 5).all())
+    assert bool((fin[0] == 5).all()) and bool((fin[3] == 5).all())
+
+
 @pytest.mark.parametrize("cu", [[0, -5, 64], [0, 100, 50], [0, 50, 10 ** 6], [-3, 20, 64], [2 ** 31 - 1, 0, 1]])
 def test_bad_lengths_stay_in_bounds(cu):
     """Lengths that do not rise or pass the tokens are read as far as they make sense: nothing
