@@ -29,6 +29,7 @@ struct DeltaSplit {
   int least;              // chunks of the shortest segments
   int per_row;            // slots of a row (equal rows)
   int fixed;              // the length: the host's (equal rows)
+  int block;              // rows of a state that a workgroup has
   int* chosen;            // or in memory (packed batch); 0: nothing is cut
   float* ends;            // [slots][H][P + N][N] of zeros, and of a unit matrix
   float* starts;          // [slots][H][P][N] the states that segments start from
@@ -60,10 +61,11 @@ struct DeltaSplit {
   };
   // The length of the least estimated time, in steps of a chunk, or 0 where cutting gains nothing:
   // each pass takes as long as its longest chain or as all its chains over the CUs; the states in
-  // between, a step each.  (Products below 2^31: at most 2^22 chunks and heads, 64 workgroups.)
+  // between, a step each.  `block`: a workgroup's rows of a state.  (Products below 2^31: at most
+  // 2^22 chunks and heads, and 64 workgroups of a sequence.)
   __host__ __device__ __forceinline__ static int best(const DeltaSplit& s, const Sums& v, int chunks, int H, int P,
-                                                      int N, int cus) {
-    const int rows = (P + 63) / 64 * H, unit = (N + 63) / 64 * H, all = chunks * rows / cus;
+                                                      int N, int block, int cus) {
+    const int rows = (P + block - 1) / block * H, unit = (N + block - 1) / block * H, all = chunks * rows / cus;
     int least = v.longest > all ? v.longest : all, length = 0;
 #pragma unroll
     for (int i = 0; i < kLengths; ++i) {

@@ -20,6 +20,7 @@ constexpr size_t kDeltaAlign = 256;
 // fp32, and where there are few of them.  Each is a sum with cancellation of products of what is
 // kept, rounded to 2^-9: over many their errors average (2.6e-3 in the 2-norm), a handful may be
 // off by several times that.
+// Pairs cost time: 2x4096 tokens, 32 heads of 128 x 128, 762 us for 549.
 constexpr int64_t kDeltaFewGates = 65536;
 
 constexpr int kDeltaLeast = 16;          // chunks of the shortest segments of a sequence
@@ -85,13 +86,14 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   a.gate_bf16 = p->gate_dtype == SSD_BF16;
   a.clear = p->nseq > 0 && p->clear_outside == 1;
   a.scale = p->scale;
-  // sequences may be cut where one's heads fill at most a quarter of the device, which few
-  // sequences then do not either (a packed batch's lengths are not known here)
-  const int blocks = (a.P + 63) / 64, longest = p->nseq > 0 ? a.max_chunks : a.nc_row;
+  // sequences may be cut where one's heads fill at most a quarter of the device (16384 tokens of 64
+  // workgroups: 467 -> 376 us; 8192 of 128: 273 -> 321); a packed batch's lengths are not known here
+  const int block = a.bf16 || a.N < 128 ? 64 : 32, blocks = (a.P + block - 1) / block, longest = p->nseq > 0 ? a.max_chunks : a.nc_row;
   const int least = longest / 64 > kDeltaLeast ? (longest + 63) / 64 : kDeltaLeast;
   const bool few = p->nseq > 0 ? a.nstates <= DeltaSplit::kSequences && a.H * blocks <= kDeltaCutUnits
                                : (int64_t)a.nstates * a.H * blocks <= kDeltaCutUnits;
-  // what a packed batch pays to find that nothing is to be cut is 12 us: MEASUREDS
+  // a packed batch pays 4 to 8 us to find that nothing is to be cut (17 sequences of 400 tokens,
+  // 32 heads: 128 -> 136 us), where 9 sequences of which one has half the tokens gain 70 (292 -> 222)
   if (few && longest >= (p->nseq > 0 ? 4 : 2) * least) {
     a.split.least = least;
     a.split.per_row = a.nc_row / least + 1;

@@ -20,11 +20,22 @@
 // a barrier after each; each half of the operands is read in one and replaced in the other,
 // so one copy in LDS is enough:
 //              state waves                         helper waves
-//   phase 1    W by K, T, V; S and W as operands   loads of the next chunk's operands; K^T of
-//              to LDS                              this one to LDS; O of the chunk before
+//   phase 1    W by K, T, V; S and W as operands   loads of the next chunk's operands; O of the
+//              to LDS                              chunk before
 //   phase 2    S by K^T                            next K, T, V to LDS
+// K^T is read out of K's rows by transposing reads, so bf16's K has two copies; fp32 has no such
+// reads, and takes K^T from memory (ssd_delta_prep.hip).
 //
-// 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): MEASURED.
+// Long sequences of few heads leave most of the device idle for as long as their chains are.  They
+// are cut (DeltaSplit): each segment runs once from zeros, for what it adds to a state (B), and with
+// as many more rows as the state has columns from a unit matrix without values, for what becomes of
+// a state (M); delta_starts_kernel makes the states that segments start from out of these; then all
+// run side by side.  1x8192 tokens, 24 heads of 64 x 128: 233 -> 139 us a forward, of which B and M
+// 52, the states 16, the segments of 16 chunks 44.
+//
+// 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): 299 us,
+// 2.3 us a step, of which the state waves work 1.9 and the helpers 2.1; LDS, with some 370 KB read
+// and written a step at 128 bytes a clock, is busy for 1.2.
 #include <type_traits>
 
 #include "ssd_delta_device.h"
@@ -185,13 +196,6 @@ template <int M, typename T>
 __device__ __forceinline__ void lds_ss(const char* p, uint32_t slot, typename Opnd<T>::S (&x)[M]) {
 #pragma unroll
   for (int m = 0; m < M; ++m) x[m] = piece_s(p + m * Opnd<T>::PS * kPiece, slot, T{});
-}
-
-__device__ __forceinline__ bf16x8 opnd_of(const uint4 (&q)[1], bf16) { return __builtin_bit_cast(bf16x8, q[0]); }
-__device__ __forceinline__ F8 opnd_of(const uint4 (&q)[2], float) {
-  F8 f;
-  block8(__builtin_bit_cast(f32x4, q[0]), __builtin_bit_cast(f32x4, q[1]), f.v);
-  return f;
 }
 
 // Values 32 cb + 8 (lane / 16) .. + 7 of a row of C floats.
@@ -863,7 +867,8 @@ __global__ __launch_bounds__(64) void delta_split_kernel(const DeltaArgs a, cons
       v.later[i] += __shfl_xor(v.later[i], off);
     }
   }
-  if (threadIdx.x == 0) *a.split.chosen = DeltaSplit::best(a.split, v, cm.seq_range(a.nstates - 1).y, a.H, a.P, a.N, cus);
+  if (threadIdx.x == 0) 
+    *a.split.chosen = DeltaSplit::best(a.split, v, cm.seq_range(a.nstates - 1).y, a.H, a.P, a.N, a.split.block, cus);
 }
 
 template <Chain K, typename T, int N, int NW, bool PAIR>
@@ -878,13 +883,19 @@ hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Two state waves where heads have no more rows, where fp32 operands of dstate 128 leave LDS for
+// no more, and where four would leave half the device idle (200 tokens of 32 heads of 128 x 128:
+// 21.6 us a forward with two, 23.2 with four; 2x4096 tokens, backward 549 and 592; 4x8192 tokens,
+// which fill the device with four, 553 and 431).
+int state_waves(const DeltaArgs& a) {
+  const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H * ((a.P + 63) / 64);
+  return a.P <= 32 || (!a.bf16 && a.N == 128) || 2 * units <= device_cus() ? 2 : 4;
+}
+
 template <Chain K, typename T, bool PAIR>
 hipError_t chain_n(const DeltaArgs& a, hipStream_t s) {
-  // fp32 operands of dstate 128 leave LDS for two state waves
-  constexpr int most = sizeof(T) == 4 ? 2 : 4;
-  // two state waves where heads have no more rows, or four would leave half the device idle
-  const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H * ((a.P + 63) / 64);
-  if (a.P <= 32 || 2 * units <= device_cus()) {
+  constexpr int most = sizeof(T) == 4 ? 2 : 4;    // dstate 128
+  if (state_waves(a) == 2) {
     switch (a.N) {
       case 32: return chain_go<K, T, 32, 2, PAIR>(a, s);
       case 64: return chain_go<K, T, 64, 2, PAIR>(a, s);
@@ -924,11 +935,12 @@ hipError_t starts(const DeltaArgs& a, hipStream_t s) {
 hipError_t launch_delta_chain(const DeltaArgs& given, bool keep, hipStream_t s) {
   DeltaArgs a = given;
   hipError_t e = hipSuccess;
+  a.split.block = 16 * state_waves(a);
   if (a.split.slots && !a.cu) {
     // equal rows: the host knows the best length
     DeltaSplit::Sums v = {};
     v.add(a.split, a.nc_row, a.nstates);
-    a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, device_cus());
+    a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, a.split.block, device_cus());
     if (a.split.fixed == 0) a.split.slots = 0;
   }
   if (a.split.slots && a.cu) {

@@ -124,7 +124,7 @@ __device__ __forceinline__ f32x4 mma(const A& a, const B& b, f32x4 c) {
   for (int i = 0; i < Steps<A, B>::n; ++i) c = Steps<A, B>::step(i, a, b, c);
   return c;
 }
-// c[m] += a[m] b, or a b[m], for M results: an instruction that adds to the result of the
+// c[m] += a[m] b for M results: an instruction that adds to the result of the
 // one before waits for it, so the results take turns.
 template <int M, typename A, typename B>
 __device__ __forceinline__ void mma_rows(const A (&a)[M], const B& b, f32x4* c) {
@@ -132,13 +132,6 @@ __device__ __forceinline__ void mma_rows(const A (&a)[M], const B& b, f32x4* c) 
   for (int i = 0; i < Steps<A, B>::n; ++i)
 #pragma unroll
     for (int m = 0; m < M; ++m) c[m] = Steps<A, B>::step(i, a[m], b, c[m]);
-}
-template <int M, typename A, typename B>
-__device__ __forceinline__ void mma_cols(const A& a, const B (&b)[M], f32x4* c) {
-#pragma unroll
-  for (int i = 0; i < Steps<A, B>::n; ++i)
-#pragma unroll
-    for (int m = 0; m < M; ++m) c[m] = Steps<A, B>::step(i, a, b[m], c[m]);
 }
 
 constexpr f32x4 kZero4 = {0.f, 0.f, 0.f, 0.f};
@@ -213,6 +206,13 @@ __device__ __forceinline__ bf16x8 piece_x(const char* p, uint32_t slot, bf16) {
 __device__ __forceinline__ F8 piece_x(const char* p, uint32_t slot, float) {
   F8 f;
   block8(*reinterpret_cast<const f32x4*>(p + slot), *reinterpret_cast<const f32x4*>(p + kPiece + slot), f.v);
+  return f;
+}
+// An operand from its 16-byte pieces.
+__device__ __forceinline__ bf16x8 opnd_of(const uint4 (&q)[1], bf16) { return __builtin_bit_cast(bf16x8, q[0]); }
+__device__ __forceinline__ F8 opnd_of(const uint4 (&q)[2], float) {
+  F8 f;
+  block8(__builtin_bit_cast(f32x4, q[0]), __builtin_bit_cast(f32x4, q[1]), f.v);
   return f;
 }
 __device__ __forceinline__ Pair piece_s(const char* p, uint32_t slot, bf16) {

@@ -9,7 +9,9 @@
 // sines are made once, into LDS; a lane keeps its channels' in registers for all heads of its
 // token.  The other channel of a pair is the lane's own (neighbours), or comes by a second load
 // of the row from the cache (halves, where they are whole vectors); where rows or halves are no
-// whole vectors it comes from the row in LDS.  MEASUREDQ
+// whole vectors it comes from the row in LDS.  32768 tokens of 16 + 16 heads of 128, bf16, forward
+// without rotation: 99 us, 5.4 TB/s; 8192 of 32 + 8, backward with it: 47 us, 5.4 TB/s, and 4 for
+// the weights' sums (through LDS for every pair, and a row's heads and tokens found by division: 79).
 //
 // Angles are taken by turns in fp64: pos freq / 2 pi less the nearest whole number, off by
 // 2^-52 of the turns and then, in fp32, by 2^-26 of a turn at most.
@@ -310,7 +312,8 @@ template <typename T, int V, Pairs M>
 hipError_t qn_go(const QkNormArgs& a, bool bwd, hipStream_t s) {
   const int lpr = row_lanes(a.D, V), rows = kQnThreads / lpr;
   // a token's row groups: no more than its heads of q; a token a workgroup where there are few
-  // tokens, else four at least, which share their angles' barrier
+  // tokens, else four at least, which share their angles' barrier (forward, 32 + 8 heads of 128:
+  // 4 tokens 4.9 us, in fours 7.1; 16384 tokens 70 us, one by one 98)
   const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
   int gpt = rows;
   while (gpt > 1 && gpt > a.heads[0]) gpt /= 2;
