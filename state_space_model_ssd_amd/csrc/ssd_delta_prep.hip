@@ -18,8 +18,8 @@
 // none; its LDS holds k's rows first, then each head's T.
 //
 // 4x8192 tokens, 32 heads in 16 groups of 128 x 128, bf16: 131 us for 595 MB read and written
-// (4.5 TB/s), a bound of memory.  One chunk takes 10 us: loads, products, fp64 sums and the inverse,
-// one after another in one wave.
+// (4.5 TB/s), a bound of memory.  One chunk takes 10 us (7 of 32 tokens at most): loads, products,
+// fp64 sums and the inverse, one after another in one wave.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
@@ -88,25 +88,26 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The [C][N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.  `then`: what
+// The first ROWS [N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.  `then`: what
 // is loaded behind them, before they are waited for.
-template <typename T, int N, typename F>
+template <typename T, int N, int ROWS, typename F>
 __device__ __forceinline__ void stage_rows(T* lds, __amdgpu_buffer_rsrc_t r, uint32_t row, int pitch, int lane, F then) {
   constexpr int PR = N * (int)sizeof(T) / 16, PL = 64 / PR > 0 ? 64 / PR : 1;   // lanes a row, rows a load
   static_assert(PR <= 64, "a row is at most a wave's load");
-  uint4 v[C / PL];
+  uint4 v[ROWS / PL];
 #pragma unroll
-  for (int i = 0; i < C / PL; ++i) v[i] = buf_load16(r, (i * PL + lane / PR) * row + lane % PR * 16);
+  for (int i = 0; i < ROWS / PL; ++i) v[i] = buf_load16(r, (i * PL + lane / PR) * row + lane % PR * 16);
   then();
 #pragma unroll
-  for (int i = 0; i < C / PL; ++i)
+  for (int i = 0; i < ROWS / PL; ++i)
     *reinterpret_cast<uint4*>(lds + (i * PL + lane / PR) * pitch + lane % PR * (16 / (int)sizeof(T))) = v[i];
 }
 
 // The tile (block of rows i, block of columns j), j <= i, of a lower triangle of 16x16 blocks.
 __device__ __forceinline__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
 
-template <typename T, int N, bool BWD>
+// BL: blocks of 16 tokens that a chunk has at most.
+template <typename T, int N, bool BWD, int BL>
 __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm, int nh) {
   using O = Opnd<T>;
   using X = typename O::X;
@@ -138,12 +139,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   };
   constexpr bool QF = sizeof(T) == 2;       // all of q on its way with k; fp32's would not fit the registers
   X qs[QF ? NK : 1][4];
-  stage_rows<T, N>(Ks, kr, row, XP, lane, [&]() {
+  stage_rows<T, N, 16 * BL>(Ks, kr, row, XP, lane, [&]() {
     if constexpr (QF) {
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qs[kb][i] = q_opnd(i, kb);
+        for (int i = 0; i < BL; ++i) qs[kb][i] = q_opnd(i, kb);
     }
   });
   // the first head's gates on their way
@@ -161,9 +162,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   for (int kb = 0; kb < NK; ++kb) {
     X kf[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kf[i] = load_opnd(&Ks[(16 * i + l16) * XP + 32 * kb + 8 * la]);
+    for (int i = 0; i < BL; ++i) kf[i] = load_opnd(&Ks[(16 * i + l16) * XP + 32 * kb + 8 * la]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < BL; ++i) {
       const X qf = QF ? qs[QF ? kb : 0][i] : q_opnd(i, kb);
 #pragma unroll
       for (int c = 0; c <= i; ++c) {
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       put_piece(static_cast<char*>(a.kt) + (jg * TP + x) * O::PX * kPiece, slot, transposed_opnd(Ks, XP, x % (N / 16), x / (N / 16), lane));
     if constexpr (BWD) {
       wave_sync();
-      stage_rows<T, N>(Ks, qr, row, XP, lane, []() {});
+      stage_rows<T, N, C>(Ks, qr, row, XP, lane, []() {});
       wave_sync();
 #pragma unroll 4
       for (int x = 0; x < TP; ++x)
@@ -215,8 +216,15 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
     }
     // L as first operands, the diagonal's blocks to LDS; A (or its transpose)
     f32x4 L[10];
+    if constexpr (BL < 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      for (int x = 0; x < 6; ++x) {
+        const int2 t = lower_tile(x);
+        if (t.x >= BL) put_piece(static_cast<char*>(a.A) + (jh * 6 + x) * O::PX * kPiece, slot, X{});
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
       const int c = 16 * i + l16;
       const double Gc = Gs[c];
       const float bc = bs[c];
@@ -290,30 +298,30 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
     {
       f32x4 blk[10], dia[4];                      // T's blocks as second operands, the diagonal's as first
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < BL; ++i) {
         dia[i] = *reinterpret_cast<const f32x4*>(&Ts[(16 * i + l16) * LP + 16 * i + 4 * la]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) blk[tri(i, i)][r] = Ts[(16 * i + 4 * la + r) * LP + 16 * i + l16];
       }
 #pragma unroll
-      for (int n = 1; n < 4; ++n) {
+      for (int n = 1; n < BL; ++n) {
         f32x4 s[3], o[3];
 #pragma unroll
-        for (int c = 0; c < 4 - n; ++c) s[c] = o[c] = kZero4;
+        for (int c = 0; c < BL - n; ++c) s[c] = o[c] = kZero4;
 #pragma unroll
         for (int k = 0; k < n; ++k)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 4 - n; ++c)
+            for (int c = 0; c < BL - n; ++c)
               s[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(L[tri(c + n, c + k)][r], blk[tri(c + k, c)][r], s[c], 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < 4 - n; ++c)
+          for (int c = 0; c < BL - n; ++c)
             o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(dia[c + n][r], s[c][r], o[c], 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < 4 - n; ++c)
+        for (int c = 0; c < BL - n; ++c)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             blk[tri(c + n, c)][r] = -o[c][r];
@@ -327,10 +335,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
     for (int x = 0; x < 6; ++x) {
       const int2 t = lower_tile(x);
       const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
-      float f[8];
-      block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
+      float f[8] = {};
+      if (32 * (t.x / 2) < 16 * BL) {
+        block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] * bs[c0 + e] : 0.f;
+        for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] * bs[c0 + e] : 0.f;
+      }
       put_piece(static_cast<char*>(a.T) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
     }
     if constexpr (BWD) {
@@ -368,8 +378,19 @@ hipError_t prep_go(const DeltaArgs& a, bool bwd, hipStream_t s) {
   const int nh = (int64_t)a.max_chunks * a.G <= 4 * cus ? 1 : a.H / a.G;
   const int64_t items = (int64_t)a.max_chunks * (a.H / nh);
   const dim3 grid((unsigned)((items + kPrepWaves - 1) / kPrepWaves)), th(64 * kPrepWaves);
-  if (bwd) hipLaunchKernelGGL((delta_prep_kernel<T, N, true>), grid, th, 0, s, a, a.cmap(), nh);
-  else hipLaunchKernelGGL((delta_prep_kernel<T, N, false>), grid, th, 0, s, a, a.cmap(), nh);
+  if (bwd) {
+    hipLaunchKernelGGL((delta_prep_kernel<T, N, true, 4>), grid, th, 0, s, a, a.cmap(), nh);
+    return hipGetLastError();
+  }
+  // no more than 32 tokens: half of the blocks (a forward of 17 tokens, 32 heads: 13.5 us,
+  // with all of them 16.9)
+  if constexpr (sizeof(T) == 2) {
+    if ((a.cu ? a.total : a.seqlen) <= 32) {
+      hipLaunchKernelGGL((delta_prep_kernel<T, N, false, 2>), grid, th, 0, s, a, a.cmap(), nh);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((delta_prep_kernel<T, N, false, 4>), grid, th, 0, s, a, a.cmap(), nh);
   return hipGetLastError();
 }
 

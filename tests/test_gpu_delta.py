@@ -40,6 +40,17 @@ def test_backward(shape, dtype, gate):
     check_bwd(got, x, dout, dfin, 0.7)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [15, 16, 17, 31, 32, 33])
+def test_short_prompts(T, dtype):
+    """Around one and two blocks of 16 tokens, rows and packed."""
+    x = draw(2, T, 4, 2, 32, 64, dtype)
+    check_fwd(binding.delta_fwd(**dev(x)), x, 64 ** -0.5)
+    x = draw(1, T, 4, 2, 64, 128, dtype, nseq=3)
+    cu = torch.tensor([0, 3, 3, T - 1], dtype=torch.int32)
+    check_fwd(binding.delta_fwd(**dev(x), cu_seqlens=cu.cuda()), x, 128 ** -0.5, cu)
+
+
 # sequences of no, one and many tokens; tokens before the first and behind the last
 CUS = [[0, 64, 128], [3, 3, 4, 70, 70, 199], [0, 1, 2, 3, 67, 200], [0, 0, 0], [200, 200], [17, 150],
        [0, 31, 96, 160, 200, 200]]
