@@ -92,8 +92,8 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   const int least = longest / 64 > kDeltaLeast ? (longest + 63) / 64 : kDeltaLeast;
   const bool few = p->nseq > 0 ? a.nstates <= DeltaSplit::kSequences && a.H * blocks <= kDeltaCutUnits
                                : (int64_t)a.nstates * a.H * blocks <= kDeltaCutUnits;
-  // a packed batch pays 4 to 8 us to find that nothing is to be cut (17 sequences of 400 tokens,
-  // 32 heads: 128 -> 136 us), where 9 sequences of which one has half the tokens gain 70 (292 -> 222)
+  // a packed batch pays 4 to 8 us, backward 16, to find that nothing is to be cut (17 sequences of
+  // 400 tokens, 32 heads: 128 -> 136 us; backward, 16 heads: 309 -> 325), where 9 sequences of which one has half the tokens gain 70 (292 -> 222)
   if (few && longest >= (p->nseq > 0 ? 4 : 2) * least) {
     a.split.least = least;
     a.split.per_row = a.nc_row / least + 1;

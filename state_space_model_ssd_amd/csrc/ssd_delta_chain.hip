@@ -27,11 +27,11 @@
 // reads, and takes K^T from memory (ssd_delta_prep.hip).
 //
 // Long sequences of few heads leave most of the device idle for as long as their chains are.  They
-// are cut (DeltaSplit): each segment runs once from zeros, for what it adds to a state (B), and with
+// are cut (DeltaSplit), backward too: each segment runs once from zeros, for what it adds to a state (B), and with
 // as many more rows as the state has columns from a unit matrix without values, for what becomes of
 // a state (M); delta_starts_kernel makes the states that segments start from out of these; then all
 // run side by side.  1x8192 tokens, 24 heads of 64 x 128: 233 -> 139 us a forward, of which B and M
-// 52, the states 16, the segments of 16 chunks 44.
+// 52, the states 16, the segments of 16 chunks 44; 16 heads of 64 x 64, backward: 430 -> 227 us.
 //
 // 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): 299 us,
 // 2.3 us a step, of which the state waves work 1.9 and the helpers 2.1; LDS, with some 370 KB read
@@ -253,7 +253,7 @@ struct ChainTask {
   __device__ __forceinline__ int len(int i) const { return i < 0 ? 0 : min(C, tokens - i * C); }
 };
 
-// S^T in its tiles from row p of a state, zeros where there is none; and back.
+// S^T in its tiles from row p of a state, zeros where there is none; of a unit matrix; and back.
 template <int N>
 __device__ __forceinline__ void load_state(const float* row, bool in, int lane, f32x4 (&S)[N / 16]) {
 #pragma unroll
@@ -265,6 +265,13 @@ __device__ __forceinline__ void load_state(const float* row, bool in, int lane, 
       S[2 * kb + 1][e] = in ? r[4 + e] : 0.f;
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void unit_state(int row, int la, f32x4 (&S)[N / 16]) {
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[i][e] = 32 * (i / 2) + 8 * la + 4 * (i % 2) + e == row ? 1.f : 0.f;
 }
 template <int N>
 __device__ __forceinline__ void store_state(float* row, int lane, const f32x4 (&S)[N / 16]) {
@@ -315,7 +322,7 @@ template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
   }
 };
 
-enum class Chain { fwd, keep, ends, bwd };
+enum class Chain { fwd, keep, ends, bwd, bwd_ends };
 
 // keep: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
 // ends: neither; what a segment makes of a state of zeros (the first one of the initial state),
@@ -363,12 +370,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       some = p < rows;
     }
     load_state<N>(from, some, lane, S);
-    if (unit) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[i][e] = 32 * (i / 2) + 8 * la + 4 * (i % 2) + e == p0 + p ? 1.f : 0.f;
-    }
+    if (unit) unit_state<N>(p0 + p, la, S);
     __syncthreads();
     for (int j = 0; j < t.chunks; ++j) {
       // phase 1
@@ -596,7 +598,9 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
 }
 
 // Backward: dS (before the update) and dR are kept for ssd_delta_local.hip (PAIR: as pairs).
-template <typename T, int N, int NW, bool PAIR>
+// ENDS: neither; what a segment makes of a gradient of zeros (the last one of the final state's),
+// and, by rows past P's, of a unit matrix without outputs' gradients.
+template <typename T, int N, int NW, bool ENDS, bool PAIR>
 __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const DeltaArgs a, const ChunkMap cm,
                                                                           int blocks) {
   using O = Opnd<T>;
@@ -609,14 +613,18 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oA = oK + (TR ? 2 : 1) * kK, oT = oA + 6 * PS * kPiece;
   constexpr int oG = oT + 6 * PS * kPiece, oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece;
   constexpr int oX = oKt + (TR ? 0 : TP * kPiece);
-  constexpr int kX = NW * EX * PE * kPiece;
+  constexpr int kX = ENDS ? 0 : NW * EX * PE * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
   const ChainTask t(a, cm, blockIdx.x, blocks);
-  if (t.none) return;
+  if (t.none || (ENDS && t.part == 0)) return;
+  const int valued = (a.P + 16 * NW - 1) / (16 * NW);
+  const bool unit = ENDS && t.block >= valued, first = t.part + 1 == t.parts;   // the first to run
+  if (unit && first) return;
   const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4;
-  const int h = t.h, p0 = t.block * 16 * NW, rows = min(16 * NW, a.P - p0);
+  const int h = t.h, p0 = (unit ? t.block - valued : t.block) * 16 * NW;
+  const int rows = min(16 * NW, (unit ? N : a.P) - p0);
   const float* gt = reinterpret_cast<const float*>(lds + oG);
 
   if (wave < NW) {
@@ -624,7 +632,15 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     const int64_t srow = (((int64_t)t.seq * a.H + h) * a.P + p0 + p) * N;
     const uint32_t rs = lane * 16, rk[2] = {KR::read(lane, 0), KR::read(lane, 1)};
     f32x4 S[NT];
-    load_state<N>(a.dfinal + srow, a.dfinal && p < rows, lane, S);
+    const float* from = a.dfinal + srow;
+    bool some = a.dfinal && p < rows;
+    if (ENDS && !first) some = false;
+    if (!ENDS && !first) {
+      from = a.split.starts + (((int64_t)t.slot * a.H + h) * a.P + p0 + p) * N;
+      some = p < rows;
+    }
+    load_state<N>(from, some, lane, S);
+    if (unit) unit_state<N>(p0 + p, la, S);
     __syncthreads();
     for (int j = t.chunks - 1; j >= 0; --j) {
       // phase 1
@@ -680,12 +696,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
       mma_rows(t1, rf[1], y);
       char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < NK; ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
+      for (int kb = 0; kb < (ENDS ? 0 : NK); ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
+        if constexpr (!ENDS) put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= -bE[cb][e];
         rf[cb] = O::split(f);
@@ -704,7 +720,9 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
       }
       __syncthreads();
     }
-    if (a.dinit && p < rows) store_state<N>(a.dinit + srow, lane, S);
+    if (ENDS && p < rows)
+      store_state<N>(a.split.ends + (((int64_t)t.slot * a.H + h) * (a.P + N) + (unit ? a.P : 0) + p0 + p) * N, lane, S);
+    if (!ENDS && a.dinit && t.part == 0 && p < rows) store_state<N>(a.dinit + srow, lane, S);
     return;
   }
 
@@ -732,7 +750,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     cK.load(buf_rsrc(kp, rows_bytes(t.len(j), qrow, N * sizeof(T))), qrow, w, lane);
     cA.load(Ap, some, w, lane);
     cT.load(Tp, some, w, lane);
-    cV.load(buf_rsrc(vp, rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
+    cV.load(buf_rsrc(vp, unit ? 0 : rows_bytes(t.len(j), vrow, rows * sizeof(T))), vrow, rows, w, lane);
     cG = buf_load16(buf_rsrc(gp, some ? kGateFloats * 4 : 0), lane * 16);
     kp -= C * (int64_t)qrow;
     vp -= C * (int64_t)vrow;
@@ -780,22 +798,23 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     cQt.store(lds + oQt, w, lane);
     if constexpr (!TR) cKt.store(lds + oKt, w, lane);
     fetch2(j - 1);
-    if (DX && j < last) finish(j + 1);
+    if (!ENDS && DX && j < last) finish(j + 1);
     __syncthreads();
     // phase 2
-    if constexpr (!DX) finish(j);
+    if constexpr (!ENDS && !DX) finish(j);
     put1(j - 1);
     __syncthreads();
   }
-  if (DX && t.chunks > 0) finish(0);
+  if (!ENDS && DX && t.chunks > 0) finish(0);
 }
 
 // The states entering each segment but the first, from what the segments make of a state of zeros
-// (B) and of a unit matrix (M):  S_1 = B_0,  S_(i+1) = S_i M_i + B_i.
+// (B) and of a unit matrix (M):  S_1 = B_0,  S_(i+1) = S_i M_i + B_i.  BACK: their gradients, from
+// the last segment on.
 //
 // A workgroup has 16 rows of a head's state, a wave 16 columns; by fp32 matrix instructions.
 // M and B of the next segment are on their way while one is used.
-template <int N>
+template <int N, bool BACK>
 __global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, const ChunkMap cm) {
   constexpr int pitch = N + 4;
   __shared__ float row[2][16 * pitch];
@@ -807,12 +826,13 @@ __global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, 
   DeltaSplit::cut(r.y - r.x, length, parts, per);
   if (parts < 2) return;
   const int base = a.split.base(cm, seq);
+  auto slot = [&](int i) { return (int64_t)(BACK ? base + parts - 1 - i : base + i); };   // the i-th to run
   const int lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4, col = 16 * wave_id() + l16;
   struct Next {
     float m[N / 4], b[4];
   };
   auto load = [&](Next& n, int i) {
-    const float* B = a.split.ends + ((int64_t)(base + i) * a.H + h) * (a.P + N) * N + col;
+    const float* B = a.split.ends + (slot(i) * a.H + h) * (a.P + N) * N + col;
     const float* M = B + (int64_t)a.P * N;
 #pragma unroll
     for (int e = 0; e < 4; ++e) n.b[e] = B[(p0 + 4 * la + e) * N];
@@ -833,7 +853,7 @@ __global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, 
       }
       c += c1;
     }
-    float* to = a.split.starts + (((int64_t)(base + i + 1) * a.H + h) * a.P + p0) * N + col;
+    float* to = a.split.starts + ((slot(i + 1) * a.H + h) * a.P + p0) * N + col;
     float* y = row[(i + 1) & 1] + col;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -873,11 +893,12 @@ __global__ __launch_bounds__(64) void delta_split_kernel(const DeltaArgs a, cons
 
 template <Chain K, typename T, int N, int NW, bool PAIR>
 hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
-  const int blocks = (a.P + 16 * NW - 1) / (16 * NW) + (K == Chain::ends ? (N + 16 * NW - 1) / (16 * NW) : 0);
+  constexpr bool ends = K == Chain::ends || K == Chain::bwd_ends;
+  const int blocks = (a.P + 16 * NW - 1) / (16 * NW) + (ends ? (N + 16 * NW - 1) / (16 * NW) : 0);
   const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * blocks)), th(64 * (NW + HW));
-  if constexpr (K == Chain::bwd)
-    hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
+  if constexpr (K == Chain::bwd || K == Chain::bwd_ends)
+    hipLaunchKernelGGL((delta_chain_bwd_kernel<T, N, NW, ends, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   else
     hipLaunchKernelGGL((delta_chain_kernel<T, N, NW, K, PAIR>), grid, th, 0, s, a, a.cmap(), blocks);
   return hipGetLastError();
@@ -919,45 +940,54 @@ hipError_t chain_type(const DeltaArgs& a, hipStream_t s) {
   return chain_n<K, bf16, false>(a, s);
 }
 
+template <bool BACK>
 hipError_t starts(const DeltaArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.nstates * a.H * (a.P / 16))), th(4 * a.N);
   switch (a.N) {
-    case 32: hipLaunchKernelGGL((delta_starts_kernel<32>), grid, th, 0, s, a, a.cmap()); break;
-    case 64: hipLaunchKernelGGL((delta_starts_kernel<64>), grid, th, 0, s, a, a.cmap()); break;
-    case 128: hipLaunchKernelGGL((delta_starts_kernel<128>), grid, th, 0, s, a, a.cmap()); break;
+    case 32: hipLaunchKernelGGL((delta_starts_kernel<32, BACK>), grid, th, 0, s, a, a.cmap()); break;
+    case 64: hipLaunchKernelGGL((delta_starts_kernel<64, BACK>), grid, th, 0, s, a, a.cmap()); break;
+    case 128: hipLaunchKernelGGL((delta_starts_kernel<128, BACK>), grid, th, 0, s, a, a.cmap()); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+// The segments' length: equal rows' here, a packed batch's by a launch (`first`: not yet made).
+hipError_t settle(DeltaArgs& a, bool first, hipStream_t s) {
+  if (!a.split.slots) return hipSuccess;
+  a.split.block = 16 * state_waves(a);
+  if (a.cu) {
+    if (!first) return hipSuccess;
+    hipLaunchKernelGGL(delta_split_kernel, dim3(1), dim3(DeltaSplit::kSequences), 0, s, a, a.cmap(), device_cus());
+    return hipGetLastError();
+  }
+  DeltaSplit::Sums v = {};
+  v.add(a.split, a.nc_row, a.nstates);
+  a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, a.split.block, device_cus());
+  if (a.split.fixed == 0) a.split.slots = 0;
+  return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_delta_chain(const DeltaArgs& given, bool keep, hipStream_t s) {
   DeltaArgs a = given;
-  hipError_t e = hipSuccess;
-  a.split.block = 16 * state_waves(a);
-  if (a.split.slots && !a.cu) {
-    // equal rows: the host knows the best length
-    DeltaSplit::Sums v = {};
-    v.add(a.split, a.nc_row, a.nstates);
-    a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, a.split.block, device_cus());
-    if (a.split.fixed == 0) a.split.slots = 0;
-  }
-  if (a.split.slots && a.cu) {
-    hipLaunchKernelGGL(delta_split_kernel, dim3(1), dim3(DeltaSplit::kSequences), 0, s, a, a.cmap(), device_cus());
-    e = hipGetLastError();
-  }
-  if (a.split.slots) {
-    if (e == hipSuccess) e = chain_type<Chain::ends>(a, s);
-    if (e == hipSuccess) e = starts(a, s);
+  hipError_t e = settle(a, true, s);
+  if (e == hipSuccess && a.split.slots) {
+    e = chain_type<Chain::ends>(a, s);
+    if (e == hipSuccess) e = starts<false>(a, s);
   }
   if (e != hipSuccess) return e;
   return keep ? chain_type<Chain::keep>(a, s) : chain_type<Chain::fwd>(a, s);
 }
 hipError_t launch_delta_chain_bwd(const DeltaArgs& given, hipStream_t s) {
   DeltaArgs a = given;
-  a.split.slots = 0;
-  return chain_type<Chain::bwd>(a, s);
+  hipError_t e = settle(a, false, s);
+  if (e == hipSuccess && a.split.slots) {
+    e = chain_type<Chain::bwd_ends>(a, s);
+    if (e == hipSuccess) e = starts<true>(a, s);
+  }
+  return e == hipSuccess ? chain_type<Chain::bwd>(a, s) : e;
 }
 
 }  // namespace ssd
