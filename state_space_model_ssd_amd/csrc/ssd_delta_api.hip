@@ -18,7 +18,7 @@ constexpr size_t kDeltaAlign = 256;
 
 // Backward, bf16: what the chains keep is kept as pairs where the gates' gradients are wanted in
 // fp32, and where there are few of them.  Each is a sum with cancellation of products of what is
-// kept, rounded to 2^-9: over many their errors average (2.6e-3 in the 2-norm), a handful may be
+// kept, rounded to 2^-8: over many their errors average (2.6e-3 in the 2-norm), a handful may be
 // off by several times that.
 // Pairs cost time: 2x4096 tokens, 32 heads of 128 x 128, 762 us for 549.
 constexpr int64_t kDeltaFewGates = 65536;

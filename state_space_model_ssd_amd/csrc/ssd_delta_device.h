@@ -13,9 +13,9 @@
 // the first) of a product that contracts these rows.
 //
 // With bf16 inputs a value that is not an input goes into a product either rounded once
-// (2^-9 of it, where the result is rounded to bf16 itself), or as the sum of two bf16
-// (2^-18 of it, where it is part of a state, whose error would last): the products of two
-// such pairs leave out the two low parts' product.
+// (2^-8 of it at most, where the result is rounded to bf16 itself), or as the sum of two bf16
+// (2^-17 of it, where it is part of a state, whose error would last): the products of two
+// such pairs leave out the two low parts' product (2^-16 at most).
 #pragma once
 
 #include "ssd_common.h"
@@ -33,7 +33,7 @@ struct F8 {
 template <typename T> struct Opnd;
 template <> struct Opnd<bf16> {
   using X = bf16x8;                    // exact or rounded
-  using S = Pair;                      // to 2^-18
+  using S = Pair;                      // to 2^-17
   static constexpr int PX = 1, PS = 2; // 16-byte pieces per lane
   // Two values at a time, as the conversion takes them.
   __device__ __forceinline__ static X round(const float (&f)[8]) {

@@ -3,10 +3,11 @@
 Tolerances, from what the chunked form rounds to fewer bits:
   fp32 inputs: nothing.  Outputs and gradients as the SSD's, relative L2 1e-5 and 1e-4.
   bf16 inputs: every operand on the way to a state is a pair of bf16, off by at most 2^-17 of
-    the value; a state of the forward passes eight of those at most (k decayed, w, its two
-    terms, the matrix 1 / (1 + L), its product, the state itself and the chunk's last row), so
-    2^-14; a gradient of the starting state as many again on the forward's side, 2^-13, and
-    the gradients of fp32 gates, sums over both of them, 2^-13.
+    the value, and a product of two pairs, without the two low parts', by 2^-16 more.  A chunk
+    adds to a state what passes six units of 2^-17 (the state, what it leaves of v, the matrix
+    1 / (1 + L) and its product with that, the rows w decayed), so 2^-14; the gradient of the
+    starting state as much by itself and on the forward's side, 2^-13, and the gradients of
+    fp32 gates, sums over both of them, 2^-13.
     What is rounded to bf16 once on the way (the output and the gradients of q, k, v, and of
     bf16 gates over many tokens) is held to the SSD's bf16 tolerance.
 """
