@@ -965,7 +965,7 @@ def delta_fwd(q, k, v, g, beta, scale=None, initial_states=None, cu_seqlens=None
     dev, sshape, prob = _delta_checked("delta_fwd", q, k, v, g, beta, scale, initial_states,
                                        cu_seqlens, out is None)
     if out is None:
-        out = v.new_empty(v.shape)
+        out = torch.empty_like(v)
     else:
         _need(out, "out", v.dtype, v.shape, dev)
     if final_states is not None:
@@ -991,8 +991,8 @@ def delta_bwd(q, k, v, g, beta, dout, dfinal_states=None, scale=None, initial_st
     _need(dfinal_states, "dfinal_states", torch.float32, sshape, dev)
     if dout is None:
         raise ValueError("dout is missing")
-    grads = {"q": q.new_empty(q.shape), "k": k.new_empty(k.shape), "v": v.new_empty(v.shape),
-             "g": g.new_empty(g.shape), "beta": beta.new_empty(beta.shape),
+    grads = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v),
+             "g": torch.empty_like(g), "beta": torch.empty_like(beta),
              "initial_states": v.new_empty(sshape, dtype=torch.float32)
              if initial_states is not None else None}
     workspace = _workspace(workspace, prob[3], dev)
@@ -1083,7 +1083,7 @@ def qk_norm_fwd(q, k, q_weight=None, k_weight=None, norm="rms", eps=1e-6, positi
     dev, prob = _qk_norm_checked("qk_norm_fwd", q, k, q_weight, k_weight, norm, eps, positions,
                                  inv_freq, interleaved)
     if outs is None:
-        outs = (q.new_empty(q.shape), k.new_empty(k.shape))
+        outs = tuple(torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k))
     else:
         if len(outs) != 2:
             raise ValueError("outs are two tensors")
@@ -1112,8 +1112,8 @@ def qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm="rms", 
         raise ValueError("dq_out and dk_out are the outputs' gradients")
     _need(dq_out, "dq_out", q.dtype, q.shape, dev)
     _need(dk_out, "dk_out", q.dtype, k.shape, dev)
-    g = {"q": q.new_empty(q.shape) if dq is None else dq,
-         "k": k.new_empty(k.shape) if dk is None else dk,
+    g = {"q": torch.empty_like(q, memory_format=torch.contiguous_format) if dq is None else dq,
+         "k": torch.empty_like(k, memory_format=torch.contiguous_format) if dk is None else dk,
          "q_weight": torch.empty_like(q_weight) if q_weight is not None else None,
          "k_weight": torch.empty_like(k_weight) if k_weight is not None else None}
     need = prob[2] if q_weight is not None or k_weight is not None else 0

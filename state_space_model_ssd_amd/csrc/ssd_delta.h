@@ -105,7 +105,6 @@ struct DeltaArgs {
   int H, G, P, N;
   int max_chunks, nc_row;
   bool bf16, gate_bf16;
-  bool clear;             // rows outside every sequence become zeros
   bool pairs;             // backward: what the chains keep is kept as pairs (bf16)
   float scale;
   const void* q;
@@ -157,12 +156,16 @@ struct DeltaArgs {
 };
 
 bool delta_dstate_ok(int64_t N);
-// Zeros in the rows that no sequence of a packed batch has, of n tensors and `row` bytes each.
+// n tensors of `row` bytes a token, whose rows that no sequence of a packed batch has become zeros.
 struct DeltaClear {
+  int n;
   void* p[5];
   int64_t row[5];
 };
-hipError_t launch_delta_clear(const DeltaArgs& a, const DeltaClear& c, int n, hipStream_t s);
+// A packed batch's chunk table, its clearing, and how it is cut.
+hipError_t launch_delta_plan(const DeltaArgs& a, const DeltaClear& c, hipStream_t s);
+// The rows of a state that a workgroup of the chain has.
+int delta_chain_rows(const DeltaArgs& a);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s);
 // The chain of states; `keep`: for the backward, which wants S0 and Wt and no output.
 hipError_t launch_delta_chain(const DeltaArgs& a, bool keep, hipStream_t s);

@@ -84,7 +84,6 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   a.nc_row = (int)((p->seqlen + kDeltaChunk - 1) / kDeltaChunk);
   a.bf16 = p->dtype == SSD_BF16;
   a.gate_bf16 = p->gate_dtype == SSD_BF16;
-  a.clear = p->nseq > 0 && p->clear_outside == 1;
   a.scale = p->scale;
   // sequences may be cut where one's heads fill at most a quarter of the device (16384 tokens of 64
   // workgroups: 467 -> 376 us; 8192 of 128: 273 -> 321); a packed batch's lengths are not known here
@@ -169,22 +168,6 @@ struct DeltaSpans {
   Span states(const void* x) const { return bytes_of(x, n * H * P * N * 4); }
   Span packing(const void* cu) const { return bytes_of(cu, (uint64_t)(p->nseq + 1) * 4); }
 };
-
-// A packed batch's chunk table, by the SSD's own launch.
-hipError_t plan(const DeltaArgs& a, hipStream_t s) {
-  if (!a.cu) return hipSuccess;
-  FwdArgs f{};
-  f.batch = 1;
-  f.seqlen = a.total;
-  f.L = kDeltaChunk;
-  f.nstates = a.nstates;
-  f.max_chunks = a.max_chunks;
-  f.packed = true;
-  f.cu_seqlens = a.cu;
-  f.table = a.table;
-  f.seq_chunks = a.seq_chunks;
-  return launch_plan(f, s);
-}
 
 ssd_status_t check_delta_step(const ssd_delta_step_problem_t* p) {
   if (!p) return SSD_ERR_INVALID_ARG;
@@ -278,10 +261,9 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
   a.out = out; a.final_states = final_states;
   if (a.total == 0) a.nc_row = a.max_chunks = a.split.slots = 0;
   ssd::delta_layout(a, p->nseq > 0, false, workspace);
+  a.split.block = ssd::delta_chain_rows(a);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = ssd::plan(a, s);
-  if (e == hipSuccess && a.clear && a.cu)
-    e = ssd::launch_delta_clear(a, {{out}, {(int64_t)(m.H * m.P * m.e)}}, 1, s);
+  hipError_t e = ssd::launch_delta_plan(a, {p->clear_outside, {out}, {(int64_t)(m.H * m.P * m.e)}}, s);
   if (e == hipSuccess) e = ssd::launch_delta_prep(a, false, s);
   if (e == hipSuccess) e = ssd::launch_delta_chain(a, false, s);
   return ssd::status_of(e);
@@ -320,12 +302,11 @@ ssd_status_t ssd_delta_bwd(const ssd_delta_problem_t* p, const void* q, const vo
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dinit = dinitial_states;
   if (a.total == 0) a.nc_row = a.max_chunks = a.split.slots = 0;
   ssd::delta_layout(a, p->nseq > 0, true, workspace);
+  a.split.block = ssd::delta_chain_rows(a);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = ssd::plan(a, s);
-  if (e == hipSuccess && a.clear && a.cu) {
-    const int64_t qk = (int64_t)(m.G * m.N * m.e), v = (int64_t)(m.H * m.P * m.e), gate = (int64_t)(m.H * m.ge);
-    e = ssd::launch_delta_clear(a, {{dq, dk, dv, dg, dbeta}, {qk, qk, v, gate, gate}}, 5, s);
-  }
+  const int64_t qk = (int64_t)(m.G * m.N * m.e), v_row = (int64_t)(m.H * m.P * m.e), gate = (int64_t)(m.H * m.ge);
+  hipError_t e = ssd::launch_delta_plan(
+      a, {p->clear_outside ? 5 : 0, {dq, dk, dv, dg, dbeta}, {qk, qk, v_row, gate, gate}}, s);
   if (e == hipSuccess) e = ssd::launch_delta_prep(a, true, s);
   if (e == hipSuccess) e = ssd::launch_delta_chain(a, true, s);
   if (e == hipSuccess) e = ssd::launch_delta_chain_bwd(a, s);

@@ -870,27 +870,6 @@ __global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, 
   }
 }
 
-// A packed batch's segment length, from its sequences' chunks (a lane each: DeltaSplit::kSequences
-// is a wave).
-__global__ __launch_bounds__(64) void delta_split_kernel(const DeltaArgs a, const ChunkMap cm, int cus) {
-  DeltaSplit::Sums v = {};
-  if ((int)threadIdx.x < a.nstates) {
-    const int2 r = cm.seq_range(threadIdx.x);
-    v.add(a.split, r.y - r.x, 1);
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    v.longest = max(v.longest, __shfl_xor(v.longest, off));
-#pragma unroll
-    for (int i = 0; i < DeltaSplit::kLengths; ++i) {
-      v.first[i] += __shfl_xor(v.first[i], off);
-      v.later[i] += __shfl_xor(v.later[i], off);
-    }
-  }
-  if (threadIdx.x == 0) 
-    *a.split.chosen = DeltaSplit::best(a.split, v, cm.seq_range(a.nstates - 1).y, a.H, a.P, a.N, a.split.block, cus);
-}
-
 template <Chain K, typename T, int N, int NW, bool PAIR>
 hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
   constexpr bool ends = K == Chain::ends || K == Chain::bwd_ends;
@@ -952,28 +931,24 @@ hipError_t starts(const DeltaArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The segments' length: equal rows' here, a packed batch's by a launch (`first`: not yet made).
-hipError_t settle(DeltaArgs& a, bool first, hipStream_t s) {
-  if (!a.split.slots) return hipSuccess;
-  a.split.block = 16 * state_waves(a);
-  if (a.cu) {
-    if (!first) return hipSuccess;
-    hipLaunchKernelGGL(delta_split_kernel, dim3(1), dim3(DeltaSplit::kSequences), 0, s, a, a.cmap(), device_cus());
-    return hipGetLastError();
-  }
+// The segments' length of equal rows; a packed batch's is in memory by now.
+void settle(DeltaArgs& a) {
+  if (!a.split.slots || a.cu) return;
   DeltaSplit::Sums v = {};
   v.add(a.split, a.nc_row, a.nstates);
   a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, a.split.block, device_cus());
   if (a.split.fixed == 0) a.split.slots = 0;
-  return hipSuccess;
 }
 
 }  // namespace
 
+int delta_chain_rows(const DeltaArgs& a) { return 16 * state_waves(a); }
+
 hipError_t launch_delta_chain(const DeltaArgs& given, bool keep, hipStream_t s) {
   DeltaArgs a = given;
-  hipError_t e = settle(a, true, s);
-  if (e == hipSuccess && a.split.slots) {
+  hipError_t e = hipSuccess;
+  settle(a);
+  if (a.split.slots) {
     e = chain_type<Chain::ends>(a, s);
     if (e == hipSuccess) e = starts<false>(a, s);
   }
@@ -982,8 +957,9 @@ hipError_t launch_delta_chain(const DeltaArgs& given, bool keep, hipStream_t s) 
 }
 hipError_t launch_delta_chain_bwd(const DeltaArgs& given, hipStream_t s) {
   DeltaArgs a = given;
-  hipError_t e = settle(a, false, s);
-  if (e == hipSuccess && a.split.slots) {
+  hipError_t e = hipSuccess;
+  settle(a);
+  if (a.split.slots) {
     e = chain_type<Chain::bwd_ends>(a, s);
     if (e == hipSuccess) e = starts<true>(a, s);
   }

@@ -359,17 +359,6 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
   }
 }
 
-// Rows [0, cu[0]) and [cu[nstates], total) of the tensors, each by its grid row.
-__global__ __launch_bounds__(256) void delta_clear_kernel(const int32_t* __restrict__ cu, int nstates,
-                                                          int total, const DeltaClear c) {
-  const int64_t n2 = c.row[blockIdx.y] / 2, lo = min(max(cu[0], 0), total) * n2;
-  const int64_t hi = min(max(cu[nstates], 0), total) * n2, end = total * n2;
-  unsigned short* o = static_cast<unsigned short*>(c.p[blockIdx.y]);
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = at; i < lo; i += step) o[i] = 0;
-  for (int64_t i = max(lo, hi) + at; i < end; i += step) o[i] = 0;
-}
-
 template <typename T, int N>
 hipError_t prep_go(const DeltaArgs& a, bool bwd, hipStream_t s) {
   // a head per wave while that does not fill the device's SIMDs once (a forward of 32 heads: 17
@@ -411,15 +400,6 @@ bool delta_dstate_ok(int64_t N) { return N == 32 || N == 64 || N == 128; }
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s) {
   if (a.max_chunks <= 0) return hipSuccess;
   return a.bf16 ? prep_type<bf16>(a, bwd, s) : prep_type<float>(a, bwd, s);
-}
-
-hipError_t launch_delta_clear(const DeltaArgs& a, const DeltaClear& c, int n, hipStream_t s) {
-  int64_t most = 0;
-  for (int i = 0; i < n; ++i) most = c.row[i] > most ? c.row[i] : most;
-  const int64_t blocks = ((int64_t)a.total * most / 2 + 256 * 16 - 1) / (256 * 16);
-  hipLaunchKernelGGL(delta_clear_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), n), dim3(256), 0, s,
-                     a.cu, a.nstates, a.total, c);
-  return hipGetLastError();
 }
 
 }  // namespace ssd

@@ -31,6 +31,7 @@ constexpr int kQnThreads = 256;
 constexpr int kQnTok = 4;               // tokens a workgroup takes at a time where there are many
 constexpr int kQnMaxParts = 1024;       // partial rows the workspace holds
 constexpr int kQnSegment = 32;
+constexpr int64_t kQnGridX = 1 << 18;
 
 __device__ __forceinline__ float2 turn(int pos, float freq) {
   const double t = (double)pos * (double)freq * 0.15915494309189533577;
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(kQnThreads) void qk_norm_fwd_kernel(const QkNormArg
   extern __shared__ float lds[];        // angles of `per` tokens, then (lds) the groups' rows
   float2* cs = reinterpret_cast<float2*>(lds);
   const RowLane<V> L(a.D, lpr);
-  const int64_t tok0 = (int64_t)blockIdx.x * per;
+  const int64_t tok0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * per;
+  if (tok0 >= a.tokens) return;
   const int ntok = (int)min((int64_t)per, a.tokens - tok0);
   const int group = threadIdx.x / lpr, gpt = L.rows / per, t = group / gpt, h0 = group % gpt;
   float* row = lds + 2 * per * a.R + group * a.D;
@@ -324,7 +326,10 @@ hipError_t qn_go(const QkNormArgs& a, bool bwd, hipStream_t s) {
   const int64_t tiles = (a.tokens + per - 1) / per;
   if (!bwd) {
     if (tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, V, M, 2>), dim3((unsigned)tiles), dim3(kQnThreads), lds, s, a, lpr, per);
+    // rows of the grid, which may have 2^32 threads in each direction
+    const int64_t x = tiles < kQnGridX ? tiles : kQnGridX;
+    const dim3 grid((unsigned)x, (unsigned)((tiles + x - 1) / x));
+    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, V, M, 2>), grid, dim3(kQnThreads), lds, s, a, lpr, per);
     return hipGetLastError();
   }
   const int64_t most = a.part ? kQnMaxParts : (int64_t)1 << 22;

@@ -285,6 +285,21 @@ def test_many_sequences_and_heads(dtype):
     check_bwd(got, x, dout, dfin, 32 ** -0.5, cu)
 
 
+@pytest.mark.parametrize("n", [64, 65, 150])
+def test_more_sequences_than_a_wave(n):
+    """Up to 64 sequences are planned in one launch, more in several; tokens outside cleared."""
+    lens = [(11 * i) % 7 + (70 if i == 3 else 0) for i in range(n)]
+    cu = torch.tensor(list(np.cumsum([4] + lens)), dtype=torch.int32)
+    x = draw(1, int(cu[-1]) + 6, 2, 1, 16, 32, nseq=n, seed=9)
+    c = cu.cuda()
+    got = binding.delta_fwd(**dev(x), cu_seqlens=c)
+    check_fwd(got, x, 32 ** -0.5, cu)
+    assert not got[0][:, :4].any() and not got[0][:, -6:].any()
+    dout, dfin = draw_grads(x)
+    grads = binding.delta_bwd(**dev(x), cu_seqlens=c, dout=dout.cuda(), dfinal_states=dfin.cuda())
+    check_bwd(grads, x, dout, dfin, 32 ** -0.5, cu)
+
+
 def test_long_prompt_of_one_head():
     x = draw(1, 5000, 1, 1, 16, 32, "f32", decay=0.01)
     check_fwd(binding.delta_fwd(**dev(x)), x, 32 ** -0.5)

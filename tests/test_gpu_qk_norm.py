@@ -142,6 +142,20 @@ def test_far_positions(interleaved):
     check_bwd(bwd, x, interleaved=interleaved)
 
 
+def test_more_tokens_than_a_row_of_the_grid():
+    """2^20 tokens, four a workgroup: the same as their parts."""
+    n, cut = 2 ** 20 + 5, 2 ** 20 - 3
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn((n, 64, 8), device="cuda", generator=g).bfloat16()
+    k = torch.randn((n, 1, 8), device="cuda", generator=g).bfloat16()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    freq = torch.tensor([1.0, 0.1], device="cuda")
+    whole = binding.qk_norm_fwd(q, k, positions=pos, inv_freq=freq)
+    for at in (slice(cut, n), slice(0, 2000)):
+        part = binding.qk_norm_fwd(q[at], k[at], positions=pos[at], inv_freq=freq)
+        assert torch.equal(whole[0][at], part[0]) and torch.equal(whole[1][at], part[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_zero_and_tiny_rows(dtype):
     x = inputs(dtype=dtype)
