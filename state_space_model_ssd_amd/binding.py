@@ -598,6 +598,9 @@ def _row_stride(t, name, rows):
     """Elements from one row to the next of a tensor whose last axes are
     contiguous and whose first `rows` axes lie evenly behind one another."""
     st, sh = t.stride(), t.shape
+    if (rows == 1 and len(sh) == 3 and sh[0] > 1 and st[2] == 1 and st[1] == sh[2]
+            and st[0] >= sh[1] * sh[2] > 0):
+        return st[0]                      # the usual case first: a call costs what this does
     if t.is_contiguous():
         return math.prod(sh[rows:])
     inner = 1
@@ -934,7 +937,8 @@ def _delta_checked(what, q, k, v, g, beta, scale, initial_states, cu_seqlens, cl
     _need(q, "q", q.dtype, (b, T, G, N), dev)
     _need(k, "k", q.dtype, (b, T, G, N), dev)
     _need(v, "v", q.dtype, (b, T, H, P), dev)
-    _gates_checked(g, beta, (b, T, H), q.dtype, dev)
+    if g.dtype != torch.float32 and g.dtype != q.dtype:
+        raise ValueError(f"g has dtype {g.dtype}, expected torch.float32 or {q.dtype}")
     _need(g, "g", g.dtype, (b, T, H), dev)
     _need(beta, "beta", g.dtype, (b, T, H), dev)
     nseq = 0
@@ -1083,7 +1087,8 @@ def qk_norm_fwd(q, k, q_weight=None, k_weight=None, norm="rms", eps=1e-6, positi
     dev, prob = _qk_norm_checked("qk_norm_fwd", q, k, q_weight, k_weight, norm, eps, positions,
                                  inv_freq, interleaved)
     if outs is None:
-        outs = tuple(torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k))
+        outs = (torch.empty_like(q, memory_format=torch.contiguous_format),
+                torch.empty_like(k, memory_format=torch.contiguous_format))
     else:
         if len(outs) != 2:
             raise ValueError("outs are two tensors")
