@@ -145,6 +145,19 @@ def test_gates_and_keys_at_their_ends(kind, dtype):
     check_bwd(got, x, dout, dfin, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("T", [100, 3300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_with_only_one_of_the_states(dtype, T):
+    """A gradient of the final states without initial ones, and the other way round."""
+    x = draw(1, T, 2, 1, 32, 64, dtype, decay=0.003)
+    dout, dfin = draw_grads(x)
+    got = binding.delta_bwd(**dev(x), dout=dout.cuda())
+    check_bwd(got, x, dout, None, 64 ** -0.5)
+    x["initial_states"] = None
+    got = binding.delta_bwd(**dev(x), dout=dout.cuda(), dfinal_states=dfin.cuda())
+    check_bwd(got, x, dout, dfin, 64 ** -0.5)
+
+
 def test_no_length_no_sequences():
     for b, T in ((2, 0), (0, 50)):
         x = draw(b, T, 4, 2, 32, 64)
@@ -320,6 +333,14 @@ def test_long_sequences_are_cut(dtype, P, N, cu):
     dout, dfin = draw_grads(x)
     got = binding.delta_bwd(**dev(x), **kw, dout=dout.cuda(), dfinal_states=dfin.cuda())
     check_bwd(got, x, dout, dfin, N ** -0.5, c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_sequences_that_do_not_decay(dtype):
+    """g = 0: what segments hand on is only forgotten where a key comes again."""
+    x = draw(1, 12000, 1, 1, 16, 64, dtype)
+    x["g"].zero_()
+    check_fwd(binding.delta_fwd(**dev(x)), x, 64 ** -0.5)
 
 
 def test_rows_are_cut_alike():
