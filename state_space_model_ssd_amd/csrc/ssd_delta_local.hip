@@ -373,7 +373,6 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         const int at = p0 + 8 * (lane & 3), tok = 16 * w + lane / 4;
         if (at < a.P && tok < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)tok * a.H * a.P + at, O::round(r8));
       }
-      fetch(q, h, p0 + AHEAD * kSlab, tid);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
@@ -389,6 +388,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         else mma_rows(r, od, Px + 2 * cb);
         mma_rows(r, half ? wo : ro, Lx + 2 * cb);
       }
+      fetch(q, h, p0 + AHEAD * kSlab, tid);
       __builtin_amdgcn_sched_barrier(0);
       {
         KV f[NH];
