@@ -598,9 +598,6 @@ def _row_stride(t, name, rows):
     """Elements from one row to the next of a tensor whose last axes are
     contiguous and whose first `rows` axes lie evenly behind one another."""
     st, sh = t.stride(), t.shape
-    if (rows == 1 and len(sh) == 3 and sh[0] > 1 and st[2] == 1 and st[1] == sh[2]
-            and st[0] >= sh[1] * sh[2] > 0):
-        return st[0]                      # the usual case first: a call costs what this does
     if t.is_contiguous():
         return math.prod(sh[rows:])
     inner = 1
@@ -907,25 +904,43 @@ def _delta_problem(*sizes):
     return p, ref, int(lib.ssd_delta_fwd_workspace_size(ref)), int(lib.ssd_delta_bwd_workspace_size(ref))
 
 
+def _stride_of(shape, stride, name, rows):
+    return _row_stride(torch.empty_strided(shape, stride, device="meta"), name, rows)
+
+
+# What a call's sizes, strides and types come to; the small calls cost what the host does for
+# them, so it is found once for each.
 @functools.lru_cache(maxsize=1024)
-def _delta_step_problem(*sizes):
-    p = DeltaStepProblemC(*sizes)
-    return p, ctypes.byref(p)
+def _delta_step_problem(q, k, v, g, beta, strides, nslots, dtype, gate_dtype, scale):
+    if len(q) != 3 or len(v) != 3:
+        raise ValueError("q and k are (batch, groups, dstate), v (batch, heads, headdim)")
+    b, G, N = q
+    H, P = v[1], v[2]
+    for shape, want, name in ((k, (b, G, N), "k"), (v, (b, H, P), "v"), (g, (b, H), "g"), (beta, (b, H), "beta")):
+        if shape != want:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+    if gate_dtype not in (torch.float32, dtype):
+        raise ValueError(f"g has dtype {gate_dtype}, expected torch.float32 or {dtype}")
+    rows = [_stride_of(t, st, name, 1) for t, st, name in zip((q, k, v, g, beta), strides, ("q", "k", "v", "g", "beta"))]
+    p = DeltaStepProblemC(b, H, P, N, G, nslots, *rows, _DT[dtype], _DT[gate_dtype],
+                          N ** -0.5 if scale is None else scale)
+    return p, ctypes.byref(p), (b, H, P), (nslots, H, P, N), (b,)
 
 
 @functools.lru_cache(maxsize=1024)
-def _qk_norm_problem(*sizes):
-    p = QkNormProblemC(*sizes)
-    return p, ctypes.byref(p), int(load_library().ssd_qk_norm_bwd_workspace_size(ctypes.byref(p)))
-
-
-def _gates_checked(g, beta, shape, x_dtype, dev):
-    for t, name in ((g, "g"), (beta, "beta")):
-        if t.device != dev or t.shape != shape or t.dtype != g.dtype:
-            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                             f"{g.dtype} {shape} on {dev}")
-    if g.dtype != torch.float32 and g.dtype != x_dtype:
-        raise ValueError(f"g has dtype {g.dtype}, expected torch.float32 or {x_dtype}")
+def _qk_norm_problem(q, q_stride, k, k_stride, dtype, R, dq_stride, dk_stride, norm, eps, interleaved):
+    if len(q) < 2 or len(k) != len(q) or k[:-2] != q[:-2] or k[-1] != q[-1]:
+        raise ValueError("q is (..., heads, headdim), k the same but for its heads")
+    if norm not in _QK_NORMS:
+        raise ValueError("norm is 'rms' or 'l2'")
+    lead, D = tuple(q[:-2]), q[-1]
+    if R is not None and (R < 1 or 2 * R > D):
+        raise ValueError(f"inv_freq has {R} entries, expected 1 to {D // 2}")
+    p = QkNormProblemC(math.prod(lead), q[-2], k[-2], D, R or 0, _stride_of(q, q_stride, "q", len(lead)),
+                       _stride_of(k, k_stride, "k", len(lead)), dq_stride, dk_stride, _DT[dtype],
+                       _QK_NORMS[norm], int(interleaved), eps)
+    ref = ctypes.byref(p)
+    return p, ref, int(load_library().ssd_qk_norm_bwd_workspace_size(ref)), lead, (D,)
 
 
 def _delta_checked(what, q, k, v, g, beta, scale, initial_states, cu_seqlens, clear):
@@ -1018,26 +1033,19 @@ def delta_step(q, k, v, g, beta, states, scale=None, slots=None, out=None):
     are such states); slots as for conv_step.  Returns out (batch, H, P); padding's rows of
     it keep what they held (zeros where the call makes it)."""
     dev = _on_gpu(q, "q", "delta_step")
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and k are (batch, groups, dstate), v (batch, heads, headdim)")
-    b, G, N = q.shape
-    H, P = v.shape[1], v.shape[2]
-    for t, name, shape in ((k, "k", (b, G, N)), (v, "v", (b, H, P))):
-        if t.device != dev or t.dtype != q.dtype or t.shape != shape:
-            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                             f"{q.dtype} {shape} on {dev}")
-    _gates_checked(g, beta, (b, H), q.dtype, dev)
-    nslots = states.shape[0]
-    _need(states, "states", torch.float32, (nslots, H, P, N), dev)
-    _need(slots, "slots", torch.int32, (b,), dev)
+    for t, name, dtype in ((k, "k", q.dtype), (v, "v", q.dtype), (g, "g", g.dtype), (beta, "beta", g.dtype)):
+        if t.device != dev or t.dtype != dtype:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {dev}")
+    prob = _delta_step_problem(q.shape, k.shape, v.shape, g.shape, beta.shape,
+                               (q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()),
+                               states.shape[0], q.dtype, g.dtype, None if scale is None else float(scale))
+    _need(states, "states", torch.float32, prob[3], dev)
+    _need(slots, "slots", torch.int32, prob[4], dev)
     if out is None:
         make = torch.empty if slots is None else torch.zeros
-        out = make((b, H, P), dtype=v.dtype, device=dev)
-    _need(out, "out", v.dtype, (b, H, P), dev)
-    prob = _delta_step_problem(b, H, P, N, G, nslots, _row_stride(q, "q", 1), _row_stride(k, "k", 1),
-                               _row_stride(v, "v", 1), _row_stride(g, "g", 1),
-                               _row_stride(beta, "beta", 1), _DT[q.dtype], _DT[g.dtype],
-                               N ** -0.5 if scale is None else float(scale))
+        out = make(prob[2], dtype=v.dtype, device=dev)
+    else:
+        _need(out, "out", v.dtype, prob[2], dev)
     _launch(dev, load_library().ssd_delta_step, prob[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), states.data_ptr(), _addr(slots), out.data_ptr())
     return out
@@ -1049,29 +1057,18 @@ _QK_NORMS = {"rms": 0, "l2": 1}
 def _qk_norm_checked(what, q, k, q_weight, k_weight, norm, eps, positions, inv_freq, interleaved,
                      dq_stride=0, dk_stride=0):
     dev = _on_gpu(q, "q", what)
-    if q.dim() < 2 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
-        raise ValueError("q is (..., heads, headdim), k the same but for its heads")
     if k.dtype != q.dtype or k.device != dev:
         raise ValueError(f"k is {k.dtype} on {k.device}, expected {q.dtype} on {dev}")
-    lead, D = tuple(q.shape[:-2]), q.shape[-1]
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(t, name, torch.float32, (D,), dev)
-    if norm not in _QK_NORMS:
-        raise ValueError("norm is 'rms' or 'l2'")
     if (positions is None) != (inv_freq is None):
         raise ValueError("the rotation takes both positions and inv_freq")
-    R = 0
+    R = None if inv_freq is None else inv_freq.numel()
+    prob = _qk_norm_problem(q.shape, q.stride(), k.shape, k.stride(), q.dtype, R, dq_stride, dk_stride,
+                            norm, float(eps), bool(interleaved))
+    _need(q_weight, "q_weight", torch.float32, prob[4], dev)
+    _need(k_weight, "k_weight", torch.float32, prob[4], dev)
     if inv_freq is not None:
-        R = inv_freq.numel()
-        if R < 1 or 2 * R > D:
-            raise ValueError(f"inv_freq has {R} entries, expected 1 to {D // 2}")
         _need(inv_freq, "inv_freq", torch.float32, (R,), dev)
-        _need(positions, "positions", torch.int32, lead, dev)
-    rows = len(lead)
-    prob = _qk_norm_problem(math.prod(lead), q.shape[-2], k.shape[-2], D, R,
-                            _row_stride(q, "q", rows), _row_stride(k, "k", rows), dq_stride,
-                            dk_stride, _DT[q.dtype], _QK_NORMS[norm], int(bool(interleaved)),
-                            float(eps))
+        _need(positions, "positions", torch.int32, prob[3], dev)
     return dev, prob
 
 
