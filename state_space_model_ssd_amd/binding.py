@@ -897,19 +897,31 @@ def block_norm_bwd(x, residual, pre_weight, dout, dresidual_out=None, gate=None,
 # ---------------------------------------------------------------------------
 # The gated delta rule, and the norm of queries and keys in front of it
 # ---------------------------------------------------------------------------
-@functools.lru_cache(maxsize=1024)
-def _delta_problem(*sizes):
-    p = DeltaProblemC(*sizes)
-    ref, lib = ctypes.byref(p), load_library()
-    return p, ref, int(lib.ssd_delta_fwd_workspace_size(ref)), int(lib.ssd_delta_bwd_workspace_size(ref))
-
-
 def _stride_of(shape, stride, name, rows):
     return _row_stride(torch.empty_strided(shape, stride, device="meta"), name, rows)
 
 
 # What a call's sizes, strides and types come to; the small calls cost what the host does for
 # them, so it is found once for each.
+@functools.lru_cache(maxsize=1024)
+def _delta_problem(q, k, v, g, beta, nseq, dtype, gate_dtype, scale, clear):
+    if len(q) != 4 or len(v) != 4:
+        raise ValueError("q and k are (batch, seqlen, groups, dstate), v (batch, seqlen, heads, headdim)")
+    b, T, G, N = q
+    H, P = v[2], v[3]
+    for shape, want, name in ((k, (b, T, G, N), "k"), (v, (b, T, H, P), "v"), (g, (b, T, H), "g"),
+                              (beta, (b, T, H), "beta")):
+        if shape != want:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+    if gate_dtype not in (torch.float32, dtype):
+        raise ValueError(f"g has dtype {gate_dtype}, expected torch.float32 or {dtype}")
+    p = DeltaProblemC(b, T, H, P, N, G, nseq, _DT[dtype], _DT[gate_dtype],
+                      N ** -0.5 if scale is None else scale, int(nseq > 0 and clear))
+    ref, lib = ctypes.byref(p), load_library()
+    return (p, ref, int(lib.ssd_delta_fwd_workspace_size(ref)), int(lib.ssd_delta_bwd_workspace_size(ref)),
+            (nseq if nseq > 0 else b, H, P, N))
+
+
 @functools.lru_cache(maxsize=1024)
 def _delta_step_problem(q, k, v, g, beta, strides, nslots, dtype, gate_dtype, scale):
     if len(q) != 3 or len(v) != 3:
@@ -945,27 +957,20 @@ def _qk_norm_problem(q, q_stride, k, k_stride, dtype, R, dq_stride, dk_stride, n
 
 def _delta_checked(what, q, k, v, g, beta, scale, initial_states, cu_seqlens, clear):
     dev = _on_gpu(q, "q", what)
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and k are (batch, seqlen, groups, dstate), v (batch, seqlen, heads, headdim)")
-    b, T, G, N = q.shape
-    H, P = v.shape[2], v.shape[3]
-    _need(q, "q", q.dtype, (b, T, G, N), dev)
-    _need(k, "k", q.dtype, (b, T, G, N), dev)
-    _need(v, "v", q.dtype, (b, T, H, P), dev)
-    if g.dtype != torch.float32 and g.dtype != q.dtype:
-        raise ValueError(f"g has dtype {g.dtype}, expected torch.float32 or {q.dtype}")
-    _need(g, "g", g.dtype, (b, T, H), dev)
-    _need(beta, "beta", g.dtype, (b, T, H), dev)
+    for t, name, dtype in ((q, "q", q.dtype), (k, "k", q.dtype), (v, "v", q.dtype), (g, "g", g.dtype),
+                           (beta, "beta", g.dtype)):
+        if t.device != dev or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {dev}, contiguous")
     nseq = 0
     if cu_seqlens is not None:
         nseq = cu_seqlens.numel() - 1
         if nseq < 1:
             raise ValueError("cu_seqlens needs at least two entries")
         _need(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
-    sshape = (nseq if nseq > 0 else b, H, P, N)
+    prob = _delta_problem(q.shape, k.shape, v.shape, g.shape, beta.shape, nseq, q.dtype, g.dtype,
+                          None if scale is None else float(scale), clear)
+    sshape = prob[4]
     _need(initial_states, "initial_states", torch.float32, sshape, dev)
-    prob = _delta_problem(b, T, H, P, N, G, nseq, _DT[q.dtype], _DT[g.dtype],
-                          N ** -0.5 if scale is None else float(scale), int(nseq > 0 and clear))
     return dev, sshape, prob
 
 
