@@ -20,7 +20,7 @@ constexpr size_t kDeltaAlign = 256;
 // fp32, and where there are few of them.  Each is a sum with cancellation of products of what is
 // kept, rounded to 2^-8: over many their errors average (2.6e-3 in the 2-norm), a handful may be
 // off by several times that.
-// Pairs cost time: 2x4096 tokens, 32 heads of 128 x 128, 762 us for 549.
+// Pairs cost time: 2x4096 tokens, 32 heads of 128 x 128, 730 us for 551.
 constexpr int64_t kDeltaFewGates = 65536;
 
 constexpr int kDeltaLeast = 16;          // chunks of the shortest segments of a sequence
