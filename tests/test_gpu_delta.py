@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 SHAPES = [  # (b, T, H, G, P, N)
     (1, 1, 4, 2, 16, 32), (2, 2, 2, 1, 64, 128), (1, 63, 3, 3, 48, 64), (1, 64, 4, 1, 32, 128),
     (3, 65, 4, 2, 64, 32), (1, 127, 5, 5, 96, 64), (1, 200, 6, 2, 128, 128), (2, 130, 8, 8, 80, 32),
-    (1, 300, 4, 4, 256, 64), (1, 90, 12, 1, 16, 128),
+    (1, 300, 4, 4, 256, 64), (1, 90, 12, 1, 16, 128), (2, 70, 2, 1, 256, 128), (1, 70, 64, 1, 16, 32),
 ]
 IDS = ["x".join(map(str, s)) for s in SHAPES]
 TYPES = [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")]
