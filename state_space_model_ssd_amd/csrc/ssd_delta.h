@@ -105,6 +105,7 @@ struct DeltaArgs {
   int H, G, P, N;
   int max_chunks, nc_row;
   bool bf16, gate_bf16;
+  bool back;              // the backward's launches
   bool pairs;             // backward: what the chains keep is kept as pairs (bf16)
   float scale;
   const void* q;
@@ -130,7 +131,7 @@ struct DeltaArgs {
   int4* table;            // packed batch: [max_chunks]
   int* seq_chunks;        // packed batch: [nstates + 1]
   float* gates;           // [kGateFloats]
-  void* T;                // (1 + L)^-1, lower, pairs
+  void* T;                // T beta, or for the backward T' (ssd_delta_prep.hip), lower, pairs
   void* A;                // scale (D * q k^T), lower (forward)
   void* kt;               // per (chunk, group), fp32: k transposed
   // backward
@@ -140,8 +141,8 @@ struct DeltaArgs {
   void* S0;               // [P][N] the state entering the chunk, dtype (two with pairs: high
                           // and low parts; so the next three)
   void* dS;               // [P][N] the gradient of the state leaving it
-  void* Wt;               // [P][64] the rows w, transposed
-  void* dRt;              // [P][64] their gradient before T, transposed
+  void* Rt;               // [P][64] the rows r, transposed
+  void* dRt;              // [P][64] the gradient of the rows w, transposed
   DeltaSplit split;
 
   ChunkMap cmap() const {
@@ -167,7 +168,7 @@ hipError_t launch_delta_plan(const DeltaArgs& a, const DeltaClear& c, hipStream_
 // The rows of a state that a workgroup of the chain has.
 int delta_chain_rows(const DeltaArgs& a);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bwd, hipStream_t s);
-// The chain of states; `keep`: for the backward, which wants S0 and Wt and no output.
+// The chain of states; `keep`: for the backward, which wants S0 and Rt and no output.
 hipError_t launch_delta_chain(const DeltaArgs& a, bool keep, hipStream_t s);
 hipError_t launch_delta_chain_bwd(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_local_bwd(const DeltaArgs& a, hipStream_t s);

@@ -136,7 +136,7 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
   const size_t ke = a.pairs ? 4 : e;
   part(a.S0, mh * a.P * a.N * ke);
   part(a.dS, mh * a.P * a.N * ke);
-  part(a.Wt, mh * a.P * C * ke);
+  part(a.Rt, mh * a.P * C * ke);
   part(a.dRt, mh * a.P * C * ke);
   return off;
 }
@@ -299,6 +299,7 @@ ssd_status_t ssd_delta_bwd(const ssd_delta_problem_t* p, const void* q, const vo
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
   a.init = initial_states; a.cu = a.total > 0 ? cu_seqlens : nullptr;
   a.dout = dout; a.dfinal = dfinal_states;
+  a.back = true;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dinit = dinitial_states;
   if (a.total == 0) a.nc_row = a.max_chunks = a.split.slots = 0;
   ssd::delta_layout(a, p->nseq > 0, true, workspace);

@@ -3,8 +3,10 @@
 //   W = (T beta) (V - E K S^T)
 //   O = scale E (Q S^T) + A W
 //   S <- E_C S + (D W)^T K,     D_i = exp(G_C - G_i)
+// (for the backward R = T' (V - E K S^T), W = beta R: R is kept, also where beta is 0)
 // and backward, from the last chunk to the first, with dO the output's gradient, dS that of
-// the state leaving the chunk and dR that of beta V - beta E K S^T:
+// the state leaving the chunk and dR that of beta V - beta E K S^T, which is W's with all that
+// later rows make of it:
 //   dW = A^T dO + D K dS^T,   dR = T^T dW
 //   dS <- E_C dS + dO^T (scale E Q) - dR^T (beta E K)
 //
@@ -292,9 +294,9 @@ __device__ __forceinline__ uint32_t left_slot(int a, int i, int kb) {
   return (uint32_t)(16 * a + (i ^ ((a + 4 * kb) & 15))) * 16;
 }
 
-// Operands that the state waves left in LDS ([wave][EX of them], from the `from`-th on, each 32
-// columns of 16 dealt rows) to rows of a [P][COLS] matrix of T, or of two, one behind the other.
-template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
+// Operands that the state waves left in LDS ([wave][LEFT pieces], from the `from`-th piece on, each
+// 32 columns of 16 dealt rows) to rows of a [P][COLS] matrix of T, or of two, one behind the other.
+template <typename T, int NW, int LEFT, int COLS, bool PAIR> struct LeftRows {
   static constexpr int PX = Opnd<T>::PX, PL = kPlanes<T, PAIR>, V = 16 / (int)sizeof(T), PR = COLS / V;
   static constexpr int all = 16 * NW * PR, n = (all + 64 * HW - 1) / (64 * HW);
   uint4 q[n][PL];
@@ -307,7 +309,7 @@ template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
       const int kb = c / 32, a = c % 32 / 8, px = c % 8 / V;
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl)
-        q[i][pl] = *reinterpret_cast<const uint4*>(x + ((s * EX + from + kb) * PX * PL + pl + px) * kPiece + left_slot(a, l16, kb));
+        q[i][pl] = *reinterpret_cast<const uint4*>(x + (s * LEFT + from + kb * PX * PL + pl + px) * kPiece + left_slot(a, l16, kb));
     }
   }
   // To the first of `rows` rows at dst; planes `plane` elements apart.
@@ -324,7 +326,7 @@ template <typename T, int NW, int EX, int COLS, bool PAIR> struct LeftRows {
 
 enum class Chain { fwd, keep, ends, bwd, bwd_ends };
 
-// keep: for the backward, S and W are kept (PAIR: as pairs, else rounded) and O is not made.
+// keep: for the backward, S and R are kept (PAIR: as pairs, else rounded) and O is not made.
 // ends: neither; what a segment makes of a state of zeros (the first one of the initial state),
 // and, by rows of their own past P's, of a unit matrix without values.
 template <typename T, int N, int NW, Chain K, bool PAIR>
@@ -336,12 +338,13 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
   constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
+  constexpr int LEFT = EX * PE;                   // and of all that a state wave leaves
   // K is read in both phases where it is transposed on the way: two copies
   constexpr bool TR = sizeof(T) == 2;
   constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oT = oK + (TR ? 2 : 1) * kK, oG = oT + 6 * PS * kPiece;
   constexpr int QS = sizeof(T) == 2 ? NK : 1;     // 32-blocks of Q that a helper's corner takes
   constexpr int oV = oG + kPiece, oKt = oV + VB::bytes, oQ = oKt + (TR ? 0 : TP * kPiece);
-  constexpr int oX = oQ + (K == Chain::fwd ? HW * QS * PX * kPiece : 0), kX = ENDS ? 0 : NW * EX * PE * kPiece;
+  constexpr int oX = oQ + (K == Chain::fwd ? HW * QS * PX * kPiece : 0), kX = ENDS ? 0 : NW * LEFT * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;   // two copies of what the state waves leave
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       y[0] = y[1] = y[2] = y[3] = kZero4;
       mma_rows(t0, rf[0], y);
       mma_rows(t1, rf[1], y + 2);
-      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
+      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * LEFT * kPiece;
 #pragma unroll
       for (int kb = 0; kb < (ENDS ? 0 : NK); ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
@@ -417,6 +420,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
         if constexpr (!ENDS) put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
+        if (KEEP || (ENDS && a.back)) {           // R to W
+          float b[8];
+          row8(gt, cb, lane, b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= b[e];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= D[cb][e];
         rf[cb] = O::split(f);
@@ -550,13 +559,13 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
     if constexpr (KEEP) {
       const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
       const int64_t jh = jh0 + (int64_t)j * a.H;
+      LeftRows<T, NW, LEFT, N, PAIR> ls;
+      LeftRows<T, NW, LEFT, C, PAIR> lr;
       constexpr int PL = kPlanes<T, PAIR>;
-      LeftRows<T, NW, EX, N, PAIR> ls;
-      LeftRows<T, NW, EX, C, PAIR> lw;
       ls.load(x, 0, w, lane);
-      lw.load(x, NK, w, lane);
+      lr.load(x, NK * PE, w, lane);
       ls.store(static_cast<T*>(a.S0) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-      lw.store(static_cast<T*>(a.Wt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
+      lr.store(static_cast<T*>(a.Rt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
     } else if constexpr (K == Chain::fwd) {
       const int c = 16 * w + l16;
       T* out = static_cast<T*>(a.out) + ((int64_t)(t.start(j) + c) * a.H + h) * a.P + p0 + 8 * la;
@@ -597,7 +606,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
   }
 }
 
-// Backward: dS (before the update) and dR are kept for ssd_delta_local.hip (PAIR: as pairs).
+// Backward: dS (before the update; PAIR: as pairs) and dR (as pairs) are kept for ssd_delta_local.hip.
 // ENDS: neither; what a segment makes of a gradient of zeros (the last one of the final state's),
 // and, by rows past P's, of a unit matrix without outputs' gradients.
 template <typename T, int N, int NW, bool ENDS, bool PAIR>
@@ -606,14 +615,15 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   using O = Opnd<T>;
   using KR = Rows<T, N>;
   using VB = Block<T, NW>;
-  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX, EX = NK + 2;
-  constexpr int PE = PX * kPlanes<T, PAIR>;       // pieces of what is kept
+  constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX;
+  // pieces of an operand of dS and of dR as they are left, and of all that a state wave leaves
+  constexpr int ES = PX * kPlanes<T, PAIR>, ER = PX * kPlanes<T, PAIR>, LEFT = NK * ES + 2 * ER;
   // as above; Q, which is read transposed only, lies in rows or transposed
   constexpr bool TR = sizeof(T) == 2;
   constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oA = oK + (TR ? 2 : 1) * kK, oT = oA + 6 * PS * kPiece;
   constexpr int oG = oT + 6 * PS * kPiece, oV = oG + kPiece, oQt = oV + VB::bytes, oKt = oQt + TP * kPiece;
   constexpr int oX = oKt + (TR ? 0 : TP * kPiece);
-  constexpr int kX = ENDS ? 0 : NW * EX * PE * kPiece;
+  constexpr int kX = ENDS ? 0 : NW * LEFT * kPiece;
   constexpr bool DX = oX + 2 * kX <= kLdsBytes;
   __shared__ __attribute__((aligned(16))) char lds[oX + (DX ? 2 : 1) * kX];
 
@@ -694,14 +704,14 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
       y[0] = y[1] = y[2] = y[3] = kZero4;
       mma_rows(t0, rf[0], y);
       mma_rows(t1, rf[1], y);
-      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * EX * PE * kPiece;
+      char* x = lds + oX + ((DX && (j & 1) ? NW : 0) + wave) * LEFT * kPiece;
 #pragma unroll
-      for (int kb = 0; kb < (ENDS ? 0 : NK); ++kb) put_piece(x + kb * PE * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
+      for (int kb = 0; kb < (ENDS ? 0 : NK); ++kb) put_piece(x + kb * ES * kPiece, left_slot(la, l16, kb), keep<T, PAIR>(sf[kb]));
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        if constexpr (!ENDS) put_piece(x + (NK + cb) * PE * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
+        if constexpr (!ENDS) put_piece(x + (NK * ES + cb * ER) * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= -bE[cb][e];
         rf[cb] = O::split(f);
@@ -778,13 +788,12 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   auto finish = [&](int j) {
     const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
     const int64_t jh = jh0 + (int64_t)j * a.H;
-    constexpr int PL = kPlanes<T, PAIR>;
-    LeftRows<T, NW, EX, N, PAIR> ls;
-    LeftRows<T, NW, EX, C, PAIR> lr;
+    LeftRows<T, NW, LEFT, N, PAIR> ls;
+    LeftRows<T, NW, LEFT, C, PAIR> lr;
     ls.load(x, 0, w, lane);
-    lr.load(x, NK, w, lane);
-    ls.store(static_cast<T*>(a.dS) + (jh * PL * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-    lr.store(static_cast<T*>(a.dRt) + (jh * PL * a.P + p0) * C, a.P * C, rows, w, lane);
+    lr.load(x, NK * ES, w, lane);
+    ls.store(static_cast<T*>(a.dS) + (jh * kPlanes<T, PAIR> * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
+    lr.store(static_cast<T*>(a.dRt) + (jh * kPlanes<T, PAIR> * a.P + p0) * C, a.P * C, rows, w, lane);
   };
   if (t.chunks > 0) {
     fetch1(last);

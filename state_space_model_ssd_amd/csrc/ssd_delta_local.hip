@@ -1,11 +1,13 @@
 // The gated delta rule's backward inside each chunk, from what the two chains left
 // (ssd_delta_chain.hip): the state S entering the chunk, the gradient dS of the state
-// leaving it, the rows W and their gradient dR before T.  With L, A, D, E as there, and
+// leaving it, the rows R and the gradient dR of W = beta R.  With A, D, E as there, and
 //   P = tril(dO W^T) * D,   M = -tril(dR W^T, -1) * D   (the gradients of q k^T and, per beta, k k^T)
 // the gradients are
 //   dq = scale (E dO S + P K)
-//   X  = M K - E dR S,    dbeta = dR.v + k.X (rows of M * k k^T, and k.(E dR S)),    dv = beta dR
+//   X  = M K - E dR S,    dbeta = dR.R,    dv = beta dR
 //   dk = beta X + scale P^T Q + D_C W dS + (beta M)^T K
+// (dbeta is dR.v + k.X as well, but that adds what R is the sum of: where keys are alike, each
+// of up to 64 rows W brings its own rounding, and dbeta was off by 9.7e-3 for 2.3e-3, 2112 tokens.)
 // and that of the log decay of token i sums what crosses it:
 //   dg_i = sum over pairs c >= i > c' of (P scale q k^T + M beta k k^T)_cc'
 //        + sum_{c >= i} (scale E q.(dO S) - beta E k.(dR S))_c  + sum_{c < i} (k.(D_C W dS))_c
@@ -19,8 +21,8 @@
 // are sums over a lane's rows, and P and M go into the next product as they lie.  The first of
 // the two makes P and M of its tokens' rows, the second P^T and M^T (products of their own, not
 // exchanged over tokens); they swap these through LDS, and each has half of dq's and dk's
-// channels.  The axis of values is walked in slabs of 32, whose W, dR, S and dS lie in LDS with
-// the values as rows (read transposed) and whose dO as operands; the next slabs' loads are in
+// channels.  The axis of values is walked in slabs of 32, whose R, dR, S and dS lie in LDS with
+// the values as rows (read transposed) and whose dO as operands; beta joins R in the results; the next slabs' loads are in
 // flight meanwhile, also those of the next head.
 //
 // 2x4096 tokens, 32 heads in 16 groups of 128 x 128, bf16: 234 us for 700 MB (3 TB/s).  A head and
@@ -93,18 +95,18 @@ __device__ __forceinline__ float dot16(uint4 x, uint4 y, float) {
 template <typename T, int COLS, bool PAIR>
 __device__ __forceinline__ typename Kept<T, PAIR>::V kept_dealt(const T* t, int u, int lane) {
   using TT = Tile<T, COLS>;
-  if constexpr (PAIR) return {TT::dealt(t, u, lane), TT::dealt(t + TT::size, u, lane)};
+  if constexpr (kPlanes<T, PAIR> == 2) return {TT::dealt(t, u, lane), TT::dealt(t + TT::size, u, lane)};
   else return TT::dealt(t, u, lane);
 }
 template <typename T, int COLS, bool PAIR>
 __device__ __forceinline__ typename Kept<T, PAIR>::V kept_plain(const T* t, int c0, int lane) {
   using TT = Tile<T, COLS>;
-  if constexpr (PAIR) return {TT::plain(t, c0, lane), TT::plain(t + TT::size, c0, lane)};
+  if constexpr (kPlanes<T, PAIR> == 2) return {TT::plain(t, c0, lane), TT::plain(t + TT::size, c0, lane)};
   else return TT::plain(t, c0, lane);
 }
 template <typename T, bool PAIR>
 __device__ __forceinline__ void kept_get(const typename Kept<T, PAIR>::V& v, float (&f)[8]) {
-  if constexpr (PAIR) {
+  if constexpr (kPlanes<T, PAIR> == 2) {
     float lo[8];
     Opnd<T>::get(v.hi, f);
     Opnd<T>::get(v.lo, lo);
@@ -196,12 +198,11 @@ __device__ __forceinline__ V by_rows(V v, int lane) {
   return v;
 }
 
-// What a slab needs from memory.  The first waves' threads take W and their tokens' values, the
-// others dR and dO.
+// What a slab needs from memory.  The first waves' threads take R, the others dR.
 template <typename T, int N, int PL> struct Loads {
-  Slab<T, C, kLocalThreads / 2> wr[PL];
+  Slab<T, C, kLocalThreads / 2> r[PL];
   Slab<T, N, kLocalThreads> s[PL], d[PL];
-  Tokens<T, kSlab, kLocalThreads / 2> vo;         // v: eight values of row 16 wave + lane / 4
+  Tokens<T, kSlab, kLocalThreads> o;              // dO
 };
 
 __device__ __forceinline__ double buf_load_double(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   using X = typename O::X;
   using TC = Tile<T, C>;
   using TN = Tile<T, N>;
-  using TS = Tokens<T, kSlab, kLocalThreads / 2>;
+  using TS = Tokens<T, kSlab, kLocalThreads>;
   using TK = Tokens<T, N, kLocalThreads>;
   constexpr int NK = N / 32, NH = N / 32, PX = O::PX;   // NH: a wave's tiles of dq and dk
   using KV = typename Kept<T, PAIR>::V;
@@ -237,12 +238,12 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   constexpr int BUF = sizeof(T) == 2 && !PAIR ? 2 : 1;  // slabs in LDS
   // k and q of the chunk lie there too, where the slabs leave room
   constexpr bool KQ = sizeof(T) == 2 || N < 128;
-  __shared__ __attribute__((aligned(16))) T Ws[BUF][PL * TC::size], Rs[BUF][PL * TC::size];
+  __shared__ __attribute__((aligned(16))) T Rs[BUF][PL * TC::size], dRs[BUF][PL * TC::size];
   __shared__ __attribute__((aligned(16))) T Ss[BUF][PL * TN::size], Ds[BUF][PL * TN::size];
   __shared__ __attribute__((aligned(16))) char dOs[BUF][TS::bytes], swap[4 * 8 * PX * kPiece];
   __shared__ __attribute__((aligned(16))) char kqs[KQ ? 2 * TK::bytes : 16];
   __shared__ double Gs[C];
-  __shared__ float bs[C], left[2][C], mid[2][C], dbs[2][C], sdots[kLocalThreads / 64];
+  __shared__ float bs[C], left[2][C], mid[2][C], dbs[C], sdots[kLocalThreads / 64];
   const int2 jg = xcd_chunk_head(blockIdx.x, a.G);
   const int j = jg.x, g = jg.y, rep = a.H / a.G;
   if (j >= a.max_chunks) return;
@@ -281,19 +282,17 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int64_t at = (jh * PL + i) * a.P + p0;
-      q.wr[i].load(static_cast<const T*>(half ? a.dRt : a.Wt) + at * C, min(rows, kSlab), tid & (kLocalThreads / 2 - 1));
+      q.r[i].load(static_cast<const T*>(half ? a.dRt : a.Rt) + at * C, min(rows, kSlab), tid & (kLocalThreads / 2 - 1));
       q.s[i].load(static_cast<const T*>(a.S0) + at * N, min(rows, kSlab), tid);
       q.d[i].load(static_cast<const T*>(a.dS) + at * N, min(rows, kSlab), tid);
     }
-    const uint32_t vbytes = rows > 0 ? (uint32_t)(d.len - 1) * vrow + a.P * (uint32_t)sizeof(T) : 0;
-    const __amdgpu_buffer_rsrc_t r = buf_rsrc(static_cast<const T*>(half ? a.dout : a.v) + vo, vbytes);
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(static_cast<const T*>(a.dout) + vo, rows > 0 ? (uint32_t)(d.len - 1) * vrow + a.P * (uint32_t)sizeof(T) : 0);
     const uint32_t cols = a.P * (uint32_t)sizeof(T), col = p0 * (uint32_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < TS::n; ++i) {
-      const int at = i * (kLocalThreads / 2) + (tid & (kLocalThreads / 2 - 1));
-      const uint32_t b = col + (half ? at % TS::PR * 16 : 8 * (tid & 3) * (uint32_t)sizeof(T) + 16 * i);
-      const uint32_t tok = half ? at / TS::PR : 16 * w + (tid & 63) / 4;
-      q.vo.q[i] = buf_load16(r, b < cols ? tok * vrow + b : 0xffffff00u);
+      const int at = i * kLocalThreads + tid;
+      const uint32_t b = col + at % TS::PR * 16;
+      q.o.q[i] = buf_load16(r, at < TS::all && b < cols ? at / TS::PR * vrow + b : 0xffffff00u);
     }
   };
   // head h's decays
@@ -333,7 +332,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       Gs[tid] = Gt;
       bs[tid] = bt;
     }
-    const float be = gates[0], E = gates[1], Dc = gates[2], EC = gates[3], br = gates[4];
+    const float be = gates[0], E = gates[1], bD = be * gates[2], EC = gates[3], br = gates[4];
 
     f32x4 Px[4], Lx[4];                           // [c'][c] of P's and M's sources, or of their transposes
 #pragma unroll
@@ -341,52 +340,59 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     f32x4 yq[NH], yx[NH], yd[NH];
 #pragma unroll
     for (int i = 0; i < NH; ++i) yq[i] = yx[i] = yd[i] = kZero4;
-    float sdot = 0.f, rv = 0.f;
+    float sdot = 0.f, db = 0.f;
     auto slab = [&](Loads<T, N, PL>& q, int p0, int b) {
       if constexpr (BUF == 1) __syncthreads();    // the slab before is read
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
-        q.wr[i].store((half ? Rs : Ws)[b] + i * TC::size, tid & (kLocalThreads / 2 - 1));
+        q.r[i].store((half ? dRs : Rs)[b] + i * TC::size, tid & (kLocalThreads / 2 - 1));
         q.s[i].store(Ss[b] + i * TN::size, tid);
         q.d[i].store(Ds[b] + i * TN::size, tid);
       }
-      if (half) q.vo.store(dOs[b], tid & (kLocalThreads / 2 - 1));
+      q.o.store(dOs[b], tid);
 #pragma unroll
       for (int i = 0; i < Slab<T, N, kLocalThreads>::n; ++i) {
         sdot += dot16(q.s[0].q[i], q.d[0].q[i], T{});
         if constexpr (PL == 2) sdot += dot16(q.s[0].q[i], q.d[1].q[i], T{}) + dot16(q.s[1].q[i], q.d[0].q[i], T{});
       }
       __syncthreads();
-      const KV wo = kept_plain<T, C, PAIR>(Ws[b], 16 * w, lane), ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane);
+      const KV ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane), go = kept_plain<T, C, PAIR>(dRs[b], 16 * w, lane);
       const X od = TS::token(dOs[b], 0, c, lane);
       if (half == 0) {
-        // dR in the order of rows, four lanes each, as v comes and dv goes: one lane a row would
-        // issue four times slower
-        float r8[8], v8[8];
-        kept_get<T, PAIR>(by_rows(ro, lane), r8);
-        O::get(opnd_of(q.vo.q, T{}), v8);
+        float r8[8], g8[8];
+        kept_get<T, PAIR>(ro, r8);
+        kept_get<T, PAIR>(go, g8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          rv += r8[e] * v8[e];
-          r8[e] *= br;
-        }
+        for (int e = 0; e < 8; ++e) db += r8[e] * g8[e];
+        // dR in the order of rows, four lanes each, as dv goes: one lane a row would issue four
+        // times slower
+        kept_get<T, PAIR>(by_rows(go, lane), g8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g8[e] *= br;
         const int at = p0 + 8 * (lane & 3), tok = 16 * w + lane / 4;
-        if (at < a.P && tok < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)tok * a.H * a.P + at, O::round(r8));
+        if (at < a.P && tok < d.len) store_opnd(static_cast<T*>(a.dv) + vo + (int64_t)tok * a.H * a.P + at, O::round(g8));
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         if (half ? cb < w / 2 : cb > w / 2) continue;   // no pairs there
-        X f[2];
-        KV r[2];
+        if (half) {
+          X f[2];
+          KV r[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (half) f[t] = TS::dealt(dOs[b], 0, 2 * cb + t, lane);
-          r[t] = kept_dealt<T, C, PAIR>(half ? Rs[b] : Ws[b], 2 * cb + t, lane);
+          for (int t = 0; t < 2; ++t) {
+            f[t] = TS::dealt(dOs[b], 0, 2 * cb + t, lane);
+            r[t] = kept_dealt<T, C, PAIR>(dRs[b], 2 * cb + t, lane);
+          }
+          mma_rows(f, ro, Px + 2 * cb);
+          mma_rows(r, ro, Lx + 2 * cb);
+        } else {
+          KV r[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) r[t] = kept_dealt<T, C, PAIR>(Rs[b], 2 * cb + t, lane);
+          mma_rows(r, od, Px + 2 * cb);
+          mma_rows(r, go, Lx + 2 * cb);
         }
-        if (half) mma_rows(f, wo, Px + 2 * cb);
-        else mma_rows(r, od, Px + 2 * cb);
-        mma_rows(r, half ? wo : ro, Lx + 2 * cb);
       }
       fetch(q, h, p0 + AHEAD * kSlab, tid);
       __builtin_amdgcn_sched_barrier(0);
@@ -395,11 +401,11 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
 #pragma unroll
         for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ss[b], half * NH + i, lane);
         mma_rows(f, od, yq);
-        mma_rows(f, ro, yx);
+        mma_rows(f, go, yx);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NH; ++i) f[i] = kept_dealt<T, N, PAIR>(Ds[b], half * NH + i, lane);
-        mma_rows(f, wo, yd);
+        mma_rows(f, ro, yd);
       }
     };
     for (int p0 = 0; p0 < a.P; p0 += AHEAD * kSlab) {
@@ -416,7 +422,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     }
     // P and M, or their transposes, and their part of the pairs' sums.  A pair's term is the same
     // number as row and as column, so that what crosses no token cancels.
-    float pairs = 0.f, mk = 0.f;                  // mk: k's reader's sum of M k k^T
+    float pairs = 0.f;
     {
       char* x = swap + (w * 8 + half * 4) * PX * kPiece;
 #pragma unroll
@@ -442,12 +448,11 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
           for (int r = 0; r < 4; ++r) {
             const int e = 4 * t + r, o = 32 * cb + 8 * la + e;
             const int hi = half ? o : c, lo = half ? c : o;       // the pair's later and earlier token
-            const float D = fexp<T>((float)(Gs[hi] - Gs[lo]));    // of use where lo <= hi
+            const float bo = bs[o], D = (half ? be : bo) * fexp<T>((float)(Gs[hi] - Gs[lo]));    // of use where lo <= hi
             const float p = lo <= hi ? Px[u][r] * D * a.scale : 0.f;
-            const float m = lo < hi ? -Lx[u][r] * D : 0.f, mb = m * (half ? bs[o] : be);
+            const float m = lo < hi ? -Lx[u][r] * D : 0.f, mb = m * (half ? bo : be);
             const float term = lo < hi ? p * qk[r] + mb * kk[r] : 0.f;
             pairs += half ? term : -term;
-            if (!half) mk += m * kk[r];
             p8[e] = p;
             m8[e] = half ? mb : m;
           }
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      f32x4 q = yq[i] * (a.scale * E), x = yx[i] * -E, k = yd[i] * Dc;
+      f32x4 q = yq[i] * (a.scale * E), x = yx[i] * -E, k = yd[i] * bD;
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
         X kf, qf;
@@ -515,18 +520,14 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       dk[i] += k + x * be;
       if (i % 2) __builtin_amdgcn_sched_barrier(0);
     }
-    // a row's sum of dR v from its four lanes to its column's
-    rv += __shfl_xor(rv, 1);
-    rv += __shfl_xor(rv, 2);
-    const float rc = __shfl(rv, 4 * l16);
-    const float db = column_sum((la == 0 ? rc : 0.f) + mk - E * kx);
-    const float lf = column_sum(a.scale * E * ql - be * E * kx), md = column_sum(Dc * kd + pairs);
+    db = column_sum(db);
+    const float lf = column_sum(a.scale * E * ql - be * E * kx), md = column_sum(bD * kd + pairs);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sdot += __shfl_xor(sdot, off);
     if (la == 0) {
       left[half][c] = lf;
       mid[half][c] = md;
-      dbs[half][c] = db;
+      if (half == 0) dbs[c] = db;
     }
     if (lane == 0) sdots[wave] = sdot;
     __syncthreads();
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
       if (lane < d.len) {
         const int64_t at = (int64_t)(d.start + lane) * a.H + h;
         store_gate(a.dg, a.gate_bf16, at, (float)(s + (b - own) + EC * sd));
-        store_gate(a.dbeta, a.gate_bf16, at, dbs[0][lane] + dbs[1][lane]);
+        store_gate(a.dbeta, a.gate_bf16, at, dbs[lane]);
       }
     }
   }

@@ -2,7 +2,10 @@
 // head, with G_i the running sum of the chunk's log decays, D_ij = exp(G_i - G_j) for
 // j <= i, E_i = exp(G_i),
 //   L_ij = beta_i D_ij k_i.k_j  (j < i),   T = (1 + L)^-1,   A_ij = scale D_ij q_i.k_j  (j <= i)
-// so that the rows w (ssd_delta_chain.hip) are W = (T beta) (V - E K S^T).
+// so that the rows w (ssd_delta_chain.hip) are W = (T beta) (V - E K S^T).  For the backward, T^T
+// and, with L = beta B,
+//   T' = (1 + B beta)^-1 = 1 - B T beta,
+// so that W = beta R, R = T' (V - E K S^T): what beta is multiplied with, also where it is 0.
 //
 // G is summed in fp64: its differences are what counts, and a chunk's sum may be large
 // beside them.  T is inverted in fp32: the four 16x16 blocks of the diagonal by
@@ -108,7 +111,7 @@ __device__ __forceinline__ constexpr int tri(int i, int j) { return i * (i + 1) 
 
 // BL: blocks of 16 tokens that a chunk has at most.
 template <typename T, int N, bool BWD, int BL>
-__global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm, int nh) {
+__global__ __launch_bounds__(64 * kPrepWaves, BWD ? 2 : 1) void delta_prep_kernel(const DeltaArgs a, const ChunkMap cm, int nh) {
   using O = Opnd<T>;
   using X = typename O::X;
   constexpr int V = 16 / (int)sizeof(T), XP = N + V, NK = N / 32, TP = N / 16 * 2;
@@ -214,8 +217,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       }
       wave_sync();
     }
-    // L as first operands, the diagonal's blocks to LDS; A (or its transpose)
+    // L as first operands (backward: B), the diagonal's blocks to LDS; A (or its transpose)
     f32x4 L[10];
+    float bi[4];
     if constexpr (BL < 4) {
 #pragma unroll
       for (int x = 0; x < 6; ++x) {
@@ -227,7 +231,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
     for (int i = 0; i < BL; ++i) {
       const int c = 16 * i + l16;
       const double Gc = Gs[c];
-      const float bc = bs[c];
+      const float bc = bi[i] = bs[c];
 #pragma unroll
       for (int x = 0; x <= i; ++x) {
         f32x4 f;
@@ -235,10 +239,10 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
         for (int r = 0; r < 4; ++r) {
           const int o = 16 * x + 4 * la + r;
           const float D = fexp<T>((float)(Gc - Gs[o]));
-          L[tri(i, x)][r] = o < c ? bc * D * kk[tri(i, x)][r] : 0.f;
+          L[tri(i, x)][r] = o < c ? (BWD ? 1.f : bc) * D * kk[tri(i, x)][r] : 0.f;
           if constexpr (!BWD) f[r] = o <= c ? a.scale * D * qk[tri(i, x)][r] : 0.f;
         }
-        if (x == i) *reinterpret_cast<f32x4*>(&Ts[(16 * i + l16) * LP + 16 * i + 4 * la]) = L[tri(i, i)];
+        if (x == i) *reinterpret_cast<f32x4*>(&Ts[(16 * i + l16) * LP + 16 * i + 4 * la]) = BWD ? bc * L[tri(i, i)] : L[tri(i, i)];
         if constexpr (!BWD) {
           // four of the eight values of a lane
           const uint32_t at = 16u * (16 * (2 * (x & 1) + (la >> 1)) + l16);
@@ -314,7 +318,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
           for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < BL - n; ++c)
-              s[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(L[tri(c + n, c + k)][r], blk[tri(c + k, c)][r], s[c], 0, 0, 0);
+              s[c] = __builtin_amdgcn_mfma_f32_16x16x4f32((BWD ? bi[c + n] : 1.f) * L[tri(c + n, c + k)][r], blk[tri(c + k, c)][r], s[c], 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -330,20 +334,8 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
       }
     }
     wave_sync();
-    // T, its columns times beta; for the backward T's transpose, without
-#pragma unroll
-    for (int x = 0; x < 6; ++x) {
-      const int2 t = lower_tile(x);
-      const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
-      float f[8] = {};
-      if (32 * (t.x / 2) < 16 * BL) {
-        block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? f[e] * bs[c0 + e] : 0.f;
-      }
-      put_piece(static_cast<char*>(a.T) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
-    }
     if constexpr (BWD) {
+      // T's transpose; then T' where T was, a column of blocks at a time
 #pragma unroll
       for (int x = 0; x < 6; ++x) {
         const int2 t = upper_tile(x);
@@ -355,6 +347,44 @@ __global__ __launch_bounds__(64 * kPrepWaves) void delta_prep_kernel(const Delta
         for (int e = 0; e < 8; ++e) f[e] = c0 + e >= r ? f[e] : 0.f;
         put_piece(static_cast<char*>(a.Tt) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
       }
+      wave_sync();
+#pragma unroll
+      for (int c = 0; c < BL; ++c) {
+        f32x4 t[4], o[4];                         // T's blocks as second operands
+#pragma unroll
+        for (int k = c; k < BL; ++k) {
+          o[k] = kZero4;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) t[k][r] = Ts[(16 * k + 4 * la + r) * LP + 16 * c + l16];
+        }
+#pragma unroll
+        for (int k = c; k < BL; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = k; i < BL; ++i)
+              o[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(L[tri(i, k)][r], t[k][r], o[i], 0, 0, 0);
+#pragma unroll
+        for (int i = c; i < BL; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            Ts[(16 * i + 4 * la + r) * LP + 16 * c + l16] = i == c && 4 * la + r == l16 ? 1.f : -bi[c] * o[i][r];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wave_sync();
+    }
+    // T, its columns times beta, or T'
+#pragma unroll
+    for (int x = 0; x < 6; ++x) {
+      const int2 t = lower_tile(x);
+      const int r = tile_row(t.x, l16), c0 = 32 * t.y + 8 * la;
+      float f[8] = {};
+      if (32 * (t.x / 2) < 16 * BL) {
+        block8(*reinterpret_cast<const f32x4*>(&Ts[r * LP + c0]), *reinterpret_cast<const f32x4*>(&Ts[r * LP + c0 + 4]), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c0 + e <= r ? (BWD ? f[e] : f[e] * bs[c0 + e]) : 0.f;
+      }
+      put_piece(static_cast<char*>(a.T) + (jh * 6 + x) * O::PS * kPiece, slot, O::split(f));
     }
   }
 }
