@@ -714,10 +714,15 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
  * dinitial_states like initial_states (nullable: not computed, also given without an
  * initial state); dfinal_states nullable: 0.  dq and dk sum over the heads of a group.
  * The forward's states are computed again.  The gradient of the state is carried as the
- * state is; with bf16 inputs the other products round their operands to bf16 once.  dg and
- * dbeta in fp32 are of fp32's kind (1e-5 relative in the 2-norm): what they are summed from
- * is then kept to 2^-17.  In bf16 they are rounded at the end only while tokens * nheads is
- * below 65536, and summed from operands rounded to bf16 (some 3e-3) above.
+ * state is; with bf16 inputs the other products round their operands to bf16 once.
+ * dbeta[t] is w's gradient times w / beta, and dg[t] the sum of the decayed state times its
+ * gradient.  fp32 gates' are summed from values kept to 2^-17: relative to the 2-norm of the
+ * products that are summed, 1e-5 as a rule.  bf16 gates' are too while tokens * nheads is below
+ * 65536.  Above, the state, its gradient and w / beta are rounded to bf16 once before: dbeta is
+ * off by 2.4e-3 in the 2-norm, and dg by up to 2^-8 of that of its products, 2.5e-3 to 3.3e-3
+ * of dg as a rule.  Where dg is small beside its products it is off by more of its own size (beta
+ * 1 and keys 0.02 apart: 1e-2; beta 1, equal keys and no decay: dg is zero but for this error);
+ * fp32 gates are for callers to whom that matters.
  * Workspace: ssd_delta_bwd_workspace_size bytes, as for the forward.
  */
 size_t ssd_delta_bwd_workspace_size(const ssd_delta_problem_t* p);

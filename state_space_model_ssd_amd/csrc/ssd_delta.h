@@ -106,7 +106,7 @@ struct DeltaArgs {
   int max_chunks, nc_row;
   bool bf16, gate_bf16;
   bool back;              // the backward's launches
-  bool pairs;             // backward: what the chains keep is kept as pairs (bf16)
+  bool pairs;             // backward: S, dS and R are kept as pairs (bf16), as dR always is
   float scale;
   const void* q;
   const void* k;
@@ -139,10 +139,10 @@ struct DeltaArgs {
   void* At;               // A transposed, upper, pairs
   void* qt;               // per (chunk, group), fp32: q transposed
   void* S0;               // [P][N] the state entering the chunk, dtype (two with pairs: high
-                          // and low parts; so the next three)
+                          // and low parts; so the next two)
   void* dS;               // [P][N] the gradient of the state leaving it
   void* Rt;               // [P][64] the rows r, transposed
-  void* dRt;              // [P][64] the gradient of the rows w, transposed
+  void* dRt;              // [P][64] the gradient of the rows w, transposed, fp32 or pairs
   DeltaSplit split;
 
   ChunkMap cmap() const {

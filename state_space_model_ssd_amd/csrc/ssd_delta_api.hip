@@ -16,11 +16,16 @@ namespace {
 
 constexpr size_t kDeltaAlign = 256;
 
-// Backward, bf16: what the chains keep is kept as pairs where the gates' gradients are wanted in
-// fp32, and where there are few of them.  Each is a sum with cancellation of products of what is
-// kept, rounded to 2^-8: over many their errors average (2.6e-3 in the 2-norm), a handful may be
-// off by several times that.
-// Pairs cost time: 2x4096 tokens, 32 heads of 128 x 128, 730 us for 551.
+// Backward, bf16: S, dS and R are kept as pairs where the gates' gradients are wanted in fp32, and
+// where there are few of them, else rounded to bf16.  A gate's gradient is a sum with cancellation
+// of products of these, so single ones are off by more than many are together: dg of random keys
+// without decay, rounded, is off by up to 5.5e-3 in the 2-norm over 64 gates, 3.8e-3 over 4096 and
+// 3.2e-3 over 65536 (with pairs 2.4e-3 and 1.7e-3, the result's own rounding).  Pairs cost little
+// while there are few, and a fifth where there are many: 1x1024 tokens, 32 heads of 128 x 128, 118
+// -> 130 us; 1x2048 203 -> 230; 2x2048 295 -> 368; 2x4096 582 -> 711.
+// dR is kept as pairs always: where keys are alike and beta is 1, dg is the small difference of
+// <dS, S> and dv.v, and was off by 2.4e-2 with dR rounded (keys 0.02 apart) for 1.0e-2; 547 -> 582
+// us at 2x4096 tokens.
 constexpr int64_t kDeltaFewGates = 65536;
 
 constexpr int kDeltaLeast = 16;          // chunks of the shortest segments of a sequence
@@ -137,7 +142,7 @@ size_t delta_layout(DeltaArgs& a, bool packed, bool bwd, void* base) {
   part(a.S0, mh * a.P * a.N * ke);
   part(a.dS, mh * a.P * a.N * ke);
   part(a.Rt, mh * a.P * C * ke);
-  part(a.dRt, mh * a.P * C * ke);
+  part(a.dRt, mh * a.P * C * 4);
   return off;
 }
 

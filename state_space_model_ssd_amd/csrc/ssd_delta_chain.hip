@@ -617,7 +617,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
   using VB = Block<T, NW>;
   constexpr int NK = N / 32, NT = N / 16, PX = O::PX, PS = O::PS, TP = NT * 2 * PX;
   // pieces of an operand of dS and of dR as they are left, and of all that a state wave leaves
-  constexpr int ES = PX * kPlanes<T, PAIR>, ER = PX * kPlanes<T, PAIR>, LEFT = NK * ES + 2 * ER;
+  constexpr int ES = PX * kPlanes<T, PAIR>, ER = PX * kPlanes<T, true>, LEFT = NK * ES + 2 * ER;
   // as above; Q, which is read transposed only, lies in rows or transposed
   constexpr bool TR = sizeof(T) == 2;
   constexpr int kK = 4 * NK * PX * kPiece, oK = 0, oA = oK + (TR ? 2 : 1) * kK, oT = oA + 6 * PS * kPiece;
@@ -711,7 +711,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
       for (int cb = 0; cb < 2; ++cb) {
         float f[8];
         block8(y[2 * cb], y[2 * cb + 1], f);
-        if constexpr (!ENDS) put_piece(x + (NK * ES + cb * ER) * kPiece, left_slot(la, l16, cb), keep<T, PAIR>(f));
+        if constexpr (!ENDS) put_piece(x + (NK * ES + cb * ER) * kPiece, left_slot(la, l16, cb), keep<T, true>(f));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= -bE[cb][e];
         rf[cb] = O::split(f);
@@ -789,11 +789,11 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_bwd_kernel(const D
     const char* x = lds + oX + (DX && (j & 1) ? kX : 0);
     const int64_t jh = jh0 + (int64_t)j * a.H;
     LeftRows<T, NW, LEFT, N, PAIR> ls;
-    LeftRows<T, NW, LEFT, C, PAIR> lr;
+    LeftRows<T, NW, LEFT, C, true> lr;
     ls.load(x, 0, w, lane);
     lr.load(x, NK * ES, w, lane);
     ls.store(static_cast<T*>(a.dS) + (jh * kPlanes<T, PAIR> * a.P + p0) * N, (int64_t)a.P * N, rows, w, lane);
-    lr.store(static_cast<T*>(a.dRt) + (jh * kPlanes<T, PAIR> * a.P + p0) * C, a.P * C, rows, w, lane);
+    lr.store(static_cast<T*>(a.dRt) + (jh * kPlanes<T, true> * a.P + p0) * C, a.P * C, rows, w, lane);
   };
   if (t.chunks > 0) {
     fetch1(last);

@@ -200,7 +200,7 @@ __device__ __forceinline__ V by_rows(V v, int lane) {
 
 // What a slab needs from memory.  The first waves' threads take R, the others dR.
 template <typename T, int N, int PL> struct Loads {
-  Slab<T, C, kLocalThreads / 2> r[PL];
+  Slab<T, C, kLocalThreads / 2> r[kPlanes<T, true>];
   Slab<T, N, kLocalThreads> s[PL], d[PL];
   Tokens<T, kSlab, kLocalThreads> o;              // dO
 };
@@ -223,7 +223,7 @@ __device__ __forceinline__ f32x4 channels4(const typename Opnd<T>::X& x, bool se
   return second ? hi : lo;
 }
 
-// PAIR: what the chains kept comes as pairs.
+// dR comes as pairs; PAIR: S, dS and R too.
 template <typename T, int N, bool PAIR>
 __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const DeltaArgs a, const ChunkMap cm) {
   using O = Opnd<T>;
@@ -234,11 +234,12 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
   using TK = Tokens<T, N, kLocalThreads>;
   constexpr int NK = N / 32, NH = N / 32, PX = O::PX;   // NH: a wave's tiles of dq and dk
   using KV = typename Kept<T, PAIR>::V;
-  constexpr int PL = kPlanes<T, PAIR>;
+  using KG = typename Kept<T, true>::V;           // of dR
+  constexpr int PL = kPlanes<T, PAIR>, PG = kPlanes<T, true>;
   constexpr int BUF = sizeof(T) == 2 && !PAIR ? 2 : 1;  // slabs in LDS
   // k and q of the chunk lie there too, where the slabs leave room
   constexpr bool KQ = sizeof(T) == 2 || N < 128;
-  __shared__ __attribute__((aligned(16))) T Rs[BUF][PL * TC::size], dRs[BUF][PL * TC::size];
+  __shared__ __attribute__((aligned(16))) T Rs[BUF][PL * TC::size], dRs[BUF][PG * TC::size];
   __shared__ __attribute__((aligned(16))) T Ss[BUF][PL * TN::size], Ds[BUF][PL * TN::size];
   __shared__ __attribute__((aligned(16))) char dOs[BUF][TS::bytes], swap[4 * 8 * PX * kPiece];
   __shared__ __attribute__((aligned(16))) char kqs[KQ ? 2 * TK::bytes : 16];
@@ -280,9 +281,12 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     const int rows = h < (g + 1) * rep ? a.P - p0 : 0;
     const int64_t jh = (int64_t)j * a.H + h, vo = ((int64_t)d.start * a.H + h) * a.P;
 #pragma unroll
+    for (int i = 0; i < PG; ++i)                  // a resource of no bytes where R has no low part
+      q.r[i].load(static_cast<const T*>(half ? a.dRt : a.Rt) + ((jh * (half ? PG : PL) + i) * a.P + p0) * C,
+                  half || i < PL ? min(rows, kSlab) : 0, tid & (kLocalThreads / 2 - 1));
+#pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int64_t at = (jh * PL + i) * a.P + p0;
-      q.r[i].load(static_cast<const T*>(half ? a.dRt : a.Rt) + at * C, min(rows, kSlab), tid & (kLocalThreads / 2 - 1));
       q.s[i].load(static_cast<const T*>(a.S0) + at * N, min(rows, kSlab), tid);
       q.d[i].load(static_cast<const T*>(a.dS) + at * N, min(rows, kSlab), tid);
     }
@@ -344,8 +348,10 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
     auto slab = [&](Loads<T, N, PL>& q, int p0, int b) {
       if constexpr (BUF == 1) __syncthreads();    // the slab before is read
 #pragma unroll
+      for (int i = 0; i < PG; ++i)
+        if (half || i < PL) q.r[i].store((half ? dRs[b] : Rs[b]) + i * TC::size, tid & (kLocalThreads / 2 - 1));
+#pragma unroll
       for (int i = 0; i < PL; ++i) {
-        q.r[i].store((half ? dRs : Rs)[b] + i * TC::size, tid & (kLocalThreads / 2 - 1));
         q.s[i].store(Ss[b] + i * TN::size, tid);
         q.d[i].store(Ds[b] + i * TN::size, tid);
       }
@@ -356,17 +362,18 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         if constexpr (PL == 2) sdot += dot16(q.s[0].q[i], q.d[1].q[i], T{}) + dot16(q.s[1].q[i], q.d[0].q[i], T{});
       }
       __syncthreads();
-      const KV ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane), go = kept_plain<T, C, PAIR>(dRs[b], 16 * w, lane);
+      const KV ro = kept_plain<T, C, PAIR>(Rs[b], 16 * w, lane);
+      const KG go = kept_plain<T, C, true>(dRs[b], 16 * w, lane);
       const X od = TS::token(dOs[b], 0, c, lane);
       if (half == 0) {
         float r8[8], g8[8];
         kept_get<T, PAIR>(ro, r8);
-        kept_get<T, PAIR>(go, g8);
+        kept_get<T, true>(go, g8);
 #pragma unroll
         for (int e = 0; e < 8; ++e) db += r8[e] * g8[e];
         // dR in the order of rows, four lanes each, as dv goes: one lane a row would issue four
         // times slower
-        kept_get<T, PAIR>(by_rows(go, lane), g8);
+        kept_get<T, true>(by_rows(go, lane), g8);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g8[e] *= br;
         const int at = p0 + 8 * (lane & 3), tok = 16 * w + lane / 4;
@@ -378,11 +385,11 @@ __global__ __launch_bounds__(kLocalThreads) void delta_local_bwd_kernel(const De
         if (half ? cb < w / 2 : cb > w / 2) continue;   // no pairs there
         if (half) {
           X f[2];
-          KV r[2];
+          KG r[2];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             f[t] = TS::dealt(dOs[b], 0, 2 * cb + t, lane);
-            r[t] = kept_dealt<T, C, PAIR>(dRs[b], 2 * cb + t, lane);
+            r[t] = kept_dealt<T, C, true>(dRs[b], 2 * cb + t, lane);
           }
           mma_rows(f, ro, Px + 2 * cb);
           mma_rows(r, ro, Lx + 2 * cb);
