@@ -87,6 +87,16 @@ struct ChunkMap {
   }
 };
 
+// Orders a wave's accesses to its LDS: what other lanes wrote before is read after.  The barrier
+// alone keeps the wave together but says nothing of memory, and the compiler, which sees one
+// lane's addresses, might move a load past another lane's store; the fences forbid that.  The
+// hardware runs a wave's LDS accesses in order, so they cost no instruction.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------
 // Element types.
 // ---------------------------------------------------------------------------

@@ -515,7 +515,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       char* q = lds + oQ + w * QS * PX * kPiece;
 #pragma unroll
       for (int k0 = 0; k0 < NK; k0 += QS) {
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
 #pragma unroll
         for (int kb = 0; kb < QS; ++kb)
 #pragma unroll
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
             const int e = (4 * i + lane % 4) * 16 / (int)sizeof(T), px = e % 8 * (int)sizeof(T) / 16;
             *reinterpret_cast<uint4*>(q + (kb * PX + px) * kPiece + KR::slot(e / 8, lane / 4, 0)) = cQ[(k0 + kb) * PX + i];
           }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
 #pragma unroll
         for (int kb = 0; kb < QS; ++kb) qf[k0 + kb] = piece_x(q + kb * PX * kPiece, KR::slot(la, l16, 0), T{});
       }

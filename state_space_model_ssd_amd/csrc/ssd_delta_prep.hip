@@ -84,13 +84,6 @@ __device__ __forceinline__ void put_half_pair(char* p, uint32_t slot, int half, 
   }
 }
 
-// Orders a wave's accesses to its LDS: what other lanes wrote before is read after.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // The first ROWS [N] rows of a chunk to LDS, `pitch` elements apart; zeros past its end.  `then`: what
 // is loaded behind them, before they are waited for.
 template <typename T, int N, int ROWS, typename F>

@@ -107,16 +107,16 @@ template <int V, Pairs M, bool BACK> struct Turns {
         f[e + 1] = y * c[e + 1] + x * s[e + 1];
       }
     } else if constexpr (M == Pairs::lds) {
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
 #pragma unroll
       for (int e = 0; e < V; ++e) row[n + e] = f[e];
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const int i = n + e;
         if (i < 2 * a.R) f[e] = f[e] * c[e] + row[a.interleaved ? i ^ 1 : i < a.R ? i + a.R : i - a.R] * s[e];
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
   }
 };
