@@ -10,6 +10,7 @@
 // with delta = 0 for l >= len (the running sum stays flat there).
 #include "ssd_device.h"
 #include "ssd_kernels.h"
+#include "ssd_plan_rule.h"
 
 namespace ssd {
 
@@ -42,7 +43,7 @@ __device__ int2 seq_bounds(int s, const int32_t* cu, const int32_t* sidx, int to
   return make_int2(st, en);
 }
 
-// One workgroup: chunk counts per sequence and their exclusive prefix sum.
+// One workgroup: chunk counts per sequence and their exclusive prefix sum, max_chunks at most.
 __global__ __launch_bounds__(kPlanThreads) void plan_seq_kernel(
     const int32_t* __restrict__ cu, const int32_t* __restrict__ sidx, int nstates, int total,
     int L, int max_chunks, int* __restrict__ seq_chunks) {
@@ -54,27 +55,27 @@ __global__ __launch_bounds__(kPlanThreads) void plan_seq_kernel(
     int cnt = 0;
     if (s < nstates) {
       int2 b = seq_bounds(s, cu, sidx, total);
-      cnt = (b.y - b.x + L - 1) / L;
+      cnt = min((b.y - b.x + L - 1) / L, max_chunks);
     }
     int v = cnt;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
       int t = __shfl_up(v, off);
-      if (lane >= off) v += t;
+      if (lane >= off) v = add_chunks(v, t, max_chunks);
     }
+    const int own = __shfl_up(v, 1);      // of the wave's sequences before this one
     if (lane == kWave - 1) wave_tot[wv] = v;
     __syncthreads();
-    int before = 0, all = 0;
+    int before = carry;
 #pragma unroll
     for (int w = 0; w < kPlanThreads / kWave; ++w) {
-      before += (w < wv) ? wave_tot[w] : 0;
-      all += wave_tot[w];
+      if (w < wv) before = add_chunks(before, wave_tot[w], max_chunks);
+      carry = add_chunks(carry, wave_tot[w], max_chunks);
     }
-    if (s < nstates) seq_chunks[s] = min(carry + before + v - cnt, max_chunks);
-    carry = min(carry + all, max_chunks);   // malformed lengths may add up past 32 bits
+    if (s < nstates) seq_chunks[s] = lane == 0 ? before : add_chunks(before, own, max_chunks);
     __syncthreads();
   }
-  if (tid == 0) seq_chunks[nstates] = min(carry, max_chunks);
+  if (tid == 0) seq_chunks[nstates] = carry;
 }
 
 // One thread per table slot: which sequence owns slot j, and where it starts.
