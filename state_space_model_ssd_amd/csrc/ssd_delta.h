@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "ssd_common.h"
+#include "ssd_delta_cut.h"
 
 namespace ssd {
 
@@ -17,16 +18,10 @@ constexpr int kPiece = 1024;                 // bytes of 64 lanes' 16: operands 
 __host__ __device__ constexpr int triangle_pieces(bool b16, bool pair) { return b16 && !pair ? 6 : 12; }
 __host__ __device__ constexpr int transposed_pieces(int N) { return N / 16 * 2 * 2; }
 
-// How long sequences are cut where they would keep few CUs busy for long: the chain of a sequence
-// is one chunk after another, but its segments' chains run side by side, once each for what the
-// segment makes of a state of zeros and of a unit matrix, and once more from the states that
-// follow from these (ssd_delta_chain.hip).
-struct DeltaSplit {
-  static constexpr int kLengths = 6;     // segments of least, 2 least, 4 least, .. chunks
+// Cut sequences' slots: DeltaCut's rule, and where segments' states lie.
+struct DeltaSplit : DeltaCut {
   static constexpr int kSequences = 64;  // most of a packed batch
-  static constexpr int kOverhead = 6;    // what the additional launches take, in chunks' steps
   int slots;              // for segments of all sequences; 0: nothing is cut
-  int least;              // chunks of the shortest segments
   int per_row;            // slots of a row (equal rows)
   int fixed;              // the length: the host's (equal rows)
   int block;              // rows of a state that a workgroup has
@@ -34,52 +29,6 @@ struct DeltaSplit {
   float* ends;            // [slots][H][P + N][N] of zeros, and of a unit matrix
   float* starts;          // [slots][H][P][N] the states that segments start from
 
-  // Segments of `per` chunks, at most `length`, for a sequence of n.
-  __host__ __device__ __forceinline__ static void cut(int n, int length, int& parts, int& per) {
-    parts = 1;
-    per = n;
-    if (length <= 0 || n < 2 * length) return;
-    parts = (n + length - 1) / length;
-    per = (n + parts - 1) / parts;
-    parts = (n + per - 1) / per;
-  }
-  // Chunks that the first passes have over all sequences, of first segments and of later ones;
-  // the longest sequence.
-  struct Sums {
-    int first[kLengths], later[kLengths], longest;
-    __host__ __device__ __forceinline__ void add(const DeltaSplit& s, int n, int times) {
-      longest = n > longest ? n : longest;
-#pragma unroll
-      for (int i = 0; i < kLengths; ++i) {
-        int parts, per;
-        cut(n, s.least << i, parts, per);
-        if (parts < 2) continue;
-        first[i] += per * times;
-        later[i] += per * (parts - 2) * times;
-      }
-    }
-  };
-  // The length of the least estimated time, in steps of a chunk, or 0 where cutting gains nothing:
-  // each pass takes as long as its longest chain or as all its chains over the CUs; the states in
-  // between, a step each.  `block`: a workgroup's rows of a state.  (Products below 2^31: at most
-  // 2^22 chunks and heads, and 64 workgroups of a sequence.)
-  __host__ __device__ __forceinline__ static int best(const DeltaSplit& s, const Sums& v, int chunks, int H, int P,
-                                                      int N, int block, int cus) {
-    const int rows = (P + block - 1) / block * H, unit = (N + block - 1) / block * H, all = chunks * rows / cus;
-    int least = v.longest > all ? v.longest : all, length = 0;
-#pragma unroll
-    for (int i = 0; i < kLengths; ++i) {
-      const int L = s.least << i;
-      if (v.longest < 2 * L) continue;
-      const int w = (v.first[i] * rows + v.later[i] * (rows + unit)) / cus;
-      const int t = (w > L ? w : L) + (all > L ? all : L) + v.longest / L + kOverhead;
-      if (t < least) {
-        least = t;
-        length = L;
-      }
-    }
-    return length;
-  }
   __device__ __forceinline__ int length() const { return chosen ? *chosen : fixed; }
   // A sequence's first slot: no less room than its segments of `least` chunks take.
   __device__ __forceinline__ int base(const ChunkMap& cm, int seq) const {

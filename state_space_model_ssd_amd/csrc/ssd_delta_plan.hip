@@ -61,6 +61,7 @@ __global__ __launch_bounds__(kPlanThreads) void delta_plan_kernel(const DeltaArg
         for (int i = 0; i < DeltaSplit::kLengths; ++i) {
           v.first[i] += __shfl_xor(v.first[i], off);
           v.later[i] += __shfl_xor(v.later[i], off);
+          v.chain[i] = max(v.chain[i], __shfl_xor(v.chain[i], off));
         }
       }
       const int all = min(__shfl(sum, 63), a.max_chunks);
