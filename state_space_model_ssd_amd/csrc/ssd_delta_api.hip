@@ -29,7 +29,8 @@ constexpr size_t kDeltaAlign = 256;
 constexpr int64_t kDeltaFewGates = 65536;
 
 constexpr int kDeltaLeast = 16;          // chunks of the shortest segments of a sequence
-constexpr int kDeltaCutUnits = 64;       // a quarter of the device's CUs
+// A quarter of an MI355X's 256 CUs; a number of its own, as the workspace must not depend on the device.
+constexpr int kDeltaCutUnits = 64;
 
 bool dtype_ok(int32_t d) { return d == SSD_F32 || d == SSD_BF16; }
 size_t elem_size(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }

@@ -501,7 +501,7 @@ __global__ __launch_bounds__(64 * (NW + HW)) void delta_chain_kernel(const Delta
       for (int cb = 0; cb < 2; ++cb)
 #pragma unroll
         for (int i = 0; i < PX; ++i)
-          cA[cb][i] = buf_load16(ar, cb == 0 || w >= 2 ? (lower_index(w, cb) * PX + i) * kPiece + lane * 16 : 0xffffff00u);
+          cA[cb][i] = buf_load16(ar, cb == 0 || w >= 2 ? (triangle_index(w, cb) * PX + i) * kPiece + lane * 16 : 0xffffff00u);
       qp += C * (int64_t)qrow;
       Ap += a.H * (6 * PX * kPiece);
     }

@@ -194,8 +194,8 @@ __device__ __forceinline__ void store_opnd(float* p, const F8& v) {
 // triangular [64][64] one the tiles that are not zero follow in the order (tile of rows,
 // block of columns): lower (0,0) (1,0) (2,0) (3,0) (2,1) (3,1), upper (0,0) (1,0) (0,1) (1,1)
 // (2,1) (3,1).
-__host__ __device__ constexpr int lower_index(int u, int cb) { return cb == 0 ? u : u + 2; }
-__host__ __device__ constexpr int upper_index(int u, int cb) { return cb == 0 ? u : u + 2; }
+// Either way tile u of the second 32 columns follows two places behind.
+__host__ __device__ constexpr int triangle_index(int u, int cb) { return u + 2 * cb; }
 __device__ __forceinline__ int2 lower_tile(int i) { return i < 4 ? make_int2(i, 0) : make_int2(i - 2, 1); }
 __device__ __forceinline__ int2 upper_tile(int i) { return i < 2 ? make_int2(i, 0) : make_int2(i - 2, 1); }
 

@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, BWD ? 2 : 1) void delta_prep_kerne
         if constexpr (!BWD) {
           // four of the eight values of a lane
           const uint32_t at = 16u * (16 * (2 * (x & 1) + (la >> 1)) + l16);
-          char* p = static_cast<char*>(a.A) + (jh * 6 + lower_index(i, x / 2)) * O::PX * kPiece;
+          char* p = static_cast<char*>(a.A) + (jh * 6 + triangle_index(i, x / 2)) * O::PX * kPiece;
           put_half<T>(p, at, la & 1, f);
           // the block right of the diagonal's in the same 32 columns
           if (x == i && i % 2 == 0) put_half<T>(p, 16u * (16 * (2 + (la >> 1)) + l16), la & 1, kZero4);
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, BWD ? 2 : 1) void delta_prep_kerne
             }
           }
           const uint32_t at = 16u * (16 * (2 * (i & 1) + (la >> 1)) + i16);
-          char* p = static_cast<char*>(a.At) + (jh * 6 + upper_index(t, i / 2)) * O::PS * kPiece;
+          char* p = static_cast<char*>(a.At) + (jh * 6 + triangle_index(t, i / 2)) * O::PS * kPiece;
           put_half_pair<T>(p, at, la & 1, f);
         }
       }
