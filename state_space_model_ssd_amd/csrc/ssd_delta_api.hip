@@ -97,10 +97,12 @@ DeltaArgs delta_args(const ssd_delta_problem_t* p) {
   const int least = longest / 64 > kDeltaLeast ? (longest + 63) / 64 : kDeltaLeast;
   const bool few = p->nseq > 0 ? a.nstates <= DeltaSplit::kSequences && a.H * blocks <= kDeltaCutUnits
                                : (int64_t)a.nstates * a.H * blocks <= kDeltaCutUnits;
-  // a packed batch pays 4 to 8 us, backward 16, to find that nothing is to be cut (17 sequences of
-  // 400 tokens, 32 heads: 128 -> 136 us; backward, 16 heads: 309 -> 325), where 9 sequences of which one has half the tokens gain 70 (292 -> 222)
+  // to find that nothing is to be cut takes a packed batch 4 to 5 us, backward 15 to 24 (17 sequences
+  // of 400 tokens, 32 heads of 64 x 128: 95 -> 100 and 421 -> 445 us; 12 of 1000, 16 heads: 74 -> 78 and
+  // 333 -> 350); 9 of which one has half the tokens, 24 heads, gain 67 and 157 (285 -> 218, 982 -> 825)
   if (few && longest >= (p->nseq > 0 ? 4 : 2) * least) {
     a.split.least = least;
+    // a row's segments are no more than these; how many, the launch says
     a.split.per_row = a.nc_row / least + 1;
     a.split.slots = p->nseq > 0 ? a.nstates + a.max_chunks / least : a.nstates * a.split.per_row;
   }

@@ -228,7 +228,9 @@ struct ChainTask {
     const DeltaSplit& sp = a.split;
     none = unit >= (sp.slots ? sp.slots : a.nstates) * a.H;
     if (none) return;
-    seq = sp.slots ? sp.sequence(cm, a.nstates, slot) : slot;
+    const int length = sp.slots ? sp.length() : 0;
+    const int2 seg = sp.slots ? sp.segment(cm, a.nstates, length, slot) : make_int2(slot, 0);
+    seq = seg.x;
     const int2 r = cm.seq_range(seq);
     c0 = r.x;
     chunks = r.y - r.x;
@@ -243,8 +245,8 @@ struct ChainTask {
     parts = 1;
     if (!sp.slots) return;
     int per;
-    DeltaSplit::cut(chunks, sp.length(), parts, per);
-    part = slot - sp.base(cm, seq);
+    DeltaSplit::cut(chunks, length, parts, per);
+    part = seg.y;
     none = part >= parts;
     c0 += part * per;
     first += part * per * C;
@@ -834,8 +836,11 @@ __global__ __launch_bounds__(4 * N) void delta_starts_kernel(const DeltaArgs a, 
   int parts, per;
   DeltaSplit::cut(r.y - r.x, length, parts, per);
   if (parts < 2) return;
-  const int base = a.split.base(cm, seq);
-  auto slot = [&](int i) { return (int64_t)(BACK ? base + parts - 1 - i : base + i); };   // the i-th to run
+  const int others = a.split.others(cm, a.nstates, length, seq);
+  auto slot = [&](int i) {                        // of the i-th to run
+    const int part = BACK ? parts - 1 - i : i;
+    return (int64_t)(part == 0 ? seq : others + part - 1);
+  };
   const int lane = threadIdx.x & 63, l16 = lane & 15, la = lane >> 4, col = 16 * wave_id() + l16;
   struct Next {
     float m[N / 4], b[4];
@@ -897,6 +902,7 @@ hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
 // 21.6 us a forward with two, 23.2 with four; 2x4096 tokens, backward 549 and 592; 4x8192 tokens,
 // which fill the device with four, 553 and 431).
 int state_waves(const DeltaArgs& a) {
+  if (a.split.slots && a.split.block) return a.split.block / 16;    // as the estimate of segments has it
   const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H * ((a.P + 63) / 64);
   return a.P <= 32 || (!a.bf16 && a.N == 128) || 2 * units <= device_cus() ? 2 : 4;
 }
@@ -946,7 +952,10 @@ void settle(DeltaArgs& a) {
   DeltaSplit::Sums v = {};
   v.add(a.split, a.nc_row, a.nstates);
   a.split.fixed = DeltaSplit::best(a.split, v, a.max_chunks, a.H, a.P, a.N, a.split.block, device_cus());
-  if (a.split.fixed == 0) a.split.slots = 0;
+  int parts, per;
+  DeltaSplit::cut(a.nc_row, a.split.fixed, parts, per);
+  a.split.per_row = parts;
+  a.split.slots = parts > 1 ? a.nstates * parts : 0;
 }
 
 }  // namespace

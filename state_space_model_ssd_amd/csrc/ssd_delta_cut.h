@@ -29,6 +29,24 @@ struct DeltaCut {
     per = (n + parts - 1) / parts;
     parts = (n + per - 1) / per;
   }
+  // Slots of a packed batch's segments: sequence seq of n has slot seq for its first (or only) one,
+  // and from others() on slots for the rest.  One of c chunks has no more than c / length of these,
+  // so there is room for them behind those of the chunks before it, `first` in number.
+  SSD_SPLIT_FN static int others(int n, int length, int first) { return n + first / length; }
+  // The sequence and segment of a slot; no segment that the sequence has: none has the slot.
+  // `first(seq)`: the chunks before a sequence.
+  template <typename F> SSD_SPLIT_FN static void segment(int n, int length, int slot, F first, int& seq, int& part) {
+    seq = slot < n ? slot : 0;
+    part = slot < n ? 0 : 1 << 30;
+    if (slot < n || length <= 0) return;
+    int hi = n - 1;                      // the last sequence whose others are not behind this slot
+    while (seq < hi) {
+      const int mid = (seq + hi + 1) >> 1;
+      if (others(n, length, first(mid)) <= slot) seq = mid;
+      else hi = mid - 1;
+    }
+    part = 1 + slot - others(n, length, first(seq));
+  }
   // Chunks that the first passes have over all sequences, of first segments and of later ones; the
   // longest chain of the second pass, which has sequences in it that are too short to be cut and
   // yet longer than a segment; the longest sequence.

@@ -22,6 +22,9 @@ extern "C" int best(const int* n, int seqs, int least, int H, int P, int N, int 
   }
   return ssd::DeltaCut::best(c, v, chunks, H, P, N, block, cus);
 }
+extern "C" void segment(const int* first, int n, int length, int slot, int* out) {
+  ssd::DeltaCut::segment(n, length, slot, [&](int i) { return first[i]; }, out[0], out[1]);
+}
 extern "C" void cut(int n, int length, int* out) { ssd::DeltaCut::cut(n, length, out[0], out[1]); }
 """
 
@@ -93,3 +96,23 @@ def test_sequences_that_stay_whole_count(lib):
     """A sequence of 47 chunks is not cut into segments of 32, so with these the second pass takes
     47 steps: segments of 16 are shorter."""
     assert best(lib, [47, 141], 16, 16, 64, 128, 32, 256) == 16
+
+
+def test_every_segment_has_a_slot(lib):
+    """The sequences' first segments in the first slots, in order, so that where nothing is cut the
+    workgroups without work are behind all others; every other one in a slot of its own."""
+    r = random.Random(6)
+    for _ in range(300):
+        n = [r.choice((0, 1, r.randint(0, 40), r.randint(0, 300))) for _ in range(r.randint(1, 64))]
+        first = [sum(n[:i]) for i in range(len(n))]
+        least = r.choice((1, 16, 20))
+        length = r.choice((0, least, 2 * least, 4 * least))
+        arr, out, seen = (ctypes.c_int * len(n))(*first), (ctypes.c_int * 2)(), []
+        for slot in range(len(n) + (sum(n) + r.randint(0, 5)) // least):
+            lib.segment(arr, len(n), length, slot, out)
+            seq, part = out
+            if part < len(segments(lib, n[seq], length)):
+                seen.append((seq, part))
+                assert (part == 0) == (slot < len(n))
+        assert seen[:len(n)] == [(i, 0) for i in range(len(n))] and len(set(seen)) == len(seen)
+        assert len(seen) == sum(len(segments(lib, c, length)) for c in n)
