@@ -682,8 +682,12 @@ ssd_status_t ssd_block_norm_bwd(const ssd_block_norm_problem_t* p, const void* x
  * up to 2^30; chunks (of 64 tokens, a sequence's last one part-filled) * nheads, and
  * sequences * nheads * ceil(headdim / 32), up to 2^22.
  * The workspace (no initial contents) is ssd_delta_fwd_workspace_size bytes, 256-byte
- * aligned; calls that may overlap need one each.  No buffer that is written may share
- * memory with another (SSD_ERR_INVALID_ARG).  Deterministic.  Errors as for ssd_fwd.
+ * aligned; calls that may overlap need one each.  It is 20 KB (fp32: 26) per 64 tokens and
+ * head, more in fp32 per group and where long sequences of few heads are cut into segments:
+ * 312 MiB for 4 x 8192 tokens of 32 heads.  No buffer that is written may share memory with
+ * another (SSD_ERR_INVALID_ARG).  Deterministic: the same call gives the same bits.  Those of
+ * one sequence may differ between batches, as a call's sizes and lengths say where its
+ * sequences are cut.  Errors as for ssd_fwd.
  */
 typedef struct {
   int64_t batch;       /* rows, up to 65535; 1 for a packed batch           */
@@ -723,7 +727,10 @@ ssd_status_t ssd_delta_fwd(const ssd_delta_problem_t* p, const void* q, const vo
  * of dg as a rule.  Where dg is small beside its products it is off by more of its own size (beta
  * 1 and keys 0.02 apart: 1e-2; beta 1, equal keys and no decay: dg is zero but for this error);
  * fp32 gates are for callers to whom that matters.
- * Workspace: ssd_delta_bwd_workspace_size bytes, as for the forward.
+ * Workspace: ssd_delta_bwd_workspace_size bytes, as for the forward, with the states of all
+ * chunks: per 64 tokens and head 38 KB and 4 P N + 384 P bytes (P headdim, N dstate), or
+ * 8 P N + 512 P in fp32, with fp32 gates and below those 65536.  4 x 8192 tokens of 32 heads of
+ * 128 x 128 take 2.3 GiB, with fp32 gates 3.6 GiB.
  */
 size_t ssd_delta_bwd_workspace_size(const ssd_delta_problem_t* p);
 
@@ -784,8 +791,10 @@ ssd_status_t ssd_delta_step(const ssd_delta_step_problem_t* p, const void* q, co
  *   positions [tokens] int32, inv_freq [rotary_pairs] fp32 (with rotary_pairs > 0)
  *   q_out, k_out  contiguous, dtype
  * Accumulation in fp32, one rounding of each output; angles are reduced in fp64, so a
- * far position is as exact as a near one.  headdim up to 256, heads up to 4096 each,
- * tokens up to 2^30 (beyond: SSD_ERR_UNSUPPORTED); any alignment of the dtype's size.
+ * far position is as exact as a near one.  Squares are summed in fp32 as well: values beyond
+ * 1e18, or with eps 0 rows of values below 1e-18, leave its range.  headdim up to 256, heads up
+ * to 4096 each, tokens up to 2^30 (beyond: SSD_ERR_UNSUPPORTED); any alignment of the dtype's
+ * size.
  * No buffer that is written may share memory with another (SSD_ERR_INVALID_ARG), but
  * strided rows may lie beside others of the same stride.  Errors as for ssd_fwd.
  */
