@@ -32,12 +32,14 @@
 // are cut (DeltaSplit), backward too: each segment runs once from zeros, for what it adds to a state (B), and with
 // as many more rows as the state has columns from a unit matrix without values, for what becomes of
 // a state (M); delta_starts_kernel makes the states that segments start from out of these; then all
-// run side by side.  1x8192 tokens, 24 heads of 64 x 128: 233 -> 139 us a forward, of which B and M
-// 52, the states 16, the segments of 16 chunks 44; 16 heads of 64 x 64, backward: 430 -> 227 us.
+// run side by side.  1x8192 tokens, 24 heads of 64 x 128: 233 -> 136 us a forward; 16 heads of 64 x 64,
+// backward: 430 -> 231 us.  The packed prompts of 14371 tokens, 24 heads of 64 x 128: B and M 87, the
+// states 20, the segments of 16 chunks 83 us.
 //
-// 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): 299 us,
-// 2.3 us a step, of which the state waves work 1.9 and the helpers 2.1; LDS, with some 370 KB read
-// and written a step at 128 bytes a clock, is busy for 1.2.
+// 4x8192 tokens, 32 heads of 128 x 128, bf16 (256 workgroups, 128 steps): 310 us in a graph, 326 with
+// counters, 2.4 to 2.5 us a step.  LDS is busy for 0.47 of it, matrix instructions for 0.25, and 1.39 GB
+// are read and written, 4.3 TB/s; half of the waves' time they wait to issue.  2x4096 tokens, backward:
+// 129 us for the states, 185 for their gradients (3 TB/s, LDS 0.3).
 #include <type_traits>
 
 #include "ssd_delta_device.h"
@@ -899,8 +901,8 @@ hipError_t chain_go(const DeltaArgs& a, hipStream_t s) {
 
 // Two state waves where heads have no more rows, where fp32 operands of dstate 128 leave LDS for
 // no more, and where four would leave half the device idle (200 tokens of 32 heads of 128 x 128:
-// 21.6 us a forward with two, 23.2 with four; 2x4096 tokens, backward 549 and 592; 4x8192 tokens,
-// which fill the device with four, 553 and 431).
+// 26.8 us a forward with two, 28.9 with four; 2x4096 tokens, backward 581 and 623; 4x8192 tokens,
+// which fill the device with four, 563 and 445).
 int state_waves(const DeltaArgs& a) {
   if (a.split.slots && a.split.block) return a.split.block / 16;    // as the estimate of segments has it
   const int64_t units = (int64_t)(a.split.slots ? a.split.slots : a.nstates) * a.H * ((a.P + 63) / 64);

@@ -25,10 +25,9 @@
 // the values as rows (read transposed) and whose dO as operands; beta joins R in the results; the next slabs' loads are in
 // flight meanwhile, also those of the next head.
 //
-// 2x4096 tokens, 32 heads in 16 groups of 128 x 128, bf16: 234 us for 700 MB (3 TB/s).  A head and
-// chunk takes a workgroup 11 us, of which the products of the slabs 1.5, what waits for them and for
-// memory 4, P and M 2.5 and dq and dk 1; 250 registers and 125 KB of LDS leave room for one
-// workgroup on a CU, so nothing else runs in the gaps.
+// 2x4096 tokens, 32 heads in 16 groups of 128 x 128, bf16: 244 us for 747 MB (3.1 TB/s); S and dS as
+// pairs too 337.  LDS is busy for 0.31 of it, matrix instructions for 0.14; 256 registers and 133 KB
+// of LDS leave room for one workgroup on a CU, so nothing else runs while its waves wait.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)

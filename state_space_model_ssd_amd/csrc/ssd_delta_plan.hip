@@ -4,7 +4,8 @@
 // Up to a wave's count of sequences in one launch, every workgroup of which adds up the sequences'
 // chunks by itself; more take the scan's two launches and one that clears.  Each of these is 2 to
 // 3 us and the gap before it (9 packed prompts of 14371 tokens, 24 heads of 64 x 128: 224 us a
-// forward with four launches, 217 with one; 340 tokens in three sequences, 16 heads: 29.6 and 26.0).
+// forward with four launches, 217 with one; 340 tokens in three sequences, 16 heads: 29.6 and 26.0, as
+// measured when they were joined).
 #include "ssd_delta.h"
 #include "ssd_kernels.h"
 

@@ -20,9 +20,10 @@
 // theirs in common.  A wave shares nothing with the others of its workgroup and waits for
 // none; its LDS holds k's rows first, then each head's T.
 //
-// 4x8192 tokens, 32 heads in 16 groups of 128 x 128, bf16: 131 us for 595 MB read and written
-// (4.5 TB/s), a bound of memory.  One chunk takes 10 us (7 of 32 tokens at most): loads, products,
-// fp64 sums and the inverse, one after another in one wave.
+// 4x8192 tokens, 32 heads in 16 groups of 128 x 128, bf16: 132 to 145 us for 617 MB read and written
+// (4.5 TB/s), a bound of memory; for the backward 2x4096 50 us for 230 MB, of which T' takes 4.
+// One chunk takes 10 us (7 of 32 tokens at most): loads, products, fp64 sums and the inverse, one
+// after another in one wave.
 #include "ssd_delta_device.h"
 
 #pragma clang fp contract(on)
