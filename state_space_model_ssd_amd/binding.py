@@ -1008,7 +1008,8 @@ def delta_bwd(q, k, v, g, beta, dout, dfinal_states=None, scale=None, initial_st
     """ssd_delta_bwd: gradients of sum(out * dout) + sum(final_states * dfinal_states) for
     delta_fwd's arguments.  Returns a dict with q, k, v, g, beta (each like its argument;
     rows of tokens outside every sequence are zeros), initial_states (None without one) and
-    the workspace."""
+    the workspace.  With bf16 g and beta of 65536 tokens times heads or more their gradients come
+    from states rounded to bf16 (include/ssd.h says how far off); fp32 ones do not."""
     dev, sshape, prob = _delta_checked("delta_bwd", q, k, v, g, beta, scale, initial_states,
                                        cu_seqlens, True)
     _need(dout, "dout", v.dtype, v.shape, dev)
